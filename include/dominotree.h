@@ -252,6 +252,96 @@ dt_status dt_tree_attention(int B, int n, int L, int Hq, int Hkv, int d, const v
                             size_t workspace_bytes, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------------------------------------------
+ * The paged key/value cache and its attention: what the target model's passes around a round need. No counterpart in
+ * the paper, whose verify pass takes attention and cache as given (gist.science, "Composants Clés — Vérification").
+ *
+ * The cache is two pools of pages, k_cache and v_cache [num_pages,Hkv,page_size,d] bf16: a page holds page_size tokens,
+ * head by head. Token i of request b sits in page page_table[b][i / page_size] at row i % page_size; its slot is
+ * page * page_size + row. Pages may be shared by requests and lie in any order; what unused rows hold is never looked
+ * at (it may be NaN). Common limits (DT_ERR_UNSUPPORTED beyond): dtype DT_BF16, d = 64 or 128, page_size a power of two
+ * in DT_MIN_PAGE .. DT_MAX_PAGE, num_pages * page_size and Hq, Hkv within 32-bit and DT_MAX_HEADS. */
+#define DT_MIN_PAGE 8
+#define DT_MAX_PAGE 256
+#define DT_MAX_HEADS 256
+#define DT_PAGED_MAX_BATCH 2048           /* requests of one dt_paged_attention call          */
+#define DT_PAGED_MAX_TOKENS (1 << 24)     /* max_pages * page_size: a request's longest cache */
+
+/* ---------------------------------------------------------------------------------------------------------------
+ * dt_kv_append — N tokens' keys and values into the paged cache, rotated by their positions on the way.
+ *
+ * Rotary embedding (arXiv 2104.09864): of each head's first `rot` elements, pair i is turned by the angle whose cosine
+ * and sine the table holds for the token's position, (a, b) -> (a cos - b sin, b cos + a sin), in fp32 with one
+ * rounding to bf16. Pair i is elements (i, i + rot/2), or (2i, 2i + 1) when `interleaved`. Elements past rot, and the
+ * values, are copied bit for bit. Queries, when given, are rotated into out_q; with out_k the rotated keys also land in
+ * a dense array (dt_prompt_attention reads it).
+ *   q [N,Hq,d], k, v [N,Hkv,d] bf16, tokens q_stride, k_stride, v_stride elements apart (multiples of 8, at least a
+ *               token's width: views of one fused projection's output serve). No queries: Hq = 0, q = out_q = NULL.
+ *   slots       [N] int32: where each token goes. A negative slot marks a padding token: nothing of it is read or
+ *               written. Slots are distinct (of two tokens that name one slot, which is kept is unspecified).
+ *   positions   [N] int32 and rope [max_pos, rot] fp32 (a position's rot / 2 cosines, then its sines), any frequency
+ *               schedule; NULL when rot = 0 (nothing is rotated). A draft tree's node has the position of its depth,
+ *               whatever its slot.
+ *   out_q       [N,Hq,d]; out_k [N,Hkv,d] or NULL. They may be q and k themselves where those are dense, and
+ *               otherwise overlap no input.
+ *   workspace   256 bytes, initialised by dt_workspace_init: the status word. A slot past the pool or a position
+ *               outside [0, max_pos) sets DT_ERR_INVALID_ARG there and its token is left out like a padding one.
+ * rot is a multiple of 16, at most d (other even values: DT_ERR_UNSUPPORTED).
+ * To keep a verified tree's accepted path, append the accepted nodes again with slots prefix + j (dt_accept_paths)
+ * and a negative slot for the rest.
+ * ------------------------------------------------------------------------------------------------------------- */
+dt_status dt_kv_append(int N, int Hq, int Hkv, int d, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                       const void* v, int64_t v_stride, dt_dtype dtype, const int32_t* slots, const int32_t* positions,
+                       const float* rope, int max_pos, int rot, int interleaved, void* out_q, void* out_k,
+                       void* k_cache, void* v_cache, int num_pages, int page_size, void* workspace,
+                       size_t workspace_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------------------------------------
+ * dt_paged_attention — attention of each request's newest n tokens over its paged cache: one new token (n = 1), or a
+ * draft tree's nodes in the verify pass. As dt_tree_attention, with a cache in pages and a length per request.
+ *
+ * Semantics: request b's cache holds lens[b] tokens, the last n of them the query tokens' own (append them first).
+ * Node i of request b sees every token before those n and, of the n, those with mask[b][i][t] = 1; without a mask the
+ * tokens up to its own (t <= i). out[b][i][h] = sum_j softmax_j(scale * q[b][i][h] . k_j) v_j over them, query head h
+ * reading key/value head h / (Hq / Hkv); a node that sees nothing gets zeros. Arithmetic as dt_tree_attention (bf16
+ * products, fp32 accumulation, softmax weights rounded to bf16), the output rounded to bf16 once. Keys and values that
+ * a node does not see do not reach its output, finite or not.
+ *   q           [B,n,Hq,d] bf16; out [B,n,Hq,d] bf16.
+ *   page_table  [B,max_pages] int32; entries past a request's last page are not read.
+ *   lens        [B] int32, in n .. max_pages * page_size. lens[b] <= 0 marks an unused row of the batch: its output is
+ *               zero. Other lengths, and pages outside the pool, set DT_ERR_INVALID_ARG in the status word; such a
+ *               length's output is zero, such a page's request's output unspecified.
+ *   mask        [B,n,n] uint8 as dt_build_trees emits it (any alignment), or NULL.
+ *   workspace   dt_paged_attention_workspace_bytes(B,n,Hq,Hkv,d) bytes on the current device, initialised by
+ *               dt_workspace_init; serves any lengths. After DT_ERR_TIMEOUT (dt_get_error) initialise it again.
+ * Supported beyond the common limits: (Hq / Hkv) * n <= 128, n <= 64, B <= DT_PAGED_MAX_BATCH, max_pages * page_size <=
+ * DT_PAGED_MAX_TOKENS.
+ * ------------------------------------------------------------------------------------------------------------- */
+size_t dt_paged_attention_workspace_bytes(int B, int n, int Hq, int Hkv, int d);
+dt_status dt_paged_attention(int B, int n, int Hq, int Hkv, int d, const void* q, const void* k_cache,
+                             const void* v_cache, dt_dtype dtype, int num_pages, int page_size,
+                             const int32_t* page_table, int max_pages, const int32_t* lens, const uint8_t* mask,
+                             float scale, void* out, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------------------------------------
+ * dt_prompt_attention — causal attention over B whole prompts, packed one after the other (before the first round).
+ *
+ * Semantics: prompt b is rows cu_seqlens[b] .. cu_seqlens[b+1] - 1; its row i sees its rows 0..i:
+ * out[row][h] = sum_j softmax_j(scale * q[row][h] . k_j) v_j, query head h reading key/value head h / (Hq / Hkv).
+ * Arithmetic as dt_paged_attention; what a row does not see (later rows, other prompts) does not reach its output,
+ * finite or not. Rows before cu_seqlens[0] and from cu_seqlens[B] on are left as they were.
+ *   q [total,Hq,d], k, v [total,Hkv,d] bf16, rows q_stride, k_stride, v_stride elements apart as in dt_kv_append;
+ *   out [total,Hq,d] bf16, dense, overlapping no input.
+ *   cu_seqlens  [B+1] int32, not decreasing, within 0 .. total (a prompt may be empty). Otherwise
+ *               DT_ERR_INVALID_ARG in the status word, and which rows are written is unspecified.
+ *   workspace   dt_prompt_attention_workspace_bytes(total,B,Hq,Hkv,d) bytes, initialised by dt_workspace_init.
+ * ------------------------------------------------------------------------------------------------------------- */
+size_t dt_prompt_attention_workspace_bytes(int total, int B, int Hq, int Hkv, int d);
+dt_status dt_prompt_attention(int total, int B, int Hq, int Hkv, int d, const void* q, int64_t q_stride, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride, dt_dtype dtype,
+                              const int32_t* cu_seqlens, float scale, void* out, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------------------------------------
  * dt_topm_static — dt_topm for callers that cannot allocate device memory.
  * No counterpart in the paper: this is a deployment variant of dt_topm, with the same arguments minus the
  * workspace and bit-identical results.

@@ -1,0 +1,429 @@
+// dt_prompt_attention — causal attention over whole prompts, packed one after the other.
+//
+// Token i of a prompt sees its prompt's tokens 0..i: out[i][h] = softmax_j<=i(scale q[i][h].k_j) v_j, query head h
+// reading key/value head h / (Hq / Hkv).
+//
+// GB300 design: bound by the tensor cores. A CTA owns 256 query rows of one head as two tiles of 128 and walks the
+// keys in blocks of 128, shared by both tiles. Per tile and block: S = Q K^T (both operands in shared memory) into
+// tensor memory, a softmax by the tile's own four warps (thread = query row, so no statistic needs a shuffle), the
+// weights written back as bf16 over their own scores in tensor memory, and O += P V with P read from there, so that
+// P never passes through shared memory. The tiles alternate: while one is in its softmax the tensor cores work on the
+// other. Softmax in base 2, fp32; the running maximum is raised (and O rescaled) only past a headroom of 2^8, which
+// keeps the weights below 2^8 and leaves O alone in nearly every block. P is rounded to bf16, the only rounding
+// before the output's; the row sums are taken in fp32 from the unrounded weights.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+
+#include "dt_internal.cuh"
+#include "umma.cuh"
+
+namespace dt {
+namespace {
+
+constexpr int kPrTile = 128;                 // query rows of a tile
+constexpr int kPrRows = 2 * kPrTile;         // of a CTA
+constexpr int kPrKeys = 128;                 // keys per block
+constexpr int kPrThreads = 384;              // warps 0-3: load, MMA, two idle; 4-7 and 8-11: the tiles' softmax
+constexpr float kPrLazy = 8.f;               // log2 headroom before the running maximum is raised
+constexpr uint64_t kPrBudgetNs = 4000000000ull;
+constexpr uint32_t kPrBox = kPrKeys * 128;   // 128 rows x 64 elements: 16 KB
+
+struct PrParams {
+  int total, B, Hq, Hkv, G, slots;
+  const int32_t* cu;           // [B + 1]
+  const unsigned short* v;     // re-read only for values that are not finite
+  long long v_stride;
+  float scale_log2;            // scale * log2(e)
+  unsigned short* out;         // [total][Hq][D]
+};
+struct PrMaps {
+  CUtensorMap q, k, v;  // [total][heads][D], box 64 x 1 x 128
+};
+
+__device__ __forceinline__ float pr_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pr_pack(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void pr_ld32(uint32_t taddr, float* v) {  // 32 columns of the thread's lane, waited for
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void pr_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// The prompt that owns tile slot `slot`. Prompt b's tiles start at slot cu[b] / 256 + b: its ceil(len / 256) tiles end
+// before the next prompt's start, so the slots are found by search, without a scan of the lengths; some stay unused.
+__device__ __forceinline__ int pr_start(const PrParams& p, int b) { return p.cu[b] / kPrRows + b; }
+__device__ __forceinline__ int pr_find(const PrParams& p, int slot, int lane) {  // -1: before the first prompt
+  int lo = 0, n = p.B;
+  while (true) {  // 32-ary: `n` shrinks to ceil(n / 32) each round
+    const int step = (n + 31) / 32;
+    const int b = lo + lane * step;
+    const bool in = lane * step < n && b < p.B && pr_start(p, b) <= slot;
+    const unsigned hits = __ballot_sync(0xFFFFFFFFu, in);
+    if (hits == 0u) return -1;
+    lo += (31 - __clz(hits)) * step;
+    if (step == 1) return lo;
+    n = step;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, const __grid_constant__ PrMaps maps,
+                                                                    WsHeader* hdr) {
+  constexpr int kHalves = D / 64;
+  constexpr uint32_t kTileBytes = kHalves * kPrBox;          // one Q tile, one K block or one V block
+  constexpr int kStages = D == 128 ? 5 : 8;                  // ring entries: K and V blocks in turn
+  extern __shared__ float4 smem_f4[];
+  unsigned char* sq =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_f4) + 1023) & ~uintptr_t(1023));
+  unsigned char* skv = sq + 2 * kTileBytes;
+  __shared__ uint64_t q_full[2], kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2], o_full[2];
+  __shared__ uint32_t s_tmem;
+  __shared__ unsigned s_issued, s_used;  // ring entries issued and waited for (failure drain)
+  __shared__ int s_bad;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+
+  if (blockIdx.x == 0 && warp == 2) {  // lengths that contradict themselves are reported once
+    bool bad = lane == 0 && (p.cu[0] < 0 || p.cu[p.B] > p.total);
+    for (int b = lane; b < p.B; b += 32) bad = bad || p.cu[b] > p.cu[b + 1];
+    if (bad) record_error(hdr, DT_ERR_INVALID_ARG);
+  }
+  // heavy tiles (late in their prompts) first; the heads of one tile next to each other share keys through L2
+  const int slot = p.slots - 1 - static_cast<int>(blockIdx.x) / p.Hq, head = static_cast<int>(blockIdx.x) % p.Hq;
+  const int b = pr_find(p, slot, lane);
+  if (b < 0) return;
+  const int lo = p.cu[b], hi = p.cu[b + 1];
+  if (lo < 0 || hi > p.total || lo >= hi) return;
+  const int len = hi - lo, q0 = (slot - pr_start(p, b)) * kPrRows;
+  if (q0 < 0 || q0 >= len) return;
+  const int kvh = head / p.G;
+  // blocks of each tile: up to its last row's own (the tiles start on block borders); a tile past the end has none
+  const int n0 = q0 / kPrKeys + 1, n1 = q0 + kPrTile < len ? n0 + 1 : 0, nblk = n1 > n0 ? n1 : n0;
+
+  if (t == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+    }
+    mbar_fence_init();
+    s_issued = s_used = 0u;
+    s_bad = 0;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                 "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = s_tmem;  // columns: S0 and P0 at 0, S1 and P1 at 128, O0 at 256, O1 at 384
+  bool ok = true;
+
+  if (warp == 0 && lane == 0) {  // TMA: Q0, K0, Q1, V0, K1, V1, ...
+    unsigned e = 0;
+    auto load_q = [&](int i) {
+      mbar_expect_tx(&q_full[i], kTileBytes);
+      for (int h = 0; h < kHalves; ++h)
+        tma_load_3d(sq + i * kTileBytes + h * kPrBox, &maps.q, 64 * h, head, lo + q0 + i * kPrTile, &q_full[i]);
+    };
+    auto load_kv = [&](const CUtensorMap* map, int j) {
+      const unsigned st = e % kStages, use = e / kStages;
+      if (use > 0 && !mbar_wait(&kv_empty[st], (use - 1) & 1u, kPrBudgetNs)) return false;
+      mbar_expect_tx(&kv_full[st], kTileBytes);
+      for (int h = 0; h < kHalves; ++h)
+        tma_load_3d(skv + st * kTileBytes + h * kPrBox, map, 64 * h, kvh, lo + j * kPrKeys, &kv_full[st]);
+      s_issued = ++e;
+      return true;
+    };
+    load_q(0);
+    for (int j = 0; j < nblk && ok; ++j) {
+      ok = load_kv(&maps.k, j);
+      if (j == 0 && n1 > 0) load_q(1);
+      if (ok) ok = load_kv(&maps.v, j);
+    }
+  } else if (warp == 1 && lane == 0) {  // MMA
+    const uint32_t id_s = umma_idesc(kPrKeys, 128), id_o = umma_idesc(D, 128) | (1u << 16);  // O: V MN-major
+    auto wait_entry = [&](unsigned e) {
+      if (!mbar_wait(&kv_full[e % kStages], (e / kStages) & 1u, kPrBudgetNs)) return false;
+      if (s_used < e + 1u) s_used = e + 1u;
+      return true;
+    };
+    auto issue_s = [&](int i, int j) {  // S_i = Q_i K_j^T (the block's keys are ring entry 2 j)
+      const uint32_t aq = smem_u32(sq + i * kTileBytes), bk = smem_u32(skv + (2 * j % kStages) * kTileBytes);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk >> 2) * kPrBox + (kk & 3) * 32u;
+        umma_f16(tmem + 128u * i, umma_desc_sw128(aq + off), umma_desc_sw128(bk + off), id_s, kk > 0 ? 1u : 0u);
+      }
+      umma_commit(&s_full[i]);
+    };
+    auto issue_o = [&](int i, int j) {  // O_i += P_i V_j (ring entry 2 j + 1)
+      const uint32_t bv = smem_u32(skv + ((2 * j + 1) % kStages) * kTileBytes);
+#pragma unroll
+      for (int kk = 0; kk < kPrKeys / 16; ++kk)
+        umma_f16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk,
+                    umma_desc_sw128_mn(bv + 2048u * kk, kPrBox, 1024u), id_o, (j > 0 || kk > 0) ? 1u : 0u);
+    };
+    const int n[2] = {n0, n1};
+    ok = wait_entry(0);
+    for (int i = 0; i < 2 && ok; ++i)
+      if (n[i] > 0) {
+        ok = mbar_wait(&q_full[i], 0, kPrBudgetNs);
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if (ok) issue_s(i, 0);
+      }
+    if (ok) umma_commit(&kv_empty[0]);
+    for (int j = 0; j < nblk && ok; ++j) {
+      ok = wait_entry(2 * j + 1);
+      if (ok && j + 1 < nblk) ok = wait_entry(2 * j + 2);
+      for (int i = 0; i < 2 && ok; ++i) {
+        if (j >= n[i]) continue;
+        ok = mbar_wait(&p_full[i], j & 1u, kPrBudgetNs);
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        issue_o(i, j);
+        if (j + 1 == n[i]) umma_commit(&o_full[i]);
+        // the next scores overwrite P: the tensor cores run this thread's products in order
+        if (j + 1 < n[i]) issue_s(i, j + 1);
+      }
+      if (ok) {
+        umma_commit(&kv_empty[(2 * j + 1) % kStages]);
+        if (j + 1 < nblk) umma_commit(&kv_empty[(2 * j + 2) % kStages]);
+      }
+    }
+  } else if (warp >= 4) {  // softmax of tile i: thread r owns query row r
+    const int i = (warp - 4) >> 2, r = t - 128 - 128 * i, nb = i ? n1 : n0;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + lanes + 128u * i, to = tmem + lanes + 256u + 128u * i;
+    const int row = q0 + i * kPrTile + r;  // the row's token in its prompt
+    float m = -INFINITY, l = 0.f;          // running maximum (of the unscaled scores) and sum
+    for (int j = 0; j < nb && ok; ++j) {
+      const bool diag = j + 1 == nb;
+      if (diag) {
+        // The block where the tile's rows see different keys. A weight of zero does not hide a value that is not
+        // finite from the tensor cores (0 x inf is NaN): rows past the prompt's end are cleared, and what is not
+        // finite among the block's values is cleared too and added to the rows that see it at the end (its weight
+        // there is positive, and any positive multiple of it gives the same sum).
+        const unsigned e = 2u * j + 1u;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&kv_full[e % kStages], (e / kStages) & 1u, kPrBudgetNs));
+        if (!ok) break;
+        unsigned char* sv = skv + (e % kStages) * kTileBytes;
+        const int valid = len - j * kPrKeys;  // keys of the block inside the prompt
+        __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
+        const __nv_bfloat162 zero = acc;
+#pragma unroll 4
+        for (int c = r; c < kHalves * kPrKeys * 8; c += 128) {  // 16-byte pieces; eight a row
+          uint4* at = reinterpret_cast<uint4*>(sv + 16 * c);
+          if (((c >> 3) & (kPrKeys - 1)) >= valid) {
+            *at = make_uint4(0u, 0u, 0u, 0u);
+          } else {
+            const uint4 x = *at;
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int k2 = 0; k2 < 4; ++k2)
+              acc = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[k2]), zero, acc);  // x 0: NaN if not finite
+          }
+        }
+        const float2 a2 = __bfloat1622float2(acc);
+        if (!(a2.x == 0.f && a2.y == 0.f)) {  // rare
+          for (int c = r; c < kHalves * kPrKeys * 8; c += 128) {
+            unsigned short* at = reinterpret_cast<unsigned short*>(sv + 16 * c);
+            for (int k2 = 0; k2 < 8; ++k2)
+              if ((at[k2] & 0x7F80u) == 0x7F80u) at[k2] = 0;
+          }
+          atomicOr(&s_bad, 1 << i);
+        }
+      }
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_full[i], j & 1u, kPrBudgetNs));
+      if (!ok) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      float s[128];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) pr_ld32(ts + 32u * h, s + 32 * h);
+      if (diag) {
+        const int lim = row - j * kPrKeys;  // the last key the row sees
+#pragma unroll
+        for (int c = 0; c < 128; ++c) s[c] = c <= lim ? s[c] : -INFINITY;
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+      const float bmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      const bool raise = (bmax - m) * p.scale_log2 > kPrLazy || (m == -INFINITY && bmax > -INFINITY);
+      const bool rescale_o = raise && m > -INFINITY;
+      const float mn = raise ? bmax : m;
+      const float alpha = rescale_o ? pr_exp2((m - mn) * p.scale_log2) : 1.f;
+      m = mn;
+      const float mref = m == -INFINITY ? 0.f : m * p.scale_log2;
+      if (__any_sync(0xFFFFFFFFu, rescale_o)) {  // S is full, so the products into O before it are complete
+#pragma unroll
+        for (int h = 0; h < D / 16; ++h) {
+          uint32_t ov[16];
+          asm volatile(
+              "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+              "\n\ttcgen05.wait::ld.sync.aligned;"
+              : "=r"(ov[0]), "=r"(ov[1]), "=r"(ov[2]), "=r"(ov[3]), "=r"(ov[4]), "=r"(ov[5]), "=r"(ov[6]), "=r"(ov[7]),
+                "=r"(ov[8]), "=r"(ov[9]), "=r"(ov[10]), "=r"(ov[11]), "=r"(ov[12]), "=r"(ov[13]), "=r"(ov[14]),
+                "=r"(ov[15])
+              : "r"(to + 16u * h)
+              : "memory");
+#pragma unroll
+          for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+          pr_st16(to + 16u * h, ov);
+        }
+      }
+      float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          const float a = pr_exp2(fmaf(s[32 * h + c], p.scale_log2, -mref));
+          const float bb = pr_exp2(fmaf(s[32 * h + c + 1], p.scale_log2, -mref));
+          ls[c & 2] += a;
+          ls[(c & 2) + 1] += bb;
+          pk[c >> 1] = pr_pack(a, bb);
+        }
+        pr_st16(ts + 16u * h, pk);
+      }
+      l = l * alpha + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      if (diag) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the cleared values
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[i]);
+    }
+    if (nb > 0 && ok) {
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&o_full[i], 0, kPrBudgetNs));
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      if (ok) {
+        const float inv = 1.f / l;  // the row's own key is visible; a sum of 0 or NaN gives NaN
+        const int bad = *reinterpret_cast<volatile int*>(&s_bad);
+        unsigned short* po = p.out + (static_cast<size_t>(lo + row) * p.Hq + head) * D;
+#pragma unroll
+        for (int h = 0; h < D / 32; ++h) {
+          float o[32];
+          pr_ld32(to + 32u * h, o);
+          if (row >= len) continue;
+          if (bad) {  // rare: tile 0's clearing reaches tile 1 too, which shares the block
+            for (int key = (n0 - 1) * kPrKeys; key <= row; ++key) {
+              const unsigned short* vr = p.v + static_cast<size_t>(lo + key) * p.v_stride + kvh * D + 32 * h;
+#pragma unroll
+              for (int c = 0; c < 32; ++c) {
+                const uint32_t bits = static_cast<uint32_t>(vr[c]) << 16;
+                if ((bits & 0x7F800000u) == 0x7F800000u) o[c] += __uint_as_float(bits);
+              }
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 32; c += 8)
+            *reinterpret_cast<uint4*>(po + 32 * h + c) =
+                make_uint4(pr_pack(o[c] * inv, o[c + 1] * inv), pr_pack(o[c + 2] * inv, o[c + 3] * inv),
+                           pr_pack(o[c + 4] * inv, o[c + 5] * inv), pr_pack(o[c + 6] * inv, o[c + 7] * inv));
+        }
+      }
+    }
+  }
+  ok = __syncthreads_and(ok);
+  if (!ok && t == 0) {
+    record_error(hdr, DT_ERR_TIMEOUT);
+    // copies issued but never waited for must land before the CTA leaves: wait for them too (bounded)
+    for (unsigned e = s_used; e < s_issued; ++e) mbar_wait(&kv_full[e % kStages], (e / kStages) & 1u, kPrBudgetNs);
+    mbar_wait(&q_full[0], 0, kPrBudgetNs);
+    if (n1 > 0 && s_issued > 0) mbar_wait(&q_full[1], 0, kPrBudgetNs);
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+template <int D>
+dt_status pr_launch(const PrParams& p, const PrMaps& maps, WsHeader* hdr, cudaStream_t stream) {
+  constexpr size_t smem = 1024 + (2 + (D == 128 ? 5 : 8)) * static_cast<size_t>(D / 64) * kPrBox;
+  const void* fn = reinterpret_cast<const void*>(prompt_attn_kernel<D>);
+  if (ensure_dynamic_smem(fn, smem) != cudaSuccess) return DT_ERR_CUDA;
+  prompt_attn_kernel<D><<<static_cast<unsigned>(p.slots * p.Hq), kPrThreads, smem, stream>>>(p, maps, hdr);
+  return cuda_status(cudaGetLastError());
+}
+
+}  // namespace
+}  // namespace dt
+
+extern "C" size_t dt_prompt_attention_workspace_bytes(int total, int B, int Hq, int Hkv, int d) {
+  if (total < 1 || B < 1 || Hq < 1 || Hkv < 1 || d < 1 || Hq % Hkv != 0) return 0;
+  return sizeof(dt::WsHeader);
+}
+
+extern "C" dt_status dt_prompt_attention(int total, int B, int Hq, int Hkv, int d, const void* q, int64_t q_stride,
+                                         const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                         dt_dtype dtype, const int32_t* cu_seqlens, float scale, void* out,
+                                         void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  using namespace dt;
+  if (total < 0 || B < 0 || Hq < 1 || Hkv < 1 || d < 1 || Hq % Hkv != 0) return DT_ERR_INVALID_ARG;
+  if (dtype != DT_F32 && dtype != DT_BF16) return DT_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return DT_ERR_INVALID_ARG;
+  if (total == 0 || B == 0) return DT_OK;
+  const void* ptrs[] = {q, k, v, out, workspace};
+  for (const void* x : ptrs)
+    if (!x || !aligned16(x)) return DT_ERR_INVALID_ARG;
+  if (!cu_seqlens || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u)) return DT_ERR_INVALID_ARG;
+  if (workspace_bytes < sizeof(WsHeader)) return DT_ERR_INVALID_ARG;
+  if (Hq > DT_MAX_HEADS) return DT_ERR_UNSUPPORTED;
+  const int64_t width[3] = {static_cast<int64_t>(Hq) * d, static_cast<int64_t>(Hkv) * d, static_cast<int64_t>(Hkv) * d};
+  const int64_t stride[3] = {q_stride, k_stride, v_stride};
+  for (int i = 0; i < 3; ++i)
+    if (stride[i] < width[i] || stride[i] % 8 != 0 || stride[i] > INT_MAX) return DT_ERR_INVALID_ARG;
+  if (dtype != DT_BF16 || (d != 64 && d != 128)) return DT_ERR_UNSUPPORTED;
+  const long long slots = total / kPrRows + static_cast<long long>(B);
+  if (total > INT_MAX / 2 || slots * Hq > INT_MAX) return DT_ERR_UNSUPPORTED;
+  PrParams p{};
+  p.total = total; p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.slots = static_cast<int>(slots);
+  p.cu = cu_seqlens;
+  p.v = static_cast<const unsigned short*>(v);
+  p.v_stride = v_stride;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.out = static_cast<unsigned short*>(out);
+  PrMaps maps{};
+  const uint64_t dd = static_cast<uint64_t>(d), rows = static_cast<uint64_t>(total);
+  if (!encode_bf16_3d_pitched(&maps.q, q, dd, static_cast<uint64_t>(Hq), rows, dd, static_cast<uint64_t>(q_stride), 64,
+                              1, kPrTile) ||
+      !encode_bf16_3d_pitched(&maps.k, k, dd, static_cast<uint64_t>(Hkv), rows, dd, static_cast<uint64_t>(k_stride), 64,
+                              1, kPrKeys) ||
+      !encode_bf16_3d_pitched(&maps.v, v, dd, static_cast<uint64_t>(Hkv), rows, dd, static_cast<uint64_t>(v_stride), 64,
+                              1, kPrKeys))
+    return DT_ERR_CUDA;
+  WsHeader* hdr = static_cast<WsHeader*>(workspace);
+  return d == 64 ? pr_launch<64>(p, maps, hdr, stream) : pr_launch<128>(p, maps, hdr, stream);
+}

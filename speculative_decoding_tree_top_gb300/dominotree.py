@@ -7,6 +7,7 @@ runs in the library's CUDA kernels; there is no fallback of any kind: without th
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import enum
@@ -42,7 +43,7 @@ class _Weights(ctypes.Structure):
                 ("b_hh", ctypes.c_void_p), ("w_c", ctypes.c_void_p)]
 
 
-_P, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_P, _I, _SZ, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
 _LIB: Optional[ctypes.CDLL] = None
 
 # Every symbol the header declares, with its ctypes signature (restype, argtypes).
@@ -63,6 +64,14 @@ SIGNATURES = {
     "dt_lmhead_topm": (_I, [_I, _I, _I, _I, _P, _P, _I, _P, _P, _P, _SZ, _P]),
     "dt_tree_attention_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "dt_tree_attention": (_I, [_I, _I, _I, _I, _I, _I, _P, _P, _P, _I, _P, ctypes.c_float, _P, _P, _SZ, _P]),
+    "dt_kv_append": (_I, [_I, _I, _I, _I, _P, _L, _P, _L, _P, _L, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _I, _I,
+                          _P, _SZ, _P]),
+    "dt_paged_attention_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "dt_paged_attention": (_I, [_I, _I, _I, _I, _I, _P, _P, _P, _I, _I, _I, _P, _I, _P, _P, ctypes.c_float, _P, _P,
+                                _SZ, _P]),
+    "dt_prompt_attention_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "dt_prompt_attention": (_I, [_I, _I, _I, _I, _I, _P, _L, _P, _L, _P, _L, _I, _P, ctypes.c_float, _P, _P, _SZ,
+                                 _P]),
     "dt_get_error": (_I, [_P, _P]),
     "dt_build_stats_read": (_I, [_P, _P, _P]),
     "dt_set_barrier_timeout_ns": (None, [ctypes.c_uint64]),
@@ -235,6 +244,163 @@ def dt_tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask: t
                                    _dev(out, "out", torch.float32, (B, n, Hq, d)),
                                    _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream)),
            "dt_tree_attention")
+    return out
+
+
+def rope_table(max_pos: int, rot: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """The rotation table of dt_kv_append for the frequencies base^(-2i/rot): [max_pos, rot] fp32, each position's
+    rot / 2 cosines then its sines, computed in fp64 (a far position's angle loses its fraction in fp32)."""
+    freq = float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
+    angle = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def new_paged_cache(num_pages: int, Hkv: int, page_size: int, d: int, device="cuda"):
+    """The two pools of a paged cache -> (k_cache, v_cache) [num_pages,Hkv,page_size,d] bf16, not initialised."""
+    shape = (num_pages, Hkv, page_size, d)
+    return tuple(torch.empty(shape, dtype=torch.bfloat16, device=device) for _ in range(2))
+
+
+def _here(device: torch.device):
+    """The library launches on the current device: tensors of another one are refused."""
+    if device.type != "cuda":
+        raise TypeError("tensors must be CUDA tensors")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _on(t: torch.Tensor, name: str, device: torch.device, dtype: torch.dtype, shape: tuple) -> int:
+    """A dense tensor's address, after the checks of ``_dev`` and that it is on ``device``."""
+    if t.device != device or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _dev(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, device: torch.device, dtype: torch.dtype, shape: tuple) -> int:
+    """``_on`` for a [rows, heads, d] tensor whose rows may lie apart (a view of a fused projection's output)."""
+    if t.device != device or t.dtype is not dtype or t.shape != shape or t.stride(2) != 1 or (
+            t.stride(1) != shape[2] and shape[1] != 1):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not {device}")
+        raise ValueError(f"{name}: the heads of a token must be dense, strides are {tuple(t.stride())}")
+    return t.data_ptr()
+
+
+def _pitch(t: torch.Tensor) -> int:
+    """Elements between two rows; a single row's stride says nothing, its width does."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _side(stream, device):
+    """Where a call's own tensors (outputs, a workspace) are allocated: on the stream that the call uses."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def dt_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, slots: torch.Tensor,
+                 positions: Optional[torch.Tensor] = None, rope: Optional[torch.Tensor] = None,
+                 interleaved: bool = False, q: Optional[torch.Tensor] = None, out_q: Optional[torch.Tensor] = None,
+                 out_k: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Tokens' k, v [N,Hkv,d] (bf16; rows may lie apart) into the pages of k_cache, v_cache [num_pages,Hkv,page_size,d]
+    at ``slots`` [N] int32 (negative: left out), keys rotated by ``positions`` [N] int32 with the table ``rope``
+    [max_pos,rot] fp32 (``rope_table``) -> the rotated queries [N,Hq,d] when ``q`` is given, else None. ``out_k``
+    [N,Hkv,d], when given, receives the rotated keys as well."""
+    N, Hkv, d = k.shape
+    dev, bf = k.device, torch.bfloat16
+    _here(dev)
+    num_pages, _, page_size, _ = k_cache.shape
+    cache = (num_pages, Hkv, page_size, d)
+    Hq = q.shape[1] if q is not None else 0
+    max_pos, rot = rope.shape if rope is not None else (0, 0)
+    if q is None and out_q is not None:
+        raise ValueError("out_q without q")
+    if workspace is None or (q is not None and out_q is None):
+        with _side(stream, dev):
+            if workspace is None:
+                workspace = new_workspace(256, dev)
+            if q is not None and out_q is None:
+                out_q = torch.empty((N, Hq, d), dtype=bf, device=dev)
+    if rope is not None and positions is None:
+        raise ValueError("rope without positions")
+    _check(lib().dt_kv_append(
+        N, Hq, Hkv, d, _rows(q, "q", dev, bf, (N, Hq, d)) if q is not None else None,
+        _pitch(q) if q is not None else 0, _rows(k, "k", dev, bf, (N, Hkv, d)), _pitch(k),
+        _rows(v, "v", dev, bf, (N, Hkv, d)), _pitch(v), BF16, _on(slots, "slots", dev, torch.int32, (N,)),
+        _on(positions, "positions", dev, torch.int32, (N,)) if positions is not None else None,
+        _on(rope, "rope", dev, torch.float32, (max_pos, rot)) if rope is not None else None, max_pos, rot,
+        int(bool(interleaved)), _on(out_q, "out_q", dev, bf, (N, Hq, d)) if q is not None else None,
+        _on(out_k, "out_k", dev, bf, (N, Hkv, d)) if out_k is not None else None,
+        _on(k_cache, "k_cache", dev, bf, cache), _on(v_cache, "v_cache", dev, bf, cache), num_pages, page_size,
+        _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream)), "dt_kv_append")
+    return out_q
+
+
+def dt_paged_attention_workspace_bytes(B: int, n: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(lib().dt_paged_attention_workspace_bytes(B, n, Hq, Hkv, d))
+
+
+def dt_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                       lens: torch.Tensor, scale: float, mask: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of each request's newest n tokens q [B,n,Hq,d] over its pages of k_cache, v_cache
+    [num_pages,Hkv,page_size,d] (all bf16): page_table [B,max_pages] int32, lens [B] int32 (the n tokens included; 0
+    for an unused row), mask [B,n,n] uint8 or None (causal among the n) -> out [B,n,Hq,d] bf16."""
+    B, n, Hq, d = q.shape
+    dev, bf = q.device, torch.bfloat16
+    _here(dev)
+    num_pages, Hkv, page_size, _ = k_cache.shape
+    cache, max_pages = (num_pages, Hkv, page_size, d), page_table.shape[1]
+    if workspace is None or out is None:
+        with _side(stream, dev):
+            if out is None:
+                out = torch.empty((B, n, Hq, d), dtype=bf, device=dev)
+            if workspace is None:
+                workspace = new_workspace(dt_paged_attention_workspace_bytes(B, n, Hq, Hkv, d), dev)
+    _check(lib().dt_paged_attention(
+        B, n, Hq, Hkv, d, _on(q, "q", dev, bf, (B, n, Hq, d)), _on(k_cache, "k_cache", dev, bf, cache),
+        _on(v_cache, "v_cache", dev, bf, cache), BF16, num_pages, page_size,
+        _on(page_table, "page_table", dev, torch.int32, (B, max_pages)), max_pages,
+        _on(lens, "lens", dev, torch.int32, (B,)),
+        _on(mask, "mask", dev, torch.uint8, (B, n, n)) if mask is not None else None, float(scale),
+        _on(out, "out", dev, bf, (B, n, Hq, d)), _dev(workspace, "workspace", torch.uint8), workspace.numel(),
+        _stream(stream)), "dt_paged_attention")
+    return out
+
+
+def dt_prompt_attention_workspace_bytes(total: int, B: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(lib().dt_prompt_attention_workspace_bytes(total, B, Hq, Hkv, d))
+
+
+def dt_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, scale: float,
+                        out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Causal attention over packed prompts: q [total,Hq,d], k, v [total,Hkv,d] (bf16; rows may lie apart), prompt b
+    the rows cu_seqlens[b] to cu_seqlens[b+1] (int32) -> out [total,Hq,d] bf16."""
+    total, Hq, d = q.shape
+    dev, bf = q.device, torch.bfloat16
+    _here(dev)
+    Hkv, B = k.shape[1], cu_seqlens.shape[0] - 1
+    if workspace is None or out is None:
+        with _side(stream, dev):
+            if out is None:
+                out = torch.empty((total, Hq, d), dtype=bf, device=dev)
+            if workspace is None:
+                workspace = new_workspace(dt_prompt_attention_workspace_bytes(total, B, Hq, Hkv, d), dev)
+    _check(lib().dt_prompt_attention(
+        total, B, Hq, Hkv, d, _rows(q, "q", dev, bf, (total, Hq, d)), _pitch(q),
+        _rows(k, "k", dev, bf, (total, Hkv, d)), _pitch(k), _rows(v, "v", dev, bf, (total, Hkv, d)), _pitch(v), BF16,
+        _on(cu_seqlens, "cu_seqlens", dev, torch.int32, (B + 1,)), float(scale),
+        _on(out, "out", dev, bf, (total, Hq, d)), _dev(workspace, "workspace", torch.uint8), workspace.numel(),
+        _stream(stream)), "dt_prompt_attention")
     return out
 
 
