@@ -143,6 +143,67 @@ __device__ __forceinline__ PaSeg pa_next(const PaParams& p, const int* cum, PaWa
   return s;
 }
 
+// A cut pair's segments: CTA c0's in slot `first`, those of c0 + 1 .. c1 in their slot 0.
+struct PaJoin {
+  int b, kvh, c0, c1, first;
+};
+// Joins them, a warp per query row: the lanes read 32 segments' (m, l) at a time, then each segment's row of O, D / 32
+// columns a lane, with several segments' loads in flight.
+template <int D>
+__device__ __forceinline__ void pa_join(const PaParams& p, const PaJoin& jn, int warp, int lane) {
+  constexpr int kCols = D / 32;
+  const int nseg = jn.c1 - jn.c0 + 1;
+  auto unit = [&](int i) { return 2 * static_cast<size_t>(jn.c0 + i) + (i == 0 ? jn.first : 0); };
+  for (int r = warp; r < p.R; r += kPaThreads / 32) {
+    float mx = -INFINITY;
+    for (int i = lane; i < nseg; i += 32) mx = fmaxf(mx, __ldcg(p.ml + (unit(i) * p.R + r) * 2));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+    const float mref = mx == -INFINITY ? 0.f : mx;
+    float den = 0.f, num[kCols];
+#pragma unroll
+    for (int e = 0; e < kCols; ++e) num[e] = 0.f;
+    for (int i0 = 0; i0 < nseg; i0 += 32) {
+      float wgt = 0.f;
+      if (i0 + lane < nseg) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ml + (unit(i0 + lane) * p.R + r) * 2));
+        wgt = exp2f(ml.x - mref);  // a segment without visible keys: 2^-inf = 0
+        den += wgt * ml.y;
+      }
+      const int here = min(32, nseg - i0);
+#pragma unroll 8
+      for (int i = 0; i < here; ++i) {
+        const float* src = p.part + (unit(i0 + i) * p.R + r) * D + kCols * lane;
+        const float wi = __shfl_sync(0xFFFFFFFFu, wgt, i);
+        if constexpr (kCols == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+          num[0] += wi * x.x;
+          num[1] += wi * x.y;
+          num[2] += wi * x.z;
+          num[3] += wi * x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+          num[0] += wi * x.x;
+          num[1] += wi * x.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xFFFFFFFFu, den, o);
+    const int node = r / p.G;
+    bool none = p.mask && p.lens[jn.b] == p.n;  // no prefix: perhaps no visible key at all
+    if (none)
+      for (int c = 0; c < p.n; ++c) none = none && p.mask[(static_cast<size_t>(jn.b) * p.n + node) * p.n + c] == 0;
+    const float inv = den == 0.f && none ? 0.f : 1.f / den;
+    unsigned short* o =
+        p.out + ((static_cast<size_t>(jn.b) * p.n + node) * p.Hq + jn.kvh * p.G + r % p.G) * D + kCols * lane;
+    if constexpr (kCols == 4)
+      *reinterpret_cast<uint2*>(o) = make_uint2(pa_pack(num[0] * inv, num[1] * inv), pa_pack(num[2] * inv, num[3] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(o) = pa_pack(num[0] * inv, num[1] * inv);
+  }
+}
+
 // Roles: warp 2 loads (its lanes look the pages up and issue one page's boxes each), warp 3 issues the MMAs, warps
 // 4 to 7 run the softmax, thread r owning query row r = node G + head (TMEM lane r).
 // Per block: S = Q K^T (M = 128, N = 64) into one of two TMEM buffers; softmax in base 2 with the running maximum
@@ -165,7 +226,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_rows(PaParams p, con
   __shared__ uint32_t s_tmem;
   __shared__ unsigned s_kv_issued, s_kv_used, s_q_issued, s_q_used;
   __shared__ int s_warp[kPaThreads / 32];
-  __shared__ int s_bad, s_last;
+  __shared__ int s_bad, s_joins;
+  __shared__ PaJoin s_join[2];
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int live_warps = (p.R + 31) / 32;
   if (t == 0) {
@@ -184,7 +246,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_rows(PaParams p, con
     mbar_init(&s_meet, live_warps);
     mbar_fence_init();
     s_kv_issued = s_kv_used = s_q_issued = s_q_used = 0u;
-    s_bad = 0;
+    s_bad = s_joins = 0;
   }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
@@ -511,53 +573,17 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_rows(PaParams p, con
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_free[qb]);
       if (whole) continue;
-      // the pair's last segment to finish joins them all
+      // the pair's last segment to finish joins them all, once the CTA is through its share
       const int c0 = pa_owner(sg.pair0, W, ctas), c1 = pa_owner(sg.pair0 + sg.nb - 1, W, ctas);
       __threadfence();
       ok = pa_sync(&s_meet, meet, lane);
       if (!ok) break;
       if (t == 128) {
         const unsigned done = atom_add_acq_rel_gpu(p.tickets + c0, 1u) + 1u;
-        s_last = done == static_cast<unsigned>(c1 - c0 + 1);
-        if (s_last) p.tickets[c0] = 0u;  // ready for the next call
-      }
-      ok = pa_sync(&s_meet, meet, lane);
-      if (!ok) break;
-      const bool join = *reinterpret_cast<volatile int*>(&s_last) != 0;
-      ok = pa_sync(&s_meet, meet, lane);  // s_last is free again
-      if (!ok) break;
-      if (!join) continue;
-      __threadfence();
-      const size_t u0 = 2 * static_cast<size_t>(c0) + (pa_share(W, ctas, c0) == sg.pair0 ? 0 : 1);
-      for (int rr = warp - 4; rr < p.R; rr += live_warps) {
-        float mx = -INFINITY;
-        for (int c = c0; c <= c1; ++c) {
-          const size_t u = c == c0 ? u0 : 2 * static_cast<size_t>(c);
-          mx = fmaxf(mx, __ldcg(p.ml + (u * p.R + rr) * 2));
+        if (done == static_cast<unsigned>(c1 - c0 + 1)) {
+          p.tickets[c0] = 0u;  // ready for the next call
+          s_join[s_joins++] = PaJoin{sg.b, sg.kvh, c0, c1, pa_share(W, ctas, c0) == sg.pair0 ? 0 : 1};
         }
-        const float mref = mx == -INFINITY ? 0.f : mx;
-        float den = 0.f, num[D / 32];
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) num[e] = 0.f;
-        for (int c = c0; c <= c1; ++c) {
-          const size_t u = c == c0 ? u0 : 2 * static_cast<size_t>(c);
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ml + (u * p.R + rr) * 2));
-          const float wgt = exp2f(ml.x - mref);  // a segment without visible keys: 2^-inf = 0
-          den += wgt * ml.y;
-#pragma unroll
-          for (int e = 0; e < D / 32; ++e) num[e] += wgt * __ldcg(p.part + (u * p.R + rr) * D + 32 * e + lane);
-        }
-        const int nd = rr / p.G;
-        bool none = pre == 0;  // no visible key at all
-        if (none && p.mask)
-          for (int c = 0; c < p.n; ++c) none = none && p.mask[(static_cast<size_t>(sg.b) * p.n + nd) * p.n + c] == 0;
-        else if (!p.mask)
-          none = false;
-        const float rinv = den == 0.f && none ? 0.f : 1.f / den;
-        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.out) +
-                           ((static_cast<size_t>(sg.b) * p.n + nd) * p.Hq + sg.kvh * p.G + rr % p.G) * D;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) o[32 * e + lane] = __float2bfloat16_rn(num[e] * rinv);
       }
     }
   }
@@ -568,6 +594,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_rows(PaParams p, con
     const unsigned ns = static_cast<unsigned>(p.stages);
     for (unsigned g = s_kv_used; g < s_kv_issued; ++g) mbar_wait(&kv_full[g % ns], (g / ns) & 1u, kPaBudgetNs);
     for (unsigned q = s_q_used; q < s_q_issued; ++q) mbar_wait(&q_full[q & 1u], (q >> 1) & 1u, kPaBudgetNs);
+  }
+  if (ok) {
+    __threadfence();  // the ticket's thread acquired the others' partials; the barrier above passed them on
+    for (int i = 0; i < s_joins; ++i) pa_join<D>(p, s_join[i], warp, lane);
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();

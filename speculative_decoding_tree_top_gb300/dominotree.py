@@ -261,41 +261,45 @@ def new_paged_cache(num_pages: int, Hkv: int, page_size: int, d: int, device="cu
     return tuple(torch.empty(shape, dtype=torch.bfloat16, device=device) for _ in range(2))
 
 
-def _here(device: torch.device):
-    """The library launches on the current device: tensors of another one are refused."""
-    if device.type != "cuda":
-        raise TypeError("tensors must be CUDA tensors")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+def _here(t: torch.Tensor, name: str) -> int:
+    """The tensor's device index. The library launches on the current device: tensors of another one are refused."""
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    dev = t.get_device()
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
 
 
-def _on(t: torch.Tensor, name: str, device: torch.device, dtype: torch.dtype, shape: tuple) -> int:
-    """A dense tensor's address, after the checks of ``_dev`` and that it is on ``device``."""
-    if t.device != device or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+def _on(t: torch.Tensor, name: str, dev: int, dtype: torch.dtype, shape: tuple) -> int:
+    """A dense tensor's address, after the checks of ``_dev`` and that it is on device ``dev``. (The checks that pass
+    come first and cost about 0.3 us a tensor.)"""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
         _dev(t, name, dtype, shape)
-        raise ValueError(f"{name} is on {t.device}, not {device}")
+        raise ValueError(f"{name} is on {t.device}, not cuda:{dev}")
     return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, name: str, device: torch.device, dtype: torch.dtype, shape: tuple) -> int:
-    """``_on`` for a [rows, heads, d] tensor whose rows may lie apart (a view of a fused projection's output)."""
-    if t.device != device or t.dtype is not dtype or t.shape != shape or t.stride(2) != 1 or (
-            t.stride(1) != shape[2] and shape[1] != 1):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _rows(t: torch.Tensor, name: str, dev: int, shape: tuple) -> tuple:
+    """The address and row pitch (elements) of a bf16 [rows, heads, d] tensor whose rows may lie apart (a view of a
+    fused projection's output); the heads of a row are dense. A single row's stride says nothing, its width does."""
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev:
+        if not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
-        if t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not {device}")
-        raise ValueError(f"{name}: the heads of a token must be dense, strides are {tuple(t.stride())}")
-    return t.data_ptr()
+        if t.dtype is not torch.bfloat16:
+            raise TypeError(f"{name} must be {torch.bfloat16}, not {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+        raise ValueError(f"{name} is on {t.device}, not cuda:{dev}")
+    rows, heads, d = shape
+    pitch, head, one = t.stride()
+    if (one != 1 and d != 1) or (head != d and heads != 1):
+        raise ValueError(f"{name}: the heads of a row must be dense, strides are {tuple(t.stride())}")
+    return t.data_ptr(), pitch if rows > 1 else heads * d
 
 
-def _pitch(t: torch.Tensor) -> int:
-    """Elements between two rows; a single row's stride says nothing, its width does."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+def _raw(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _side(stream, device):
@@ -315,33 +319,42 @@ def dt_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     at ``slots`` [N] int32 (negative: left out), keys rotated by ``positions`` [N] int32 with the table ``rope``
     [max_pos,rot] fp32 (``rope_table``) -> the rotated queries [N,Hq,d] when ``q`` is given, else None. ``out_k``
     [N,Hkv,d], when given, receives the rotated keys as well."""
-    N, Hkv, d = k.shape
-    dev, bf = k.device, torch.bfloat16
-    _here(dev)
-    num_pages, _, page_size, _ = k_cache.shape
-    cache = (num_pages, Hkv, page_size, d)
-    Hq = q.shape[1] if q is not None else 0
-    max_pos, rot = rope.shape if rope is not None else (0, 0)
-    if q is None and out_q is not None:
-        raise ValueError("out_q without q")
+    N, Hkv, d = kv = k.shape
+    dev = _here(k, "k")
+    cache = k_cache.shape
+    num_pages, _, page_size, _ = cache
     if workspace is None or (q is not None and out_q is None):
         with _side(stream, dev):
             if workspace is None:
-                workspace = new_workspace(256, dev)
+                workspace = new_workspace(256, k.device)
             if q is not None and out_q is None:
-                out_q = torch.empty((N, Hq, d), dtype=bf, device=dev)
-    if rope is not None and positions is None:
-        raise ValueError("rope without positions")
+                out_q = torch.empty(q.shape, dtype=torch.bfloat16, device=k.device)
+    Hq = max_pos = rot = q_at = q_pitch = 0
+    oq_at = ok_at = rope_at = pos_at = None
+    if q is not None:
+        Hq = q.shape[1]
+        q_at, q_pitch = _rows(q, "q", dev, (N, Hq, d))
+        oq_at = _on(out_q, "out_q", dev, torch.bfloat16, (N, Hq, d))
+    elif out_q is not None:
+        raise ValueError("out_q without q")
+    if out_k is not None:
+        ok_at = _on(out_k, "out_k", dev, torch.bfloat16, kv)
+    if rope is not None:
+        if positions is None:
+            raise ValueError("rope without positions")
+        max_pos, rot = rope.shape
+        rope_at = _on(rope, "rope", dev, torch.float32, (max_pos, rot))
+        pos_at = _on(positions, "positions", dev, torch.int32, (N,))
+    k_at, k_pitch = _rows(k, "k", dev, kv)
+    v_at, v_pitch = _rows(v, "v", dev, kv)
+    if cache[1] != Hkv or cache[3] != d:
+        raise ValueError(f"k_cache must have shape {(num_pages, Hkv, page_size, d)}, not {tuple(cache)}")
     _check(lib().dt_kv_append(
-        N, Hq, Hkv, d, _rows(q, "q", dev, bf, (N, Hq, d)) if q is not None else None,
-        _pitch(q) if q is not None else 0, _rows(k, "k", dev, bf, (N, Hkv, d)), _pitch(k),
-        _rows(v, "v", dev, bf, (N, Hkv, d)), _pitch(v), BF16, _on(slots, "slots", dev, torch.int32, (N,)),
-        _on(positions, "positions", dev, torch.int32, (N,)) if positions is not None else None,
-        _on(rope, "rope", dev, torch.float32, (max_pos, rot)) if rope is not None else None, max_pos, rot,
-        int(bool(interleaved)), _on(out_q, "out_q", dev, bf, (N, Hq, d)) if q is not None else None,
-        _on(out_k, "out_k", dev, bf, (N, Hkv, d)) if out_k is not None else None,
-        _on(k_cache, "k_cache", dev, bf, cache), _on(v_cache, "v_cache", dev, bf, cache), num_pages, page_size,
-        _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream)), "dt_kv_append")
+        N, Hq, Hkv, d, q_at, q_pitch, k_at, k_pitch, v_at, v_pitch, BF16, _on(slots, "slots", dev, torch.int32, (N,)),
+        pos_at, rope_at, max_pos, rot, 1 if interleaved else 0, oq_at, ok_at,
+        _on(k_cache, "k_cache", dev, torch.bfloat16, cache), _on(v_cache, "v_cache", dev, torch.bfloat16, cache),
+        num_pages, page_size, _on(workspace, "workspace", dev, torch.uint8, workspace.shape), workspace.numel(),
+        _raw(stream, dev)), "dt_kv_append")
     return out_q
 
 
@@ -355,25 +368,26 @@ def dt_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     """Attention of each request's newest n tokens q [B,n,Hq,d] over its pages of k_cache, v_cache
     [num_pages,Hkv,page_size,d] (all bf16): page_table [B,max_pages] int32, lens [B] int32 (the n tokens included; 0
     for an unused row), mask [B,n,n] uint8 or None (causal among the n) -> out [B,n,Hq,d] bf16."""
-    B, n, Hq, d = q.shape
-    dev, bf = q.device, torch.bfloat16
-    _here(dev)
-    num_pages, Hkv, page_size, _ = k_cache.shape
-    cache, max_pages = (num_pages, Hkv, page_size, d), page_table.shape[1]
+    B, n, Hq, d = shape = q.shape
+    dev, bf = _here(q, "q"), torch.bfloat16
+    num_pages, Hkv, page_size, _ = cache = k_cache.shape
+    max_pages = page_table.shape[1]
     if workspace is None or out is None:
         with _side(stream, dev):
             if out is None:
-                out = torch.empty((B, n, Hq, d), dtype=bf, device=dev)
+                out = torch.empty(shape, dtype=bf, device=q.device)
             if workspace is None:
-                workspace = new_workspace(dt_paged_attention_workspace_bytes(B, n, Hq, Hkv, d), dev)
+                workspace = new_workspace(dt_paged_attention_workspace_bytes(B, n, Hq, Hkv, d), q.device)
+    if cache[3] != d:
+        raise ValueError(f"k_cache must have shape {(num_pages, Hkv, page_size, d)}, not {tuple(cache)}")
     _check(lib().dt_paged_attention(
-        B, n, Hq, Hkv, d, _on(q, "q", dev, bf, (B, n, Hq, d)), _on(k_cache, "k_cache", dev, bf, cache),
+        B, n, Hq, Hkv, d, _on(q, "q", dev, bf, shape), _on(k_cache, "k_cache", dev, bf, cache),
         _on(v_cache, "v_cache", dev, bf, cache), BF16, num_pages, page_size,
         _on(page_table, "page_table", dev, torch.int32, (B, max_pages)), max_pages,
         _on(lens, "lens", dev, torch.int32, (B,)),
-        _on(mask, "mask", dev, torch.uint8, (B, n, n)) if mask is not None else None, float(scale),
-        _on(out, "out", dev, bf, (B, n, Hq, d)), _dev(workspace, "workspace", torch.uint8), workspace.numel(),
-        _stream(stream)), "dt_paged_attention")
+        _on(mask, "mask", dev, torch.uint8, (B, n, n)) if mask is not None else None, scale,
+        _on(out, "out", dev, bf, shape), _on(workspace, "workspace", dev, torch.uint8, workspace.shape),
+        workspace.numel(), _raw(stream, dev)), "dt_paged_attention")
     return out
 
 
@@ -385,22 +399,23 @@ def dt_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_se
                         out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
     """Causal attention over packed prompts: q [total,Hq,d], k, v [total,Hkv,d] (bf16; rows may lie apart), prompt b
     the rows cu_seqlens[b] to cu_seqlens[b+1] (int32) -> out [total,Hq,d] bf16."""
-    total, Hq, d = q.shape
-    dev, bf = q.device, torch.bfloat16
-    _here(dev)
+    total, Hq, d = shape = q.shape
+    dev, bf = _here(q, "q"), torch.bfloat16
     Hkv, B = k.shape[1], cu_seqlens.shape[0] - 1
     if workspace is None or out is None:
         with _side(stream, dev):
             if out is None:
-                out = torch.empty((total, Hq, d), dtype=bf, device=dev)
+                out = torch.empty(shape, dtype=bf, device=q.device)
             if workspace is None:
-                workspace = new_workspace(dt_prompt_attention_workspace_bytes(total, B, Hq, Hkv, d), dev)
+                workspace = new_workspace(dt_prompt_attention_workspace_bytes(total, B, Hq, Hkv, d), q.device)
+    q_at, q_pitch = _rows(q, "q", dev, shape)
+    k_at, k_pitch = _rows(k, "k", dev, (total, Hkv, d))
+    v_at, v_pitch = _rows(v, "v", dev, (total, Hkv, d))
     _check(lib().dt_prompt_attention(
-        total, B, Hq, Hkv, d, _rows(q, "q", dev, bf, (total, Hq, d)), _pitch(q),
-        _rows(k, "k", dev, bf, (total, Hkv, d)), _pitch(k), _rows(v, "v", dev, bf, (total, Hkv, d)), _pitch(v), BF16,
-        _on(cu_seqlens, "cu_seqlens", dev, torch.int32, (B + 1,)), float(scale),
-        _on(out, "out", dev, bf, (total, Hq, d)), _dev(workspace, "workspace", torch.uint8), workspace.numel(),
-        _stream(stream)), "dt_prompt_attention")
+        total, B, Hq, Hkv, d, q_at, q_pitch, k_at, k_pitch, v_at, v_pitch, BF16,
+        _on(cu_seqlens, "cu_seqlens", dev, torch.int32, (B + 1,)), scale, _on(out, "out", dev, bf, shape),
+        _on(workspace, "workspace", dev, torch.uint8, workspace.shape), workspace.numel(), _raw(stream, dev)),
+        "dt_prompt_attention")
     return out
 
 
