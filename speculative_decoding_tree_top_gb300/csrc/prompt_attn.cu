@@ -52,6 +52,54 @@ __device__ __forceinline__ uint32_t pr_pack(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// Pairs of fp32 in one 64-bit register: the packed FMA and add issue once for two elements.
+__device__ __forceinline__ uint64_t pr_pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void pr_unpair(uint64_t d, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(d));
+}
+__device__ __forceinline__ uint64_t pr_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pr_add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float pr_max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// 64 columns of the thread's lane; the caller waits (pr_wait_ld) before it reads them.
+__device__ __forceinline__ void pr_ld64(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,"
+      "%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]), "=f"(v[32]),
+        "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]), "=f"(v[40]),
+        "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]), "=f"(v[48]),
+        "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]), "=f"(v[56]),
+        "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
+      : "r"(taddr)
+      : "memory");
+}
+// Waits for the loads; the values pass through it, so that nothing reads them earlier.
+template <int N>
+__device__ __forceinline__ void pr_wait_ld(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
 __device__ __forceinline__ void pr_ld32(uint32_t taddr, float* v) {  // 32 columns of the thread's lane, waited for
   uint32_t r[32];
   asm volatile(
@@ -102,7 +150,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
   unsigned char* sq =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_f4) + 1023) & ~uintptr_t(1023));
   unsigned char* skv = sq + 2 * kTileBytes;
-  __shared__ uint64_t q_full[2], kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2], o_full[2];
+  __shared__ uint64_t q_full[2], kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2][2], o_full[2];
   __shared__ uint32_t s_tmem;
   __shared__ unsigned s_issued, s_used;  // ring entries issued and waited for (failure drain)
   __shared__ int s_bad;
@@ -133,7 +181,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i][0], 4);
+      mbar_init(&p_full[i][1], 4);
       mbar_init(&o_full[i], 1);
     }
     mbar_fence_init();
@@ -189,10 +238,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
       }
       umma_commit(&s_full[i]);
     };
-    auto issue_o = [&](int i, int j) {  // O_i += P_i V_j (ring entry 2 j + 1)
+    auto issue_o = [&](int i, int j, int half) {  // O_i += P_i V_j (ring entry 2 j + 1), 64 of the block's keys
       const uint32_t bv = smem_u32(skv + ((2 * j + 1) % kStages) * kTileBytes);
 #pragma unroll
-      for (int kk = 0; kk < kPrKeys / 16; ++kk)
+      for (int kk = half * (kPrKeys / 32); kk < (half + 1) * (kPrKeys / 32); ++kk)
         umma_f16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk,
                     umma_desc_sw128_mn(bv + 2048u * kk, kPrBox, 1024u), id_o, (j > 0 || kk > 0) ? 1u : 0u);
     };
@@ -210,10 +259,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
       if (ok && j + 1 < nblk) ok = wait_entry(2 * j + 2);
       for (int i = 0; i < 2 && ok; ++i) {
         if (j >= n[i]) continue;
-        ok = mbar_wait(&p_full[i], j & 1u, kPrBudgetNs);
+        for (int half = 0; half < 2 && ok; ++half) {
+          ok = mbar_wait(&p_full[i][half], j & 1u, kPrBudgetNs);
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          issue_o(i, j, half);
+        }
         if (!ok) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        issue_o(i, j);
         if (j + 1 == n[i]) umma_commit(&o_full[i]);
         // the next scores overwrite P: the tensor cores run this thread's products in order
         if (j + 1 < n[i]) issue_s(i, j + 1);
@@ -270,17 +322,22 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       float s[128];
-#pragma unroll
-      for (int h = 0; h < 4; ++h) pr_ld32(ts + 32u * h, s + 32 * h);
+      pr_ld64(ts, s);
+      pr_ld64(ts + 64u, s + 64);
+      pr_wait_ld<128>(s);
       if (diag) {
         const int lim = row - j * kPrKeys;  // the last key the row sees
 #pragma unroll
         for (int c = 0; c < 128; ++c) s[c] = c <= lim ? s[c] : -INFINITY;
       }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
+      float mx[4];
 #pragma unroll
-      for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-      const float bmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      for (int c = 0; c < 4; ++c) mx[c] = pr_max3(s[c], s[4 + c], s[8 + c]);
+#pragma unroll
+      for (int c = 12; c < 124; c += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = pr_max3(mx[e], s[c + e], s[c + 4 + e]);
+      const float bmax = fmaxf(pr_max3(mx[0], mx[1], mx[2]), pr_max3(mx[3], pr_max3(s[124], s[125], s[126]), s[127]));
       const bool raise = (bmax - m) * p.scale_log2 > kPrLazy || (m == -INFINITY && bmax > -INFINITY);
       const bool rescale_o = raise && m > -INFINITY;
       const float mn = raise ? bmax : m;
@@ -304,26 +361,33 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
           pr_st16(to + 16u * h, ov);
         }
       }
-      float ls[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint64_t scale2 = pr_pair(p.scale_log2, p.scale_log2), ref2 = pr_pair(-mref, -mref);
+      uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          const float a = pr_exp2(fmaf(s[32 * h + c], p.scale_log2, -mref));
-          const float bb = pr_exp2(fmaf(s[32 * h + c + 1], p.scale_log2, -mref));
-          ls[c & 2] += a;
-          ls[(c & 2) + 1] += bb;
-          pk[c >> 1] = pr_pack(a, bb);
+        for (int c = 0; c < 16; ++c) {
+          const int at = 32 * h + 2 * c;
+          float a, bb;
+          pr_unpair(pr_fma2(pr_pair(s[at], s[at + 1]), scale2, ref2), a, bb);
+          a = pr_exp2(a);
+          bb = pr_exp2(bb);
+          ls[c & 3] = pr_add2(ls[c & 3], pr_pair(a, bb));
+          pk[c] = pr_pack(a, bb);
         }
         pr_st16(ts + 16u * h, pk);
+        if (h & 1) {  // half of the weights are in place: their products may start
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          if (diag && h == 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the cleared values
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[i][h >> 1]);
+        }
       }
-      l = l * alpha + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
-      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-      if (diag) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the cleared values
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[i]);
+      float la, lb;
+      pr_unpair(pr_add2(pr_add2(ls[0], ls[1]), pr_add2(ls[2], ls[3])), la, lb);
+      l = l * alpha + (la + lb);
     }
     if (nb > 0 && ok) {
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(&o_full[i], 0, kPrBudgetNs));
