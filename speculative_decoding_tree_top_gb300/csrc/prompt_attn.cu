@@ -26,7 +26,8 @@ namespace {
 constexpr int kPrTile = 128;                 // query rows of a tile
 constexpr int kPrRows = 2 * kPrTile;         // of a CTA
 constexpr int kPrKeys = 128;                 // keys per block
-constexpr int kPrThreads = 384;              // warps 0-3: load, MMA, two idle; 4-7 and 8-11: the tiles' softmax
+constexpr int kPrThreads = 640;              // warps 0-3: load, MMA, two idle; 4-11 and 12-19: the tiles' softmax
+constexpr int kPrSoft = 256;                 // softmax threads of a tile
 constexpr float kPrLazy = 8.f;               // log2 headroom before the running maximum is raised
 constexpr uint64_t kPrBudgetNs = 4000000000ull;
 constexpr uint32_t kPrBox = kPrKeys * 128;   // 128 rows x 64 elements: 16 KB
@@ -76,22 +77,28 @@ __device__ __forceinline__ float pr_max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// 64 columns of the thread's lane; the caller waits (pr_wait_ld) before it reads them.
-__device__ __forceinline__ void pr_ld64(uint32_t taddr, float* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,"
-      "%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]), "=f"(v[32]),
-        "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]), "=f"(v[40]),
-        "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]), "=f"(v[48]),
-        "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]), "=f"(v[56]),
-        "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
-      : "r"(taddr)
-      : "memory");
+// Tensor memory by 16 lanes (rows) a warp: in each group of 8 columns thread l holds columns 2 (l % 4) and + 1 of rows
+// l / 4 and l / 4 + 8 (v[4 g], v[4 g + 1], then v[4 g + 2], v[4 g + 3]). The caller waits before it reads them.
+template <int kGroups>
+__device__ __forceinline__ void pr_ld(uint32_t taddr, float* v) {
+  static_assert(kGroups == 8 || kGroups == 4, "groups of 8 columns");
+  if constexpr (kGroups == 8)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr)
+        : "memory");
 }
 // Waits for the loads; the values pass through it, so that nothing reads them earlier.
 template <int N>
@@ -100,26 +107,21 @@ __device__ __forceinline__ void pr_wait_ld(float* v) {
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
 }
-__device__ __forceinline__ void pr_ld32(uint32_t taddr, float* v) {  // 32 columns of the thread's lane, waited for
-  uint32_t r[32];
+__device__ __forceinline__ void pr_st_o(uint32_t taddr, const float* v) {  // 4 groups, as pr_ld holds them
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
       : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void pr_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+// The weights of 64 keys: a pair of bf16 per 32-bit column, so a group's two values of a row are one column.
+__device__ __forceinline__ void pr_st_p(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 
@@ -181,8 +183,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i][0], 4);
-      mbar_init(&p_full[i][1], 4);
+      mbar_init(&p_full[i][0], kPrSoft / 32);
+      mbar_init(&p_full[i][1], kPrSoft / 32);
       mbar_init(&o_full[i], 1);
     }
     mbar_fence_init();
@@ -222,65 +224,94 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
       if (j == 0 && n1 > 0) load_q(1);
       if (ok) ok = load_kv(&maps.v, j);
     }
-  } else if (warp == 1 && lane == 0) {  // MMA
-    const uint32_t id_s = umma_idesc(kPrKeys, 128), id_o = umma_idesc(D, 128) | (1u << 16);  // O: V MN-major
-    auto wait_entry = [&](unsigned e) {
-      if (!mbar_wait(&kv_full[e % kStages], (e / kStages) & 1u, kPrBudgetNs)) return false;
-      if (s_used < e + 1u) s_used = e + 1u;
-      return true;
-    };
-    auto issue_s = [&](int i, int j) {  // S_i = Q_i K_j^T (the block's keys are ring entry 2 j)
-      const uint32_t aq = smem_u32(sq + i * kTileBytes), bk = smem_u32(skv + (2 * j % kStages) * kTileBytes);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * kPrBox + (kk & 3) * 32u;
-        umma_f16(tmem + 128u * i, umma_desc_sw128(aq + off), umma_desc_sw128(bk + off), id_s, kk > 0 ? 1u : 0u);
-      }
-      umma_commit(&s_full[i]);
-    };
-    auto issue_o = [&](int i, int j, int half) {  // O_i += P_i V_j (ring entry 2 j + 1), 64 of the block's keys
-      const uint32_t bv = smem_u32(skv + ((2 * j + 1) % kStages) * kTileBytes);
-#pragma unroll
-      for (int kk = half * (kPrKeys / 32); kk < (half + 1) * (kPrKeys / 32); ++kk)
-        umma_f16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk,
-                    umma_desc_sw128_mn(bv + 2048u * kk, kPrBox, 1024u), id_o, (j > 0 || kk > 0) ? 1u : 0u);
-    };
-    const int n[2] = {n0, n1};
-    ok = wait_entry(0);
-    for (int i = 0; i < 2 && ok; ++i)
-      if (n[i] > 0) {
-        ok = mbar_wait(&q_full[i], 0, kPrBudgetNs);
+  } else if (warp == 1) {  // MMA
+    if (elect_one()) {
+      const uint32_t id_s = umma_idesc(kPrKeys, 128), id_o = umma_idesc(D, 128) | (1u << 16);  // O: V MN-major
+      const int n[2] = {n0, n1};
+      const uint64_t dq = umma_desc_sw128(smem_u32(sq)), dk = umma_desc_sw128(smem_u32(skv));
+      const uint64_t dv = umma_desc_sw128_mn(smem_u32(skv), kPrBox, 1024u);
+      auto wait = [&](uint64_t* bar, unsigned parity) {
+        const bool done = mbar_wait(bar, parity, kPrBudgetNs);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (ok) issue_s(i, 0);
-      }
-    if (ok) umma_commit(&kv_empty[0]);
-    for (int j = 0; j < nblk && ok; ++j) {
-      ok = wait_entry(2 * j + 1);
-      if (ok && j + 1 < nblk) ok = wait_entry(2 * j + 2);
-      for (int i = 0; i < 2 && ok; ++i) {
-        if (j >= n[i]) continue;
-        for (int half = 0; half < 2 && ok; ++half) {
-          ok = mbar_wait(&p_full[i][half], j & 1u, kPrBudgetNs);
-          if (!ok) break;
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          issue_o(i, j, half);
+        return done;
+      };
+      auto issue_s = [&](int i, unsigned st) {  // S_i = Q_i K^T, the keys in ring entry st
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * kPrBox + (kk & 3) * 32u) >> 4;
+          umma_f16(tmem + 128u * i, dq + (i * (kTileBytes >> 4) + off), dk + (st * (kTileBytes >> 4) + off), id_s,
+                       kk > 0 ? 1u : 0u);
         }
-        if (!ok) break;
-        if (j + 1 == n[i]) umma_commit(&o_full[i]);
-        // the next scores overwrite P: the tensor cores run this thread's products in order
-        if (j + 1 < n[i]) issue_s(i, j + 1);
-      }
-      if (ok) {
-        umma_commit(&kv_empty[(2 * j + 1) % kStages]);
-        if (j + 1 < nblk) umma_commit(&kv_empty[(2 * j + 2) % kStages]);
+        umma_commit(&s_full[i]);
+      };
+      auto issue_o = [&](int i, unsigned st, int half, bool fresh) {  // O_i += P_i V, 64 of the keys of ring entry st
+#pragma unroll
+        for (int k2 = 0; k2 < kPrKeys / 32; ++k2) {
+          const int kk = half * (kPrKeys / 32) + k2;
+          umma_f16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk,
+                          dv + (st * (kTileBytes >> 4) + kk * (2048u >> 4)), id_o, fresh && kk == 0 ? 0u : 1u);
+        }
+      };
+      unsigned st = 0, par = 0;  // ring entry and its parity: K_j, V_j, K_{j+1}, ...
+      auto step = [&]() {
+        if (++st == kStages) {
+          st = 0;
+          par ^= 1u;
+        }
+      };
+      unsigned used = 0;
+      auto wait_entry = [&]() {
+        const bool done = wait(&kv_full[st], par);
+        if (done) s_used = ++used;
+        return done;
+      };
+      ok = wait_entry();
+      for (int i = 0; i < 2 && ok; ++i)
+        if (n[i] > 0) {
+          ok = wait(&q_full[i], 0);
+          if (ok) issue_s(i, 0);
+        }
+      if (ok) umma_commit(&kv_empty[0]);
+      for (int j = 0; j < nblk && ok; ++j) {
+        step();
+        const unsigned sv = st;
+        ok = wait_entry();
+        if (ok && j + 1 < nblk) {
+          step();
+          ok = wait_entry();
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (!ok || j >= n[i]) continue;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (ok) ok = wait(&p_full[i][half], j & 1u);
+            if (ok) issue_o(i, sv, half, j == 0);
+          }
+          if (!ok) continue;
+          if (j + 1 == n[i]) umma_commit(&o_full[i]);
+          // the next scores overwrite P: the tensor cores run this warp's products in order
+          if (j + 1 < n[i]) issue_s(i, st);
+        }
+        if (ok) {
+          umma_commit(&kv_empty[sv]);
+          if (j + 1 < nblk) umma_commit(&kv_empty[st]);
+        }
       }
     }
-  } else if (warp >= 4) {  // softmax of tile i: thread r owns query row r
-    const int i = (warp - 4) >> 2, r = t - 128 - 128 * i, nb = i ? n1 : n0;
-    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+  } else if (warp >= 4) {  // softmax of tile i
+    // A warp owns 16 rows of its quarter of tensor memory; four neighbouring threads share two rows (ra, ra + 8), each
+    // holding a quarter of their columns.
+    const int i = (warp - 4) >> 3, tt = t - 128 - kPrSoft * i, nb = i ? n1 : n0;
+    const int lane0 = 32 * (warp & 3) + 16 * (((warp - 4) >> 2) & 1);
+    const uint32_t lanes = static_cast<uint32_t>(lane0) << 16;
     const uint32_t ts = tmem + lanes + 128u * i, to = tmem + lanes + 256u + 128u * i;
-    const int row = q0 + i * kPrTile + r;  // the row's token in its prompt
-    float m = -INFINITY, l = 0.f;          // running maximum (of the unscaled scores) and sum
+    const int ra = lane0 + (lane >> 2), col = 2 * (lane & 3);
+    const int row0 = q0 + i * kPrTile + ra;  // row ra's token in its prompt; the other row's is 8 further
+    float ref[2] = {-INFINITY, -INFINITY};   // running maximum of the scaled scores, as last raised
+    uint64_t nref[2] = {0ull, 0ull};         // minus it, twice (0 while nothing finite was seen)
+    float l[2] = {0.f, 0.f};                 // sums of this thread's weights
+    const uint64_t scale2 = pr_pair(p.scale_log2, p.scale_log2);
     for (int j = 0; j < nb && ok; ++j) {
       const bool diag = j + 1 == nb;
       if (diag) {
@@ -296,7 +327,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
         __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
         const __nv_bfloat162 zero = acc;
 #pragma unroll 4
-        for (int c = r; c < kHalves * kPrKeys * 8; c += 128) {  // 16-byte pieces; eight a row
+        for (int c = tt; c < kHalves * kPrKeys * 8; c += kPrSoft) {  // 16-byte pieces; eight a row
           uint4* at = reinterpret_cast<uint4*>(sv + 16 * c);
           if (((c >> 3) & (kPrKeys - 1)) >= valid) {
             *at = make_uint4(0u, 0u, 0u, 0u);
@@ -310,7 +341,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
         }
         const float2 a2 = __bfloat1622float2(acc);
         if (!(a2.x == 0.f && a2.y == 0.f)) {  // rare
-          for (int c = r; c < kHalves * kPrKeys * 8; c += 128) {
+          for (int c = tt; c < kHalves * kPrKeys * 8; c += kPrSoft) {
             unsigned short* at = reinterpret_cast<unsigned short*>(sv + 16 * c);
             for (int k2 = 0; k2 < 8; ++k2)
               if ((at[k2] & 0x7F80u) == 0x7F80u) at[k2] = 0;
@@ -321,101 +352,128 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_full[i], j & 1u, kPrBudgetNs));
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      float s[128];
-      pr_ld64(ts, s);
-      pr_ld64(ts + 64u, s + 64);
-      pr_wait_ld<128>(s);
+      float s[64];
+      pr_ld<8>(ts, s);
+      pr_ld<8>(ts + 64u, s + 32);
+      pr_wait_ld<64>(s);
       if (diag) {
-        const int lim = row - j * kPrKeys;  // the last key the row sees
+        const int lim = row0 - j * kPrKeys - col;  // row ra sees this thread's columns 8 g + e up to here
 #pragma unroll
-        for (int c = 0; c < 128; ++c) s[c] = c <= lim ? s[c] : -INFINITY;
+        for (int g = 0; g < 16; ++g)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (8 * g + (e & 1) > lim + 8 * (e >> 1)) s[4 * g + e] = -INFINITY;
       }
-      float mx[4];
+      float mx[2];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) mx[c] = pr_max3(s[c], s[4 + c], s[8 + c]);
+      for (int k2 = 0; k2 < 2; ++k2) {
+        float u = fmaxf(s[2 * k2], s[2 * k2 + 1]), w = fmaxf(s[2 * k2 + 4], s[2 * k2 + 5]);
 #pragma unroll
-      for (int c = 12; c < 124; c += 8)
+        for (int g = 2; g < 16; g += 2) {
+          u = pr_max3(u, s[4 * g + 2 * k2], s[4 * g + 2 * k2 + 1]);
+          w = pr_max3(w, s[4 * g + 4 + 2 * k2], s[4 * g + 5 + 2 * k2]);
+        }
+        mx[k2] = fmaxf(u, w) * p.scale_log2;
+      }
+      if (__any_sync(0xFFFFFFFFu, mx[0] > ref[0] + kPrLazy || mx[1] > ref[1] + kPrLazy)) {  // rare: raise, rescale O
+        float alpha[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = pr_max3(mx[e], s[c + e], s[c + 4 + e]);
-      const float bmax = fmaxf(pr_max3(mx[0], mx[1], mx[2]), pr_max3(mx[3], pr_max3(s[124], s[125], s[126]), s[127]));
-      const bool raise = (bmax - m) * p.scale_log2 > kPrLazy || (m == -INFINITY && bmax > -INFINITY);
-      const bool rescale_o = raise && m > -INFINITY;
-      const float mn = raise ? bmax : m;
-      const float alpha = rescale_o ? pr_exp2((m - mn) * p.scale_log2) : 1.f;
-      m = mn;
-      const float mref = m == -INFINITY ? 0.f : m * p.scale_log2;
-      if (__any_sync(0xFFFFFFFFu, rescale_o)) {  // S is full, so the products into O before it are complete
+        for (int k2 = 0; k2 < 2; ++k2) {
+          mx[k2] = fmaxf(mx[k2], __shfl_xor_sync(0xFFFFFFFFu, mx[k2], 1));
+          mx[k2] = fmaxf(mx[k2], __shfl_xor_sync(0xFFFFFFFFu, mx[k2], 2));
+          const bool raise = mx[k2] > ref[k2] + kPrLazy;
+          alpha[k2] = raise ? pr_exp2(ref[k2] - mx[k2]) : 1.f;  // from nothing: 2^-inf = 0
+          l[k2] *= alpha[k2];
+          if (raise) {
+            ref[k2] = mx[k2];
+            nref[k2] = pr_pair(-mx[k2], -mx[k2]);
+          }
+        }
+        if (j > 0) {  // S is full, so the products into O before it are complete
+#pragma unroll 1
+          for (int h = 0; h < D / 32; ++h) {
+            float o[16];
+            pr_ld<4>(to + 32u * h, o);
+            pr_wait_ld<16>(o);
 #pragma unroll
-        for (int h = 0; h < D / 16; ++h) {
-          uint32_t ov[16];
-          asm volatile(
-              "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-              "\n\ttcgen05.wait::ld.sync.aligned;"
-              : "=r"(ov[0]), "=r"(ov[1]), "=r"(ov[2]), "=r"(ov[3]), "=r"(ov[4]), "=r"(ov[5]), "=r"(ov[6]), "=r"(ov[7]),
-                "=r"(ov[8]), "=r"(ov[9]), "=r"(ov[10]), "=r"(ov[11]), "=r"(ov[12]), "=r"(ov[13]), "=r"(ov[14]),
-                "=r"(ov[15])
-              : "r"(to + 16u * h)
-              : "memory");
-#pragma unroll
-          for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-          pr_st16(to + 16u * h, ov);
+            for (int e = 0; e < 16; ++e) o[e] *= alpha[(e >> 1) & 1];
+            pr_st_o(to + 32u * h, o);
+          }
         }
       }
-      const uint64_t scale2 = pr_pair(p.scale_log2, p.scale_log2), ref2 = pr_pair(-mref, -mref);
       uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
+      for (int h = 0; h < 2; ++h) {
         uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
+        for (int c = 0; c < 16; ++c) {  // group 8 h + c / 2, row c % 2
           const int at = 32 * h + 2 * c;
           float a, bb;
-          pr_unpair(pr_fma2(pr_pair(s[at], s[at + 1]), scale2, ref2), a, bb);
+          pr_unpair(pr_fma2(pr_pair(s[at], s[at + 1]), scale2, nref[c & 1]), a, bb);
           a = pr_exp2(a);
           bb = pr_exp2(bb);
           ls[c & 3] = pr_add2(ls[c & 3], pr_pair(a, bb));
           pk[c] = pr_pack(a, bb);
         }
-        pr_st16(ts + 16u * h, pk);
-        if (h & 1) {  // half of the weights are in place: their products may start
-          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-          if (diag && h == 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the cleared values
-          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[i][h >> 1]);
-        }
+        pr_st_p(ts + 32u * h, pk);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        if (diag && h == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the cleared values
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[i][h]);  // half of the weights are in place: their products may start
       }
-      float la, lb;
-      pr_unpair(pr_add2(pr_add2(ls[0], ls[1]), pr_add2(ls[2], ls[3])), la, lb);
-      l = l * alpha + (la + lb);
+#pragma unroll
+      for (int k2 = 0; k2 < 2; ++k2) {
+        float la, lb;
+        pr_unpair(pr_add2(ls[k2], ls[k2 + 2]), la, lb);
+        l[k2] += la + lb;
+      }
     }
     if (nb > 0 && ok) {
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(&o_full[i], 0, kPrBudgetNs));
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       if (ok) {
-        const float inv = 1.f / l;  // the row's own key is visible; a sum of 0 or NaN gives NaN
+        float inv[2];
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2) {
+          l[k2] += __shfl_xor_sync(0xFFFFFFFFu, l[k2], 1);
+          l[k2] += __shfl_xor_sync(0xFFFFFFFFu, l[k2], 2);
+          inv[k2] = 1.f / l[k2];  // the row's own key is visible; a sum of 0 or NaN gives NaN
+        }
         const int bad = *reinterpret_cast<volatile int*>(&s_bad);
-        unsigned short* po = p.out + (static_cast<size_t>(lo + row) * p.Hq + head) * D;
+        // through the tile's Q buffer (its last product is complete), so that rows leave in whole 16-byte pieces
+        unsigned char* so = sq + i * kTileBytes;
 #pragma unroll
         for (int h = 0; h < D / 32; ++h) {
-          float o[32];
-          pr_ld32(to + 32u * h, o);
-          if (row >= len) continue;
+          float o[16];
+          pr_ld<4>(to + 32u * h, o);
+          pr_wait_ld<16>(o);
           if (bad) {  // rare: tile 0's clearing reaches tile 1 too, which shares the block
-            for (int key = (n0 - 1) * kPrKeys; key <= row; ++key) {
-              const unsigned short* vr = p.v + static_cast<size_t>(lo + key) * p.v_stride + kvh * D + 32 * h;
+            for (int key = (n0 - 1) * kPrKeys; key <= row0 + 8 && key < len; ++key) {
+              const unsigned short* vr = p.v + static_cast<size_t>(lo + key) * p.v_stride + kvh * D + 32 * h + col;
 #pragma unroll
-              for (int c = 0; c < 32; ++c) {
-                const uint32_t bits = static_cast<uint32_t>(vr[c]) << 16;
-                if ((bits & 0x7F800000u) == 0x7F800000u) o[c] += __uint_as_float(bits);
+              for (int e = 0; e < 16; ++e) {
+                const uint32_t bits = static_cast<uint32_t>(vr[8 * (e >> 2) + (e & 1)]) << 16;
+                if ((bits & 0x7F800000u) == 0x7F800000u && key <= row0 + 8 * ((e >> 1) & 1)) o[e] += __uint_as_float(bits);
               }
             }
           }
 #pragma unroll
-          for (int c = 0; c < 32; c += 8)
-            *reinterpret_cast<uint4*>(po + 32 * h + c) =
-                make_uint4(pr_pack(o[c] * inv, o[c + 1] * inv), pr_pack(o[c + 2] * inv, o[c + 3] * inv),
-                           pr_pack(o[c + 4] * inv, o[c + 5] * inv), pr_pack(o[c + 6] * inv, o[c + 7] * inv));
+          for (int e = 0; e < 16; e += 2) {
+            const int r = ra + 8 * ((e >> 1) & 1), c16 = 4 * (h & 1) + (e >> 2);
+            *reinterpret_cast<uint32_t*>(so + (h >> 1) * kPrBox + r * 128 + ((c16 ^ (r & 7)) << 4) + 2 * col) =
+                pr_pack(o[e] * inv[(e >> 1) & 1], o[e + 1] * inv[(e >> 1) & 1]);
+          }
+        }
+        __syncwarp();
+        constexpr int kPieces = D / 8, kRowsAtOnce = 32 / kPieces;
+        const int piece = lane % kPieces;
+#pragma unroll
+        for (int k2 = 0; k2 < 16; k2 += kRowsAtOnce) {
+          const int r = lane0 + k2 + lane / kPieces, row = q0 + i * kPrTile + r;
+          const uint4 x = *reinterpret_cast<const uint4*>(so + (piece >> 3) * kPrBox + r * 128 + (((piece & 7) ^ (r & 7)) << 4));
+          if (row < len)
+            *reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(lo + row) * p.Hq + head) * D + 8 * piece) = x;
         }
       }
     }

@@ -34,7 +34,16 @@ __device__ __forceinline__ void umma_f16(uint32_t tmem_d, uint64_t da, uint64_t 
                "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
                ::"r"(tmem_d), "l"(da), "l"(db), "r"(idesc), "r"(acc) : "memory");
 }
-// The same with the left operand in tensor memory (one lane per row, two bf16 of consecutive K per 32-bit column).
+// One lane of a warp that is together. Code behind a branch on it keeps the operands of tcgen05.mma in uniform registers;
+// behind a branch on a lane's number they are moved there for every instruction (alone on an SM, a product with both
+// operands in shared memory issues every 40 cycles instead of 46, one with the left operand in tensor memory every 32
+// instead of 47).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+  return e != 0u;
+}
+// A product with the left operand in tensor memory (one lane per row, two bf16 of consecutive K per 32-bit column).
 __device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t db, uint32_t idesc,
                                             uint32_t acc) {
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
