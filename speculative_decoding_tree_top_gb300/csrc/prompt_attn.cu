@@ -78,34 +78,33 @@ __device__ __forceinline__ float pr_max3(float a, float b, float c) {
   return d;
 }
 // Tensor memory by 16 lanes (rows) a warp: in each group of 8 columns thread l holds columns 2 (l % 4) and + 1 of rows
-// l / 4 and l / 4 + 8 (v[4 g], v[4 g + 1], then v[4 g + 2], v[4 g + 3]). The caller waits before it reads them.
-template <int kGroups>
-__device__ __forceinline__ void pr_ld(uint32_t taddr, float* v) {
-  static_assert(kGroups == 8 || kGroups == 4, "groups of 8 columns");
-  if constexpr (kGroups == 8)
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-        : "r"(taddr)
-        : "memory");
-  else
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
-        : "r"(taddr)
-        : "memory");
+// l / 4 and l / 4 + 8 (v[4 g], v[4 g + 1], then v[4 g + 2], v[4 g + 3]). Each load waits for itself.
+__device__ __forceinline__ void pr_ld_s(uint32_t taddr, float (&v)[64]) {  // 16 groups: a block's scores
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,"
+      "%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,"
+      "%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]), "=f"(v[32]),
+        "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]), "=f"(v[40]),
+        "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]), "=f"(v[48]),
+        "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]), "=f"(v[56]),
+        "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
+      : "r"(taddr)
+      : "memory");
 }
-// Waits for the loads; the values pass through it, so that nothing reads them earlier.
-template <int N>
-__device__ __forceinline__ void pr_wait_ld(float* v) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+__device__ __forceinline__ void pr_ld_o(uint32_t taddr, float (&v)[16]) {  // 4 groups
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
 }
 __device__ __forceinline__ void pr_st_o(uint32_t taddr, const float* v) {  // 4 groups, as pr_ld holds them
   asm volatile(
@@ -353,9 +352,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       float s[64];
-      pr_ld<8>(ts, s);
-      pr_ld<8>(ts + 64u, s + 32);
-      pr_wait_ld<64>(s);
+      pr_ld_s(ts, s);
       if (diag) {
         const int lim = row0 - j * kPrKeys - col;  // row ra sees this thread's columns 8 g + e up to here
 #pragma unroll
@@ -393,8 +390,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
 #pragma unroll 1
           for (int h = 0; h < D / 32; ++h) {
             float o[16];
-            pr_ld<4>(to + 32u * h, o);
-            pr_wait_ld<16>(o);
+            pr_ld_o(to + 32u * h, o);
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] *= alpha[(e >> 1) & 1];
             pr_st_o(to + 32u * h, o);
@@ -446,8 +442,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
 #pragma unroll
         for (int h = 0; h < D / 32; ++h) {
           float o[16];
-          pr_ld<4>(to + 32u * h, o);
-          pr_wait_ld<16>(o);
+          pr_ld_o(to + 32u * h, o);
           if (bad) {  // rare: tile 0's clearing reaches tile 1 too, which shares the block
             for (int key = (n0 - 1) * kPrKeys; key <= row0 + 8 && key < len; ++key) {
               const unsigned short* vr = p.v + static_cast<size_t>(lo + key) * p.v_stride + kvh * D + 32 * h + col;
