@@ -23,7 +23,8 @@ struct WsHeader {
   unsigned long long stat_gather_bytes; // correction-row bytes the launch gathered (rows x H x element size)
   unsigned stat_waves;                  // waves run
   unsigned stat_expansions;             // expansions computed (the roots included)
-  unsigned reserved[50];
+  unsigned deal_next, deal_done;        // dt_prompt_attention: items dealt out, CTAs through (zero between calls)
+  unsigned reserved[48];
 };
 static_assert(sizeof(WsHeader) == 256, "workspace header is 256 bytes");
 

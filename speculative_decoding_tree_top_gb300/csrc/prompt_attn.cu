@@ -3,14 +3,17 @@
 // Token i of a prompt sees its prompt's tokens 0..i: out[i][h] = softmax_j<=i(scale q[i][h].k_j) v_j, query head h
 // reading key/value head h / (Hq / Hkv).
 //
-// GB300 design: bound by the tensor cores. A CTA owns 256 query rows of one head as two tiles of 128 and walks the
-// keys in blocks of 128, shared by both tiles. Per tile and block: S = Q K^T (both operands in shared memory) into
-// tensor memory, a softmax by the tile's own four warps (thread = query row, so no statistic needs a shuffle), the
-// weights written back as bf16 over their own scores in tensor memory, and O += P V with P read from there, so that
-// P never passes through shared memory. The tiles alternate: while one is in its softmax the tensor cores work on the
-// other. Softmax in base 2, fp32; the running maximum is raised (and O rescaled) only past a headroom of 2^8, which
-// keeps the weights below 2^8 and leaves O alone in nearly every block. P is rounded to bf16, the only rounding
+// GB300 design: bound by the tensor cores (long prompts) and by what a tile costs to start and finish (short ones). An
+// item is 256 query rows of one head, as two tiles of 128, and walks its keys in blocks of 128 that both tiles share.
+// Per tile and block: S = Q K^T (both operands in shared memory) into tensor memory, a softmax by the tile's own eight
+// warps, the weights written back as bf16 over their own scores in tensor memory, and O += P V with P read from there,
+// so that P never passes through shared memory. The tiles alternate: while one is in its softmax the tensor cores work
+// on the other. Softmax in base 2, fp32; the running maximum is raised (and O rescaled) only past a headroom of 2^8,
+// which keeps the weights below 2^8 and leaves O alone in nearly every block. P is rounded to bf16, the only rounding
 // before the output's; the row sums are taken in fp32 from the unrounded weights.
+// One CTA per SM stays for all of its items: the loads of the next item and its first scores run under the last block
+// and the epilogue of the one before. Items are dealt out longest first, from a counter in the workspace (the order
+// changes no result).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -26,14 +29,17 @@ namespace {
 constexpr int kPrTile = 128;                 // query rows of a tile
 constexpr int kPrRows = 2 * kPrTile;         // of a CTA
 constexpr int kPrKeys = 128;                 // keys per block
-constexpr int kPrThreads = 640;              // warps 0-3: load, MMA, two idle; 4-11 and 12-19: the tiles' softmax
+constexpr int kPrThreads = 640;              // warps 0-3: load, MMA, items, idle; 4-11 and 12-19: the tiles' softmax
 constexpr int kPrSoft = 256;                 // softmax threads of a tile
+constexpr int kPrAhead = 3;                  // items that may be known ahead
+constexpr int kPrSorted = 8;                 // prompts a lane of the item warp keeps: up to 256 are dealt out sorted
 constexpr float kPrLazy = 8.f;               // log2 headroom before the running maximum is raised
+constexpr float kPrNone = 3e38f;
 constexpr uint64_t kPrBudgetNs = 4000000000ull;
 constexpr uint32_t kPrBox = kPrKeys * 128;   // 128 rows x 64 elements: 16 KB
 
 struct PrParams {
-  int total, B, Hq, Hkv, G, slots;
+  int total, B, Hq, Hkv, G, slots, grid;
   const int32_t* cu;           // [B + 1]
   const unsigned short* v;     // re-read only for values that are not finite
   long long v_stride;
@@ -97,6 +103,18 @@ __device__ __forceinline__ void pr_ld_s(uint32_t taddr, float (&v)[64]) {  // 16
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void pr_ld_half(uint32_t taddr, float (&v)[32]) {  // 8 groups
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void pr_ld_o(uint32_t taddr, float (&v)[16]) {  // 4 groups
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
@@ -141,54 +159,137 @@ __device__ __forceinline__ int pr_find(const PrParams& p, int slot, int lane) { 
   }
 }
 
+// A wait in long sleeps: the hardware wakes the warp when the phase ends, and a warp that polls takes issue slots from
+// those that compute.
+__device__ __forceinline__ bool pr_try_wait(uint64_t* bar, unsigned parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool pr_wait(uint64_t* bar, unsigned parity) {
+  if (pr_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!pr_try_wait(bar, parity))
+    if (global_timer_ns() - t0 > kPrBudgetNs) return false;
+  return true;
+}
+
+struct PrItem {  // 256 rows of a prompt (its first row `lo`, `len` rows) from row q0 on, one head; len 0: no more items
+  int lo, len, q0, head;
+  // blocks of each tile: up to its last row's own (the tiles start on block borders); a tile past the end has none
+  __device__ __forceinline__ int n0() const { return q0 / kPrKeys + 1; }
+  __device__ __forceinline__ int n1() const { return q0 + kPrTile < len ? q0 / kPrKeys + 2 : 0; }
+  __device__ __forceinline__ int blocks() const { return q0 / kPrKeys + (q0 + kPrTile < len ? 2 : 1); }
+};
+
+// The items in order, by a whole warp. Up to 256 prompts: all prompts' tiles sorted by their number in the prompt,
+// latest (longest) first, found by counting (a lane holds the tile counts of eight prompts). More: the tile slots from
+// the last to the first, which is sorted within each prompt.
+struct PrDealer {
+  int tiles[kPrSorted];
+  int total;  // tiles (sorted) or slots
+  bool sorted;
+  __device__ __forceinline__ static int count(const PrParams& p, int b) {
+    const int lo = p.cu[b], hi = p.cu[b + 1];
+    return lo < 0 || hi > p.total || lo >= hi ? 0 : (hi - lo + kPrRows - 1) / kPrRows;
+  }
+  __device__ __forceinline__ int from(int i) const {  // tiles numbered i and up, over all prompts
+    int n = 0;
+#pragma unroll
+    for (int m = 0; m < kPrSorted; ++m) n += max(tiles[m] - i, 0);
+    return __reduce_add_sync(0xFFFFFFFFu, n);
+  }
+  __device__ __forceinline__ void init(const PrParams& p, int lane) {
+    sorted = p.B <= 32 * kPrSorted;
+#pragma unroll
+    for (int m = 0; m < kPrSorted; ++m) tiles[m] = sorted && 32 * m + lane < p.B ? count(p, 32 * m + lane) : 0;
+    total = sorted ? from(0) : p.slots;
+  }
+  __device__ __forceinline__ PrItem item(const PrParams& p, long long w, int lane) const {  // len 0: nothing there
+    PrItem it{0, 0, 0, static_cast<int>(w % p.Hq)};
+    const int r = static_cast<int>(w / p.Hq);
+    int b;
+    if (sorted) {
+      int top = 0;
+#pragma unroll
+      for (int m = 0; m < kPrSorted; ++m) top = max(top, tiles[m]);
+      int lo = 0, hi = __reduce_max_sync(0xFFFFFFFFu, top) - 1;  // the last i with from(i) > r
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (from(mid) > r) lo = mid;
+        else hi = mid - 1;
+      }
+      int left = r - from(lo + 1);  // in order among the prompts with a tile `lo`
+      b = -1;
+#pragma unroll
+      for (int m = 0; m < kPrSorted; ++m) {
+        unsigned has = __ballot_sync(0xFFFFFFFFu, tiles[m] > lo);
+        if (b < 0 && left < __popc(has)) {
+          for (; left > 0; --left) has &= has - 1u;
+          b = 32 * m + __ffs(has) - 1;
+        }
+        left -= __popc(has);
+      }
+      if (b < 0) return it;
+      it.q0 = lo * kPrRows;
+    } else {
+      const int slot = p.slots - 1 - r;
+      b = pr_find(p, slot, lane);
+      if (b < 0) return it;
+      it.q0 = (slot - pr_start(p, b)) * kPrRows;
+    }
+    const int lo = p.cu[b], hi = p.cu[b + 1];
+    if (lo < 0 || hi > p.total || lo >= hi || it.q0 < 0 || it.q0 >= hi - lo) return it;
+    it.lo = lo;
+    it.len = hi - lo;
+    return it;
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, const __grid_constant__ PrMaps maps,
                                                                     WsHeader* hdr) {
   constexpr int kHalves = D / 64;
   constexpr uint32_t kTileBytes = kHalves * kPrBox;          // one Q tile, one K block or one V block
-  constexpr int kStages = D == 128 ? 5 : 8;                  // ring entries: K and V blocks in turn
+  constexpr unsigned kStages = D == 128 ? 5 : 8;             // ring entries: K and V blocks in turn
   extern __shared__ float4 smem_f4[];
   unsigned char* sq =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_f4) + 1023) & ~uintptr_t(1023));
   unsigned char* skv = sq + 2 * kTileBytes;
-  __shared__ uint64_t q_full[2], kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2][2], o_full[2];
+  __shared__ uint64_t q_full[2], q_empty[2], kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2][2];
+  __shared__ uint64_t o_full[2], o_empty[2], it_full[kPrAhead], it_empty[kPrAhead];
+  __shared__ PrItem s_items[kPrAhead];
   __shared__ uint32_t s_tmem;
-  __shared__ unsigned s_issued, s_used;  // ring entries issued and waited for (failure drain)
-  __shared__ int s_bad;
+  __shared__ unsigned s_issued, s_used, s_qi[2], s_qu[2];  // copies issued and waited for (failure drain)
+  __shared__ int s_bad[2];  // by tile: the last item (from 1 on) in whose last block a value was not finite
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
 
-  if (blockIdx.x == 0 && warp == 2) {  // lengths that contradict themselves are reported once
-    bool bad = lane == 0 && (p.cu[0] < 0 || p.cu[p.B] > p.total);
-    for (int b = lane; b < p.B; b += 32) bad = bad || p.cu[b] > p.cu[b + 1];
-    if (bad) record_error(hdr, DT_ERR_INVALID_ARG);
-  }
-  // heavy tiles (late in their prompts) first; the heads of one tile next to each other share keys through L2
-  const int slot = p.slots - 1 - static_cast<int>(blockIdx.x) / p.Hq, head = static_cast<int>(blockIdx.x) % p.Hq;
-  const int b = pr_find(p, slot, lane);
-  if (b < 0) return;
-  const int lo = p.cu[b], hi = p.cu[b + 1];
-  if (lo < 0 || hi > p.total || lo >= hi) return;
-  const int len = hi - lo, q0 = (slot - pr_start(p, b)) * kPrRows;
-  if (q0 < 0 || q0 >= len) return;
-  const int kvh = head / p.G;
-  // blocks of each tile: up to its last row's own (the tiles start on block borders); a tile past the end has none
-  const int n0 = q0 / kPrKeys + 1, n1 = q0 + kPrTile < len ? n0 + 1 : 0, nblk = n1 > n0 ? n1 : n0;
-
   if (t == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (unsigned i = 0; i < kStages; ++i) {
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i][0], kPrSoft / 32);
       mbar_init(&p_full[i][1], kPrSoft / 32);
       mbar_init(&o_full[i], 1);
+      mbar_init(&o_empty[i], kPrSoft / 32);
+      s_qi[i] = s_qu[i] = 0u;
+      s_bad[i] = 0;
+    }
+    for (int i = 0; i < kPrAhead; ++i) {
+      mbar_init(&it_full[i], 1);
+      mbar_init(&it_empty[i], 2 + 2 * kPrSoft / 32);  // the loader, the MMA thread, the softmax warps
     }
     mbar_fence_init();
     s_issued = s_used = 0u;
-    s_bad = 0;
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
@@ -200,37 +301,94 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = s_tmem;  // columns: S0 and P0 at 0, S1 and P1 at 128, O0 at 256, O1 at 384
   bool ok = true;
+  // Item k (from 0) as a reader sees it; `arrive`: this thread counts as one of the slot's readers.
+  auto read_item = [&](int k, PrItem& it, bool arrive) {
+    const int s = k % kPrAhead;
+    if (!pr_wait(&it_full[s], static_cast<unsigned>(k / kPrAhead) & 1u)) return false;
+    it = s_items[s];
+    if (arrive) mbar_arrive(&it_empty[s]);
+    return true;
+  };
 
-  if (warp == 0 && lane == 0) {  // TMA: Q0, K0, Q1, V0, K1, V1, ...
-    unsigned e = 0;
-    auto load_q = [&](int i) {
-      mbar_expect_tx(&q_full[i], kTileBytes);
-      for (int h = 0; h < kHalves; ++h)
-        tma_load_3d(sq + i * kTileBytes + h * kPrBox, &maps.q, 64 * h, head, lo + q0 + i * kPrTile, &q_full[i]);
-    };
-    auto load_kv = [&](const CUtensorMap* map, int j) {
-      const unsigned st = e % kStages, use = e / kStages;
-      if (use > 0 && !mbar_wait(&kv_empty[st], (use - 1) & 1u, kPrBudgetNs)) return false;
-      mbar_expect_tx(&kv_full[st], kTileBytes);
-      for (int h = 0; h < kHalves; ++h)
-        tma_load_3d(skv + st * kTileBytes + h * kPrBox, map, 64 * h, kvh, lo + j * kPrKeys, &kv_full[st]);
-      s_issued = ++e;
-      return true;
-    };
-    load_q(0);
-    for (int j = 0; j < nblk && ok; ++j) {
-      ok = load_kv(&maps.k, j);
-      if (j == 0 && n1 > 0) load_q(1);
-      if (ok) ok = load_kv(&maps.v, j);
+  if (warp == 2) {  // the items
+    if (blockIdx.x == 0) {  // lengths that contradict themselves are reported once
+      bool bad = lane == 0 && (p.cu[0] < 0 || p.cu[p.B] > p.total);
+      for (int b = lane; b < p.B; b += 32) bad = bad || p.cu[b] > p.cu[b + 1];
+      if (bad) record_error(hdr, DT_ERR_INVALID_ARG);
     }
-  } else if (warp == 1) {  // MMA
-    if (elect_one()) {
+    PrDealer dealer;
+    dealer.init(p, lane);
+    const long long end = static_cast<long long>(dealer.total) * p.Hq;
+    int k = 0;
+    for (long long w = blockIdx.x; ok;) {
+      PrItem it{0, 0, 0, 0};
+      const long long at = w;
+      if (w < end) {  // the next one, for when this one is through
+        unsigned got = 0;
+        if (lane == 0) got = atomicAdd(&hdr->deal_next, 1u);
+        w = static_cast<long long>(p.grid) + __shfl_sync(0xFFFFFFFFu, got, 0);
+      } else if (lane == 0 && atomicAdd(&hdr->deal_done, 1u) == static_cast<unsigned>(p.grid) - 1u) {
+        hdr->deal_next = hdr->deal_done = 0u;  // every CTA is through with them: ready for the next call
+      }
+      if (at < end) {
+        it = dealer.item(p, at, lane);
+        if (it.len == 0) continue;
+      }
+      const int s = k % kPrAhead;
+      if (k >= kPrAhead)
+        ok = __all_sync(0xFFFFFFFFu, pr_wait(&it_empty[s], static_cast<unsigned>(k / kPrAhead - 1) & 1u));
+      if (!ok) break;
+      if (lane == 0) {
+        s_items[s] = it;
+        mbar_arrive(&it_full[s]);
+      }
+      __syncwarp();
+      ++k;
+      if (it.len == 0) break;
+    }
+  } else if (warp == 0) {
+    if (elect_one()) {  // TMA, per item: Q0, K0, Q1, V0, K1, V1, ...
+      unsigned st = 0, par = 1u, e = 0, uq[2] = {0u, 0u};
+      auto load_q = [&](int i, const PrItem& it) {
+        if (uq[i] > 0 && !pr_wait(&q_empty[i], (uq[i] - 1u) & 1u)) return false;
+        mbar_expect_tx(&q_full[i], kTileBytes);
+        for (int h = 0; h < kHalves; ++h)
+          tma_load_3d(sq + i * kTileBytes + h * kPrBox, &maps.q, 64 * h, it.head, it.lo + it.q0 + i * kPrTile, &q_full[i]);
+        s_qi[i] = ++uq[i];
+        return true;
+      };
+      auto load_kv = [&](const CUtensorMap* map, const PrItem& it, int kvh, int j) {
+        if (e >= kStages && !pr_wait(&kv_empty[st], par)) return false;
+        mbar_expect_tx(&kv_full[st], kTileBytes);
+        for (int h = 0; h < kHalves; ++h)
+          tma_load_3d(skv + st * kTileBytes + h * kPrBox, map, 64 * h, kvh, it.lo + j * kPrKeys, &kv_full[st]);
+        s_issued = ++e;
+        if (++st == kStages) {
+          st = 0;
+          par ^= 1u;
+        }
+        return true;
+      };
+      for (int k = 0; ok; ++k) {
+        PrItem it;
+        ok = read_item(k, it, true);
+        if (!ok || it.len == 0) break;
+        const int kvh = it.head / p.G, nblk = it.blocks();
+        ok = load_q(0, it);
+        for (int j = 0; j < nblk && ok; ++j) {
+          ok = load_kv(&maps.k, it, kvh, j);
+          if (ok && j == 0 && it.n1() > 0) ok = load_q(1, it);
+          if (ok) ok = load_kv(&maps.v, it, kvh, j);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (elect_one()) {  // MMA
       const uint32_t id_s = umma_idesc(kPrKeys, 128), id_o = umma_idesc(D, 128) | (1u << 16);  // O: V MN-major
-      const int n[2] = {n0, n1};
       const uint64_t dq = umma_desc_sw128(smem_u32(sq)), dk = umma_desc_sw128(smem_u32(skv));
       const uint64_t dv = umma_desc_sw128_mn(smem_u32(skv), kPrBox, 1024u);
       auto wait = [&](uint64_t* bar, unsigned parity) {
-        const bool done = mbar_wait(bar, parity, kPrBudgetNs);
+        const bool done = pr_wait(bar, parity);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         return done;
       };
@@ -239,7 +397,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * kPrBox + (kk & 3) * 32u) >> 4;
           umma_f16(tmem + 128u * i, dq + (i * (kTileBytes >> 4) + off), dk + (st * (kTileBytes >> 4) + off), id_s,
-                       kk > 0 ? 1u : 0u);
+                   kk > 0 ? 1u : 0u);
         }
         umma_commit(&s_full[i]);
       };
@@ -248,229 +406,287 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
         for (int k2 = 0; k2 < kPrKeys / 32; ++k2) {
           const int kk = half * (kPrKeys / 32) + k2;
           umma_f16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk,
-                          dv + (st * (kTileBytes >> 4) + kk * (2048u >> 4)), id_o, fresh && kk == 0 ? 0u : 1u);
+                      dv + (st * (kTileBytes >> 4) + kk * (2048u >> 4)), id_o, fresh && kk == 0 ? 0u : 1u);
         }
       };
-      unsigned st = 0, par = 0;  // ring entry and its parity: K_j, V_j, K_{j+1}, ...
+      unsigned st = 0, par = 0, used = 0;  // ring entry last waited for and its parity: K_j, V_j, K_{j+1}, ...
       auto step = [&]() {
         if (++st == kStages) {
           st = 0;
           par ^= 1u;
         }
       };
-      unsigned used = 0;
       auto wait_entry = [&]() {
         const bool done = wait(&kv_full[st], par);
         if (done) s_used = ++used;
         return done;
       };
-      ok = wait_entry();
-      for (int i = 0; i < 2 && ok; ++i)
-        if (n[i] > 0) {
-          ok = wait(&q_full[i], 0);
-          if (ok) issue_s(i, 0);
-        }
-      if (ok) umma_commit(&kv_empty[0]);
-      for (int j = 0; j < nblk && ok; ++j) {
-        step();
-        const unsigned sv = st;
-        ok = wait_entry();
-        if (ok && j + 1 < nblk) {
+      unsigned uq[2] = {0u, 0u}, up[2] = {0u, 0u}, uo[2] = {0u, 0u};  // uses so far
+      // The first scores of tile i of an item whose K0 is in entry st; q_empty follows the last scores of a tile.
+      auto start = [&](int i, int n) {
+        if (n == 0) return true;
+        if (!wait(&q_full[i], uq[i] & 1u)) return false;
+        s_qu[i] = ++uq[i];
+        issue_s(i, st);
+        if (n == 1) umma_commit(&q_empty[i]);
+        return true;
+      };
+      PrItem it;
+      ok = read_item(0, it, true);
+      int n[2] = {it.n0(), it.n1()}, nblk = it.blocks();
+      bool more = ok && it.len > 0;
+      if (more) {
+        ok = wait_entry() && start(0, n[0]) && start(1, n[1]);
+        if (ok) umma_commit(&kv_empty[0]);
+      }
+      for (int k = 0; ok && more; ++k) {
+        ok = read_item(k + 1, it, true);
+        if (!ok) break;
+        more = it.len > 0;
+        const int m[2] = {more ? it.n0() : 0, more ? it.n1() : 0};  // the next item's
+        for (int j = 0; j < nblk && ok; ++j) {
+          const bool last = j + 1 == nblk;
           step();
+          const unsigned sv = st;
           ok = wait_entry();
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (!ok || j >= n[i]) continue;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (ok) ok = wait(&p_full[i][half], j & 1u);
-            if (ok) issue_o(i, sv, half, j == 0);
+          if (ok && (!last || more)) {  // the next block's keys, or the next item's first
+            step();
+            ok = wait_entry();
           }
-          if (!ok) continue;
-          if (j + 1 == n[i]) umma_commit(&o_full[i]);
-          // the next scores overwrite P: the tensor cores run this warp's products in order
-          if (j + 1 < n[i]) issue_s(i, st);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (!ok) continue;
+            if (j < n[i]) {
+              if (j == 0) {  // the epilogue before has read O
+                if (uo[i] > 0) ok = wait(&o_empty[i], (uo[i] - 1u) & 1u);
+                ++uo[i];
+              }
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                if (ok) ok = wait(&p_full[i][half], up[i] & 1u);
+                if (ok) issue_o(i, sv, half, j == 0);
+              }
+              ++up[i];
+              if (!ok) continue;
+              if (j + 1 == n[i]) {
+                umma_commit(&o_full[i]);
+              } else {  // the next scores overwrite P: the tensor cores run this thread's products in order
+                issue_s(i, st);
+                if (j + 2 == n[i]) umma_commit(&q_empty[i]);
+              }
+            }
+            if (last) ok = start(i, m[i]);
+          }
+          if (ok) {
+            umma_commit(&kv_empty[sv]);
+            if (!last || more) umma_commit(&kv_empty[st]);
+          }
         }
-        if (ok) {
-          umma_commit(&kv_empty[sv]);
-          if (j + 1 < nblk) umma_commit(&kv_empty[st]);
-        }
+        n[0] = m[0];
+        n[1] = m[1];
+        nblk = it.blocks();
       }
     }
   } else if (warp >= 4) {  // softmax of tile i
     // A warp owns 16 rows of its quarter of tensor memory; four neighbouring threads share two rows (ra, ra + 8), each
     // holding a quarter of their columns.
-    const int i = (warp - 4) >> 3, tt = t - 128 - kPrSoft * i, nb = i ? n1 : n0;
+    const int i = (warp - 4) >> 3, tt = t - 128 - kPrSoft * i;
     const int lane0 = 32 * (warp & 3) + 16 * (((warp - 4) >> 2) & 1);
     const uint32_t lanes = static_cast<uint32_t>(lane0) << 16;
     const uint32_t ts = tmem + lanes + 128u * i, to = tmem + lanes + 256u + 128u * i;
-    const int ra = lane0 + (lane >> 2), col = 2 * (lane & 3);
-    const int row0 = q0 + i * kPrTile + ra;  // row ra's token in its prompt; the other row's is 8 further
-    float ref[2] = {-INFINITY, -INFINITY};   // running maximum of the scaled scores, as last raised
-    uint64_t nref[2] = {0ull, 0ull};         // minus it, twice (0 while nothing finite was seen)
-    float l[2] = {0.f, 0.f};                 // sums of this thread's weights
-    const uint64_t scale2 = pr_pair(p.scale_log2, p.scale_log2);
-    for (int j = 0; j < nb && ok; ++j) {
-      const bool diag = j + 1 == nb;
-      if (diag) {
-        // The block where the tile's rows see different keys. A weight of zero does not hide a value that is not
-        // finite from the tensor cores (0 x inf is NaN): rows past the prompt's end are cleared, and what is not
-        // finite among the block's values is cleared too and added to the rows that see it at the end (its weight
-        // there is positive, and any positive multiple of it gives the same sum).
-        const unsigned e = 2u * j + 1u;
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&kv_full[e % kStages], (e / kStages) & 1u, kPrBudgetNs));
-        if (!ok) break;
-        unsigned char* sv = skv + (e % kStages) * kTileBytes;
-        const int valid = len - j * kPrKeys;  // keys of the block inside the prompt
-        __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
-        const __nv_bfloat162 zero = acc;
-#pragma unroll 4
-        for (int c = tt; c < kHalves * kPrKeys * 8; c += kPrSoft) {  // 16-byte pieces; eight a row
-          uint4* at = reinterpret_cast<uint4*>(sv + 16 * c);
-          if (((c >> 3) & (kPrKeys - 1)) >= valid) {
-            *at = make_uint4(0u, 0u, 0u, 0u);
-          } else {
-            const uint4 x = *at;
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int k2 = 0; k2 < 4; ++k2)
-              acc = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[k2]), zero, acc);  // x 0: NaN if not finite
-          }
-        }
-        const float2 a2 = __bfloat1622float2(acc);
-        if (!(a2.x == 0.f && a2.y == 0.f)) {  // rare
-          for (int c = tt; c < kHalves * kPrKeys * 8; c += kPrSoft) {
-            unsigned short* at = reinterpret_cast<unsigned short*>(sv + 16 * c);
-            for (int k2 = 0; k2 < 8; ++k2)
-              if ((at[k2] & 0x7F80u) == 0x7F80u) at[k2] = 0;
-          }
-          atomicOr(&s_bad, 1 << i);
-        }
-      }
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_full[i], j & 1u, kPrBudgetNs));
+    const int ra = lane0 + (lane >> 2), quad = lane & 3, col = 2 * quad;
+    unsigned base = 0, us = 0, uo = 0;  // ring entry of the item's K0; blocks and items of this tile so far
+    for (int k = 0; ok; ++k) {
+      ok = __all_sync(0xFFFFFFFFu, pr_wait(&it_full[k % kPrAhead], static_cast<unsigned>(k / kPrAhead) & 1u));
       if (!ok) break;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      float s[64];
-      pr_ld_s(ts, s);
-      if (diag) {
-        const int lim = row0 - j * kPrKeys - col;  // row ra sees this thread's columns 8 g + e up to here
+      const PrItem& it = s_items[k % kPrAhead];  // stays until this warp is through with it
+      if (it.len == 0) break;
+      const int nb = i ? it.n1() : it.n0();
+      const int row0 = it.q0 + i * kPrTile + ra;  // row ra's token in its prompt; the other row's is 8 further
+      // minus the running maximum of the scaled scores, as last raised; at first so large that any finite score raises
+      // it, and that a score of -inf has no weight and NaN stays
+      float nref[2] = {kPrNone, kPrNone};
+      float l[2] = {0.f, 0.f};                    // sums of this thread's weights
+      for (int j = 0; j < nb && ok; ++j, ++us) {
+        const bool diag = j + 1 == nb;
+        if (diag) {
+          // The block where the tile's rows see different keys. A weight of zero does not hide a value that is not
+          // finite from the tensor cores (0 x inf is NaN): rows past the prompt's end are cleared, and what is not
+          // finite among the block's values is cleared too and added to the rows that see it at the end (its weight
+          // there is positive, and any positive multiple of it gives the same sum).
+          const unsigned e = base + 2u * j + 1u;
+          ok = __all_sync(0xFFFFFFFFu, pr_wait(&kv_full[e % kStages], (e / kStages) & 1u));
+          if (!ok) break;
+          unsigned char* sv = skv + (e % kStages) * kTileBytes;
+          const int valid = it.len - j * kPrKeys;  // keys of the block inside the prompt
+          __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
+          const __nv_bfloat162 zero = acc;
+#pragma unroll 4
+          for (int c = tt; c < kHalves * kPrKeys * 8; c += kPrSoft) {  // 16-byte pieces; eight a row
+            uint4* at = reinterpret_cast<uint4*>(sv + 16 * c);
+            if (((c >> 3) & (kPrKeys - 1)) >= valid) {
+              *at = make_uint4(0u, 0u, 0u, 0u);
+            } else {
+              const uint4 x = *at;
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int g = 0; g < 16; ++g)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (8 * g + (e & 1) > lim + 8 * (e >> 1)) s[4 * g + e] = -INFINITY;
-      }
-      float mx[2];
-#pragma unroll
-      for (int k2 = 0; k2 < 2; ++k2) {
-        float u = fmaxf(s[2 * k2], s[2 * k2 + 1]), w = fmaxf(s[2 * k2 + 4], s[2 * k2 + 5]);
-#pragma unroll
-        for (int g = 2; g < 16; g += 2) {
-          u = pr_max3(u, s[4 * g + 2 * k2], s[4 * g + 2 * k2 + 1]);
-          w = pr_max3(w, s[4 * g + 4 + 2 * k2], s[4 * g + 5 + 2 * k2]);
-        }
-        mx[k2] = fmaxf(u, w) * p.scale_log2;
-      }
-      if (__any_sync(0xFFFFFFFFu, mx[0] > ref[0] + kPrLazy || mx[1] > ref[1] + kPrLazy)) {  // rare: raise, rescale O
-        float alpha[2];
-#pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2) {
-          mx[k2] = fmaxf(mx[k2], __shfl_xor_sync(0xFFFFFFFFu, mx[k2], 1));
-          mx[k2] = fmaxf(mx[k2], __shfl_xor_sync(0xFFFFFFFFu, mx[k2], 2));
-          const bool raise = mx[k2] > ref[k2] + kPrLazy;
-          alpha[k2] = raise ? pr_exp2(ref[k2] - mx[k2]) : 1.f;  // from nothing: 2^-inf = 0
-          l[k2] *= alpha[k2];
-          if (raise) {
-            ref[k2] = mx[k2];
-            nref[k2] = pr_pair(-mx[k2], -mx[k2]);
-          }
-        }
-        if (j > 0) {  // S is full, so the products into O before it are complete
-#pragma unroll 1
-          for (int h = 0; h < D / 32; ++h) {
-            float o[16];
-            pr_ld_o(to + 32u * h, o);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] *= alpha[(e >> 1) & 1];
-            pr_st_o(to + 32u * h, o);
-          }
-        }
-      }
-      uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {  // group 8 h + c / 2, row c % 2
-          const int at = 32 * h + 2 * c;
-          float a, bb;
-          pr_unpair(pr_fma2(pr_pair(s[at], s[at + 1]), scale2, nref[c & 1]), a, bb);
-          a = pr_exp2(a);
-          bb = pr_exp2(bb);
-          ls[c & 3] = pr_add2(ls[c & 3], pr_pair(a, bb));
-          pk[c] = pr_pack(a, bb);
-        }
-        pr_st_p(ts + 32u * h, pk);
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        if (diag && h == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the cleared values
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[i][h]);  // half of the weights are in place: their products may start
-      }
-#pragma unroll
-      for (int k2 = 0; k2 < 2; ++k2) {
-        float la, lb;
-        pr_unpair(pr_add2(ls[k2], ls[k2 + 2]), la, lb);
-        l[k2] += la + lb;
-      }
-    }
-    if (nb > 0 && ok) {
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&o_full[i], 0, kPrBudgetNs));
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      if (ok) {
-        float inv[2];
-#pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2) {
-          l[k2] += __shfl_xor_sync(0xFFFFFFFFu, l[k2], 1);
-          l[k2] += __shfl_xor_sync(0xFFFFFFFFu, l[k2], 2);
-          inv[k2] = 1.f / l[k2];  // the row's own key is visible; a sum of 0 or NaN gives NaN
-        }
-        const int bad = *reinterpret_cast<volatile int*>(&s_bad);
-        // through the tile's Q buffer (its last product is complete), so that rows leave in whole 16-byte pieces
-        unsigned char* so = sq + i * kTileBytes;
-#pragma unroll
-        for (int h = 0; h < D / 32; ++h) {
-          float o[16];
-          pr_ld_o(to + 32u * h, o);
-          if (bad) {  // rare: tile 0's clearing reaches tile 1 too, which shares the block
-            for (int key = (n0 - 1) * kPrKeys; key <= row0 + 8 && key < len; ++key) {
-              const unsigned short* vr = p.v + static_cast<size_t>(lo + key) * p.v_stride + kvh * D + 32 * h + col;
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const uint32_t bits = static_cast<uint32_t>(vr[8 * (e >> 2) + (e & 1)]) << 16;
-                if ((bits & 0x7F800000u) == 0x7F800000u && key <= row0 + 8 * ((e >> 1) & 1)) o[e] += __uint_as_float(bits);
-              }
+              for (int k2 = 0; k2 < 4; ++k2)
+                acc = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[k2]), zero, acc);  // x 0: NaN if not finite
             }
           }
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const int r = ra + 8 * ((e >> 1) & 1), c16 = 4 * (h & 1) + (e >> 2);
-            *reinterpret_cast<uint32_t*>(so + (h >> 1) * kPrBox + r * 128 + ((c16 ^ (r & 7)) << 4) + 2 * col) =
-                pr_pack(o[e] * inv[(e >> 1) & 1], o[e + 1] * inv[(e >> 1) & 1]);
+          const float2 a2 = __bfloat1622float2(acc);
+          if (!(a2.x == 0.f && a2.y == 0.f)) {  // rare
+            for (int c = tt; c < kHalves * kPrKeys * 8; c += kPrSoft) {
+              unsigned short* at = reinterpret_cast<unsigned short*>(sv + 16 * c);
+              for (int k2 = 0; k2 < 8; ++k2)
+                if ((at[k2] & 0x7F80u) == 0x7F80u) at[k2] = 0;
+            }
+            atomicMax(&s_bad[i], k + 1);
           }
         }
-        __syncwarp();
-        constexpr int kPieces = D / 8, kRowsAtOnce = 32 / kPieces;
-        const int piece = lane % kPieces;
+        ok = __all_sync(0xFFFFFFFFu, pr_wait(&s_full[i], us & 1u));
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        float s[64];
+        pr_ld_s(ts, s);
+        if (diag) {
+          const int lim = row0 - j * kPrKeys - col;  // row ra sees this thread's columns 8 g + e up to here
 #pragma unroll
-        for (int k2 = 0; k2 < 16; k2 += kRowsAtOnce) {
-          const int r = lane0 + k2 + lane / kPieces, row = q0 + i * kPrTile + r;
-          const uint4 x = *reinterpret_cast<const uint4*>(so + (piece >> 3) * kPrBox + r * 128 + (((piece & 7) ^ (r & 7)) << 4));
-          if (row < len)
-            *reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(lo + row) * p.Hq + head) * D + 8 * piece) = x;
+          for (int g = 0; g < 16; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (8 * g + (e & 1) > lim + 8 * (e >> 1)) s[4 * g + e] = -INFINITY;
+        }
+        float mx[2];
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2) {
+          float u = fmaxf(s[2 * k2], s[2 * k2 + 1]), w = fmaxf(s[2 * k2 + 4], s[2 * k2 + 5]);
+#pragma unroll
+          for (int g = 2; g < 16; g += 2) {
+            u = pr_max3(u, s[4 * g + 2 * k2], s[4 * g + 2 * k2 + 1]);
+            w = pr_max3(w, s[4 * g + 4 + 2 * k2], s[4 * g + 5 + 2 * k2]);
+          }
+          mx[k2] = fmaxf(u, w) * p.scale_log2;
+        }
+        if (__any_sync(0xFFFFFFFFu, mx[0] + nref[0] > kPrLazy || mx[1] + nref[1] > kPrLazy)) {  // rare: raise, rescale O
+          float alpha[2];
+#pragma unroll
+          for (int k2 = 0; k2 < 2; ++k2) {
+            mx[k2] = fmaxf(mx[k2], __shfl_xor_sync(0xFFFFFFFFu, mx[k2], 1));
+            mx[k2] = fmaxf(mx[k2], __shfl_xor_sync(0xFFFFFFFFu, mx[k2], 2));
+            const bool raise = mx[k2] + nref[k2] > kPrLazy;
+            alpha[k2] = raise ? pr_exp2(-nref[k2] - mx[k2]) : 1.f;  // from nothing: 0
+            l[k2] *= alpha[k2];
+            if (raise) nref[k2] = -mx[k2];
+          }
+          if (j > 0) {  // S is full, so the products into O before it are complete
+#pragma unroll 1
+            for (int h = 0; h < D / 32; ++h) {
+              float o[16];
+              pr_ld_o(to + 32u * h, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= alpha[(e >> 1) & 1];
+              pr_st_o(to + 32u * h, o);
+            }
+          }
+        }
+        const uint64_t scale2 = pr_pair(p.scale_log2, p.scale_log2);
+        const uint64_t nref2[2] = {pr_pair(nref[0], nref[0]), pr_pair(nref[1], nref[1])};
+        uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {  // group 8 h + c / 2, row c % 2
+            const int at = 32 * h + 2 * c;
+            float a, bb;
+            pr_unpair(pr_fma2(pr_pair(s[at], s[at + 1]), scale2, nref2[c & 1]), a, bb);
+            a = pr_exp2(a);
+            bb = pr_exp2(bb);
+            ls[c & 3] = pr_add2(ls[c & 3], pr_pair(a, bb));
+            pk[c] = pr_pack(a, bb);
+          }
+          pr_st_p(ts + 32u * h, pk);
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          if (diag && h == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the cleared values
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[i][h]);  // half of the weights are in place: their products may start
+        }
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2) {
+          float la, lb;
+          pr_unpair(pr_add2(ls[k2], ls[k2 + 2]), la, lb);
+          l[k2] += la + lb;
         }
       }
+      if (!ok) break;
+      base += 2u * it.blocks();
+      if (nb == 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&it_empty[k % kPrAhead]);
+        continue;
+      }
+      ok = __all_sync(0xFFFFFFFFu, pr_wait(&o_full[i], uo & 1u));
+      if (!ok) break;
+      ++uo;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      float inv[2];
+#pragma unroll
+      for (int k2 = 0; k2 < 2; ++k2) {
+        l[k2] += __shfl_xor_sync(0xFFFFFFFFu, l[k2], 1);
+        l[k2] += __shfl_xor_sync(0xFFFFFFFFu, l[k2], 2);
+        inv[k2] = 1.f / l[k2];  // the row's own key is visible; a sum of 0 or NaN gives NaN
+      }
+      // a later item's mark counts too: adding what is not finite to rows that see it changes nothing
+      const bool bad = *reinterpret_cast<volatile int*>(&s_bad[0]) > k || *reinterpret_cast<volatile int*>(&s_bad[1]) > k;
+      unsigned short* po = p.out + (static_cast<size_t>(it.lo + row0) * p.Hq + it.head) * D + 8 * quad;
+      float o[D / 2];
+      if constexpr (D == 128)
+        pr_ld_s(to, o);
+      else
+        pr_ld_half(to, o);
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_empty[i]);  // O is free for the next item
+      if (bad) {  // rare: tile 0's clearing reaches tile 1 too, which shares the block
+        for (int key = (it.n0() - 1) * kPrKeys; key <= row0 + 8 && key < it.len; ++key) {
+          const unsigned short* vr = p.v + static_cast<size_t>(it.lo + key) * p.v_stride + it.head / p.G * D + col;
+#pragma unroll
+          for (int e = 0; e < D / 2; ++e) {
+            const uint32_t bits = static_cast<uint32_t>(vr[8 * (e >> 2) + (e & 1)]) << 16;
+            if ((bits & 0x7F800000u) == 0x7F800000u && key <= row0 + 8 * ((e >> 1) & 1)) o[e] += __uint_as_float(bits);
+          }
+        }
+      }
+      // four threads hold the four words of each 16 bytes: transposed among them, so that each stores 16 bytes
+      const bool in[2] = {row0 < it.len, row0 + 8 < it.len};
+#pragma unroll
+      for (int h = 0; h < D / 32; ++h)
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2) {
+          uint32_t x[4];
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            x[g] = pr_pack(o[16 * h + 4 * g + 2 * k2] * inv[k2], o[16 * h + 4 * g + 2 * k2 + 1] * inv[k2]);
+#pragma unroll
+          for (int g = 0; g < 4; g += 2) {
+            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, quad & 1 ? x[g] : x[g + 1], 1);
+            if (quad & 1) x[g] = got;
+            else x[g + 1] = got;
+          }
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, quad & 2 ? x[g] : x[g + 2], 2);
+            if (quad & 2) x[g] = got;
+            else x[g + 2] = got;
+          }
+          if (in[k2])
+            *reinterpret_cast<uint4*>(po + static_cast<size_t>(8 * k2) * p.Hq * D + 32 * h) =
+                make_uint4(x[0], x[1], x[2], x[3]);
+        }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&it_empty[k % kPrAhead]);
     }
   }
   ok = __syncthreads_and(ok);
@@ -478,8 +694,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
     record_error(hdr, DT_ERR_TIMEOUT);
     // copies issued but never waited for must land before the CTA leaves: wait for them too (bounded)
     for (unsigned e = s_used; e < s_issued; ++e) mbar_wait(&kv_full[e % kStages], (e / kStages) & 1u, kPrBudgetNs);
-    mbar_wait(&q_full[0], 0, kPrBudgetNs);
-    if (n1 > 0 && s_issued > 0) mbar_wait(&q_full[1], 0, kPrBudgetNs);
+    for (int i = 0; i < 2; ++i)
+      for (unsigned e = s_qu[i]; e < s_qi[i]; ++e) mbar_wait(&q_full[i], e & 1u, kPrBudgetNs);
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
@@ -491,7 +707,7 @@ dt_status pr_launch(const PrParams& p, const PrMaps& maps, WsHeader* hdr, cudaSt
   constexpr size_t smem = 1024 + (2 + (D == 128 ? 5 : 8)) * static_cast<size_t>(D / 64) * kPrBox;
   const void* fn = reinterpret_cast<const void*>(prompt_attn_kernel<D>);
   if (ensure_dynamic_smem(fn, smem) != cudaSuccess) return DT_ERR_CUDA;
-  prompt_attn_kernel<D><<<static_cast<unsigned>(p.slots * p.Hq), kPrThreads, smem, stream>>>(p, maps, hdr);
+  prompt_attn_kernel<D><<<static_cast<unsigned>(p.grid), kPrThreads, smem, stream>>>(p, maps, hdr);
   return cuda_status(cudaGetLastError());
 }
 
@@ -527,6 +743,9 @@ extern "C" dt_status dt_prompt_attention(int total, int B, int Hq, int Hkv, int 
   if (total > INT_MAX / 2 || slots * Hq > INT_MAX) return DT_ERR_UNSUPPORTED;
   PrParams p{};
   p.total = total; p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.slots = static_cast<int>(slots);
+  DeviceInfo di{};
+  if (current_device_info(&di) != cudaSuccess) return DT_ERR_CUDA;
+  p.grid = slots * Hq < di.sms ? static_cast<int>(slots * Hq) : di.sms;
   p.cu = cu_seqlens;
   p.v = static_cast<const unsigned short*>(v);
   p.v_stride = v_stride;
