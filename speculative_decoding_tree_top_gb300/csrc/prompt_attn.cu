@@ -29,7 +29,7 @@ namespace {
 constexpr int kPrTile = 128;                 // query rows of a tile
 constexpr int kPrRows = 2 * kPrTile;         // of a CTA
 constexpr int kPrKeys = 128;                 // keys per block
-constexpr int kPrThreads = 640;              // warps 0-3: load, MMA, items, idle; 4-11 and 12-19: the tiles' softmax
+constexpr int kPrThreads = 640;              // warps 0-3: load, MMA, items, MMA (D = 64); 4-11 and 12-19: the tiles' softmax
 constexpr int kPrSoft = 256;                 // softmax threads of a tile
 constexpr int kPrAhead = 3;                  // items that may be known ahead
 constexpr int kPrSorted = 8;                 // prompts a lane of the item warp keeps: up to 256 are dealt out sorted
@@ -256,15 +256,19 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
   constexpr int kHalves = D / 64;
   constexpr uint32_t kTileBytes = kHalves * kPrBox;          // one Q tile, one K block or one V block
   constexpr unsigned kStages = D == 128 ? 5 : 8;             // ring entries: K and V blocks in turn
+  // Tensor memory, 512 columns. D = 64 leaves room for P beside S: the next scores are computed while the softmax is at
+  // work, and its warps go from block to block. D = 128: P lies over S, and the next scores follow P V.
+  constexpr bool kApart = D == 64;
+  constexpr uint32_t kColP = kApart ? 256 : 0, kStepP = kApart ? 64 : 128, kColO = kApart ? 384 : 256, kStepO = D;
   extern __shared__ float4 smem_f4[];
   unsigned char* sq =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_f4) + 1023) & ~uintptr_t(1023));
   unsigned char* skv = sq + 2 * kTileBytes;
   __shared__ uint64_t q_full[2], q_empty[2], kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2][2];
-  __shared__ uint64_t o_full[2], o_empty[2], it_full[kPrAhead], it_empty[kPrAhead];
+  __shared__ uint64_t s_empty[2], p_empty[2], o_full[2], o_empty[2], it_full[kPrAhead], it_empty[kPrAhead];
   __shared__ PrItem s_items[kPrAhead];
   __shared__ uint32_t s_tmem;
-  __shared__ unsigned s_issued, s_used, s_qi[2], s_qu[2];  // copies issued and waited for (failure drain)
+  __shared__ unsigned s_issued, s_used[2], s_qi[2], s_qu[2];  // copies issued and waited for (failure drain)
   __shared__ int s_bad[2];  // by tile: the last item (from 1 on) in whose last block a value was not finite
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
 
@@ -279,17 +283,19 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i][0], kPrSoft / 32);
       mbar_init(&p_full[i][1], kPrSoft / 32);
+      mbar_init(&s_empty[i], kPrSoft / 32);
+      mbar_init(&p_empty[i], 1);
       mbar_init(&o_full[i], 1);
       mbar_init(&o_empty[i], kPrSoft / 32);
-      s_qi[i] = s_qu[i] = 0u;
+      s_qi[i] = s_qu[i] = s_used[i] = 0u;
       s_bad[i] = 0;
     }
     for (int i = 0; i < kPrAhead; ++i) {
       mbar_init(&it_full[i], 1);
-      mbar_init(&it_empty[i], 2 + 2 * kPrSoft / 32);  // the loader, the MMA thread, the softmax warps
+      mbar_init(&it_empty[i], (kApart ? 3 : 2) + 2 * kPrSoft / 32);  // the loader, MMA threads, softmax warps
     }
     mbar_fence_init();
-    s_issued = s_used = 0u;
+    s_issued = 0u;
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
@@ -299,7 +305,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = s_tmem;  // columns: S0 and P0 at 0, S1 and P1 at 128, O0 at 256, O1 at 384
+  const uint32_t tmem = s_tmem;
   bool ok = true;
   // Item k (from 0) as a reader sees it; `arrive`: this thread counts as one of the slot's readers.
   auto read_item = [&](int k, PrItem& it, bool arrive) {
@@ -382,8 +388,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
         }
       }
     }
-  } else if (warp == 1) {
-    if (elect_one()) {  // MMA
+  } else if (warp < 4) {
+    if ((kApart || warp == 1) && elect_one()) {  // MMA
       const uint32_t id_s = umma_idesc(kPrKeys, 128), id_o = umma_idesc(D, 128) | (1u << 16);  // O: V MN-major
       const uint64_t dq = umma_desc_sw128(smem_u32(sq)), dk = umma_desc_sw128(smem_u32(skv));
       const uint64_t dv = umma_desc_sw128_mn(smem_u32(skv), kPrBox, 1024u);
@@ -405,86 +411,133 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
 #pragma unroll
         for (int k2 = 0; k2 < kPrKeys / 32; ++k2) {
           const int kk = half * (kPrKeys / 32) + k2;
-          umma_f16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk,
+          umma_f16_ts(tmem + kColO + kStepO * i, tmem + kColP + kStepP * i + 8u * kk,
                       dv + (st * (kTileBytes >> 4) + kk * (2048u >> 4)), id_o, fresh && kk == 0 ? 0u : 1u);
         }
       };
-      unsigned st = 0, par = 0, used = 0;  // ring entry last waited for and its parity: K_j, V_j, K_{j+1}, ...
-      auto step = [&]() {
-        if (++st == kStages) {
-          st = 0;
-          par ^= 1u;
-        }
-      };
-      auto wait_entry = [&]() {
-        const bool done = wait(&kv_full[st], par);
-        if (done) s_used = ++used;
-        return done;
-      };
-      unsigned uq[2] = {0u, 0u}, up[2] = {0u, 0u}, uo[2] = {0u, 0u};  // uses so far
-      // The first scores of tile i of an item whose K0 is in entry st; q_empty follows the last scores of a tile.
-      auto start = [&](int i, int n) {
-        if (n == 0) return true;
-        if (!wait(&q_full[i], uq[i] & 1u)) return false;
-        s_qu[i] = ++uq[i];
-        issue_s(i, st);
-        if (n == 1) umma_commit(&q_empty[i]);
-        return true;
-      };
-      PrItem it;
-      ok = read_item(0, it, true);
-      int n[2] = {it.n0(), it.n1()}, nblk = it.blocks();
-      bool more = ok && it.len > 0;
-      if (more) {
-        ok = wait_entry() && start(0, n[0]) && start(1, n[1]);
-        if (ok) umma_commit(&kv_empty[0]);
-      }
-      for (int k = 0; ok && more; ++k) {
-        ok = read_item(k + 1, it, true);
-        if (!ok) break;
-        more = it.len > 0;
-        const int m[2] = {more ? it.n0() : 0, more ? it.n1() : 0};  // the next item's
-        for (int j = 0; j < nblk && ok; ++j) {
-          const bool last = j + 1 == nblk;
-          step();
-          const unsigned sv = st;
-          ok = wait_entry();
-          if (ok && (!last || more)) {  // the next block's keys, or the next item's first
-            step();
-            ok = wait_entry();
-          }
+      if constexpr (kApart) {
+        // Scores and outputs are independent: warp 1 issues the scores, warp 3 the outputs. (One thread's waits would
+        // take longer than the products.)
+        unsigned e = warp == 1 ? 0u : 1u, uses[2] = {0u, 0u}, first[2] = {0u, 0u};
+        for (int k = 0; ok; ++k) {
+          PrItem it;
+          ok = read_item(k, it, true);
+          if (!ok || it.len == 0) break;
+          const int n[2] = {it.n0(), it.n1()}, nblk = it.blocks();
+          for (int j = 0; j < nblk && ok; ++j, e += 2u) {
+            const unsigned st = e % kStages;
+            ok = wait(&kv_full[st], (e / kStages) & 1u);
+            if (!ok) break;
+            s_used[warp >> 1] = e + 1u;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (!ok) continue;
-            if (j < n[i]) {
-              if (j == 0) {  // the epilogue before has read O
-                if (uo[i] > 0) ok = wait(&o_empty[i], (uo[i] - 1u) & 1u);
-                ++uo[i];
-              }
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                if (ok) ok = wait(&p_full[i][half], up[i] & 1u);
-                if (ok) issue_o(i, sv, half, j == 0);
-              }
-              ++up[i];
-              if (!ok) continue;
-              if (j + 1 == n[i]) {
-                umma_commit(&o_full[i]);
-              } else {  // the next scores overwrite P: the tensor cores run this thread's products in order
+            for (int i = 0; i < 2; ++i) {
+              if (!ok || j >= n[i]) continue;
+              if (warp == 1) {
+                if (j == 0) {
+                  ok = wait(&q_full[i], first[i] & 1u);
+                  if (!ok) continue;
+                  s_qu[i] = ++first[i];
+                }
+                if (uses[i] > 0) ok = wait(&s_empty[i], (uses[i] - 1u) & 1u);  // the scores before have been read
+                ++uses[i];
+                if (!ok) continue;
                 issue_s(i, st);
-                if (j + 2 == n[i]) umma_commit(&q_empty[i]);
+                if (j + 1 == n[i]) umma_commit(&q_empty[i]);
+              } else {
+                if (j == 0) {  // the epilogue before has read O
+                  if (first[i] > 0) ok = wait(&o_empty[i], (first[i] - 1u) & 1u);
+                  ++first[i];
+                }
+                if (ok) ok = wait(&p_full[i][1], uses[i] & 1u);
+                ++uses[i];
+                if (!ok) continue;
+                issue_o(i, st, 0, j == 0);
+                issue_o(i, st, 1, false);
+                umma_commit(&p_empty[i]);
+                if (j + 1 == n[i]) umma_commit(&o_full[i]);
               }
             }
-            if (last) ok = start(i, m[i]);
-          }
-          if (ok) {
-            umma_commit(&kv_empty[sv]);
-            if (!last || more) umma_commit(&kv_empty[st]);
+            if (ok) umma_commit(&kv_empty[st]);
           }
         }
-        n[0] = m[0];
-        n[1] = m[1];
-        nblk = it.blocks();
+      } else {
+        unsigned st = 0, par = 0, used = 0;  // ring entry last waited for and its parity: K_j, V_j, K_{j+1}, ...
+        auto step = [&]() {
+          if (++st == kStages) {
+            st = 0;
+            par ^= 1u;
+          }
+        };
+        auto wait_entry = [&]() {
+          const bool done = wait(&kv_full[st], par);
+          if (done) s_used[0] = ++used;
+          return done;
+        };
+        unsigned uq[2] = {0u, 0u}, up[2] = {0u, 0u}, uo[2] = {0u, 0u};  // uses so far
+        // The first scores of tile i of an item whose K0 is in entry st; q_empty follows the last scores of a tile.
+        auto start = [&](int i, int n) {
+          if (n == 0) return true;
+          if (!wait(&q_full[i], uq[i] & 1u)) return false;
+          s_qu[i] = ++uq[i];
+          issue_s(i, st);
+          if (n == 1) umma_commit(&q_empty[i]);
+          return true;
+        };
+        PrItem it;
+        ok = read_item(0, it, true);
+        int n[2] = {it.n0(), it.n1()}, nblk = it.blocks();
+        bool more = ok && it.len > 0;
+        if (more) {
+          ok = wait_entry() && start(0, n[0]) && start(1, n[1]);
+          if (ok) umma_commit(&kv_empty[0]);
+        }
+        for (int k = 0; ok && more; ++k) {
+          ok = read_item(k + 1, it, true);
+          if (!ok) break;
+          more = it.len > 0;
+          const int m[2] = {more ? it.n0() : 0, more ? it.n1() : 0};  // the next item's
+          for (int j = 0; j < nblk && ok; ++j) {
+            const bool last = j + 1 == nblk;
+            step();
+            const unsigned sv = st;
+            ok = wait_entry();
+            if (ok && (!last || more)) {  // the next block's keys, or the next item's first
+              step();
+              ok = wait_entry();
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (!ok) continue;
+              if (j < n[i]) {
+                if (j == 0) {  // the epilogue before has read O
+                  if (uo[i] > 0) ok = wait(&o_empty[i], (uo[i] - 1u) & 1u);
+                  ++uo[i];
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  if (ok) ok = wait(&p_full[i][half], up[i] & 1u);
+                  if (ok) issue_o(i, sv, half, j == 0);
+                }
+                ++up[i];
+                if (!ok) continue;
+                if (j + 1 == n[i]) {
+                  umma_commit(&o_full[i]);
+                } else {  // the next scores overwrite P: the tensor cores run this thread's products in order
+                  issue_s(i, st);
+                  if (j + 2 == n[i]) umma_commit(&q_empty[i]);
+                }
+              }
+              if (last) ok = start(i, m[i]);
+            }
+            if (ok) {
+              umma_commit(&kv_empty[sv]);
+              if (!last || more) umma_commit(&kv_empty[st]);
+            }
+          }
+          n[0] = m[0];
+          n[1] = m[1];
+          nblk = it.blocks();
+        }
       }
     }
   } else if (warp >= 4) {  // softmax of tile i
@@ -493,7 +546,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
     const int i = (warp - 4) >> 3, tt = t - 128 - kPrSoft * i;
     const int lane0 = 32 * (warp & 3) + 16 * (((warp - 4) >> 2) & 1);
     const uint32_t lanes = static_cast<uint32_t>(lane0) << 16;
-    const uint32_t ts = tmem + lanes + 128u * i, to = tmem + lanes + 256u + 128u * i;
+    const uint32_t ts = tmem + lanes + 128u * i, tp = tmem + lanes + kColP + kStepP * i;
+    const uint32_t to = tmem + lanes + kColO + kStepO * i;
     const int ra = lane0 + (lane >> 2), quad = lane & 3, col = 2 * quad;
     unsigned base = 0, us = 0, uo = 0;  // ring entry of the item's K0; blocks and items of this tile so far
     for (int k = 0; ok; ++k) {
@@ -549,6 +603,15 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         float s[64];
         pr_ld_s(ts, s);
+        if (kApart) {
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_empty[i]);
+          // the weights before have been read, and their products are in O
+          if (us > 0) ok = __all_sync(0xFFFFFFFFu, pr_wait(&p_empty[i], (us - 1u) & 1u));
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        }
         if (diag) {
           const int lim = row0 - j * kPrKeys - col;  // row ra sees this thread's columns 8 g + e up to here
 #pragma unroll
@@ -579,7 +642,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
             l[k2] *= alpha[k2];
             if (raise) nref[k2] = -mx[k2];
           }
-          if (j > 0) {  // S is full, so the products into O before it are complete
+          if (j > 0) {  // the products into O so far are complete: S (or the wait above) came after them
 #pragma unroll 1
             for (int h = 0; h < D / 32; ++h) {
               float o[16];
@@ -606,12 +669,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
             ls[c & 3] = pr_add2(ls[c & 3], pr_pair(a, bb));
             pk[c] = pr_pack(a, bb);
           }
-          pr_st_p(ts + 32u * h, pk);
+          pr_st_p(tp + 32u * h, pk);
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           if (diag && h == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the cleared values
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[i][h]);  // half of the weights are in place: their products may start
+          // half of the weights are in place: their products may start (apart, all of them start together)
+          if (lane == 0 && (!kApart || h == 1)) mbar_arrive(&p_full[i][h]);
         }
 #pragma unroll
         for (int k2 = 0; k2 < 2; ++k2) {
@@ -693,7 +757,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
   if (!ok && t == 0) {
     record_error(hdr, DT_ERR_TIMEOUT);
     // copies issued but never waited for must land before the CTA leaves: wait for them too (bounded)
-    for (unsigned e = s_used; e < s_issued; ++e) mbar_wait(&kv_full[e % kStages], (e / kStages) & 1u, kPrBudgetNs);
+    // (with two MMA threads, entries one of them has seen may be counted again: their phase is over or comes)
+    for (unsigned e = kApart ? min(s_used[0], s_used[1]) : s_used[0]; e < s_issued; ++e) mbar_wait(&kv_full[e % kStages], (e / kStages) & 1u, kPrBudgetNs);
     for (int i = 0; i < 2; ++i)
       for (unsigned e = s_qu[i]; e < s_qi[i]; ++e) mbar_wait(&q_full[i], e & 1u, kPrBudgetNs);
   }
