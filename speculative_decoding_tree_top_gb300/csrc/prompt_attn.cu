@@ -159,8 +159,8 @@ __device__ __forceinline__ int pr_find(const PrParams& p, int slot, int lane) { 
   }
 }
 
-// A wait in long sleeps: the hardware wakes the warp when the phase ends, and a warp that polls takes issue slots from
-// those that compute.
+// A phase that has ended is seen at once (45 cycles; the form with a time limit takes 100). Otherwise a wait in long
+// sleeps: the hardware wakes the warp when the phase ends, and a warp that polls takes issue slots from those that compute.
 __device__ __forceinline__ bool pr_try_wait(uint64_t* bar, unsigned parity) {
   uint32_t done;
   asm volatile(
@@ -171,7 +171,7 @@ __device__ __forceinline__ bool pr_try_wait(uint64_t* bar, unsigned parity) {
   return done != 0;
 }
 __device__ __forceinline__ bool pr_wait(uint64_t* bar, unsigned parity) {
-  if (pr_try_wait(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   while (!pr_try_wait(bar, parity))
     if (global_timer_ns() - t0 > kPrBudgetNs) return false;
@@ -569,8 +569,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
           // finite among the block's values is cleared too and added to the rows that see it at the end (its weight
           // there is positive, and any positive multiple of it gives the same sum).
           const unsigned e = base + 2u * j + 1u;
-          ok = __all_sync(0xFFFFFFFFu, pr_wait(&kv_full[e % kStages], (e / kStages) & 1u));
-          if (!ok) break;
+          ok = pr_wait(&kv_full[e % kStages], (e / kStages) & 1u) && ok;
           unsigned char* sv = skv + (e % kStages) * kTileBytes;
           const int valid = it.len - j * kPrKeys;  // keys of the block inside the prompt
           __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
@@ -598,8 +597,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
             atomicMax(&s_bad[i], k + 1);
           }
         }
-        ok = __all_sync(0xFFFFFFFFu, pr_wait(&s_full[i], us & 1u));
-        if (!ok) break;
+        ok = pr_wait(&s_full[i], us & 1u) && ok;
+        __syncwarp();
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         float s[64];
         pr_ld_s(ts, s);
@@ -607,11 +606,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_empty[i]);
-          // the weights before have been read, and their products are in O
-          if (us > 0) ok = __all_sync(0xFFFFFFFFu, pr_wait(&p_empty[i], (us - 1u) & 1u));
-          if (!ok) break;
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         }
+        // Apart, the weights before have been read and their products are in O only after this.
+        auto p_free = [&]() {
+          if (kApart && us > 0) ok = pr_wait(&p_empty[i], (us - 1u) & 1u) && ok;
+          __syncwarp();
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        };
         if (diag) {
           const int lim = row0 - j * kPrKeys - col;  // row ra sees this thread's columns 8 g + e up to here
 #pragma unroll
@@ -642,7 +643,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
             l[k2] *= alpha[k2];
             if (raise) nref[k2] = -mx[k2];
           }
-          if (j > 0) {  // the products into O so far are complete: S (or the wait above) came after them
+          if (j > 0) {
+            p_free();  // (not apart, S is full only after the products into O before it)
 #pragma unroll 1
             for (int h = 0; h < D / 32; ++h) {
               float o[16];
@@ -669,6 +671,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
             ls[c & 3] = pr_add2(ls[c & 3], pr_pair(a, bb));
             pk[c] = pr_pack(a, bb);
           }
+          if (kApart && h == 0) p_free();
           pr_st_p(tp + 32u * h, pk);
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           if (diag && h == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the cleared values
@@ -683,6 +686,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
           pr_unpair(pr_add2(ls[k2], ls[k2 + 2]), la, lb);
           l[k2] += la + lb;
         }
+        ok = __all_sync(0xFFFFFFFFu, ok);
       }
       if (!ok) break;
       base += 2u * it.blocks();
