@@ -7,7 +7,7 @@
 // GB300 design (flash decoding on the 5th-generation tensor cores): the n nodes of the G = Hq / Hkv query heads that
 // share a key/value head are one block of R = G n <= 128 query rows, so each cached row is read once per (request,
 // key/value head) and feeds R rows of dot products. Only the device knows the lengths: every CTA (one per SM) scans
-// them, and the 64-key blocks of all (request, key/value head) pairs, laid end to end, are split evenly over the CTAs.
+// them, and the 128-key blocks of all (request, key/value head) pairs, laid end to end, are split evenly over the CTAs.
 // A CTA's run inside one pair is a segment; a segment that covers its pair writes the output, the others leave
 // (O, m, l) in the CTA's two partial slots (only the first and the last segment of a share can be cut), and the CTA
 // that finishes a cut pair last joins its segments in slot order, so the result does not depend on who that is.
@@ -18,26 +18,24 @@
 #include <climits>
 #include <cmath>
 
-#include "dt_internal.cuh"
-#include "umma.cuh"
+#include "attn_common.cuh"
 
 namespace dt {
 namespace {
 
 constexpr int kPaRows = 128;      // query rows per pair: G n at most
 constexpr int kPaNodes = 64;      // n at most (a node's mask row is one 64-bit word)
-constexpr int kPaKeys = 64;       // keys per block
-constexpr int kPaThreads = 256;
-constexpr int kPaMaxStages = 10;
-constexpr float kPaLazy = 8.f;    // log2 headroom before the running maximum is raised
-constexpr uint64_t kPaBudgetNs = 4000000000ull;
-constexpr uint32_t kPaBox = kPaKeys * 128;  // 64 rows x 64 elements: 8 KB
+constexpr int kPaKeys = 128;      // keys per block
+constexpr int kPaThreads = 384;   // warps 0 and 1: values that must not reach the tensor cores; 2: load; 3: MMA; 4-11: softmax
+constexpr int kPaMaxStages = 12;
+constexpr int kPaCleans = 8;      // barriers of cleaned blocks: more than the ring can hold
+constexpr uint32_t kPaBox = kPaKeys * 128;  // 128 rows x 64 elements: 16 KB
 constexpr size_t kPaSmemCap = 232448 - 1024;  // opt-in shared memory of a CTA, less the static part
 
 struct PaParams {
   int B, n, Hq, Hkv, G, R, grid, stages;
   int page_size, num_pages, max_pages;
-  uint32_t q_box, p_bytes;         // one 64-element box of Q, one P buffer: rows rounded up to 64 or 128, x 128 bytes
+  uint32_t q_box;                  // one 64-element box of Q: rows rounded up to 8, x 128 bytes
   const unsigned short* v_cache;   // [num_pages][Hkv][page_size][D], re-read only for values that are not finite
   const int32_t* page_table;       // [B][max_pages]
   const int32_t* lens;             // [B]
@@ -50,34 +48,9 @@ struct PaParams {
 };
 struct PaMaps {
   CUtensorMap q;     // [B][n][Hq][D], box 64 x G x n x 1
-  CUtensorMap k, v;  // [num_pages][Hkv][page_size][D], box 64 x min(page_size, 64) x 1 x 1
+  CUtensorMap k, v;  // [num_pages][Hkv][page_size][D], box 64 x min(page_size, 128) x 1 x 1
 };
 
-__device__ __forceinline__ float pa_exp2(float x) {  // relative error about 2^-22, results below 2^-126 flushed
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pa_pack(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ void pa_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void pa_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
 __device__ __forceinline__ bool nonfinite_bf16x2(uint32_t w) {
   return (w & 0x7F800000u) == 0x7F800000u || (w & 0x7F80u) == 0x7F80u;
 }
@@ -86,10 +59,10 @@ __device__ __forceinline__ bool nonfinite_bf16x2(uint32_t w) {
 __device__ __forceinline__ bool pa_sync(uint64_t* bar, unsigned& count, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
-  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, count++ & 1u, kPaBudgetNs));
+  return __all_sync(0xFFFFFFFFu, at_wait(bar, count++ & 1u));
 }
 
-// The lengths' plan. cum[b] = 64-key blocks of one head of requests before b; a request whose length is not in
+// The lengths' plan. cum[b] = 128-key blocks of one head of requests before b; a request whose length is not in
 // [n, max_pages * page_size] has none (0 and below: an unused row of the batch; otherwise an error).
 __device__ __forceinline__ int pa_length(const PaParams& p, int b, bool* bad) {
   const int len = p.lens[b];
@@ -198,43 +171,52 @@ __device__ __forceinline__ void pa_join(const PaParams& p, const PaJoin& jn, int
     unsigned short* o =
         p.out + ((static_cast<size_t>(jn.b) * p.n + node) * p.Hq + jn.kvh * p.G + r % p.G) * D + kCols * lane;
     if constexpr (kCols == 4)
-      *reinterpret_cast<uint2*>(o) = make_uint2(pa_pack(num[0] * inv, num[1] * inv), pa_pack(num[2] * inv, num[3] * inv));
+      *reinterpret_cast<uint2*>(o) = make_uint2(at_pack(num[0] * inv, num[1] * inv), at_pack(num[2] * inv, num[3] * inv));
     else
-      *reinterpret_cast<uint32_t*>(o) = pa_pack(num[0] * inv, num[1] * inv);
+      *reinterpret_cast<uint32_t*>(o) = at_pack(num[0] * inv, num[1] * inv);
   }
 }
 
-// Roles: warp 2 loads (its lanes look the pages up and issue one page's boxes each), warp 3 issues the MMAs, warps
-// 4 to 7 run the softmax, thread r owning query row r = node G + head (TMEM lane r).
-// Per block: S = Q K^T (M = 128, N = 64) into one of two TMEM buffers; softmax in base 2 with the running maximum
-// raised only past a headroom of 2^8 (O is rescaled then), P rounded to bf16 into shared memory; O += P V with V as an
-// MN-major operand. Rows past R are padding and are left to whatever their rows of Q and P hold.
+// The keys of a pair from here on are not the same for all rows (the nodes' own), or not all there (the last block's
+// rows past the request's end): blocks that reach past it are masked, and their values cleaned.
+__device__ __forceinline__ int pa_common(const PaParams& p, int len) { return p.n > 1 || p.mask ? len - p.n : len; }
+
+// Roles: warp 2 loads (its lanes look the pages up and issue one page's boxes each), warp 3 issues the MMAs, the softmax
+// warps own 16 query rows each (row r = node G + head, tensor memory lane r; four neighbouring threads share two rows),
+// warps 0 and 1 clean values. Per block: S = Q K^T (M = 128, N = 128) into one of two buffers in tensor memory, so that
+// the next block's scores are computed during a block's softmax, also across segments; softmax in base 2 with the
+// running maximum raised only past a headroom of 2^8 (O is rescaled then); the weights over their scores as bf16;
+// O += P V with P from tensor memory and V as an MN-major operand, into one of two buffers by segment. Rows past R are
+// padding and are left to whatever their rows of Q hold. A block takes the tensor cores 1024 cycles at D = 128 and the
+// softmax about as long, where its 64 KB take 2800 at the memory's rate.
 template <int D>
-__global__ void __launch_bounds__(kPaThreads, 1) paged_attn_rows(PaParams p, const __grid_constant__ PaMaps maps,
-                                                                 WsHeader* hdr) {
+__global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, const __grid_constant__ PaMaps maps,
+                                                                   WsHeader* hdr) {
   constexpr int kHalves = D / 64;
-  constexpr uint32_t kStage = 2 * kHalves * kPaBox;  // K boxes, then V boxes
+  constexpr uint32_t kEntry = kHalves * kPaBox;  // a ring entry: a block's keys or values
+  constexpr uint32_t kColO = 256, kStepO = D;    // tensor memory: S at 0 and 128, O behind
   extern __shared__ float4 smem_f4[];
   unsigned char* sq =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_f4) + 1023) & ~uintptr_t(1023));
   const uint32_t q_bytes = kHalves * p.q_box;
-  unsigned char* sp = sq + 2 * q_bytes;
-  unsigned char* skv = sp + 2 * p.p_bytes;
-  int* cum = reinterpret_cast<int*>(skv + p.stages * kStage);  // [B + 1]
-  __shared__ uint64_t kv_full[kPaMaxStages], kv_empty[kPaMaxStages], s_full[2], p_full[2], o_done[2];
+  unsigned char* skv = sq + 2 * q_bytes;
+  int* cum = reinterpret_cast<int*>(skv + p.stages * kEntry);  // [B + 1]
+  __shared__ uint64_t kv_full[kPaMaxStages], kv_empty[kPaMaxStages], v_clean[kPaCleans], s_full[2], p_full[2], o_done[2];
   __shared__ uint64_t q_full[2], q_empty[2], o_free[2], s_meet;
   __shared__ uint32_t s_tmem;
-  __shared__ unsigned s_kv_issued, s_kv_used, s_q_issued, s_q_used;
+  __shared__ unsigned s_kv_issued, s_kv_used, s_q_issued, s_q_used;  // copies issued and waited for (failure drain)
   __shared__ int s_warp[kPaThreads / 32];
   __shared__ int s_bad, s_joins;
   __shared__ PaJoin s_join[2];
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int live_warps = (p.R + 31) / 32;
+  const int live_warps = (p.R + 15) / 16;
+  const unsigned stages = static_cast<unsigned>(p.stages);
   if (t == 0) {
-    for (int i = 0; i < p.stages; ++i) {
+    for (unsigned i = 0; i < stages; ++i) {
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_empty[i], 1);
     }
+    for (int i = 0; i < kPaCleans; ++i) mbar_init(&v_clean[i], 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], live_warps);
@@ -248,11 +230,13 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_rows(PaParams p, con
     s_kv_issued = s_kv_used = s_q_issued = s_q_used = 0u;
     s_bad = s_joins = 0;
   }
-  if (warp == 0) {
+  if (warp == 3) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
                  "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  if (warp == 2 && lane < 3)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v) : "memory");
   // the plan: block counts scanned over the requests; rows of requests without blocks are zero
   int carry = 0;
   for (int b0 = 0; b0 < p.B; b0 += kPaThreads) {
@@ -280,14 +264,20 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_rows(PaParams p, con
   const int ctas = W < p.grid ? static_cast<int>(W) : p.grid;  // that take a share: a block each at least
   PaWalk w = pa_walk(p, cum, W, ctas);
 
-  if (warp == 2) {  // TMA producer: the whole warp, one page's boxes a lane
-    unsigned st = 0, use = 0, g = 0;
+  if (warp == 2) {  // TMA: the whole warp, one page's boxes a lane
+    unsigned st = 0, par = 1u, e = 0;  // ring entry, the parity of its last release, entries so far
     const int box_rows = p.page_size < kPaKeys ? p.page_size : kPaKeys;
     const int per_block = kPaKeys / box_rows;  // pages a block spans (1 when a page holds whole blocks)
     for (int si = 0; w.x < w.x1 && ok; ++si) {
       const PaSeg sg = pa_next(p, cum, w);
       const unsigned qb = static_cast<unsigned>(si) & 1u;
-      if (si >= 2) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&q_empty[qb], static_cast<unsigned>((si >> 1) - 1) & 1u, kPaBudgetNs));
+      const int used = (p.lens[sg.b] + p.page_size - 1) / p.page_size;  // pages the request holds
+      const int32_t* table = p.page_table + static_cast<size_t>(sg.b) * p.max_pages;
+      // page ids, 32 at a time and one window ahead
+      int win = static_cast<int>(static_cast<long long>(sg.j0) * kPaKeys / p.page_size) / 32;
+      int cur = 32 * win + lane < used ? table[32 * win + lane] : 0;
+      int nxt = 32 * (win + 1) + lane < used ? table[32 * (win + 1) + lane] : 0;
+      if (si >= 2) ok = __all_sync(0xFFFFFFFFu, at_wait(&q_empty[qb], static_cast<unsigned>((si >> 1) - 1) & 1u));
       if (!ok) break;
       if (lane == 0) {
         unsigned char* qd = sq + qb * q_bytes;
@@ -296,15 +286,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_rows(PaParams p, con
           tma_load_4d(qd + h * p.q_box, &maps.q, 64 * h, sg.kvh * p.G, 0, sg.b, &q_full[qb]);
         s_q_issued = static_cast<unsigned>(si) + 1u;
       }
-      const int used = (p.lens[sg.b] + p.page_size - 1) / p.page_size;  // pages the request holds
-      const int32_t* table = p.page_table + static_cast<size_t>(sg.b) * p.max_pages;
-      // page ids, 32 at a time and one window ahead
-      int win = static_cast<int>(static_cast<long long>(sg.j0) * kPaKeys / p.page_size) / 32;
-      int cur = 32 * win + lane < used ? table[32 * win + lane] : 0;
-      int nxt = 32 * (win + 1) + lane < used ? table[32 * (win + 1) + lane] : 0;
-      for (int j = 0; j < sg.nblk; ++j, ++g) {
-        if (use > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&kv_empty[st], (use - 1) & 1u, kPaBudgetNs));
-        if (!ok) break;
+      for (int j = 0; j < sg.nblk && ok; ++j) {
         const int key = (sg.j0 + j) * kPaKeys, first = key / p.page_size, row = key % p.page_size;
         if (first / 32 != win) {
           ++win;
@@ -312,267 +294,295 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_rows(PaParams p, con
           nxt = 32 * (win + 1) + lane < used ? table[32 * (win + 1) + lane] : 0;
         }
         const int pages = used - first < per_block ? used - first : per_block;
-        if (lane == 0) mbar_expect_tx(&kv_full[st], static_cast<uint32_t>(pages * box_rows * 128 * 2 * kHalves));
         int page = __shfl_sync(0xFFFFFFFFu, cur, (first + lane) & 31);
-        if (lane < pages) {
-          if (page < 0 || page >= p.num_pages) {
-            record_error(hdr, DT_ERR_INVALID_ARG);
-            page = 0;
-          }
-          unsigned char* d = skv + st * kStage + lane * box_rows * 128;
-          for (int h = 0; h < kHalves; ++h) {
-            tma_load_4d(d + h * kPaBox, &maps.k, 64 * h, row, sg.kvh, page, &kv_full[st]);
-            tma_load_4d(d + (kHalves + h) * kPaBox, &maps.v, 64 * h, row, sg.kvh, page, &kv_full[st]);
-          }
+        if (lane < pages && (page < 0 || page >= p.num_pages)) {
+          record_error(hdr, DT_ERR_INVALID_ARG);
+          page = 0;
         }
-        if (lane == 0) s_kv_issued = g + 1u;
-        if (++st == static_cast<unsigned>(p.stages)) {
-          st = 0;
-          ++use;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {  // the keys, then the values
+          if (ok && e >= stages) ok = __all_sync(0xFFFFFFFFu, at_wait(&kv_empty[st], par));
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(&kv_full[st], static_cast<uint32_t>(pages * box_rows * 128 * kHalves));
+          __syncwarp();
+          if (lane < pages) {
+            unsigned char* d = skv + st * kEntry + lane * box_rows * 128;
+            for (int h = 0; h < kHalves; ++h)
+              tma_load_4d(d + h * kPaBox, kv ? &maps.v : &maps.k, 64 * h, row, sg.kvh, page, &kv_full[st]);
+          }
+          ++e;
+          if (lane == 0) s_kv_issued = e;
+          if (++st == stages) {
+            st = 0;
+            par ^= 1u;
+          }
         }
       }
     }
-  } else if (warp == 3 && lane == 0) {  // MMA issuer
-    const uint32_t id_s = umma_idesc(kPaKeys, 128), id_o = umma_idesc(D, 128) | (1u << 16);  // O: V MN-major
-    unsigned g = 0, st = 0;           // the block whose P V comes next, and its stage
-    unsigned st_s = 0, par_s = 0;     // the same of the block whose S comes next
-    unsigned gs = 0;
-    for (int si = 0; w.x < w.x1 && ok; ++si) {
-      const PaSeg sg = pa_next(p, cum, w);
-      const unsigned qb = static_cast<unsigned>(si) & 1u;
-      const uint32_t aq = smem_u32(sq + qb * q_bytes), to = tmem + 128u + 128u * qb;
-      ok = mbar_wait(&q_full[qb], static_cast<unsigned>(si >> 1) & 1u, kPaBudgetNs);
-      if (ok) s_q_used = static_cast<unsigned>(si) + 1u;
-      if (ok && si >= 2) ok = mbar_wait(&o_free[qb], static_cast<unsigned>((si >> 1) - 1) & 1u, kPaBudgetNs);
-      if (!ok) break;
-      auto issue_s = [&]() {
-        if (!mbar_wait(&kv_full[st_s], par_s, kPaBudgetNs)) return false;
-        s_kv_used = gs + 1u;
+  } else if (warp == 3) {
+    if (elect_one()) {  // MMA
+      const uint32_t id_s = umma_idesc(kPaKeys, 128), id_o = umma_idesc(D, 128) | (1u << 16);  // O: V MN-major
+      const uint64_t dk = umma_desc_sw128(smem_u32(skv)), dv = umma_desc_sw128_mn(smem_u32(skv), kPaBox, 1024u);
+      auto wait = [&](uint64_t* bar, unsigned parity) {
+        const bool done = at_wait(bar, parity);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t bk = smem_u32(skv + st_s * kStage);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_f16(tmem + (gs & 1u) * kPaKeys, umma_desc_sw128(aq + (kk >> 2) * p.q_box + (kk & 3) * 32u),
-                   umma_desc_sw128(bk + (kk >> 2) * kPaBox + (kk & 3) * 32u), id_s, kk > 0 ? 1u : 0u);
-        umma_commit(&s_full[gs & 1u]);
-        ++gs;
-        if (++st_s == static_cast<unsigned>(p.stages)) {
-          st_s = 0;
-          par_s ^= 1u;
-        }
-        return true;
+        return done;
       };
-      ok = issue_s();
-      if (ok && sg.nblk == 1) umma_commit(&q_empty[qb]);
-      for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
-        if (j + 1 < sg.nblk) {  // its S buffer was freed by block g - 1's softmax (waited for below, one block ago)
-          ok = issue_s();
-          if (ok && j + 2 == sg.nblk) umma_commit(&q_empty[qb]);
-        }
-        if (ok) ok = mbar_wait(&p_full[g & 1u], (g >> 1) & 1u, kPaBudgetNs);
-        if (!ok) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t ap = smem_u32(sp + (g & 1u) * p.p_bytes), bv = smem_u32(skv + st * kStage + kHalves * kPaBox);
-#pragma unroll
-        for (int kk = 0; kk < kPaKeys / 16; ++kk)
-          umma_f16(to, umma_desc_sw128(ap + 32u * kk), umma_desc_sw128_mn(bv + 2048u * kk, kPaBox, 1024u), id_o,
-                   (j > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(&kv_empty[st]);
-        umma_commit(&o_done[g & 1u]);
-        if (++st == static_cast<unsigned>(p.stages)) st = 0;
-      }
-    }
-  } else if (warp >= 4 && warp - 4 < live_warps) {  // softmax
-    const int r = t - 128;
-    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp - 4)) << 16);
-    const bool live = r < p.R;
-    const int node = live ? r / p.G : 0, gi = live ? r % p.G : 0;
-    const int workers = 32 * live_warps;
-    unsigned g = 0, st = 0, par = 0, meet = 0;
-    for (int si = 0; w.x < w.x1 && ok; ++si) {
-      const PaSeg sg = pa_next(p, cum, w);
-      const unsigned qb = static_cast<unsigned>(si) & 1u;
-      const uint32_t to = tl + 128u + 128u * qb;
-      const int len = p.lens[sg.b], pre = len - p.n;  // keys below pre are visible to every node
-      const int last_key = (sg.j0 + sg.nblk) * kPaKeys;
-      unsigned long long mbits = 0;  // bit c: the key of node c is visible to this row's node
-      if (live && (last_key > pre || p.n == 1)) {
-        if (!p.mask) {
-          mbits = node == 63 ? ~0ull : (2ull << node) - 1ull;
-        } else {
-          const uint8_t* mr = p.mask + (static_cast<size_t>(sg.b) * p.n + node) * p.n;
-          for (int c = 0; c < p.n; ++c) mbits |= static_cast<unsigned long long>(mr[c] != 0) << c;
-        }
-      }
-      float m = -INFINITY, l = 0.f;
-      bool bad_v = false;  // a value of the segment's nodes is not finite
-      for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_full[g & 1u], (g >> 1) & 1u, kPaBudgetNs));
-        if (!ok) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const int kbase = (sg.j0 + j) * kPaKeys;
-        // A weight of zero does not hide a value that is not finite from the tensor cores (0 x inf is NaN). So rows
-        // past the request's end (stale, or left in the ring by another block) are cleared, and what is not finite
-        // among the nodes' values is cleared here and added to the rows that see it at the end: its weight there is
-        // positive, and any positive multiple of it gives the same sum.
-        const bool tail = kbase + kPaKeys > len, nodes = p.n > 1 && kbase + kPaKeys > pre;
-        if (tail || nodes) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&kv_full[st], par, kPaBudgetNs));  // done: S is complete
-          if (!ok) break;
-          unsigned char* sv = skv + st * kStage + kHalves * kPaBox;
-          bool found = false;
-          for (int i = t - 128; i < kPaKeys * kHalves; i += workers) {
-            const int c = i % kPaKeys, key = kbase + c;
-            uint4* row = reinterpret_cast<uint4*>(sv + (i / kPaKeys) * kPaBox + c * 128);
-            if (key >= len) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) row[e] = make_uint4(0u, 0u, 0u, 0u);
-            } else if (nodes && key >= pre) {
-              for (int e = 0; e < 8; ++e) {
-                uint4 x = row[e];
-                uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
-                bool hit = false;
-#pragma unroll
-                for (int k2 = 0; k2 < 4; ++k2)
-                  if (nonfinite_bf16x2(xw[k2])) {
-                    if ((xw[k2] & 0x7F80u) == 0x7F80u) xw[k2] &= 0xFFFF0000u;
-                    if ((xw[k2] & 0x7F800000u) == 0x7F800000u) xw[k2] &= 0xFFFFu;
-                    hit = true;
-                  }
-                if (hit) {
-                  row[e] = x;
-                  found = true;
-                }
-              }
-            }
-          }
-          if (nodes) {
-            if (found) s_bad = si + 1;
-            ok = pa_sync(&s_meet, meet, lane);
-            if (!ok) break;
-            bad_v = bad_v || *reinterpret_cast<volatile int*>(&s_bad) > si;  // a later segment's counts too: only slower
-          }
-        }
-        uint32_t sv[4][16];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) pa_ld16(tl + (g & 1u) * kPaKeys + 16u * h, sv[h]);
-        const int rel = pre - kbase, lim = len - kbase;
-        unsigned long long visb = 0;
-        if (live) {
-          const unsigned long long pbits = rel >= 64 ? ~0ull : rel <= 0 ? 0ull : (1ull << rel) - 1ull;
-          unsigned long long tbits = 0;
-          if (rel < 64) tbits = rel >= 0 ? mbits << rel : rel > -64 ? mbits >> (-rel) : 0ull;
-          const unsigned long long lbits = lim >= 64 ? ~0ull : lim <= 0 ? 0ull : (1ull << lim) - 1ull;
-          visb = (pbits | tbits) & lbits;
-        }
-        float s[64];
-        float bmax = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 64; ++c) {
-          s[c] = (visb >> c) & 1ull ? __uint_as_float(sv[c >> 4][c & 15]) * p.scale_log2 : -INFINITY;
-          bmax = fmaxf(bmax, s[c]);
-        }
-        const bool raise = bmax > m + kPaLazy || (m == -INFINITY && bmax > -INFINITY);
-        const bool rescale_o = raise && m > -INFINITY;
-        const float mn = raise ? bmax : m;
-        const float alpha = rescale_o ? pa_exp2(m - mn) : 1.f;
-        m = mn;
-        const float mref = m == -INFINITY ? 0.f : m;  // nothing visible yet: every weight is 2^-inf = 0
-        float ls = 0.f;
-        uint32_t pk[32];
-#pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          const float a = pa_exp2(s[c] - mref), bb = pa_exp2(s[c + 1] - mref);
-          ls += a + bb;
-          pk[c >> 1] = pa_pack(a, bb);
-        }
-        l = l * alpha + ls;
-        // P's buffer was last read by the O MMA of block g - 2; a rescale needs block g - 1's O MMA complete (of this
-        // segment: m was finite). Commits complete in order.
-        const bool any_rescale = __any_sync(0xFFFFFFFFu, rescale_o);
-        if (g >= 2 || any_rescale) {
-          const unsigned gw = any_rescale ? g - 1 : g - 2;
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&o_done[gw & 1u], (gw >> 1) & 1u, kPaBudgetNs));
-          if (!ok) break;
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        }
-        if (any_rescale) {
-#pragma unroll
-          for (int h = 0; h < D / 16; ++h) {
-            uint32_t ov[16];
-            pa_ld16(to + 16u * h, ov);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-            pa_st16(to + 16u * h, ov);
-          }
-          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        }
-        unsigned char* prow = sp + (g & 1u) * p.p_bytes + r * 128;
-#pragma unroll
-        for (int cc = 0; cc < 8; ++cc)
-          *reinterpret_cast<uint4*>(prow + ((cc ^ (r & 7)) << 4)) =
-              make_uint4(pk[4 * cc], pk[4 * cc + 1], pk[4 * cc + 2], pk[4 * cc + 3]);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads P and V through the async proxy
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[g & 1u]);
-        if (++st == static_cast<unsigned>(p.stages)) {
+      unsigned st = 0, par = 0, seen = 0;  // the ring entry that comes next, in order: K, V, K, V, ...
+      auto take = [&](unsigned& at) {
+        at = st;
+        if (!wait(&kv_full[st], par)) return false;
+        s_kv_used = ++seen;
+        if (++st == stages) {
           st = 0;
           par ^= 1u;
         }
+        return true;
+      };
+      // The scores run one block ahead of the outputs, through the same segments.
+      PaWalk ws = w;
+      PaSeg ss{};
+      int js = 0, sis = -1;
+      unsigned gs = 0;
+      auto scores = [&]() {  // of the next block, if there is one
+        if (js == ss.nblk) {
+          if (ws.x >= ws.x1) return true;
+          ss = pa_next(p, cum, ws);
+          js = 0;
+          ++sis;
+          if (!wait(&q_full[sis & 1], static_cast<unsigned>(sis >> 1) & 1u)) return false;
+          s_q_used = static_cast<unsigned>(sis) + 1u;
+        }
+        unsigned at;
+        if (!take(at)) return false;
+        const uint64_t q0 = umma_desc_sw128(smem_u32(sq + (sis & 1) * q_bytes)), k0 = dk + at * (kEntry >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_f16(tmem + (gs & 1u) * kPaKeys, q0 + (((kk >> 2) * p.q_box + (kk & 3) * 32u) >> 4),
+                   k0 + (((kk >> 2) * kPaBox + (kk & 3) * 32u) >> 4), id_s, kk > 0 ? 1u : 0u);
+        umma_commit(&s_full[gs & 1u]);
+        umma_commit(&kv_empty[at]);
+        if (++js == ss.nblk) umma_commit(&q_empty[sis & 1]);
+        ++gs;
+        return true;
+      };
+      unsigned g = 0, cleans = 0;
+      ok = scores();
+      for (int si = 0; w.x < w.x1 && ok; ++si) {
+        const PaSeg sg = pa_next(p, cum, w);
+        const unsigned qb = static_cast<unsigned>(si) & 1u;
+        const uint32_t to = tmem + kColO + kStepO * qb;
+        const int common = pa_common(p, p.lens[sg.b]);
+        for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
+          unsigned sv;
+          ok = take(sv);
+          // its buffer was freed by block g - 1's softmax (waited for below, one block ago)
+          if (ok) ok = scores();
+          if (ok && j == 0 && si >= 2) ok = wait(&o_free[qb], static_cast<unsigned>((si >> 1) - 1) & 1u);
+          if (ok && (sg.j0 + j + 1) * kPaKeys > common) {
+            ok = wait(&v_clean[cleans % kPaCleans], (cleans / kPaCleans) & 1u);
+            ++cleans;
+          }
+          if (ok) ok = wait(&p_full[g & 1u], (g >> 1) & 1u);
+          if (!ok) break;
+          const uint64_t v0 = dv + sv * (kEntry >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kPaKeys / 16; ++kk)
+            umma_f16_ts(to, tmem + (g & 1u) * kPaKeys + 8u * kk, v0 + 128u * kk, id_o, (j > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&kv_empty[sv]);
+          umma_commit(&o_done[g & 1u]);
+        }
       }
-      if (!ok) break;
-      const unsigned gl = g - 1;
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&o_done[gl & 1u], (gl >> 1) & 1u, kPaBudgetNs));
-      if (!ok) break;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const bool whole = sg.nblk == sg.nb;
-      const bool empty = pre == 0 && mbits == 0;  // (only read where l == 0)
-      const size_t unit = 2 * static_cast<size_t>(blockIdx.x) + (sg.first ? 0 : 1);
-      unsigned short* po = p.out + ((static_cast<size_t>(sg.b) * p.n + node) * p.Hq + sg.kvh * p.G + gi) * D;
-      float* pp = p.part + (unit * p.R + r) * D;
-      const float inv = l == 0.f && empty ? 0.f : 1.f / l;
+    }
+  } else if (warp < 2) {
+    // A weight of zero does not hide a value that is not finite from the tensor cores (0 x inf is NaN). So rows past the
+    // request's end (stale, or left in the ring by another block) are cleared, and what is not finite among the nodes'
+    // values is cleared here and added to the rows that see it at the end: its weight there is positive, and any
+    // positive multiple of it gives the same sum.
+    unsigned g = 0, cleans = 0;
+    for (int si = 0; w.x < w.x1 && ok; ++si) {
+      const PaSeg sg = pa_next(p, cum, w);
+      const int len = p.lens[sg.b], common = pa_common(p, len);
+      for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
+        const int kbase = (sg.j0 + j) * kPaKeys;
+        if (kbase + kPaKeys <= common) continue;
+        const unsigned e = 2u * g + 1u, at = e % stages;
+        ok = __all_sync(0xFFFFFFFFu, at_issued(&s_kv_issued, e) && at_wait(&kv_full[at], (e / stages) & 1u));
+        if (!ok) break;
+        unsigned char* sv = skv + at * kEntry;
+        bool found = false;
+        for (int c = t; c < kHalves * kPaKeys * 8; c += 64) {  // 16-byte pieces; eight a row
+          const int key = kbase + ((c >> 3) & (kPaKeys - 1));
+          uint4* piece = reinterpret_cast<uint4*>(sv + 16 * c);
+          if (key >= len) {
+            *piece = make_uint4(0u, 0u, 0u, 0u);
+          } else if (key >= common) {
+            uint4 x = *piece;
+            uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
+            bool hit = false;
 #pragma unroll
-      for (int h = 0; h < D / 16; ++h) {
-        uint32_t ov[16];
-        pa_ld16(to + 16u * h, ov);
-        if (!live) continue;
-        if (bad_v) {  // rare: the nodes' values that are not finite, from global memory
-          for (int c = 0; c < p.n; ++c) {
-            const int key = pre + c;
-            if (!((mbits >> c) & 1ull) || key < sg.j0 * kPaKeys || key >= last_key) continue;
-            const int page = p.page_table[static_cast<size_t>(sg.b) * p.max_pages + key / p.page_size];
-            if (page < 0 || page >= p.num_pages) continue;
-            const unsigned short* vr =
-                p.v_cache + ((static_cast<size_t>(page) * p.Hkv + sg.kvh) * p.page_size + key % p.page_size) * D + 16 * h;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const uint32_t bits = static_cast<uint32_t>(vr[e]) << 16;
-              if ((bits & 0x7F800000u) == 0x7F800000u)
-                ov[e] = __float_as_uint(__uint_as_float(ov[e]) + __uint_as_float(bits));
+            for (int k2 = 0; k2 < 4; ++k2)
+              if (nonfinite_bf16x2(xw[k2])) {
+                if ((xw[k2] & 0x7F80u) == 0x7F80u) xw[k2] &= 0xFFFF0000u;
+                if ((xw[k2] & 0x7F800000u) == 0x7F800000u) xw[k2] &= 0xFFFFu;
+                hit = true;
+              }
+            if (hit) {
+              *piece = x;
+              found = true;
             }
           }
         }
-        if (whole) {
-          uint32_t w8[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            w8[e] = pa_pack(__uint_as_float(ov[2 * e]) * inv, __uint_as_float(ov[2 * e + 1]) * inv);
-          *reinterpret_cast<uint4*>(po + 16 * h) = make_uint4(w8[0], w8[1], w8[2], w8[3]);
-          *reinterpret_cast<uint4*>(po + 16 * h + 8) = make_uint4(w8[4], w8[5], w8[6], w8[7]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<float4*>(pp + 16 * h + e) =
-                make_float4(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), __uint_as_float(ov[e + 2]),
-                            __uint_as_float(ov[e + 3]));
-        }
+        if (found) atomicMax(&s_bad, si + 1);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads V through the async proxy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_clean[cleans % kPaCleans]);
+        ++cleans;
       }
-      if (live && !whole) *reinterpret_cast<float2*>(p.ml + (unit * p.R + r) * 2) = make_float2(m, l);
+    }
+  } else if (32 * (warp & 3) + 16 * ((warp - 4) >> 2) < p.R) {  // softmax
+    const int lane0 = 32 * (warp & 3) + 16 * ((warp - 4) >> 2);
+    const uint32_t lanes = static_cast<uint32_t>(lane0) << 16;
+    const int ra = lane0 + (lane >> 2), quad = lane & 3, col = 2 * quad;
+    int node[2], head[2];
+    bool live[2];
+#pragma unroll
+    for (int k2 = 0; k2 < 2; ++k2) {
+      live[k2] = ra + 8 * k2 < p.R;
+      node[k2] = live[k2] ? (ra + 8 * k2) / p.G : 0;
+      head[k2] = live[k2] ? (ra + 8 * k2) % p.G : 0;
+    }
+    unsigned g = 0, meet = 0;
+    for (int si = 0; w.x < w.x1 && ok; ++si) {
+      const PaSeg sg = pa_next(p, cum, w);
+      const unsigned qb = static_cast<unsigned>(si) & 1u;
+      const uint32_t to = tmem + lanes + kColO + kStepO * qb;
+      const int len = p.lens[sg.b], pre = len - p.n, common = pa_common(p, len);
+      const int last_key = (sg.j0 + sg.nblk) * kPaKeys;
+      unsigned long long mbits[2] = {0ull, 0ull};  // bit c: the key of node c is visible to the row's node
+      if (last_key > common)
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2) {
+          if (!p.mask) {
+            mbits[k2] = node[k2] == 63 ? ~0ull : (2ull << node[k2]) - 1ull;
+          } else {
+            const uint8_t* mr = p.mask + (static_cast<size_t>(sg.b) * p.n + node[k2]) * p.n;
+            for (int c = 0; c < p.n; ++c) mbits[k2] |= static_cast<unsigned long long>(mr[c] != 0) << c;
+          }
+        }
+      float nref[2] = {kAtNone, kAtNone}, l[2] = {0.f, 0.f};
+      for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
+        const uint32_t ts = tmem + lanes + (g & 1u) * kPaKeys;
+        ok = at_wait(&s_full[g & 1u], (g >> 1) & 1u) && ok;
+        __syncwarp();
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        float s[64];
+        at_ld_s(ts, s);
+        const int kbase = (sg.j0 + j) * kPaKeys;
+        if (kbase + kPaKeys > common) {
+          const int end = len - kbase - col, own = pre - kbase - col;  // of this thread's columns 8 g + e
+#pragma unroll
+          for (int g8 = 0; g8 < 16; ++g8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int c = 8 * g8 + (e & 1);
+              const bool seen = c < own || (c < end && ((mbits[e >> 1] >> ((c - own) & 63)) & 1ull));
+              if (!seen) s[4 * g8 + e] = -INFINITY;
+            }
+        }
+        float mx[2];
+        at_max(s, p.scale_log2, mx);
+        if (__any_sync(0xFFFFFFFFu, mx[0] + nref[0] > kAtLazy || mx[1] + nref[1] > kAtLazy)) {  // rare: rescale O
+          float alpha[2];
+          at_raise(mx, nref, l, alpha);
+          if (j > 0) {
+            ok = at_wait(&o_done[(g - 1u) & 1u], ((g - 1u) >> 1) & 1u) && ok;
+            __syncwarp();
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll 1
+            for (int h = 0; h < D / 32; ++h) {
+              float o[16];
+              at_ld_o(to + 32u * h, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= alpha[(e >> 1) & 1];
+              at_st_o(to + 32u * h, o);
+            }
+          }
+        }
+        uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+        uint32_t pk[16];
+        at_weights<0>(s, p.scale_log2, nref, ls, pk);
+        at_st_p(ts, pk);
+        at_weights<1>(s, p.scale_log2, nref, ls, pk);
+        at_st_p(ts + 32u, pk);
+        at_sums(ls, l);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[g & 1u]);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+      }
+      if (!ok) break;
+      ok = __all_sync(0xFFFFFFFFu, at_wait(&o_done[(g - 1u) & 1u], ((g - 1u) >> 1) & 1u));
+      if (!ok) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      float o[D / 2];
+      if constexpr (D == 128)
+        at_ld_s(to, o);
+      else
+        at_ld_half(to, o);
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_free[qb]);
-      if (whole) continue;
+      const bool whole = sg.nblk == sg.nb;
+      const bool bad = *reinterpret_cast<volatile int*>(&s_bad) > si;  // (a later segment's mark counts too: only slower)
+      if (bad) {  // rare: the nodes' values that are not finite, from global memory
+        for (int c = 0; c < p.n; ++c) {
+          const int key = pre + c;
+          if (key < sg.j0 * kPaKeys || key >= last_key) continue;
+          const int page = p.page_table[static_cast<size_t>(sg.b) * p.max_pages + key / p.page_size];
+          if (page < 0 || page >= p.num_pages) continue;
+          const unsigned short* vr =
+              p.v_cache + ((static_cast<size_t>(page) * p.Hkv + sg.kvh) * p.page_size + key % p.page_size) * D + col;
+#pragma unroll
+          for (int e = 0; e < D / 2; ++e) {
+            const uint32_t bits = static_cast<uint32_t>(vr[8 * (e >> 2) + (e & 1)]) << 16;
+            if ((bits & 0x7F800000u) == 0x7F800000u && ((mbits[(e >> 1) & 1] >> c) & 1ull)) o[e] += __uint_as_float(bits);
+          }
+        }
+      }
+#pragma unroll
+      for (int k2 = 0; k2 < 2; ++k2) {
+        l[k2] += __shfl_xor_sync(0xFFFFFFFFu, l[k2], 1);
+        l[k2] += __shfl_xor_sync(0xFFFFFFFFu, l[k2], 2);
+      }
+      if (whole) {
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2) {
+          // no visible key at all: zero; visible keys of weight 0 alone: NaN
+          const float inv = l[k2] == 0.f && common == 0 && mbits[k2] == 0ull ? 0.f : 1.f / l[k2];
+          unsigned short* po =
+              p.out + ((static_cast<size_t>(sg.b) * p.n + node[k2]) * p.Hq + sg.kvh * p.G + head[k2]) * D + 8 * quad;
+#pragma unroll
+          for (int h = 0; h < D / 32; ++h) {
+            const uint4 x = at_row16(o + 16 * h, k2, inv, quad);
+            if (live[k2]) *reinterpret_cast<uint4*>(po + 32 * h) = x;
+          }
+        }
+        continue;
+      }
+      const size_t unit = 2 * static_cast<size_t>(blockIdx.x) + (sg.first ? 0 : 1);
+#pragma unroll
+      for (int k2 = 0; k2 < 2; ++k2) {
+        if (!live[k2]) continue;
+        const size_t row = unit * p.R + ra + 8 * k2;
+#pragma unroll
+        for (int g8 = 0; g8 < D / 8; ++g8)
+          *reinterpret_cast<float2*>(p.part + row * D + 8 * g8 + col) =
+              make_float2(o[4 * g8 + 2 * k2], o[4 * g8 + 2 * k2 + 1]);
+        if (quad == 0)
+          *reinterpret_cast<float2*>(p.ml + 2 * row) = make_float2(nref[k2] == kAtNone ? -INFINITY : -nref[k2], l[k2]);
+      }
       // the pair's last segment to finish joins them all, once the CTA is through its share
       const int c0 = pa_owner(sg.pair0, W, ctas), c1 = pa_owner(sg.pair0 + sg.nb - 1, W, ctas);
       __threadfence();
@@ -591,9 +601,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_rows(PaParams p, con
   if (!ok && t == 0) {
     record_error(hdr, DT_ERR_TIMEOUT);
     // copies issued but never waited for must land before the CTA leaves: wait for them too (bounded)
-    const unsigned ns = static_cast<unsigned>(p.stages);
-    for (unsigned g = s_kv_used; g < s_kv_issued; ++g) mbar_wait(&kv_full[g % ns], (g / ns) & 1u, kPaBudgetNs);
-    for (unsigned q = s_q_used; q < s_q_issued; ++q) mbar_wait(&q_full[q & 1u], (q >> 1) & 1u, kPaBudgetNs);
+    for (unsigned e = s_kv_used; e < s_kv_issued; ++e) mbar_wait(&kv_full[e % stages], (e / stages) & 1u, kAtBudgetNs);
+    for (unsigned q = s_q_used; q < s_q_issued; ++q) mbar_wait(&q_full[q & 1u], (q >> 1) & 1u, kAtBudgetNs);
   }
   if (ok) {
     __threadfence();  // the ticket's thread acquired the others' partials; the barrier above passed them on
@@ -601,7 +610,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_rows(PaParams p, con
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  if (warp == 3) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
 struct PaPlan {
@@ -620,16 +629,15 @@ inline PaPlan pa_plan(int R, int d, int sms) {
 
 template <int D>
 dt_status pa_launch(PaParams& p, const PaMaps& maps, WsHeader* hdr, cudaStream_t stream) {
-  const uint32_t rows = p.R <= 64 ? 64 : 128, halves = D / 64, stage = 2 * halves * kPaBox;
-  p.q_box = rows * 128;
-  p.p_bytes = rows * 128;
-  const size_t fixed = 1024 + 2 * halves * p.q_box + 2 * p.p_bytes + align_up(sizeof(int) * (p.B + 1), 16);
-  int stages = static_cast<int>((kPaSmemCap - fixed) / stage);
-  p.stages = stages > kPaMaxStages ? kPaMaxStages : stages;
-  const size_t smem = fixed + static_cast<size_t>(p.stages) * stage;
-  const void* fn = reinterpret_cast<const void*>(paged_attn_rows<D>);
+  const uint32_t halves = D / 64, entry = halves * kPaBox;
+  p.q_box = static_cast<uint32_t>((p.R + 7) / 8 * 8) * 128;
+  const size_t fixed = 1024 + 2 * halves * p.q_box + align_up(sizeof(int) * (p.B + 1), 16);
+  const int fit = static_cast<int>((kPaSmemCap - fixed) / entry);
+  p.stages = fit > kPaMaxStages ? kPaMaxStages : fit;
+  const size_t smem = fixed + static_cast<size_t>(p.stages) * entry;
+  const void* fn = reinterpret_cast<const void*>(paged_attn_kernel<D>);
   if (ensure_dynamic_smem(fn, kPaSmemCap) != cudaSuccess) return DT_ERR_CUDA;
-  paged_attn_rows<D><<<static_cast<unsigned>(p.grid), kPaThreads, smem, stream>>>(p, maps, hdr);
+  paged_attn_kernel<D><<<static_cast<unsigned>(p.grid), kPaThreads, smem, stream>>>(p, maps, hdr);
   return cuda_status(cudaGetLastError());
 }
 

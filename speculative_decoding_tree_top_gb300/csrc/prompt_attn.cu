@@ -20,8 +20,7 @@
 #include <climits>
 #include <cmath>
 
-#include "dt_internal.cuh"
-#include "umma.cuh"
+#include "attn_common.cuh"
 
 namespace dt {
 namespace {
@@ -33,9 +32,6 @@ constexpr int kPrThreads = 640;              // warps 0-3: load, MMA, items, MMA
 constexpr int kPrSoft = 256;                 // softmax threads of a tile
 constexpr int kPrAhead = 3;                  // items that may be known ahead
 constexpr int kPrSorted = 8;                 // prompts a lane of the item warp keeps: up to 256 are dealt out sorted
-constexpr float kPrLazy = 8.f;               // log2 headroom before the running maximum is raised
-constexpr float kPrNone = 3e38f;
-constexpr uint64_t kPrBudgetNs = 4000000000ull;
 constexpr uint32_t kPrBox = kPrKeys * 128;   // 128 rows x 64 elements: 16 KB
 
 struct PrParams {
@@ -49,98 +45,6 @@ struct PrParams {
 struct PrMaps {
   CUtensorMap q, k, v;  // [total][heads][D], box 64 x 1 x 128
 };
-
-__device__ __forceinline__ float pr_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pr_pack(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-// Pairs of fp32 in one 64-bit register: the packed FMA and add issue once for two elements.
-__device__ __forceinline__ uint64_t pr_pair(float lo, float hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ void pr_unpair(uint64_t d, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(d));
-}
-__device__ __forceinline__ uint64_t pr_fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t pr_add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ float pr_max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-// Tensor memory by 16 lanes (rows) a warp: in each group of 8 columns thread l holds columns 2 (l % 4) and + 1 of rows
-// l / 4 and l / 4 + 8 (v[4 g], v[4 g + 1], then v[4 g + 2], v[4 g + 3]). Each load waits for itself.
-__device__ __forceinline__ void pr_ld_s(uint32_t taddr, float (&v)[64]) {  // 16 groups: a block's scores
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,"
-      "%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,"
-      "%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]), "=f"(v[32]),
-        "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]), "=f"(v[40]),
-        "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]), "=f"(v[48]),
-        "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]), "=f"(v[56]),
-        "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void pr_ld_half(uint32_t taddr, float (&v)[32]) {  // 8 groups
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void pr_ld_o(uint32_t taddr, float (&v)[16]) {  // 4 groups
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void pr_st_o(uint32_t taddr, const float* v) {  // 4 groups, as pr_ld holds them
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-      ::"r"(taddr),
-        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
-        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
-      : "memory");
-}
-// The weights of 64 keys: a pair of bf16 per 32-bit column, so a group's two values of a row are one column.
-__device__ __forceinline__ void pr_st_p(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-      ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
 
 // The prompt that owns tile slot `slot`. Prompt b's tiles start at slot cu[b] / 256 + b: its ceil(len / 256) tiles end
 // before the next prompt's start, so the slots are found by search, without a scan of the lengths; some stay unused.
@@ -157,25 +61,6 @@ __device__ __forceinline__ int pr_find(const PrParams& p, int slot, int lane) { 
     if (step == 1) return lo;
     n = step;
   }
-}
-
-// A phase that has ended is seen at once (45 cycles; the form with a time limit takes 100). Otherwise a wait in long
-// sleeps: the hardware wakes the warp when the phase ends, and a warp that polls takes issue slots from those that compute.
-__device__ __forceinline__ bool pr_try_wait(uint64_t* bar, unsigned parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n}"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
-      : "memory");
-  return done != 0;
-}
-__device__ __forceinline__ bool pr_wait(uint64_t* bar, unsigned parity) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (!pr_try_wait(bar, parity))
-    if (global_timer_ns() - t0 > kPrBudgetNs) return false;
-  return true;
 }
 
 struct PrItem {  // 256 rows of a prompt (its first row `lo`, `len` rows) from row q0 on, one head; len 0: no more items
@@ -310,7 +195,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
   // Item k (from 0) as a reader sees it; `arrive`: this thread counts as one of the slot's readers.
   auto read_item = [&](int k, PrItem& it, bool arrive) {
     const int s = k % kPrAhead;
-    if (!pr_wait(&it_full[s], static_cast<unsigned>(k / kPrAhead) & 1u)) return false;
+    if (!at_wait(&it_full[s], static_cast<unsigned>(k / kPrAhead) & 1u)) return false;
     it = s_items[s];
     if (arrive) mbar_arrive(&it_empty[s]);
     return true;
@@ -342,7 +227,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
       }
       const int s = k % kPrAhead;
       if (k >= kPrAhead)
-        ok = __all_sync(0xFFFFFFFFu, pr_wait(&it_empty[s], static_cast<unsigned>(k / kPrAhead - 1) & 1u));
+        ok = __all_sync(0xFFFFFFFFu, at_wait(&it_empty[s], static_cast<unsigned>(k / kPrAhead - 1) & 1u));
       if (!ok) break;
       if (lane == 0) {
         s_items[s] = it;
@@ -356,7 +241,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
     if (elect_one()) {  // TMA, per item: Q0, K0, Q1, V0, K1, V1, ...
       unsigned st = 0, par = 1u, e = 0, uq[2] = {0u, 0u};
       auto load_q = [&](int i, const PrItem& it) {
-        if (uq[i] > 0 && !pr_wait(&q_empty[i], (uq[i] - 1u) & 1u)) return false;
+        if (uq[i] > 0 && !at_wait(&q_empty[i], (uq[i] - 1u) & 1u)) return false;
         mbar_expect_tx(&q_full[i], kTileBytes);
         for (int h = 0; h < kHalves; ++h)
           tma_load_3d(sq + i * kTileBytes + h * kPrBox, &maps.q, 64 * h, it.head, it.lo + it.q0 + i * kPrTile, &q_full[i]);
@@ -364,7 +249,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
         return true;
       };
       auto load_kv = [&](const CUtensorMap* map, const PrItem& it, int kvh, int j) {
-        if (e >= kStages && !pr_wait(&kv_empty[st], par)) return false;
+        if (e >= kStages && !at_wait(&kv_empty[st], par)) return false;
         mbar_expect_tx(&kv_full[st], kTileBytes);
         for (int h = 0; h < kHalves; ++h)
           tma_load_3d(skv + st * kTileBytes + h * kPrBox, map, 64 * h, kvh, it.lo + j * kPrKeys, &kv_full[st]);
@@ -394,7 +279,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
       const uint64_t dq = umma_desc_sw128(smem_u32(sq)), dk = umma_desc_sw128(smem_u32(skv));
       const uint64_t dv = umma_desc_sw128_mn(smem_u32(skv), kPrBox, 1024u);
       auto wait = [&](uint64_t* bar, unsigned parity) {
-        const bool done = pr_wait(bar, parity);
+        const bool done = at_wait(bar, parity);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         return done;
       };
@@ -551,15 +436,14 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
     const int ra = lane0 + (lane >> 2), quad = lane & 3, col = 2 * quad;
     unsigned base = 0, us = 0, uo = 0;  // ring entry of the item's K0; blocks and items of this tile so far
     for (int k = 0; ok; ++k) {
-      ok = __all_sync(0xFFFFFFFFu, pr_wait(&it_full[k % kPrAhead], static_cast<unsigned>(k / kPrAhead) & 1u));
+      ok = __all_sync(0xFFFFFFFFu, at_wait(&it_full[k % kPrAhead], static_cast<unsigned>(k / kPrAhead) & 1u));
       if (!ok) break;
       const PrItem& it = s_items[k % kPrAhead];  // stays until this warp is through with it
       if (it.len == 0) break;
       const int nb = i ? it.n1() : it.n0();
       const int row0 = it.q0 + i * kPrTile + ra;  // row ra's token in its prompt; the other row's is 8 further
-      // minus the running maximum of the scaled scores, as last raised; at first so large that any finite score raises
-      // it, and that a score of -inf has no weight and NaN stays
-      float nref[2] = {kPrNone, kPrNone};
+      // minus the running maximum of the scaled scores, as last raised
+      float nref[2] = {kAtNone, kAtNone};
       float l[2] = {0.f, 0.f};                    // sums of this thread's weights
       for (int j = 0; j < nb && ok; ++j, ++us) {
         const bool diag = j + 1 == nb;
@@ -569,7 +453,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
           // finite among the block's values is cleared too and added to the rows that see it at the end (its weight
           // there is positive, and any positive multiple of it gives the same sum).
           const unsigned e = base + 2u * j + 1u;
-          ok = pr_wait(&kv_full[e % kStages], (e / kStages) & 1u) && ok;
+          ok = at_issued(&s_issued, e) && at_wait(&kv_full[e % kStages], (e / kStages) & 1u) && ok;
           unsigned char* sv = skv + (e % kStages) * kTileBytes;
           const int valid = it.len - j * kPrKeys;  // keys of the block inside the prompt
           __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
@@ -597,11 +481,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
             atomicMax(&s_bad[i], k + 1);
           }
         }
-        ok = pr_wait(&s_full[i], us & 1u) && ok;
+        ok = at_wait(&s_full[i], us & 1u) && ok;
         __syncwarp();
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         float s[64];
-        pr_ld_s(ts, s);
+        at_ld_s(ts, s);
         if (kApart) {
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           __syncwarp();
@@ -609,7 +493,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
         }
         // Apart, the weights before have been read and their products are in O only after this.
         auto p_free = [&]() {
-          if (kApart && us > 0) ok = pr_wait(&p_empty[i], (us - 1u) & 1u) && ok;
+          if (kApart && us > 0) ok = at_wait(&p_empty[i], (us - 1u) & 1u) && ok;
           __syncwarp();
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         };
@@ -622,57 +506,30 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
               if (8 * g + (e & 1) > lim + 8 * (e >> 1)) s[4 * g + e] = -INFINITY;
         }
         float mx[2];
-#pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2) {
-          float u = fmaxf(s[2 * k2], s[2 * k2 + 1]), w = fmaxf(s[2 * k2 + 4], s[2 * k2 + 5]);
-#pragma unroll
-          for (int g = 2; g < 16; g += 2) {
-            u = pr_max3(u, s[4 * g + 2 * k2], s[4 * g + 2 * k2 + 1]);
-            w = pr_max3(w, s[4 * g + 4 + 2 * k2], s[4 * g + 5 + 2 * k2]);
-          }
-          mx[k2] = fmaxf(u, w) * p.scale_log2;
-        }
-        if (__any_sync(0xFFFFFFFFu, mx[0] + nref[0] > kPrLazy || mx[1] + nref[1] > kPrLazy)) {  // rare: raise, rescale O
+        at_max(s, p.scale_log2, mx);
+        if (__any_sync(0xFFFFFFFFu, mx[0] + nref[0] > kAtLazy || mx[1] + nref[1] > kAtLazy)) {  // rare: raise, rescale O
           float alpha[2];
-#pragma unroll
-          for (int k2 = 0; k2 < 2; ++k2) {
-            mx[k2] = fmaxf(mx[k2], __shfl_xor_sync(0xFFFFFFFFu, mx[k2], 1));
-            mx[k2] = fmaxf(mx[k2], __shfl_xor_sync(0xFFFFFFFFu, mx[k2], 2));
-            const bool raise = mx[k2] + nref[k2] > kPrLazy;
-            alpha[k2] = raise ? pr_exp2(-nref[k2] - mx[k2]) : 1.f;  // from nothing: 0
-            l[k2] *= alpha[k2];
-            if (raise) nref[k2] = -mx[k2];
-          }
+          at_raise(mx, nref, l, alpha);
           if (j > 0) {
             p_free();  // (not apart, S is full only after the products into O before it)
 #pragma unroll 1
             for (int h = 0; h < D / 32; ++h) {
               float o[16];
-              pr_ld_o(to + 32u * h, o);
+              at_ld_o(to + 32u * h, o);
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] *= alpha[(e >> 1) & 1];
-              pr_st_o(to + 32u * h, o);
+              at_st_o(to + 32u * h, o);
             }
           }
         }
-        const uint64_t scale2 = pr_pair(p.scale_log2, p.scale_log2);
-        const uint64_t nref2[2] = {pr_pair(nref[0], nref[0]), pr_pair(nref[1], nref[1])};
         uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t pk[16];
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {  // group 8 h + c / 2, row c % 2
-            const int at = 32 * h + 2 * c;
-            float a, bb;
-            pr_unpair(pr_fma2(pr_pair(s[at], s[at + 1]), scale2, nref2[c & 1]), a, bb);
-            a = pr_exp2(a);
-            bb = pr_exp2(bb);
-            ls[c & 3] = pr_add2(ls[c & 3], pr_pair(a, bb));
-            pk[c] = pr_pack(a, bb);
-          }
+          if (h == 0) at_weights<0>(s, p.scale_log2, nref, ls, pk);
+          else at_weights<1>(s, p.scale_log2, nref, ls, pk);
           if (kApart && h == 0) p_free();
-          pr_st_p(tp + 32u * h, pk);
+          at_st_p(tp + 32u * h, pk);
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           if (diag && h == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the cleared values
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -680,12 +537,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
           // half of the weights are in place: their products may start (apart, all of them start together)
           if (lane == 0 && (!kApart || h == 1)) mbar_arrive(&p_full[i][h]);
         }
-#pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2) {
-          float la, lb;
-          pr_unpair(pr_add2(ls[k2], ls[k2 + 2]), la, lb);
-          l[k2] += la + lb;
-        }
+        at_sums(ls, l);
         ok = __all_sync(0xFFFFFFFFu, ok);
       }
       if (!ok) break;
@@ -695,7 +547,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
         if (lane == 0) mbar_arrive(&it_empty[k % kPrAhead]);
         continue;
       }
-      ok = __all_sync(0xFFFFFFFFu, pr_wait(&o_full[i], uo & 1u));
+      ok = __all_sync(0xFFFFFFFFu, at_wait(&o_full[i], uo & 1u));
       if (!ok) break;
       ++uo;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -711,9 +563,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
       unsigned short* po = p.out + (static_cast<size_t>(it.lo + row0) * p.Hq + it.head) * D + 8 * quad;
       float o[D / 2];
       if constexpr (D == 128)
-        pr_ld_s(to, o);
+        at_ld_s(to, o);
       else
-        pr_ld_half(to, o);
+        at_ld_half(to, o);
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_empty[i]);  // O is free for the next item
@@ -727,31 +579,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
           }
         }
       }
-      // four threads hold the four words of each 16 bytes: transposed among them, so that each stores 16 bytes
-      const bool in[2] = {row0 < it.len, row0 + 8 < it.len};
 #pragma unroll
       for (int h = 0; h < D / 32; ++h)
 #pragma unroll
         for (int k2 = 0; k2 < 2; ++k2) {
-          uint32_t x[4];
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-            x[g] = pr_pack(o[16 * h + 4 * g + 2 * k2] * inv[k2], o[16 * h + 4 * g + 2 * k2 + 1] * inv[k2]);
-#pragma unroll
-          for (int g = 0; g < 4; g += 2) {
-            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, quad & 1 ? x[g] : x[g + 1], 1);
-            if (quad & 1) x[g] = got;
-            else x[g + 1] = got;
-          }
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, quad & 2 ? x[g] : x[g + 2], 2);
-            if (quad & 2) x[g] = got;
-            else x[g + 2] = got;
-          }
-          if (in[k2])
-            *reinterpret_cast<uint4*>(po + static_cast<size_t>(8 * k2) * p.Hq * D + 32 * h) =
-                make_uint4(x[0], x[1], x[2], x[3]);
+          const uint4 x = at_row16(o + 16 * h, k2, inv[k2], quad);
+          if (row0 + 8 * k2 < it.len)
+            *reinterpret_cast<uint4*>(po + static_cast<size_t>(8 * k2) * p.Hq * D + 32 * h) = x;
         }
       __syncwarp();
       if (lane == 0) mbar_arrive(&it_empty[k % kPrAhead]);
@@ -762,9 +596,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
     record_error(hdr, DT_ERR_TIMEOUT);
     // copies issued but never waited for must land before the CTA leaves: wait for them too (bounded)
     // (with two MMA threads, entries one of them has seen may be counted again: their phase is over or comes)
-    for (unsigned e = kApart ? min(s_used[0], s_used[1]) : s_used[0]; e < s_issued; ++e) mbar_wait(&kv_full[e % kStages], (e / kStages) & 1u, kPrBudgetNs);
+    for (unsigned e = kApart ? min(s_used[0], s_used[1]) : s_used[0]; e < s_issued; ++e) mbar_wait(&kv_full[e % kStages], (e / kStages) & 1u, kAtBudgetNs);
     for (int i = 0; i < 2; ++i)
-      for (unsigned e = s_qu[i]; e < s_qi[i]; ++e) mbar_wait(&q_full[i], e & 1u, kPrBudgetNs);
+      for (unsigned e = s_qu[i]; e < s_qi[i]; ++e) mbar_wait(&q_full[i], e & 1u, kAtBudgetNs);
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
