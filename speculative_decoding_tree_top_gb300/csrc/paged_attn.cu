@@ -30,7 +30,7 @@ constexpr int kPaThreads = 384;   // warps 0 and 1: values that must not reach t
 constexpr int kPaMaxStages = 12;
 constexpr int kPaCleans = 8;      // barriers of cleaned blocks: more than the ring can hold
 constexpr uint32_t kPaBox = kPaKeys * 128;  // 128 rows x 64 elements: 16 KB
-constexpr size_t kPaSmemCap = 232448 - 1024;  // opt-in shared memory of a CTA, less the static part
+constexpr size_t kPaSmemCap = 232448 - 5120;  // opt-in shared memory of a CTA, less the static part
 
 struct PaParams {
   int B, n, Hq, Hkv, G, R, grid, stages;
@@ -48,7 +48,7 @@ struct PaParams {
 };
 struct PaMaps {
   CUtensorMap q;     // [B][n][Hq][D], box 64 x G x n x 1
-  CUtensorMap k, v;  // [num_pages][Hkv][page_size][D], box 64 x min(page_size, 128) x 1 x 1
+  CUtensorMap k, v;  // [num_pages * Hkv][page_size][D] in 8-row atoms, boxes of min(page_size, 128) rows
 };
 
 __device__ __forceinline__ bool nonfinite_bf16x2(uint32_t w) {
@@ -181,6 +181,14 @@ __device__ __forceinline__ void pa_join(const PaParams& p, const PaJoin& jn, int
 // rows past the request's end): blocks that reach past it are masked, and their values cleaned.
 __device__ __forceinline__ int pa_common(const PaParams& p, int len) { return p.n > 1 || p.mask ? len - p.n : len; }
 
+// Of 64 consecutive keys: all before `own` are visible, key own + c where bit c of `nodes` is set, none from `end` on.
+__device__ __forceinline__ unsigned long long pa_visible(int own, int end, unsigned long long nodes) {
+  const unsigned long long before = own >= 64 ? ~0ull : own <= 0 ? 0ull : (1ull << own) - 1ull;
+  const unsigned long long there = end >= 64 ? ~0ull : end <= 0 ? 0ull : (1ull << end) - 1ull;
+  const unsigned long long tree = own >= 64 || own <= -64 ? 0ull : own >= 0 ? nodes << own : nodes >> -own;
+  return (before | tree) & there;
+}
+
 // Roles: warp 2 loads (its lanes look the pages up and issue one page's boxes each), warp 3 issues the MMAs, the softmax
 // warps own 16 query rows each (row r = node G + head, tensor memory lane r; four neighbouring threads share two rows),
 // warps 0 and 1 clean values. Per block: S = Q K^T (M = 128, N = 128) into one of two buffers in tensor memory, so that
@@ -194,6 +202,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
                                                                    WsHeader* hdr) {
   constexpr int kHalves = D / 64;
   constexpr uint32_t kEntry = kHalves * kPaBox;  // a ring entry: a block's keys or values
+  constexpr uint32_t kAtoms = kHalves * 1024;    // eight of its rows
   constexpr uint32_t kColO = 256, kStepO = D;    // tensor memory: S at 0 and 128, O behind
   extern __shared__ float4 smem_f4[];
   unsigned char* sq =
@@ -208,6 +217,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
   __shared__ int s_warp[kPaThreads / 32];
   __shared__ int s_bad, s_joins;
   __shared__ PaJoin s_join[2];
+  __shared__ unsigned long long s_mbits[kPaCleans][kPaNodes];  // bit c: the key of node c is visible to the node
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int live_warps = (p.R + 15) / 16;
   const unsigned stages = static_cast<unsigned>(p.stages);
@@ -306,9 +316,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
           if (lane == 0) mbar_expect_tx(&kv_full[st], static_cast<uint32_t>(pages * box_rows * 128 * kHalves));
           __syncwarp();
           if (lane < pages) {
-            unsigned char* d = skv + st * kEntry + lane * box_rows * 128;
-            for (int h = 0; h < kHalves; ++h)
-              tma_load_4d(d + h * kPaBox, kv ? &maps.v : &maps.k, 64 * h, row, sg.kvh, page, &kv_full[st]);
+            tma_load_5d(skv + st * kEntry + lane * box_rows * (128 * kHalves), kv ? &maps.v : &maps.k, 0, 0, 0, row / 8,
+                        page * p.Hkv + sg.kvh, &kv_full[st]);
           }
           ++e;
           if (lane == 0) s_kv_issued = e;
@@ -322,7 +331,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
   } else if (warp == 3) {
     if (elect_one()) {  // MMA
       const uint32_t id_s = umma_idesc(kPaKeys, 128), id_o = umma_idesc(D, 128) | (1u << 16);  // O: V MN-major
-      const uint64_t dk = umma_desc_sw128(smem_u32(skv)), dv = umma_desc_sw128_mn(smem_u32(skv), kPaBox, 1024u);
+      const uint64_t dk = umma_desc_sw128_strided(smem_u32(skv), kAtoms);
+      const uint64_t dv = umma_desc_sw128_mn(smem_u32(skv), 1024u, kAtoms);
       auto wait = [&](uint64_t* bar, unsigned parity) {
         const bool done = at_wait(bar, parity);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -359,7 +369,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           umma_f16(tmem + (gs & 1u) * kPaKeys, q0 + (((kk >> 2) * p.q_box + (kk & 3) * 32u) >> 4),
-                   k0 + (((kk >> 2) * kPaBox + (kk & 3) * 32u) >> 4), id_s, kk > 0 ? 1u : 0u);
+                   k0 + (((kk >> 2) * 1024u + (kk & 3) * 32u) >> 4), id_s, kk > 0 ? 1u : 0u);
         umma_commit(&s_full[gs & 1u]);
         umma_commit(&kv_empty[at]);
         if (++js == ss.nblk) umma_commit(&q_empty[sis & 1]);
@@ -388,7 +398,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
           const uint64_t v0 = dv + sv * (kEntry >> 4);
 #pragma unroll
           for (int kk = 0; kk < kPaKeys / 16; ++kk)
-            umma_f16_ts(to, tmem + (g & 1u) * kPaKeys + 8u * kk, v0 + 128u * kk, id_o, (j > 0 || kk > 0) ? 1u : 0u);
+            umma_f16_ts(to, tmem + (g & 1u) * kPaKeys + 8u * kk, v0 + kk * (2u * kAtoms >> 4), id_o, (j > 0 || kk > 0) ? 1u : 0u);
           umma_commit(&kv_empty[sv]);
           umma_commit(&o_done[g & 1u]);
         }
@@ -407,12 +417,24 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
         const int kbase = (sg.j0 + j) * kPaKeys;
         if (kbase + kPaKeys <= common) continue;
         const unsigned e = 2u * g + 1u, at = e % stages;
-        ok = __all_sync(0xFFFFFFFFu, at_issued(&s_kv_issued, e) && at_wait(&kv_full[at], (e / stages) & 1u));
+        ok = __all_sync(0xFFFFFFFFu, at_issued(&s_kv_issued, e));
+        if (!ok) break;
+        if (t < p.n) {  // the nodes' mask rows, for the softmax
+          unsigned long long bits = t == 63 ? ~0ull : (2ull << t) - 1ull;
+          if (p.mask) {
+            const uint8_t* mr = p.mask + (static_cast<size_t>(sg.b) * p.n + t) * p.n;
+            bits = 0ull;
+#pragma unroll 8
+            for (int c = 0; c < p.n; ++c) bits |= static_cast<unsigned long long>(mr[c] != 0) << c;
+          }
+          s_mbits[cleans % kPaCleans][t] = bits;
+        }
+        ok = __all_sync(0xFFFFFFFFu, at_wait(&kv_full[at], (e / stages) & 1u));
         if (!ok) break;
         unsigned char* sv = skv + at * kEntry;
         bool found = false;
         for (int c = t; c < kHalves * kPaKeys * 8; c += 64) {  // 16-byte pieces; eight a row
-          const int key = kbase + ((c >> 3) & (kPaKeys - 1));
+          const int key = kbase + c / (kAtoms / 16) * 8 + ((c >> 3) & 7);
           uint4* piece = reinterpret_cast<uint4*>(sv + 16 * c);
           if (key >= len) {
             *piece = make_uint4(0u, 0u, 0u, 0u);
@@ -452,7 +474,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
       node[k2] = live[k2] ? (ra + 8 * k2) / p.G : 0;
       head[k2] = live[k2] ? (ra + 8 * k2) % p.G : 0;
     }
-    unsigned g = 0, meet = 0;
+    unsigned g = 0, meet = 0, cleans = 0;
     for (int si = 0; w.x < w.x1 && ok; ++si) {
       const PaSeg sg = pa_next(p, cum, w);
       const unsigned qb = static_cast<unsigned>(si) & 1u;
@@ -460,16 +482,6 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
       const int len = p.lens[sg.b], pre = len - p.n, common = pa_common(p, len);
       const int last_key = (sg.j0 + sg.nblk) * kPaKeys;
       unsigned long long mbits[2] = {0ull, 0ull};  // bit c: the key of node c is visible to the row's node
-      if (last_key > common)
-#pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2) {
-          if (!p.mask) {
-            mbits[k2] = node[k2] == 63 ? ~0ull : (2ull << node[k2]) - 1ull;
-          } else {
-            const uint8_t* mr = p.mask + (static_cast<size_t>(sg.b) * p.n + node[k2]) * p.n;
-            for (int c = 0; c < p.n; ++c) mbits[k2] |= static_cast<unsigned long long>(mr[c] != 0) << c;
-          }
-        }
       float nref[2] = {kAtNone, kAtNone}, l[2] = {0.f, 0.f};
       for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
         const uint32_t ts = tmem + lanes + (g & 1u) * kPaKeys;
@@ -480,15 +492,23 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
         at_ld_s(ts, s);
         const int kbase = (sg.j0 + j) * kPaKeys;
         if (kbase + kPaKeys > common) {
-          const int end = len - kbase - col, own = pre - kbase - col;  // of this thread's columns 8 g + e
+          ok = at_wait(&v_clean[cleans % kPaCleans], (cleans / kPaCleans) & 1u) && ok;
+          __syncwarp();
 #pragma unroll
-          for (int g8 = 0; g8 < 16; ++g8)
+          for (int k2 = 0; k2 < 2; ++k2) {
+            mbits[k2] = s_mbits[cleans % kPaCleans][node[k2]];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int c = 8 * g8 + (e & 1);
-              const bool seen = c < own || (c < end && ((mbits[e >> 1] >> ((c - own) & 63)) & 1ull));
-              if (!seen) s[4 * g8 + e] = -INFINITY;
+            for (int half = 0; half < 2; ++half) {  // bit i: this thread's column 64 half + i (from its own first) is visible
+              const int at = kbase + col + 64 * half;
+              const unsigned long long bits = pa_visible(pre - at, len - at, mbits[k2]);
+#pragma unroll
+              for (int g8 = 0; g8 < 8; ++g8)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (!((bits >> (8 * g8 + e)) & 1ull)) s[32 * half + 4 * g8 + 2 * k2 + e] = -INFINITY;
             }
+          }
+          ++cleans;
         }
         float mx[2];
         at_max(s, p.scale_log2, mx);
@@ -675,7 +695,8 @@ extern "C" dt_status dt_paged_attention(int B, int n, int Hq, int Hkv, int d, co
   if (n > kPaNodes || static_cast<long long>(G) * n > kPaRows || B > DT_PAGED_MAX_BATCH) return DT_ERR_UNSUPPORTED;
   if (Hq > DT_MAX_HEADS) return DT_ERR_UNSUPPORTED;
   if (page_size < DT_MIN_PAGE || page_size > DT_MAX_PAGE || (page_size & (page_size - 1))) return DT_ERR_UNSUPPORTED;
-  if (static_cast<long long>(num_pages) * page_size > INT_MAX) return DT_ERR_UNSUPPORTED;
+  if (static_cast<long long>(num_pages) * page_size > INT_MAX || static_cast<long long>(num_pages) * Hkv > INT_MAX)
+    return DT_ERR_UNSUPPORTED;
   if (static_cast<long long>(max_pages) * page_size > DT_PAGED_MAX_TOKENS) return DT_ERR_UNSUPPORTED;
   DeviceInfo di{};
   if (current_device_info(&di) != cudaSuccess) return DT_ERR_CUDA;
@@ -698,8 +719,8 @@ extern "C" dt_status dt_paged_attention(int B, int n, int Hq, int Hkv, int d, co
   const uint32_t box = page_size < kPaKeys ? static_cast<uint32_t>(page_size) : kPaKeys;
   if (!encode_bf16_4d(&maps.q, q, dd, static_cast<uint64_t>(Hq), static_cast<uint64_t>(n), static_cast<uint64_t>(B), 64,
                       static_cast<uint32_t>(G), static_cast<uint32_t>(n)) ||
-      !encode_bf16_4d(&maps.k, k_cache, dd, ps, hkv, np, 64, box, 1) ||
-      !encode_bf16_4d(&maps.v, v_cache, dd, ps, hkv, np, 64, box, 1))
+      !encode_bf16_atoms(&maps.k, k_cache, dd, ps, hkv * np, box) ||
+      !encode_bf16_atoms(&maps.v, v_cache, dd, ps, hkv * np, box))
     return DT_ERR_CUDA;
   WsHeader* hdr = reinterpret_cast<WsHeader*>(ws);
   return d == 64 ? pa_launch<64>(p, maps, hdr, stream) : pa_launch<128>(p, maps, hdr, stream);

@@ -18,6 +18,12 @@ __device__ __forceinline__ uint64_t umma_desc_sw128(uint32_t saddr) {  // K-majo
   return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
          (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
 }
+// The same with the 8-row atoms `row_stride` bytes apart.
+__device__ __forceinline__ uint64_t umma_desc_sw128_strided(uint32_t saddr, uint32_t row_stride) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
+         (static_cast<uint64_t>((row_stride >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(2) << 61);
+}
 // MN-major tile with 128-byte swizzle: 64 elements of M (or N) contiguous in a 128-byte row, eight K rows per 1 KB
 // atom; atoms `mn_stride` bytes apart along M (N) and `k_stride` bytes apart along K.
 __device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t saddr, uint32_t mn_stride, uint32_t k_stride) {
@@ -68,6 +74,12 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
       ::"r"(smem_u32(dst)), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, int c4,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+      ::"r"(smem_u32(dst)), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar)) : "memory");
 }
 // Four 32-lane x 8-column TMEM loads, `stride` columns apart, and the wait for them, in one statement (nothing can
 // read the registers before the wait).
@@ -148,6 +160,22 @@ inline bool encode_bf16_3d_pitched(CUtensorMap* m, const void* ptr, uint64_t d0,
   const cuuint32_t box[3] = {b0, b1, b2};
   const cuuint32_t estride[3] = {1, 1, 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), gdim, gstride, box, estride,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Planes of `rows` rows of `cols` (a multiple of 64) elements, rows a multiple of 8, as a 5-D map [planes][rows / 8]
+// [cols / 64][8][64]: a box of `box_rows` rows of one plane lands as 8-row atoms of 1 KB (128-byte swizzle), an atom's
+// column groups of 64 next to each other, so that one copy brings whole rows whatever their width.
+inline bool encode_bf16_atoms(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t planes,
+                              uint32_t box_rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (!encode) return false;
+  const cuuint64_t gdim[5] = {64, 8, cols / 64, rows / 8, planes};
+  const cuuint64_t gstride[4] = {cols * 2, 128, cols * 16, cols * rows * 2};
+  const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(cols / 64), box_rows / 8, 1};
+  const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), gdim, gstride, box, estride,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
