@@ -120,60 +120,54 @@ __device__ __forceinline__ PaSeg pa_next(const PaParams& p, const int* cum, PaWa
 struct PaJoin {
   int b, kvh, c0, c1, first;
 };
-// Joins them, a warp per query row: the lanes read 32 segments' (m, l) at a time, then each segment's row of O, D / 32
-// columns a lane, with several segments' loads in flight.
-template <int D>
-__device__ __forceinline__ void pa_join(const PaParams& p, const PaJoin& jn, int warp, int lane) {
-  constexpr int kCols = D / 32;
-  const int nseg = jn.c1 - jn.c0 + 1;
-  auto unit = [&](int i) { return 2 * static_cast<size_t>(jn.c0 + i) + (i == 0 ? jn.first : 0); };
-  for (int r = warp; r < p.R; r += kPaThreads / 32) {
-    float mx = -INFINITY;
-    for (int i = lane; i < nseg; i += 32) mx = fmaxf(mx, __ldcg(p.ml + (unit(i) * p.R + r) * 2));
+// Joins them with every thread of the CTA: a thread takes four columns of a query row, several rows' loads in flight, and
+// runs through the segments with a maximum that may rise.
+template <int D, int kAtOnce>
+__device__ __forceinline__ void pa_join(const PaParams& p, const PaJoin& jn) {
+  constexpr int kQuads = D / 4, kSegments = 8 / kAtOnce;  // loads in flight: kAtOnce rows of kSegments segments
+  const int nseg = jn.c1 - jn.c0 + 1, total = p.R * kQuads;
+  for (int i0 = threadIdx.x; i0 < total; i0 += kAtOnce * kPaThreads) {
+    float4 num[kAtOnce];
+    float m[kAtOnce], den[kAtOnce];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    const float mref = mx == -INFINITY ? 0.f : mx;
-    float den = 0.f, num[kCols];
+    for (int u = 0; u < kAtOnce; ++u) {
+      num[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      m[u] = -INFINITY;
+      den[u] = 0.f;
+    }
+#pragma unroll kSegments
+    for (int c = 0; c < nseg; ++c) {
+      const size_t unit = 2 * static_cast<size_t>(jn.c0 + c) + (c == 0 ? jn.first : 0);
 #pragma unroll
-    for (int e = 0; e < kCols; ++e) num[e] = 0.f;
-    for (int i0 = 0; i0 < nseg; i0 += 32) {
-      float wgt = 0.f;
-      if (i0 + lane < nseg) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ml + (unit(i0 + lane) * p.R + r) * 2));
-        wgt = exp2f(ml.x - mref);  // a segment without visible keys: 2^-inf = 0
-        den += wgt * ml.y;
-      }
-      const int here = min(32, nseg - i0);
-#pragma unroll 8
-      for (int i = 0; i < here; ++i) {
-        const float* src = p.part + (unit(i0 + i) * p.R + r) * D + kCols * lane;
-        const float wi = __shfl_sync(0xFFFFFFFFu, wgt, i);
-        if constexpr (kCols == 4) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
-          num[0] += wi * x.x;
-          num[1] += wi * x.y;
-          num[2] += wi * x.z;
-          num[3] += wi * x.w;
-        } else {
-          const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-          num[0] += wi * x.x;
-          num[1] += wi * x.y;
-        }
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int i = min(i0 + u * kPaThreads, total - 1);
+        const size_t row = unit * p.R + i / kQuads;
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ml + 2 * row));
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part + row * D + 4 * (i % kQuads)));
+        const float mn = fmaxf(m[u], ml.x), ref = mn == -INFINITY ? 0.f : mn;  // nothing visible so far: 2^-inf = 0
+        const float a = exp2f(m[u] - ref), b = exp2f(ml.x - ref);
+        m[u] = mn;
+        den[u] = den[u] * a + b * ml.y;
+        num[u].x = num[u].x * a + b * x.x;
+        num[u].y = num[u].y * a + b * x.y;
+        num[u].z = num[u].z * a + b * x.z;
+        num[u].w = num[u].w * a + b * x.w;
       }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xFFFFFFFFu, den, o);
-    const int node = r / p.G;
-    bool none = p.mask && p.lens[jn.b] == p.n;  // no prefix: perhaps no visible key at all
-    if (none)
-      for (int c = 0; c < p.n; ++c) none = none && p.mask[(static_cast<size_t>(jn.b) * p.n + node) * p.n + c] == 0;
-    const float inv = den == 0.f && none ? 0.f : 1.f / den;
-    unsigned short* o =
-        p.out + ((static_cast<size_t>(jn.b) * p.n + node) * p.Hq + jn.kvh * p.G + r % p.G) * D + kCols * lane;
-    if constexpr (kCols == 4)
-      *reinterpret_cast<uint2*>(o) = make_uint2(at_pack(num[0] * inv, num[1] * inv), at_pack(num[2] * inv, num[3] * inv));
-    else
-      *reinterpret_cast<uint32_t*>(o) = at_pack(num[0] * inv, num[1] * inv);
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = i0 + u * kPaThreads;
+      if (i >= total) break;
+      const int r = i / kQuads, node = r / p.G;
+      bool none = den[u] == 0.f && p.mask && p.lens[jn.b] == p.n;  // no prefix: perhaps no visible key at all
+      if (none)
+        for (int c = 0; c < p.n; ++c) none = none && p.mask[(static_cast<size_t>(jn.b) * p.n + node) * p.n + c] == 0;
+      const float inv = none ? 0.f : 1.f / den[u];
+      unsigned short* o =
+          p.out + ((static_cast<size_t>(jn.b) * p.n + node) * p.Hq + jn.kvh * p.G + r % p.G) * D + 4 * (i % kQuads);
+      *reinterpret_cast<uint2*>(o) =
+          make_uint2(at_pack(num[u].x * inv, num[u].y * inv), at_pack(num[u].z * inv, num[u].w * inv));
+    }
   }
 }
 
@@ -626,7 +620,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
   }
   if (ok) {
     __threadfence();  // the ticket's thread acquired the others' partials; the barrier above passed them on
-    for (int i = 0; i < s_joins; ++i) pa_join<D>(p, s_join[i], warp, lane);
+    for (int i = 0; i < s_joins; ++i) {
+      if (p.R * (D / 4) <= kPaThreads) pa_join<D, 1>(p, s_join[i]);  // few rows, perhaps of many segments
+      else pa_join<D, 4>(p, s_join[i]);
+    }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
