@@ -7,7 +7,8 @@
 // GB300 design (flash decoding on the 5th-generation tensor cores): the n nodes of the G = Hq / Hkv query heads that
 // share a key/value head are one block of R = G n <= 128 query rows, so each cached row is read once per (request,
 // key/value head) and feeds R rows of dot products. Only the device knows the lengths: every CTA (one per SM) scans
-// them, and the 128-key blocks of all (request, key/value head) pairs, laid end to end, are split evenly over the CTAs.
+// them, and the 128-key blocks of all (request, key/value head) pairs, laid end to end with a unit more for each pair
+// (its start and end cost about what a block does), are split evenly over the CTAs.
 // A CTA's run inside one pair is a segment; a segment that covers its pair writes the output, the others leave
 // (O, m, l) in the CTA's two partial slots (only the first and the last segment of a share can be cut), and the CTA
 // that finishes a cut pair last joins its segments in slot order, so the result does not depend on who that is.
@@ -62,8 +63,9 @@ __device__ __forceinline__ bool pa_sync(uint64_t* bar, unsigned& count, int lane
   return __all_sync(0xFFFFFFFFu, at_wait(bar, count++ & 1u));
 }
 
-// The lengths' plan. cum[b] = 128-key blocks of one head of requests before b; a request whose length is not in
-// [n, max_pages * page_size] has none (0 and below: an unused row of the batch; otherwise an error).
+// The lengths' plan. cum[b]: units of one head of the requests before b, a request's being its 128-key blocks and one
+// more; a request whose length is not in [n, max_pages * page_size] has none (0 and below: an unused row of the batch;
+// otherwise an error).
 __device__ __forceinline__ int pa_length(const PaParams& p, int b, bool* bad) {
   const int len = p.lens[b];
   if (len <= 0) return 0;
@@ -78,9 +80,8 @@ __device__ __forceinline__ int pa_owner(long long x, long long W, int grid) {
   return static_cast<int>(((x + 1) * grid - 1) / W);
 }
 struct PaSeg {
-  int b, kvh, nb, j0, nblk;
-  long long pair0;  // the pair's first block in the flattened order
-  bool first;       // the CTA's first segment
+  int b, kvh, nb, j0, nblk;  // blocks j0 .. j0 + nblk - 1 of the pair's nb
+  long long pair0;           // the pair's first block in the flattened order (after the pair's extra unit)
 };
 struct PaWalk {  // a CTA's segments, in order
   int b;
@@ -100,31 +101,39 @@ __device__ __forceinline__ PaWalk pa_walk(const PaParams& p, const int* cum, lon
   w.b = lo;
   return w;
 }
-__device__ __forceinline__ PaSeg pa_next(const PaParams& p, const int* cum, PaWalk& w) {  // call while w.x < w.x1
-  while (static_cast<long long>(cum[w.b + 1]) * p.Hkv <= w.x) ++w.b;
-  PaSeg s;
-  s.b = w.b;
-  s.nb = cum[w.b + 1] - cum[w.b];
-  const long long rel = w.x - static_cast<long long>(cum[w.b]) * p.Hkv;
-  s.kvh = static_cast<int>(rel / s.nb);
-  s.j0 = static_cast<int>(rel - static_cast<long long>(s.kvh) * s.nb);
-  s.pair0 = w.x - s.j0;
-  const long long left = w.x1 - w.x;
-  s.nblk = left < s.nb - s.j0 ? static_cast<int>(left) : s.nb - s.j0;
-  s.first = w.x == w.x0;
-  w.x += s.nblk;
+// The next segment, nblk 0 when there is none.
+__device__ __forceinline__ PaSeg pa_next(const PaParams& p, const int* cum, PaWalk& w) {
+  PaSeg s{};
+  while (w.x < w.x1) {
+    while (static_cast<long long>(cum[w.b + 1]) * p.Hkv <= w.x) ++w.b;
+    const int units = cum[w.b + 1] - cum[w.b];
+    const long long start = static_cast<long long>(cum[w.b]) * p.Hkv, rel = w.x - start;
+    const int kvh = static_cast<int>(rel / units), at = static_cast<int>(rel - static_cast<long long>(kvh) * units);
+    const long long left = w.x1 - w.x;
+    const int take = left < units - at ? static_cast<int>(left) : units - at;
+    w.x += take;
+    s.nblk = at == 0 ? take - 1 : take;
+    if (s.nblk == 0) continue;  // the share ends behind the pair's extra unit
+    s.b = w.b;
+    s.kvh = kvh;
+    s.nb = units - 1;
+    s.j0 = at == 0 ? 0 : at - 1;
+    s.pair0 = start + static_cast<long long>(kvh) * units + 1;
+    break;
+  }
   return s;
 }
 
-// A cut pair's segments: CTA c0's in slot `first`, those of c0 + 1 .. c1 in their slot 0.
+// A cut pair's segments are those of CTAs c0 .. c1. A CTA's slot 1 holds the segment that starts its pair, slot 0 one that
+// goes on with another CTA's.
 struct PaJoin {
-  int b, kvh, c0, c1, first;
+  int b, kvh, c0, c1;
 };
 // Joins them with every thread of the CTA: a thread takes four columns of a query row, several rows' loads in flight, and
 // runs through the segments with a maximum that may rise.
 template <int D, int kAtOnce>
 __device__ __forceinline__ void pa_join(const PaParams& p, const PaJoin& jn) {
-  constexpr int kQuads = D / 4, kSegments = 8 / kAtOnce;  // loads in flight: kAtOnce rows of kSegments segments
+  constexpr int kQuads = D / 4, kSegments = kAtOnce == 1 ? 8 : 2;  // loads in flight: kAtOnce rows of kSegments segments
   const int nseg = jn.c1 - jn.c0 + 1, total = p.R * kQuads;
   for (int i0 = threadIdx.x; i0 < total; i0 += kAtOnce * kPaThreads) {
     float4 num[kAtOnce];
@@ -137,7 +146,7 @@ __device__ __forceinline__ void pa_join(const PaParams& p, const PaJoin& jn) {
     }
 #pragma unroll kSegments
     for (int c = 0; c < nseg; ++c) {
-      const size_t unit = 2 * static_cast<size_t>(jn.c0 + c) + (c == 0 ? jn.first : 0);
+      const size_t unit = 2 * static_cast<size_t>(jn.c0 + c) + (c == 0 ? 1 : 0);
 #pragma unroll
       for (int u = 0; u < kAtOnce; ++u) {
         const int i = min(i0 + u * kPaThreads, total - 1);
@@ -249,7 +258,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
     const int len = b < p.B ? pa_length(p, b, &bad) : 0;
     if (bad && blockIdx.x == 0) record_error(hdr, DT_ERR_INVALID_ARG);
     int total;
-    const int before = block_exclusive_scan<kPaThreads / 32>((len + kPaKeys - 1) / kPaKeys, &total, s_warp);
+    const int units = len > 0 ? (len + kPaKeys - 1) / kPaKeys + 1 : 0;
+    const int before = block_exclusive_scan<kPaThreads / 32>(units, &total, s_warp);
     if (b < p.B) cum[b] = carry + before;
     carry += total;
   }
@@ -272,8 +282,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
     unsigned st = 0, par = 1u, e = 0;  // ring entry, the parity of its last release, entries so far
     const int box_rows = p.page_size < kPaKeys ? p.page_size : kPaKeys;
     const int per_block = kPaKeys / box_rows;  // pages a block spans (1 when a page holds whole blocks)
-    for (int si = 0; w.x < w.x1 && ok; ++si) {
+    for (int si = 0; ok; ++si) {
       const PaSeg sg = pa_next(p, cum, w);
+      if (sg.nblk == 0) break;
       const unsigned qb = static_cast<unsigned>(si) & 1u;
       const int used = (p.lens[sg.b] + p.page_size - 1) / p.page_size;  // pages the request holds
       const int32_t* table = p.page_table + static_cast<size_t>(sg.b) * p.max_pages;
@@ -350,9 +361,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
       unsigned gs = 0;
       auto scores = [&]() {  // of the next block, if there is one
         if (js == ss.nblk) {
-          if (ws.x >= ws.x1) return true;
           ss = pa_next(p, cum, ws);
           js = 0;
+          if (ss.nblk == 0) return true;
           ++sis;
           if (!wait(&q_full[sis & 1], static_cast<unsigned>(sis >> 1) & 1u)) return false;
           s_q_used = static_cast<unsigned>(sis) + 1u;
@@ -372,8 +383,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
       };
       unsigned g = 0, cleans = 0;
       ok = scores();
-      for (int si = 0; w.x < w.x1 && ok; ++si) {
+      for (int si = 0; ok; ++si) {
         const PaSeg sg = pa_next(p, cum, w);
+        if (sg.nblk == 0) break;
         const unsigned qb = static_cast<unsigned>(si) & 1u;
         const uint32_t to = tmem + kColO + kStepO * qb;
         const int common = pa_common(p, p.lens[sg.b]);
@@ -404,8 +416,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
     // values is cleared here and added to the rows that see it at the end: its weight there is positive, and any
     // positive multiple of it gives the same sum.
     unsigned g = 0, cleans = 0;
-    for (int si = 0; w.x < w.x1 && ok; ++si) {
+    for (int si = 0; ok; ++si) {
       const PaSeg sg = pa_next(p, cum, w);
+      if (sg.nblk == 0) break;
       const int len = p.lens[sg.b], common = pa_common(p, len);
       for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
         const int kbase = (sg.j0 + j) * kPaKeys;
@@ -469,8 +482,9 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
       head[k2] = live[k2] ? (ra + 8 * k2) % p.G : 0;
     }
     unsigned g = 0, meet = 0, cleans = 0;
-    for (int si = 0; w.x < w.x1 && ok; ++si) {
+    for (int si = 0; ok; ++si) {
       const PaSeg sg = pa_next(p, cum, w);
+      if (sg.nblk == 0) break;
       const unsigned qb = static_cast<unsigned>(si) & 1u;
       const uint32_t to = tmem + lanes + kColO + kStepO * qb;
       const int len = p.lens[sg.b], pre = len - p.n, common = pa_common(p, len);
@@ -585,7 +599,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
         }
         continue;
       }
-      const size_t unit = 2 * static_cast<size_t>(blockIdx.x) + (sg.first ? 0 : 1);
+      const size_t unit = 2 * static_cast<size_t>(blockIdx.x) + (sg.j0 == 0 ? 1 : 0);
 #pragma unroll
       for (int k2 = 0; k2 < 2; ++k2) {
         if (!live[k2]) continue;
@@ -606,7 +620,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
         const unsigned done = atom_add_acq_rel_gpu(p.tickets + c0, 1u) + 1u;
         if (done == static_cast<unsigned>(c1 - c0 + 1)) {
           p.tickets[c0] = 0u;  // ready for the next call
-          s_join[s_joins++] = PaJoin{sg.b, sg.kvh, c0, c1, pa_share(W, ctas, c0) == sg.pair0 ? 0 : 1};
+          s_join[s_joins++] = PaJoin{sg.b, sg.kvh, c0, c1};
         }
       }
     }
@@ -622,7 +636,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
     __threadfence();  // the ticket's thread acquired the others' partials; the barrier above passed them on
     for (int i = 0; i < s_joins; ++i) {
       if (p.R * (D / 4) <= kPaThreads) pa_join<D, 1>(p, s_join[i]);  // few rows, perhaps of many segments
-      else pa_join<D, 4>(p, s_join[i]);
+      else pa_join<D, 6>(p, s_join[i]);
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
