@@ -75,9 +75,15 @@ __device__ __forceinline__ int pa_length(const PaParams& p, int b, bool* bad) {
   }
   return len;
 }
-__device__ __forceinline__ long long pa_share(long long W, int grid, int c) { return W * c / grid; }
+// CTA c's share of W units starts here; the CTA whose share holds unit x. (A 64-bit division takes half a microsecond on
+// the way to the first load; a batch's units nearly always fit 32 bits.)
+__device__ __forceinline__ long long pa_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
+__device__ __forceinline__ long long pa_share(long long W, int grid, int c) { return pa_div(W * c, grid); }
 __device__ __forceinline__ int pa_owner(long long x, long long W, int grid) {
-  return static_cast<int>(((x + 1) * grid - 1) / W);
+  return static_cast<int>(pa_div((x + 1) * grid - 1, W));
 }
 struct PaSeg {
   int b, kvh, nb, j0, nblk;  // blocks j0 .. j0 + nblk - 1 of the pair's nb
@@ -107,8 +113,8 @@ __device__ __forceinline__ PaSeg pa_next(const PaParams& p, const int* cum, PaWa
   while (w.x < w.x1) {
     while (static_cast<long long>(cum[w.b + 1]) * p.Hkv <= w.x) ++w.b;
     const int units = cum[w.b + 1] - cum[w.b];
-    const long long start = static_cast<long long>(cum[w.b]) * p.Hkv, rel = w.x - start;
-    const int kvh = static_cast<int>(rel / units), at = static_cast<int>(rel - static_cast<long long>(kvh) * units);
+    const long long start = static_cast<long long>(cum[w.b]) * p.Hkv;
+    const int rel = static_cast<int>(w.x - start), kvh = rel / units, at = rel - kvh * units;  // rel < units Hkv < 2^26
     const long long left = w.x1 - w.x;
     const int take = left < units - at ? static_cast<int>(left) : units - at;
     w.x += take;
@@ -129,53 +135,83 @@ __device__ __forceinline__ PaSeg pa_next(const PaParams& p, const int* cum, PaWa
 struct PaJoin {
   int b, kvh, c0, c1;
 };
-// Joins them with every thread of the CTA: a thread takes four columns of a query row, several rows' loads in flight, and
-// runs through the segments with a maximum that may rise.
+// Joins them with every thread of the CTA: a thread takes four columns of a query row and runs through the segments with a
+// maximum that may rise. Many rows: several at once, so that their loads are in flight together. Few rows (kAtOnce 1):
+// as many threads a row as there are, each with every so many segments, joined in order through shared memory `red`.
+struct PaSum {
+  float4 num;
+  float m, den;
+  __device__ __forceinline__ void add(const float4& x, float mx, float d) {
+    const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.f : mn;  // nothing visible so far: 2^-inf = 0
+    const float a = exp2f(m - ref), b = exp2f(mx - ref);
+    m = mn;
+    den = den * a + b * d;
+    num.x = num.x * a + b * x.x;
+    num.y = num.y * a + b * x.y;
+    num.z = num.z * a + b * x.z;
+    num.w = num.w * a + b * x.w;
+  }
+};
+template <int D>
+__device__ __forceinline__ void pa_join_out(const PaParams& p, const PaJoin& jn, int i, const PaSum& s) {
+  constexpr int kQuads = D / 4;
+  const int r = i / kQuads, node = r / p.G;
+  bool none = s.den == 0.f && p.mask && p.lens[jn.b] == p.n;  // no prefix: perhaps no visible key at all
+  if (none)
+    for (int c = 0; c < p.n; ++c) none = none && p.mask[(static_cast<size_t>(jn.b) * p.n + node) * p.n + c] == 0;
+  const float inv = none ? 0.f : 1.f / s.den;
+  unsigned short* o =
+      p.out + ((static_cast<size_t>(jn.b) * p.n + node) * p.Hq + jn.kvh * p.G + r % p.G) * D + 4 * (i % kQuads);
+  *reinterpret_cast<uint2*>(o) =
+      make_uint2(at_pack(s.num.x * inv, s.num.y * inv), at_pack(s.num.z * inv, s.num.w * inv));
+}
 template <int D, int kAtOnce>
-__device__ __forceinline__ void pa_join(const PaParams& p, const PaJoin& jn) {
+__device__ __forceinline__ void pa_join(const PaParams& p, const PaJoin& jn, PaSum* red) {
   constexpr int kQuads = D / 4, kSegments = kAtOnce == 1 ? 8 : 2;  // loads in flight: kAtOnce rows of kSegments segments
   const int nseg = jn.c1 - jn.c0 + 1, total = p.R * kQuads;
-  for (int i0 = threadIdx.x; i0 < total; i0 += kAtOnce * kPaThreads) {
-    float4 num[kAtOnce];
-    float m[kAtOnce], den[kAtOnce];
+  const int groups = kAtOnce == 1 ? kPaThreads / total : 1, group = kAtOnce == 1 ? threadIdx.x / total : 0;
+  const int first = kAtOnce == 1 ? static_cast<int>(threadIdx.x) % total : static_cast<int>(threadIdx.x);
+  for (int i0 = first; i0 < total; i0 += kAtOnce * kPaThreads) {
+    PaSum s[kAtOnce];
 #pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) {
-      num[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      m[u] = -INFINITY;
-      den[u] = 0.f;
-    }
-#pragma unroll kSegments
-    for (int c = 0; c < nseg; ++c) {
-      const size_t unit = 2 * static_cast<size_t>(jn.c0 + c) + (c == 0 ? 1 : 0);
+    for (int u = 0; u < kAtOnce; ++u) s[u] = PaSum{make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
+    for (int c0 = group; group < groups && c0 < nseg; c0 += kSegments * groups) {
+      float2 ml[kSegments][kAtOnce];
+      float4 x[kSegments][kAtOnce];
 #pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        const int i = min(i0 + u * kPaThreads, total - 1);
-        const size_t row = unit * p.R + i / kQuads;
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ml + 2 * row));
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part + row * D + 4 * (i % kQuads)));
-        const float mn = fmaxf(m[u], ml.x), ref = mn == -INFINITY ? 0.f : mn;  // nothing visible so far: 2^-inf = 0
-        const float a = exp2f(m[u] - ref), b = exp2f(ml.x - ref);
-        m[u] = mn;
-        den[u] = den[u] * a + b * ml.y;
-        num[u].x = num[u].x * a + b * x.x;
-        num[u].y = num[u].y * a + b * x.y;
-        num[u].z = num[u].z * a + b * x.z;
-        num[u].w = num[u].w * a + b * x.w;
+      for (int k = 0; k < kSegments; ++k) {
+        const int c = c0 + k * groups;
+        const size_t unit = 2 * static_cast<size_t>(jn.c0 + c) + (c == 0 ? 1 : 0);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int i = i0 + u * kPaThreads;
+          const size_t row = unit * p.R + i / kQuads;
+          ml[k][u] = make_float2(-INFINITY, 0.f);
+          x[k][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (c < nseg && i < total) {
+            ml[k][u] = __ldcg(reinterpret_cast<const float2*>(p.ml + 2 * row));
+            x[k][u] = __ldcg(reinterpret_cast<const float4*>(p.part + row * D + 4 * (i % kQuads)));
+          }
+        }
       }
-    }
 #pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) {
-      const int i = i0 + u * kPaThreads;
-      if (i >= total) break;
-      const int r = i / kQuads, node = r / p.G;
-      bool none = den[u] == 0.f && p.mask && p.lens[jn.b] == p.n;  // no prefix: perhaps no visible key at all
-      if (none)
-        for (int c = 0; c < p.n; ++c) none = none && p.mask[(static_cast<size_t>(jn.b) * p.n + node) * p.n + c] == 0;
-      const float inv = none ? 0.f : 1.f / den[u];
-      unsigned short* o =
-          p.out + ((static_cast<size_t>(jn.b) * p.n + node) * p.Hq + jn.kvh * p.G + r % p.G) * D + 4 * (i % kQuads);
-      *reinterpret_cast<uint2*>(o) =
-          make_uint2(at_pack(num[u].x * inv, num[u].y * inv), at_pack(num[u].z * inv, num[u].w * inv));
+      for (int k = 0; k < kSegments; ++k)
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) s[u].add(x[k][u], ml[k][u].x, ml[k][u].y);
+    }
+    if constexpr (kAtOnce == 1) {
+      if (group > 0 && group < groups) red[threadIdx.x] = s[0];
+      __syncthreads();
+      if (group == 0) {
+        for (int g = 1; g < groups; ++g) s[0].add(red[g * total + i0].num, red[g * total + i0].m, red[g * total + i0].den);
+        pa_join_out<D>(p, jn, i0, s[0]);
+      }
+      __syncthreads();
+      break;  // every thread had one
+    } else {
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+        if (i0 + u * kPaThreads < total) pa_join_out<D>(p, jn, i0 + u * kPaThreads, s[u]);
     }
   }
 }
@@ -213,6 +249,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
   const uint32_t q_bytes = kHalves * p.q_box;
   unsigned char* skv = sq + 2 * q_bytes;
   int* cum = reinterpret_cast<int*>(skv + p.stages * kEntry);  // [B + 1]
+  int* lens = cum + p.B + 1;                                   // [B]
   __shared__ uint64_t kv_full[kPaMaxStages], kv_empty[kPaMaxStages], v_clean[kPaCleans], s_full[2], p_full[2], o_done[2];
   __shared__ uint64_t q_full[2], q_empty[2], o_free[2], s_meet;
   __shared__ uint32_t s_tmem;
@@ -260,7 +297,10 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
     int total;
     const int units = len > 0 ? (len + kPaKeys - 1) / kPaKeys + 1 : 0;
     const int before = block_exclusive_scan<kPaThreads / 32>(units, &total, s_warp);
-    if (b < p.B) cum[b] = carry + before;
+    if (b < p.B) {
+      cum[b] = carry + before;
+      lens[b] = len;
+    }
     carry += total;
   }
   if (t == 0) cum[p.B] = carry;
@@ -286,7 +326,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
       const PaSeg sg = pa_next(p, cum, w);
       if (sg.nblk == 0) break;
       const unsigned qb = static_cast<unsigned>(si) & 1u;
-      const int used = (p.lens[sg.b] + p.page_size - 1) / p.page_size;  // pages the request holds
+      const int used = (lens[sg.b] + p.page_size - 1) / p.page_size;  // pages the request holds
       const int32_t* table = p.page_table + static_cast<size_t>(sg.b) * p.max_pages;
       // page ids, 32 at a time and one window ahead
       int win = static_cast<int>(static_cast<long long>(sg.j0) * kPaKeys / p.page_size) / 32;
@@ -388,7 +428,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
         if (sg.nblk == 0) break;
         const unsigned qb = static_cast<unsigned>(si) & 1u;
         const uint32_t to = tmem + kColO + kStepO * qb;
-        const int common = pa_common(p, p.lens[sg.b]);
+        const int common = pa_common(p, lens[sg.b]);
         for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
           unsigned sv;
           ok = take(sv);
@@ -419,7 +459,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
     for (int si = 0; ok; ++si) {
       const PaSeg sg = pa_next(p, cum, w);
       if (sg.nblk == 0) break;
-      const int len = p.lens[sg.b], common = pa_common(p, len);
+      const int len = lens[sg.b], common = pa_common(p, len);
       for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
         const int kbase = (sg.j0 + j) * kPaKeys;
         if (kbase + kPaKeys <= common) continue;
@@ -487,7 +527,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
       if (sg.nblk == 0) break;
       const unsigned qb = static_cast<unsigned>(si) & 1u;
       const uint32_t to = tmem + lanes + kColO + kStepO * qb;
-      const int len = p.lens[sg.b], pre = len - p.n, common = pa_common(p, len);
+      const int len = lens[sg.b], pre = len - p.n, common = pa_common(p, len);
       const int last_key = (sg.j0 + sg.nblk) * kPaKeys;
       unsigned long long mbits[2] = {0ull, 0ull};  // bit c: the key of node c is visible to the row's node
       float nref[2] = {kAtNone, kAtNone}, l[2] = {0.f, 0.f};
@@ -613,8 +653,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
       }
       // the pair's last segment to finish joins them all, once the CTA is through its share
       const int c0 = pa_owner(sg.pair0, W, ctas), c1 = pa_owner(sg.pair0 + sg.nb - 1, W, ctas);
-      __threadfence();
-      ok = pa_sync(&s_meet, meet, lane);
+      ok = pa_sync(&s_meet, meet, lane);  // the ticket's release covers what the other warps wrote before it
       if (!ok) break;
       if (t == 128) {
         const unsigned done = atom_add_acq_rel_gpu(p.tickets + c0, 1u) + 1u;
@@ -633,10 +672,11 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
     for (unsigned q = s_q_used; q < s_q_issued; ++q) mbar_wait(&q_full[q & 1u], (q >> 1) & 1u, kAtBudgetNs);
   }
   if (ok) {
-    __threadfence();  // the ticket's thread acquired the others' partials; the barrier above passed them on
+    // the ticket's thread acquired the others' partials; the barrier above passed them on
     for (int i = 0; i < s_joins; ++i) {
-      if (p.R * (D / 4) <= kPaThreads) pa_join<D, 1>(p, s_join[i]);  // few rows, perhaps of many segments
-      else pa_join<D, 6>(p, s_join[i]);
+      PaSum* red = reinterpret_cast<PaSum*>(skv);  // the ring is empty by now
+      if (p.R * (D / 4) <= kPaThreads) pa_join<D, 1>(p, s_join[i], red);
+      else pa_join<D, 6>(p, s_join[i], red);
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -662,7 +702,7 @@ template <int D>
 dt_status pa_launch(PaParams& p, const PaMaps& maps, WsHeader* hdr, cudaStream_t stream) {
   const uint32_t halves = D / 64, entry = halves * kPaBox;
   p.q_box = static_cast<uint32_t>((p.R + 7) / 8 * 8) * 128;
-  const size_t fixed = 1024 + 2 * halves * p.q_box + align_up(sizeof(int) * (p.B + 1), 16);
+  const size_t fixed = 1024 + 2 * halves * p.q_box + align_up(sizeof(int) * (2 * p.B + 1), 16);
   const int fit = static_cast<int>((kPaSmemCap - fixed) / entry);
   p.stages = fit > kPaMaxStages ? kPaMaxStages : fit;
   const size_t smem = fixed + static_cast<size_t>(p.stages) * entry;
