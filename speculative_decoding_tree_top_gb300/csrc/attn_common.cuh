@@ -21,6 +21,11 @@ __device__ __forceinline__ float at_exp2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float at_rcp(float x) {  // off by at most 2^-23 of it; 0 gives infinity
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ uint32_t at_pack(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -199,6 +204,16 @@ __device__ __forceinline__ bool at_wait(uint64_t* bar, unsigned parity) {
   return true;
 }
 
+// Whether the phase has ended, without waiting.
+__device__ __forceinline__ bool at_test(uint64_t* bar, unsigned parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 // Waits until the loader has issued more than `e` ring entries (its count, in shared memory). A waiter that skips entries
 // calls this before it waits for entry e's phase: by then the phase before, of the same parity as the next, is over.
 __device__ __forceinline__ bool at_issued(const unsigned* count, unsigned e) {

@@ -238,38 +238,51 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
       if (it.len == 0) break;
     }
   } else if (warp == 0) {
-    if (elect_one()) {  // TMA, per item: Q0, K0, Q1, V0, K1, V1, ...
+    if (elect_one()) {  // TMA, per item: Q0, K0, Q1, V0, K1, V1, ..., a Q when its buffer is free
       unsigned st = 0, par = 1u, e = 0, uq[2] = {0u, 0u};
-      auto load_q = [&](int i, const PrItem& it) {
-        if (uq[i] > 0 && !at_wait(&q_empty[i], (uq[i] - 1u) & 1u)) return false;
-        mbar_expect_tx(&q_full[i], kTileBytes);
-        for (int h = 0; h < kHalves; ++h)
-          tma_load_3d(sq + i * kTileBytes + h * kPrBox, &maps.q, 64 * h, it.head, it.lo + it.q0 + i * kPrTile, &q_full[i]);
-        s_qi[i] = ++uq[i];
-        return true;
-      };
-      auto load_kv = [&](const CUtensorMap* map, const PrItem& it, int kvh, int j) {
-        if (e >= kStages && !at_wait(&kv_empty[st], par)) return false;
-        mbar_expect_tx(&kv_full[st], kTileBytes);
-        for (int h = 0; h < kHalves; ++h)
-          tma_load_3d(skv + st * kTileBytes + h * kPrBox, map, 64 * h, kvh, it.lo + j * kPrKeys, &kv_full[st]);
-        s_issued = ++e;
-        if (++st == kStages) {
-          st = 0;
-          par ^= 1u;
-        }
-        return true;
-      };
       for (int k = 0; ok; ++k) {
         PrItem it;
         ok = read_item(k, it, true);
         if (!ok || it.len == 0) break;
         const int kvh = it.head / p.G, nblk = it.blocks();
-        ok = load_q(0, it);
+        bool pending[2] = {true, it.n1() > 0};
+        auto load_q = [&](int i) {  // if it is still to come and can
+          if (!pending[i] || (uq[i] > 0 && !at_test(&q_empty[i], (uq[i] - 1u) & 1u))) return;
+          pending[i] = false;
+          mbar_expect_tx(&q_full[i], kTileBytes);
+          for (int h = 0; h < kHalves; ++h)
+            tma_load_3d(sq + i * kTileBytes + h * kPrBox, &maps.q, 64 * h, it.head, it.lo + it.q0 + i * kPrTile, &q_full[i]);
+          s_qi[i] = ++uq[i];
+        };
+        auto load_kv = [&](const CUtensorMap* map, int j) {
+          if (e >= kStages && !at_test(&kv_empty[st], par)) {
+            const uint64_t t0 = global_timer_ns();
+            while (!at_test(&kv_empty[st], par)) {
+              load_q(0);
+              load_q(1);
+              if (global_timer_ns() - t0 > kAtBudgetNs) return false;
+              __nanosleep(40);
+            }
+          }
+          mbar_expect_tx(&kv_full[st], kTileBytes);
+          for (int h = 0; h < kHalves; ++h)
+            tma_load_3d(skv + st * kTileBytes + h * kPrBox, map, 64 * h, kvh, it.lo + j * kPrKeys, &kv_full[st]);
+          s_issued = ++e;
+          if (++st == kStages) {
+            st = 0;
+            par ^= 1u;
+          }
+          return true;
+        };
         for (int j = 0; j < nblk && ok; ++j) {
-          ok = load_kv(&maps.k, it, kvh, j);
-          if (ok && j == 0 && it.n1() > 0) ok = load_q(1, it);
-          if (ok) ok = load_kv(&maps.v, it, kvh, j);
+          load_q(0);
+          ok = load_kv(&maps.k, j);
+          load_q(1);
+          if (ok) ok = load_kv(&maps.v, j);
+        }
+        for (int i = 0; i < 2 && ok; ++i) {
+          if (pending[i]) ok = at_wait(&q_empty[i], (uq[i] - 1u) & 1u);
+          if (ok) load_q(i);
         }
       }
     }
@@ -556,7 +569,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
       for (int k2 = 0; k2 < 2; ++k2) {
         l[k2] += __shfl_xor_sync(0xFFFFFFFFu, l[k2], 1);
         l[k2] += __shfl_xor_sync(0xFFFFFFFFu, l[k2], 2);
-        inv[k2] = 1.f / l[k2];  // the row's own key is visible; a sum of 0 or NaN gives NaN
+        inv[k2] = at_rcp(l[k2]);  // the row's own key is visible; a sum of 0 or NaN gives NaN
       }
       // a later item's mark counts too: adding what is not finite to rows that see it changes nothing
       const bool bad = *reinterpret_cast<volatile int*>(&s_bad[0]) > k || *reinterpret_cast<volatile int*>(&s_bad[1]) > k;
