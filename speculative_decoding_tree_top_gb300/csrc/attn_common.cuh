@@ -16,6 +16,27 @@ constexpr float kAtNone = 3e38f; // minus a running maximum that has seen nothin
                                  // -inf has no weight under it and NaN stays
 constexpr uint64_t kAtBudgetNs = 4000000000ull;
 
+// These kernels are launched so that their set-up (barriers, tensor memory, descriptors) may run while the kernel before
+// them in the stream ends; everything they read or write in global memory comes after this. The kernel after them may be
+// set up as soon as every CTA has come here; it waits for this one's end in the same way.
+__device__ __forceinline__ void at_launch_order() {
+  asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+}
+template <class Kernel, class... Args>
+inline dt_status at_launch(Kernel kernel, int grid, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, args...));
+}
+
 __device__ __forceinline__ float at_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

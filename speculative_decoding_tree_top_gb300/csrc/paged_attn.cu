@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
   }
   if (warp == 2 && lane < 3)
     asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v) : "memory");
+  at_launch_order();
   // the plan: block counts scanned over the requests; rows of requests without blocks are zero
   int carry = 0;
   for (int b0 = 0; b0 < p.B; b0 += kPaThreads) {
@@ -708,8 +709,7 @@ dt_status pa_launch(PaParams& p, const PaMaps& maps, WsHeader* hdr, cudaStream_t
   const size_t smem = fixed + static_cast<size_t>(p.stages) * entry;
   const void* fn = reinterpret_cast<const void*>(paged_attn_kernel<D>);
   if (ensure_dynamic_smem(fn, kPaSmemCap) != cudaSuccess) return DT_ERR_CUDA;
-  paged_attn_kernel<D><<<static_cast<unsigned>(p.grid), kPaThreads, smem, stream>>>(p, maps, hdr);
-  return cuda_status(cudaGetLastError());
+  return at_launch(paged_attn_kernel<D>, p.grid, kPaThreads, smem, stream, p, maps, hdr);
 }
 
 }  // namespace

@@ -75,13 +75,9 @@ struct PrItem {  // 256 rows of a prompt (its first row `lo`, `len` rows) from r
 // latest (longest) first, found by counting (a lane holds the tile counts of eight prompts). More: the tile slots from
 // the last to the first, which is sorted within each prompt.
 struct PrDealer {
-  int tiles[kPrSorted];
+  int first[kPrSorted], rows[kPrSorted], tiles[kPrSorted];  // of the lane's prompts 32 m + lane
   int total;  // tiles (sorted) or slots
   bool sorted;
-  __device__ __forceinline__ static int count(const PrParams& p, int b) {
-    const int lo = p.cu[b], hi = p.cu[b + 1];
-    return lo < 0 || hi > p.total || lo >= hi ? 0 : (hi - lo + kPrRows - 1) / kPrRows;
-  }
   __device__ __forceinline__ int from(int i) const {  // tiles numbered i and up, over all prompts
     int n = 0;
 #pragma unroll
@@ -91,13 +87,18 @@ struct PrDealer {
   __device__ __forceinline__ void init(const PrParams& p, int lane) {
     sorted = p.B <= 32 * kPrSorted;
 #pragma unroll
-    for (int m = 0; m < kPrSorted; ++m) tiles[m] = sorted && 32 * m + lane < p.B ? count(p, 32 * m + lane) : 0;
+    for (int m = 0; m < kPrSorted; ++m) {
+      const int b = 32 * m + lane;
+      const int lo = sorted && b < p.B ? p.cu[b] : 0, hi = sorted && b < p.B ? p.cu[b + 1] : 0;
+      first[m] = lo;
+      rows[m] = lo < 0 || hi > p.total || lo >= hi ? 0 : hi - lo;
+      tiles[m] = (rows[m] + kPrRows - 1) / kPrRows;
+    }
     total = sorted ? from(0) : p.slots;
   }
   __device__ __forceinline__ PrItem item(const PrParams& p, long long w, int lane) const {  // len 0: nothing there
     PrItem it{0, 0, 0, static_cast<int>(w % p.Hq)};
     const int r = static_cast<int>(w / p.Hq);
-    int b;
     if (sorted) {
       int top = 0;
 #pragma unroll
@@ -109,28 +110,29 @@ struct PrDealer {
         else hi = mid - 1;
       }
       int left = r - from(lo + 1);  // in order among the prompts with a tile `lo`
-      b = -1;
+      bool found = false;
 #pragma unroll
       for (int m = 0; m < kPrSorted; ++m) {
         unsigned has = __ballot_sync(0xFFFFFFFFu, tiles[m] > lo);
-        if (b < 0 && left < __popc(has)) {
-          for (; left > 0; --left) has &= has - 1u;
-          b = 32 * m + __ffs(has) - 1;
+        if (!found && left < __popc(has)) {
+          found = true;
+          for (int skip = left; skip > 0; --skip) has &= has - 1u;
+          it.lo = __shfl_sync(0xFFFFFFFFu, first[m], __ffs(has) - 1);
+          it.len = __shfl_sync(0xFFFFFFFFu, rows[m], __ffs(has) - 1);
         }
         left -= __popc(has);
       }
-      if (b < 0) return it;
       it.q0 = lo * kPrRows;
     } else {
       const int slot = p.slots - 1 - r;
-      b = pr_find(p, slot, lane);
+      const int b = pr_find(p, slot, lane);
       if (b < 0) return it;
       it.q0 = (slot - pr_start(p, b)) * kPrRows;
+      const int lo = p.cu[b], hi = p.cu[b + 1];
+      if (lo < 0 || hi > p.total || lo >= hi || it.q0 < 0 || it.q0 >= hi - lo) return it;
+      it.lo = lo;
+      it.len = hi - lo;
     }
-    const int lo = p.cu[b], hi = p.cu[b + 1];
-    if (lo < 0 || hi > p.total || lo >= hi || it.q0 < 0 || it.q0 >= hi - lo) return it;
-    it.lo = lo;
-    it.len = hi - lo;
     return it;
   }
 };
@@ -182,6 +184,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
     mbar_fence_init();
     s_issued = 0u;
   }
+  if (warp == 0 && lane < 3)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v) : "memory");
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
                  "r"(512) : "memory");
@@ -191,6 +195,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = s_tmem;
+  at_launch_order();
   bool ok = true;
   // Item k (from 0) as a reader sees it; `arrive`: this thread counts as one of the slot's readers.
   auto read_item = [&](int k, PrItem& it, bool arrive) {
@@ -623,8 +628,7 @@ dt_status pr_launch(const PrParams& p, const PrMaps& maps, WsHeader* hdr, cudaSt
   constexpr size_t smem = 1024 + (2 + (D == 128 ? 5 : 8)) * static_cast<size_t>(D / 64) * kPrBox;
   const void* fn = reinterpret_cast<const void*>(prompt_attn_kernel<D>);
   if (ensure_dynamic_smem(fn, smem) != cudaSuccess) return DT_ERR_CUDA;
-  prompt_attn_kernel<D><<<static_cast<unsigned>(p.grid), kPrThreads, smem, stream>>>(p, maps, hdr);
-  return cuda_status(cudaGetLastError());
+  return at_launch(prompt_attn_kernel<D>, p.grid, kPrThreads, smem, stream, p, maps, hdr);
 }
 
 }  // namespace
