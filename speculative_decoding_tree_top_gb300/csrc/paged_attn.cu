@@ -733,7 +733,7 @@ extern "C" dt_status dt_paged_attention(int B, int n, int Hq, int Hkv, int d, co
   if (B < 0 || n < 1 || Hq < 1 || Hkv < 1 || d < 1 || Hq % Hkv != 0 || num_pages < 1 || page_size < 1 || max_pages < 1)
     return DT_ERR_INVALID_ARG;
   if (dtype != DT_F32 && dtype != DT_BF16) return DT_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return DT_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f)) return DT_ERR_INVALID_ARG;
   if (B == 0) return DT_OK;
   const void* ptrs[] = {q, k_cache, v_cache, out, workspace};
   for (const void* x : ptrs)

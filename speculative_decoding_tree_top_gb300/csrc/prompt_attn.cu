@@ -207,11 +207,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
   };
 
   if (warp == 2) {  // the items
-    if (blockIdx.x == 0) {  // lengths that contradict themselves are reported once
-      bool bad = lane == 0 && (p.cu[0] < 0 || p.cu[p.B] > p.total);
-      for (int b = lane; b < p.B; b += 32) bad = bad || p.cu[b] > p.cu[b + 1];
-      if (bad) record_error(hdr, DT_ERR_INVALID_ARG);
-    }
     PrDealer dealer;
     dealer.init(p, lane);
     const long long end = static_cast<long long>(dealer.total) * p.Hq;
@@ -241,6 +236,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
       __syncwarp();
       ++k;
       if (it.len == 0) break;
+    }
+    if (blockIdx.x == 0) {  // lengths that contradict themselves are reported once, when the items are out
+      bool bad = lane == 0 && (p.cu[0] < 0 || p.cu[p.B] > p.total);
+      for (int b = lane; b < p.B; b += 32) bad = bad || p.cu[b] > p.cu[b + 1];
+      if (bad) record_error(hdr, DT_ERR_INVALID_ARG);
     }
   } else if (warp == 0) {
     if (elect_one()) {  // TMA, per item: Q0, K0, Q1, V0, K1, V1, ..., a Q when its buffer is free
@@ -646,7 +646,7 @@ extern "C" dt_status dt_prompt_attention(int total, int B, int Hq, int Hkv, int 
   using namespace dt;
   if (total < 0 || B < 0 || Hq < 1 || Hkv < 1 || d < 1 || Hq % Hkv != 0) return DT_ERR_INVALID_ARG;
   if (dtype != DT_F32 && dtype != DT_BF16) return DT_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return DT_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f)) return DT_ERR_INVALID_ARG;
   if (total == 0 || B == 0) return DT_OK;
   const void* ptrs[] = {q, k, v, out, workspace};
   for (const void* x : ptrs)

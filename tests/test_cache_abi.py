@@ -36,13 +36,13 @@ def test_paged_attention_rejects_bad_arguments(dtlib):
              mask=None, scale=0.1, out=A, ws=A, wsb=1 << 30):
         return f(B, n, Hq, Hkv, d, q, kc, vc, dtype, pages, page, table, width, lens, mask, scale, out, ws, wsb, None)
     for bad in [dict(B=-1), dict(n=0), dict(Hq=0), dict(Hq=7), dict(Hkv=0), dict(d=0), dict(pages=0), dict(page=0),
-                dict(width=0), dict(dtype=9), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
+                dict(width=0), dict(dtype=9), dict(scale=0.0), dict(scale=-1.0), dict(scale=3e38), dict(scale=float("nan")),
                 dict(scale=float("inf")), dict(q=None), dict(q=A + 8), dict(kc=None), dict(vc=A + 4), dict(out=None),
                 dict(ws=A + 8), dict(table=None), dict(lens=None), dict(table=A + 2), dict(lens=A + 1)]:
         assert call(**bad) == INVALID, bad
     for big in [dict(dtype=F32), dict(d=96), dict(d=256), dict(n=65, Hq=2), dict(n=33), dict(B=2049), dict(page=24),
                 dict(page=4), dict(page=512), dict(pages=1 << 28, page=16), dict(width=1 << 21, page=16),
-                dict(Hq=300, Hkv=300)]:
+                dict(Hq=300, Hkv=300), dict(pages=1 << 27, page=8, Hq=64, Hkv=32)]:
         assert call(**big) == UNSUPPORTED, big
     assert call(B=0) == OK
 
