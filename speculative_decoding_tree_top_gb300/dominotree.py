@@ -291,11 +291,21 @@ def _rows(t: torch.Tensor, name: str, dev: int, shape: tuple) -> tuple:
         if t.shape != shape:
             raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
         raise ValueError(f"{name} is on {t.device}, not cuda:{dev}")
-    rows, heads, d = shape
     pitch, head, one = t.stride()
+    rows, heads, d = shape
+    if rows > 1 and head == d and one == 1:
+        return t.data_ptr(), pitch
     if (one != 1 and d != 1) or (head != d and heads != 1):
         raise ValueError(f"{name}: the heads of a row must be dense, strides are {tuple(t.stride())}")
     return t.data_ptr(), pitch if rows > 1 else heads * d
+
+
+def _room(workspace: torch.Tensor, dev: int) -> tuple:
+    """A workspace's address and size in bytes."""
+    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != dev:
+        _dev(workspace, "workspace", torch.uint8)
+        raise ValueError(f"workspace is on {workspace.device}, not cuda:{dev}")
+    return workspace.data_ptr(), workspace.numel()
 
 
 def _raw(stream, dev: int) -> int:
@@ -320,41 +330,41 @@ def dt_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     [max_pos,rot] fp32 (``rope_table``) -> the rotated queries [N,Hq,d] when ``q`` is given, else None. ``out_k``
     [N,Hkv,d], when given, receives the rotated keys as well."""
     N, Hkv, d = kv = k.shape
-    dev = _here(k, "k")
-    cache = k_cache.shape
-    num_pages, _, page_size, _ = cache
+    dev, bf, i32 = _here(k, "k"), torch.bfloat16, torch.int32
+    num_pages, pool_heads, page_size, pool_d = cache = k_cache.shape
     if workspace is None or (q is not None and out_q is None):
         with _side(stream, dev):
             if workspace is None:
                 workspace = new_workspace(256, k.device)
             if q is not None and out_q is None:
-                out_q = torch.empty(q.shape, dtype=torch.bfloat16, device=k.device)
+                out_q = torch.empty(q.shape, dtype=bf, device=k.device)
     Hq = max_pos = rot = q_at = q_pitch = 0
     oq_at = ok_at = rope_at = pos_at = None
     if q is not None:
         Hq = q.shape[1]
-        q_at, q_pitch = _rows(q, "q", dev, (N, Hq, d))
-        oq_at = _on(out_q, "out_q", dev, torch.bfloat16, (N, Hq, d))
+        heads = (N, Hq, d)
+        q_at, q_pitch = _rows(q, "q", dev, heads)
+        oq_at = _on(out_q, "out_q", dev, bf, heads)
     elif out_q is not None:
         raise ValueError("out_q without q")
     if out_k is not None:
-        ok_at = _on(out_k, "out_k", dev, torch.bfloat16, kv)
+        ok_at = _on(out_k, "out_k", dev, bf, kv)
     if rope is not None:
         if positions is None:
             raise ValueError("rope without positions")
-        max_pos, rot = rope.shape
-        rope_at = _on(rope, "rope", dev, torch.float32, (max_pos, rot))
-        pos_at = _on(positions, "positions", dev, torch.int32, (N,))
+        max_pos, rot = table = rope.shape
+        rope_at = _on(rope, "rope", dev, torch.float32, table)
+        pos_at = _on(positions, "positions", dev, i32, (N,))
     k_at, k_pitch = _rows(k, "k", dev, kv)
     v_at, v_pitch = _rows(v, "v", dev, kv)
-    if cache[1] != Hkv or cache[3] != d:
+    if pool_heads != Hkv or pool_d != d:
         raise ValueError(f"k_cache must have shape {(num_pages, Hkv, page_size, d)}, not {tuple(cache)}")
-    _check(lib().dt_kv_append(
-        N, Hq, Hkv, d, q_at, q_pitch, k_at, k_pitch, v_at, v_pitch, BF16, _on(slots, "slots", dev, torch.int32, (N,)),
-        pos_at, rope_at, max_pos, rot, 1 if interleaved else 0, oq_at, ok_at,
-        _on(k_cache, "k_cache", dev, torch.bfloat16, cache), _on(v_cache, "v_cache", dev, torch.bfloat16, cache),
-        num_pages, page_size, _on(workspace, "workspace", dev, torch.uint8, workspace.shape), workspace.numel(),
-        _raw(stream, dev)), "dt_kv_append")
+    status = lib().dt_kv_append(
+        N, Hq, Hkv, d, q_at, q_pitch, k_at, k_pitch, v_at, v_pitch, BF16, _on(slots, "slots", dev, i32, (N,)),
+        pos_at, rope_at, max_pos, rot, 1 if interleaved else 0, oq_at, ok_at, _on(k_cache, "k_cache", dev, bf, cache),
+        _on(v_cache, "v_cache", dev, bf, cache), num_pages, page_size, *_room(workspace, dev), _raw(stream, dev))
+    if status:
+        raise DTError(status, "dt_kv_append")
     return out_q
 
 
@@ -380,14 +390,15 @@ def dt_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
                 workspace = new_workspace(dt_paged_attention_workspace_bytes(B, n, Hq, Hkv, d), q.device)
     if cache[3] != d:
         raise ValueError(f"k_cache must have shape {(num_pages, Hkv, page_size, d)}, not {tuple(cache)}")
-    _check(lib().dt_paged_attention(
+    status = lib().dt_paged_attention(
         B, n, Hq, Hkv, d, _on(q, "q", dev, bf, shape), _on(k_cache, "k_cache", dev, bf, cache),
         _on(v_cache, "v_cache", dev, bf, cache), BF16, num_pages, page_size,
         _on(page_table, "page_table", dev, torch.int32, (B, max_pages)), max_pages,
         _on(lens, "lens", dev, torch.int32, (B,)),
         _on(mask, "mask", dev, torch.uint8, (B, n, n)) if mask is not None else None, scale,
-        _on(out, "out", dev, bf, shape), _on(workspace, "workspace", dev, torch.uint8, workspace.shape),
-        workspace.numel(), _raw(stream, dev)), "dt_paged_attention")
+        _on(out, "out", dev, bf, shape), *_room(workspace, dev), _raw(stream, dev))
+    if status:
+        raise DTError(status, "dt_paged_attention")
     return out
 
 
@@ -411,11 +422,12 @@ def dt_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_se
     q_at, q_pitch = _rows(q, "q", dev, shape)
     k_at, k_pitch = _rows(k, "k", dev, (total, Hkv, d))
     v_at, v_pitch = _rows(v, "v", dev, (total, Hkv, d))
-    _check(lib().dt_prompt_attention(
+    status = lib().dt_prompt_attention(
         total, B, Hq, Hkv, d, q_at, q_pitch, k_at, k_pitch, v_at, v_pitch, BF16,
         _on(cu_seqlens, "cu_seqlens", dev, torch.int32, (B + 1,)), scale, _on(out, "out", dev, bf, shape),
-        _on(workspace, "workspace", dev, torch.uint8, workspace.shape), workspace.numel(), _raw(stream, dev)),
-        "dt_prompt_attention")
+        *_room(workspace, dev), _raw(stream, dev))
+    if status:
+        raise DTError(status, "dt_prompt_attention")
     return out
 
 
