@@ -259,7 +259,7 @@ dt_status dt_tree_attention(int B, int n, int L, int Hq, int Hkv, int d, const v
  * head by head. Token i of request b sits in page page_table[b][i / page_size] at row i % page_size; its slot is
  * page * page_size + row. Pages may be shared by requests and lie in any order; what unused rows hold is never looked
  * at (it may be NaN). Common limits (DT_ERR_UNSUPPORTED beyond): dtype DT_BF16, d = 64 or 128, page_size a power of two
- * in DT_MIN_PAGE .. DT_MAX_PAGE, num_pages * page_size and num_pages * Hkv below 2^31, Hq and Hkv up to DT_MAX_HEADS. */
+ * in DT_MIN_PAGE .. DT_MAX_PAGE, num_pages * page_size and num_pages * Hkv below 2^31, Hq, Hkv up to DT_MAX_HEADS. */
 #define DT_MIN_PAGE 8
 #define DT_MAX_PAGE 256
 #define DT_MAX_HEADS 256

@@ -11,19 +11,22 @@
 namespace dt {
 namespace {
 
-constexpr float kAtLazy = 8.f;   // log2 headroom before a running maximum is raised: the weights stay below 2^8
-constexpr float kAtNone = 3e38f; // minus a running maximum that has seen nothing: any finite score raises it, a score of
-                                 // -inf has no weight under it and NaN stays
+// log2 headroom before a running maximum is raised: the weights stay below 2^8
+constexpr float kAtLazy = 8.f;
+// minus a running maximum that has seen nothing: any finite score raises it, a score of -inf has no weight under it,
+// and NaN stays
+constexpr float kAtNone = 3e38f;
 constexpr uint64_t kAtBudgetNs = 4000000000ull;
 
-// These kernels are launched so that their set-up (barriers, tensor memory, descriptors) may run while the kernel before
-// them in the stream ends; everything they read or write in global memory comes after this. The kernel after them may be
-// set up as soon as every CTA has come here; it waits for this one's end in the same way.
+// These kernels are launched so that their set-up (barriers, tensor memory, descriptors) may run while the kernel
+// before them in the stream ends; everything they read or write in global memory comes after this. The kernel after
+// them may be set up as soon as every CTA has come here; it waits for this one's end in the same way.
 __device__ __forceinline__ void at_launch_order() {
   asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
 }
 template <class Kernel, class... Args>
-inline dt_status at_launch(Kernel kernel, int grid, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
+inline dt_status at_launch(Kernel kernel, int grid, int threads, size_t smem, cudaStream_t stream,
+                           const Args&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
@@ -79,7 +82,8 @@ __device__ __forceinline__ float at_max3(float a, float b, float c) {
 // l / 4 and l / 4 + 8 (v[4 g], v[4 g + 1], then v[4 g + 2], v[4 g + 3]). Each load waits for itself.
 __device__ __forceinline__ void at_ld_s(uint32_t taddr, float (&v)[64]) {  // 16 groups: a block's scores
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "tcgen05.ld.sync.aligned.16x256b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,"
       "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,"
       "%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,"
       "%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
@@ -207,7 +211,7 @@ __device__ __forceinline__ uint4 at_row16(const float* o, int k2, float factor, 
 }
 
 // A phase that has ended is seen at once (45 cycles; the form with a time limit takes 100). Otherwise a wait in long
-// sleeps: the hardware wakes the warp when the phase ends, and a warp that polls takes issue slots from those that compute.
+// sleeps: the hardware wakes the warp when the phase ends; a warp that polls takes issue slots from those that compute.
 __device__ __forceinline__ bool at_try_wait(uint64_t* bar, unsigned parity) {
   uint32_t done;
   asm volatile(
@@ -235,8 +239,8 @@ __device__ __forceinline__ bool at_test(uint64_t* bar, unsigned parity) {
       : "memory");
   return done != 0;
 }
-// Waits until the loader has issued more than `e` ring entries (its count, in shared memory). A waiter that skips entries
-// calls this before it waits for entry e's phase: by then the phase before, of the same parity as the next, is over.
+// Waits until the loader has issued more than `e` ring entries (its count, in shared memory). A waiter that skips
+// entries calls this before it waits for entry e's phase: by then the phase before, of the other parity, is over.
 __device__ __forceinline__ bool at_issued(const unsigned* count, unsigned e) {
   const volatile unsigned* seen = count;
   if (*seen > e) return true;

@@ -27,7 +27,7 @@ namespace {
 constexpr int kPaRows = 128;      // query rows per pair: G n at most
 constexpr int kPaNodes = 64;      // n at most (a node's mask row is one 64-bit word)
 constexpr int kPaKeys = 128;      // keys per block
-constexpr int kPaThreads = 384;   // warps 0 and 1: values that must not reach the tensor cores; 2: load; 3: MMA; 4-11: softmax
+constexpr int kPaThreads = 384;   // warps 0, 1: values kept from the tensor cores; 2: load; 3: MMA; 4-11: softmax
 constexpr int kPaMaxStages = 12;
 constexpr int kPaCleans = 8;      // barriers of cleaned blocks: more than the ring can hold
 constexpr uint32_t kPaBox = kPaKeys * 128;  // 128 rows x 64 elements: 16 KB
@@ -75,8 +75,8 @@ __device__ __forceinline__ int pa_length(const PaParams& p, int b, bool* bad) {
   }
   return len;
 }
-// CTA c's share of W units starts here; the CTA whose share holds unit x. (A 64-bit division takes half a microsecond on
-// the way to the first load; a batch's units nearly always fit 32 bits.)
+// CTA c's share of W units starts here; the CTA whose share holds unit x. (A 64-bit division takes half a microsecond
+// on the way to the first load; a batch's units nearly always fit 32 bits.)
 __device__ __forceinline__ long long pa_div(long long a, long long b) {
   if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
   return a / b;
@@ -130,14 +130,14 @@ __device__ __forceinline__ PaSeg pa_next(const PaParams& p, const int* cum, PaWa
   return s;
 }
 
-// A cut pair's segments are those of CTAs c0 .. c1. A CTA's slot 1 holds the segment that starts its pair, slot 0 one that
-// goes on with another CTA's.
+// A cut pair's segments are those of CTAs c0 .. c1. A CTA's slot 1 holds the segment that starts its pair, slot 0 one
+// that goes on with another CTA's.
 struct PaJoin {
   int b, kvh, c0, c1;
 };
-// Joins them with every thread of the CTA: a thread takes four columns of a query row and runs through the segments with a
-// maximum that may rise. Many rows: several at once, so that their loads are in flight together. Few rows (kAtOnce 1):
-// as many threads a row as there are, each with every so many segments, joined in order through shared memory `red`.
+// Joins them with every thread of the CTA: a thread takes four columns of a query row and runs through the segments
+// with a maximum that may rise. Many rows: several at once, so that their loads are in flight together. Few rows (kAtOnce
+// 1): as many threads a row as there are, each with every so many segments, joined in order through shared memory.
 struct PaSum {
   float4 num;
   float m, den;
@@ -167,7 +167,7 @@ __device__ __forceinline__ void pa_join_out(const PaParams& p, const PaJoin& jn,
 }
 template <int D, int kAtOnce>
 __device__ __forceinline__ void pa_join(const PaParams& p, const PaJoin& jn, PaSum* red) {
-  constexpr int kQuads = D / 4, kSegments = kAtOnce == 1 ? 8 : 2;  // loads in flight: kAtOnce rows of kSegments segments
+  constexpr int kQuads = D / 4, kSegments = kAtOnce == 1 ? 8 : 2;  // in flight: kAtOnce rows of kSegments segments
   const int nseg = jn.c1 - jn.c0 + 1, total = p.R * kQuads;
   const int groups = kAtOnce == 1 ? kPaThreads / total : 1, group = kAtOnce == 1 ? threadIdx.x / total : 0;
   const int first = kAtOnce == 1 ? static_cast<int>(threadIdx.x) % total : static_cast<int>(threadIdx.x);
@@ -203,7 +203,10 @@ __device__ __forceinline__ void pa_join(const PaParams& p, const PaJoin& jn, PaS
       if (group > 0 && group < groups) red[threadIdx.x] = s[0];
       __syncthreads();
       if (group == 0) {
-        for (int g = 1; g < groups; ++g) s[0].add(red[g * total + i0].num, red[g * total + i0].m, red[g * total + i0].den);
+        for (int g = 1; g < groups; ++g) {
+          const PaSum& other = red[g * total + i0];
+          s[0].add(other.num, other.m, other.den);
+        }
         pa_join_out<D>(p, jn, i0, s[0]);
       }
       __syncthreads();
@@ -228,12 +231,12 @@ __device__ __forceinline__ unsigned long long pa_visible(int own, int end, unsig
   return (before | tree) & there;
 }
 
-// Roles: warp 2 loads (its lanes look the pages up and issue one page's boxes each), warp 3 issues the MMAs, the softmax
-// warps own 16 query rows each (row r = node G + head, tensor memory lane r; four neighbouring threads share two rows),
-// warps 0 and 1 clean values. Per block: S = Q K^T (M = 128, N = 128) into one of two buffers in tensor memory, so that
-// the next block's scores are computed during a block's softmax, also across segments; softmax in base 2 with the
-// running maximum raised only past a headroom of 2^8 (O is rescaled then); the weights over their scores as bf16;
-// O += P V with P from tensor memory and V as an MN-major operand, into one of two buffers by segment. Rows past R are
+// Roles: warp 2 loads (its lanes look the pages up and issue one page's boxes each), warp 3 issues the MMAs, the
+// softmax warps own 16 query rows each (row r = node G + head, tensor memory lane r; four neighbouring threads share
+// two rows), warps 0 and 1 clean values. Per block: S = Q K^T (M = 128, N = 128) into one of two buffers in tensor
+// memory, so that the next block's scores are computed during a block's softmax, also across segments; softmax in base 2
+// with the running maximum raised only past a headroom of 2^8 (O is rescaled then); the weights over their scores as
+// bf16; // O += P V with P from tensor memory and V as an MN-major operand, into one of two buffers by segment. Rows past R are
 // padding and are left to whatever their rows of Q hold. A block takes the tensor cores 1024 cycles at D = 128 and the
 // softmax about as long, where its 64 KB take 2800 at the memory's rate.
 template <int D>
@@ -250,8 +253,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
   unsigned char* skv = sq + 2 * q_bytes;
   int* cum = reinterpret_cast<int*>(skv + p.stages * kEntry);  // [B + 1]
   int* lens = cum + p.B + 1;                                   // [B]
-  __shared__ uint64_t kv_full[kPaMaxStages], kv_empty[kPaMaxStages], v_clean[kPaCleans], s_full[2], p_full[2], o_done[2];
-  __shared__ uint64_t q_full[2], q_empty[2], o_free[2], s_meet;
+  __shared__ uint64_t kv_full[kPaMaxStages], kv_empty[kPaMaxStages], v_clean[kPaCleans];
+  __shared__ uint64_t s_full[2], p_full[2], o_done[2], q_full[2], q_empty[2], o_free[2], s_meet;
   __shared__ uint32_t s_tmem;
   __shared__ unsigned s_kv_issued, s_kv_used, s_q_issued, s_q_used;  // copies issued and waited for (failure drain)
   __shared__ int s_warp[kPaThreads / 32];
@@ -445,17 +448,18 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
           const uint64_t v0 = dv + sv * (kEntry >> 4);
 #pragma unroll
           for (int kk = 0; kk < kPaKeys / 16; ++kk)
-            umma_f16_ts(to, tmem + (g & 1u) * kPaKeys + 8u * kk, v0 + kk * (2u * kAtoms >> 4), id_o, (j > 0 || kk > 0) ? 1u : 0u);
+            umma_f16_ts(to, tmem + (g & 1u) * kPaKeys + 8u * kk, v0 + kk * (2u * kAtoms >> 4), id_o,
+                        (j > 0 || kk > 0) ? 1u : 0u);
           umma_commit(&kv_empty[sv]);
           umma_commit(&o_done[g & 1u]);
         }
       }
     }
   } else if (warp < 2) {
-    // A weight of zero does not hide a value that is not finite from the tensor cores (0 x inf is NaN). So rows past the
-    // request's end (stale, or left in the ring by another block) are cleared, and what is not finite among the nodes'
-    // values is cleared here and added to the rows that see it at the end: its weight there is positive, and any
-    // positive multiple of it gives the same sum.
+    // A weight of zero does not hide a value that is not finite from the tensor cores (0 x inf is NaN). So rows past
+    // the request's end (stale, or left in the ring by another block) are cleared, and what is not finite among the
+    // nodes' values is cleared here and added to the rows that see it at the end: its weight there is positive, and
+    // any positive multiple of it gives the same sum.
     unsigned g = 0, cleans = 0;
     for (int si = 0; ok; ++si) {
       const PaSeg sg = pa_next(p, cum, w);
@@ -547,7 +551,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
           for (int k2 = 0; k2 < 2; ++k2) {
             mbits[k2] = s_mbits[cleans % kPaCleans][node[k2]];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {  // bit i: this thread's column 64 half + i (from its own first) is visible
+            for (int half = 0; half < 2; ++half) {  // bit i: column 64 half + i, from the thread's first, is visible
               const int at = kbase + col + 64 * half;
               const unsigned long long bits = pa_visible(pre - at, len - at, mbits[k2]);
 #pragma unroll
@@ -604,7 +608,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_free[qb]);
       const bool whole = sg.nblk == sg.nb;
-      const bool bad = *reinterpret_cast<volatile int*>(&s_bad) > si;  // (a later segment's mark counts too: only slower)
+      // (a later segment's mark counts too: that is only slower)
+      const bool bad = *reinterpret_cast<volatile int*>(&s_bad) > si;
       if (bad) {  // rare: the nodes' values that are not finite, from global memory
         for (int c = 0; c < p.n; ++c) {
           const int key = pre + c;
@@ -616,7 +621,8 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
 #pragma unroll
           for (int e = 0; e < D / 2; ++e) {
             const uint32_t bits = static_cast<uint32_t>(vr[8 * (e >> 2) + (e & 1)]) << 16;
-            if ((bits & 0x7F800000u) == 0x7F800000u && ((mbits[(e >> 1) & 1] >> c) & 1ull)) o[e] += __uint_as_float(bits);
+            if ((bits & 0x7F800000u) == 0x7F800000u && ((mbits[(e >> 1) & 1] >> c) & 1ull))
+              o[e] += __uint_as_float(bits);
           }
         }
       }

@@ -28,7 +28,7 @@ namespace {
 constexpr int kPrTile = 128;                 // query rows of a tile
 constexpr int kPrRows = 2 * kPrTile;         // of a CTA
 constexpr int kPrKeys = 128;                 // keys per block
-constexpr int kPrThreads = 640;              // warps 0-3: load, MMA, items, MMA (D = 64); 4-11 and 12-19: the tiles' softmax
+constexpr int kPrThreads = 640;              // warps 0-3: load, MMA, items, MMA (D = 64); then eight a tile's softmax
 constexpr int kPrSoft = 256;                 // softmax threads of a tile
 constexpr int kPrAhead = 3;                  // items that may be known ahead
 constexpr int kPrSorted = 8;                 // prompts a lane of the item warp keeps: up to 256 are dealt out sorted
@@ -256,7 +256,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
           pending[i] = false;
           mbar_expect_tx(&q_full[i], kTileBytes);
           for (int h = 0; h < kHalves; ++h)
-            tma_load_3d(sq + i * kTileBytes + h * kPrBox, &maps.q, 64 * h, it.head, it.lo + it.q0 + i * kPrTile, &q_full[i]);
+            tma_load_3d(sq + i * kTileBytes + h * kPrBox, &maps.q, 64 * h, it.head, it.lo + it.q0 + i * kPrTile,
+                        &q_full[i]);
           s_qi[i] = ++uq[i];
         };
         auto load_kv = [&](const CUtensorMap* map, int j) {
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
         }
         float mx[2];
         at_max(s, p.scale_log2, mx);
-        if (__any_sync(0xFFFFFFFFu, mx[0] + nref[0] > kAtLazy || mx[1] + nref[1] > kAtLazy)) {  // rare: raise, rescale O
+        if (__any_sync(0xFFFFFFFFu, mx[0] + nref[0] > kAtLazy || mx[1] + nref[1] > kAtLazy)) {  // rare: rescale O
           float alpha[2];
           at_raise(mx, nref, l, alpha);
           if (j > 0) {
@@ -577,7 +578,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
         inv[k2] = at_rcp(l[k2]);  // the row's own key is visible; a sum of 0 or NaN gives NaN
       }
       // a later item's mark counts too: adding what is not finite to rows that see it changes nothing
-      const bool bad = *reinterpret_cast<volatile int*>(&s_bad[0]) > k || *reinterpret_cast<volatile int*>(&s_bad[1]) > k;
+      const volatile int* marks = s_bad;
+      const bool bad = marks[0] > k || marks[1] > k;
       unsigned short* po = p.out + (static_cast<size_t>(it.lo + row0) * p.Hq + it.head) * D + 8 * quad;
       float o[D / 2];
       if constexpr (D == 128)
@@ -614,7 +616,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
     record_error(hdr, DT_ERR_TIMEOUT);
     // copies issued but never waited for must land before the CTA leaves: wait for them too (bounded)
     // (with two MMA threads, entries one of them has seen may be counted again: their phase is over or comes)
-    for (unsigned e = kApart ? min(s_used[0], s_used[1]) : s_used[0]; e < s_issued; ++e) mbar_wait(&kv_full[e % kStages], (e / kStages) & 1u, kAtBudgetNs);
+    for (unsigned e = kApart ? min(s_used[0], s_used[1]) : s_used[0]; e < s_issued; ++e)
+      mbar_wait(&kv_full[e % kStages], (e / kStages) & 1u, kAtBudgetNs);
     for (int i = 0; i < 2; ++i)
       for (unsigned e = s_qu[i]; e < s_qi[i]; ++e) mbar_wait(&q_full[i], e & 1u, kAtBudgetNs);
   }

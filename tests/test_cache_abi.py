@@ -36,7 +36,8 @@ def test_paged_attention_rejects_bad_arguments(dtlib):
              mask=None, scale=0.1, out=A, ws=A, wsb=1 << 30):
         return f(B, n, Hq, Hkv, d, q, kc, vc, dtype, pages, page, table, width, lens, mask, scale, out, ws, wsb, None)
     for bad in [dict(B=-1), dict(n=0), dict(Hq=0), dict(Hq=7), dict(Hkv=0), dict(d=0), dict(pages=0), dict(page=0),
-                dict(width=0), dict(dtype=9), dict(scale=0.0), dict(scale=-1.0), dict(scale=3e38), dict(scale=float("nan")),
+                dict(width=0), dict(dtype=9), dict(scale=0.0), dict(scale=-1.0), dict(scale=3e38),
+                dict(scale=float("nan")),
                 dict(scale=float("inf")), dict(q=None), dict(q=A + 8), dict(kc=None), dict(vc=A + 4), dict(out=None),
                 dict(ws=A + 8), dict(table=None), dict(lens=None), dict(table=A + 2), dict(lens=A + 1)]:
         assert call(**bad) == INVALID, bad
@@ -59,7 +60,8 @@ def test_prompt_attention_rejects_bad_arguments(dtlib):
                 dict(ks=260), dict(vs=1 << 33)]:
         assert call(**bad) == INVALID, bad
     for big in [dict(dtype=F32), dict(d=96), dict(d=256, qs=2048, ks=512, vs=512),
-                dict(Hq=300, Hkv=300, qs=38400, ks=38400, vs=38400), dict(total=(1 << 31) - 1), dict(B=1 << 23, Hq=256, qs=32768)]:
+                dict(Hq=300, Hkv=300, qs=38400, ks=38400, vs=38400), dict(total=(1 << 31) - 1),
+                dict(B=1 << 23, Hq=256, qs=32768)]:
         assert call(**big) == UNSUPPORTED, big
     assert call(total=0) == OK
     assert call(B=0) == OK

@@ -222,7 +222,7 @@ def test_bad_lengths_and_pages_are_reported(dtlib):
 def test_a_captured_call_follows_the_lengths(dtlib):
     """Replayed after the lengths, the table and the pools changed in place, on a stream of its own."""
     s, other = make([300, 1, 90], 1, 8, 2, 128, 16, mask=None), make([7, 310, 0], 1, 8, 2, 128, 16, mask=None, seed=9)
-    width, pages = (max(a.shape[i] for a in x) for x, i in (((s["table"], other["table"]), 1), ((s["kc"], other["kc"]), 0)))
+    width, pages = (max(x[key].shape[dim] for x in (s, other)) for key, dim in (("table", 1), ("kc", 0)))
 
     def grown(t, rows, dim):
         pad = torch.full_like(t, -1).narrow(dim, 0, 1).repeat_interleave(rows - t.shape[dim], dim)
