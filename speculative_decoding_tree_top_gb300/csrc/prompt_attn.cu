@@ -261,14 +261,15 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
           s_qi[i] = ++uq[i];
         };
         auto load_kv = [&](const CUtensorMap* map, int j) {
-          if (e >= kStages && !at_test(&kv_empty[st], par)) {
-            const uint64_t t0 = global_timer_ns();
-            while (!at_test(&kv_empty[st], par)) {
+          if (e >= kStages) {
+            const uint64_t t0 = pending[0] || pending[1] ? global_timer_ns() : 0;
+            while ((pending[0] || pending[1]) && !at_test(&kv_empty[st], par)) {  // whichever comes first
               load_q(0);
               load_q(1);
               if (global_timer_ns() - t0 > kAtBudgetNs) return false;
               __nanosleep(40);
             }
+            if (!at_wait(&kv_empty[st], par)) return false;
           }
           mbar_expect_tx(&kv_full[st], kTileBytes);
           for (int h = 0; h < kHalves; ++h)
