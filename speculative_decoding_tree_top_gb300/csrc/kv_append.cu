@@ -18,7 +18,7 @@
 
 #include <climits>
 
-#include "dt_internal.cuh"
+#include "attn_common.cuh"
 
 namespace dt {
 namespace {
@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendParams 
     cb = ca + 8;
   }
   const int heads = p.Hq + 2 * p.Hkv;
+  at_launch_order();
   // a token's slot and position are read while the token before it is on its way
   int t = blockIdx.x;
   int slot_next = t < p.N ? p.slots[t] : -1, pos_next = p.half && t < p.N ? p.positions[t] : 0;
@@ -261,9 +262,6 @@ extern "C" dt_status dt_kv_append(int N, int Hq, int Hkv, int d, const void* q, 
   const int threads = append_threads(Hq + 2 * Hkv, d / 16);
   const int cap = kAppendPerSm / threads * di.sms, grid = N < cap ? N : cap;
   WsHeader* hdr = static_cast<WsHeader*>(workspace);
-  if (d == 64)
-    kv_append_kernel<64><<<grid, threads, 0, stream>>>(p, hdr);
-  else
-    kv_append_kernel<128><<<grid, threads, 0, stream>>>(p, hdr);
-  return cuda_status(cudaGetLastError());
+  return d == 64 ? at_launch(kv_append_kernel<64>, grid, threads, 0, stream, p, hdr)
+                 : at_launch(kv_append_kernel<128>, grid, threads, 0, stream, p, hdr);
 }
