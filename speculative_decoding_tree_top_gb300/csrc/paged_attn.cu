@@ -13,8 +13,8 @@
 // (O, m, l) in the CTA's two partial slots (only the first and the last segment of a share can be cut), and the CTA
 // that finishes a cut pair last joins its segments in slot order, so the result does not depend on who that is.
 // Bound by memory: the key and value rows are the bytes. Measured, 32/8 heads, d = 128: one new token for 64 requests
-// of 1 to 8191, pages of 16: 163 us, 6.6 TB/s, 97% of the copy rate (1.077 GB read from DRAM for 1.074 needed); three of
-// 100001 to 131072: 203 us, 103%; 64 trees of 16 nodes over 130 to 4099: 102 us, 83% (pairs of 2 to 33 blocks: starts,
+// of 1 to 8191, pages of 16: 165 us, 6.5 TB/s, 96% of the copy rate (1.077 GB read from DRAM for 1.074 needed); three of
+// 100001 to 131072: 205 us, 102%; 64 trees of 16 nodes over 130 to 4099: 103 us, 82% (pairs of 2 to 33 blocks: starts,
 // ends and joins); one of 2049: 10 us, a chain of latencies.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -15,8 +15,8 @@
 // One CTA per SM stays for all of its items: the loads of the next item and its first scores run under the last block
 // and the epilogue of the one before. Items are dealt out longest first, from a counter in the workspace (the order
 // changes no result).
-// Measured, 32/8 heads: one prompt of 16384, d = 128: 1406 us, 1.56 PFLOP/s, 81% of cuBLAS' burst rate (tensor pipe 71%
-// active; S = Q K^T takes all of shared memory's bandwidth). 12 prompts of 33 to 2500: 206 us, 1.05 PFLOP/s (a block of
+// Measured, 32/8 heads: one prompt of 16384, d = 128: 1390 us, 1.58 PFLOP/s, 82% of cuBLAS' burst rate (tensor pipe 71%
+// active; S = Q K^T takes all of shared memory's bandwidth). 12 prompts of 33 to 2500: 205 us, 1.06 PFLOP/s (a block of
 // both tiles takes 1.5 us, an item's end and start 2). 5 prompts of 1000 to 4097, d = 64: 189 us, 0.83 PFLOP/s (issue
 // slots 65% taken, exponentials 39%, tensor pipe 39%: the softmax's own chain).
 #include <cuda_bf16.h>
