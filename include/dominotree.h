@@ -333,7 +333,8 @@ dt_status dt_paged_attention(int B, int n, int Hq, int Hkv, int d, const void* q
  *   out [total,Hq,d] bf16, dense, overlapping no input.
  *   cu_seqlens  [B+1] int32, not decreasing, within 0 .. total (a prompt may be empty). Otherwise
  *               DT_ERR_INVALID_ARG in the status word, and which rows are written is unspecified.
- *   workspace   dt_prompt_attention_workspace_bytes(total,B,Hq,Hkv,d) bytes, initialised by dt_workspace_init.
+ *   workspace   dt_prompt_attention_workspace_bytes(total,B,Hq,Hkv,d) bytes, initialised by dt_workspace_init; after
+ *               DT_ERR_TIMEOUT (dt_get_error) initialise it again.
  * ------------------------------------------------------------------------------------------------------------- */
 size_t dt_prompt_attention_workspace_bytes(int total, int B, int Hq, int Hkv, int d);
 dt_status dt_prompt_attention(int total, int B, int Hq, int Hkv, int d, const void* q, int64_t q_stride, const void* k,

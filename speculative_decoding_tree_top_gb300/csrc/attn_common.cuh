@@ -11,9 +11,9 @@
 namespace dt {
 namespace {
 
-// log2 headroom before a running maximum is raised: the weights stay below 2^64, which bf16 and fp32 hold with the same
-// relative rounding as weights below 1
-constexpr float kAtLazy = 64.f;
+// log2 headroom before a running maximum is raised: the weights stay below 2^20, which bf16 and fp32 hold with the same
+// relative rounding as weights below 1, and their products with values of up to 10^31 in size stay finite
+constexpr float kAtLazy = 20.f;
 // minus a running maximum that has seen nothing: any finite score raises it, a score of -inf has no weight under it,
 // and NaN stays
 constexpr float kAtNone = 3e38f;

@@ -13,9 +13,9 @@
 // (O, m, l) in the CTA's two partial slots (only the first and the last segment of a share can be cut), and the CTA
 // that finishes a cut pair last joins its segments in slot order, so the result does not depend on who that is.
 // Bound by memory: the key and value rows are the bytes. Measured, 32/8 heads, d = 128: one new token for 64 requests
-// of 1 to 8191, pages of 16: 165 us, 6.5 TB/s, 96% of the copy rate (1.077 GB read from DRAM for 1.074 needed); three of
-// 100001 to 131072: 205 us, 102%; 64 trees of 16 nodes over 130 to 4099: 103 us, 82% (pairs of 2 to 33 blocks: starts,
-// ends and joins); one of 2049: 10 us, a chain of latencies.
+// of 1 to 8191, pages of 16: 165 us, 6.5 TB/s, 96% of the copy rate (1.077 GB read from DRAM for 1.074 needed); three
+// of 100001 to 131072: 205 us, 102%; 64 trees of 16 nodes over 130 to 4099: 103 us, 82% (pairs of 2 to 33 blocks:
+// starts, ends and joins); one of 2049: 10 us, a chain of latencies.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -239,7 +239,7 @@ __device__ __forceinline__ unsigned long long pa_visible(int own, int end, unsig
 // softmax warps own 16 query rows each (row r = node G + head, tensor memory lane r; four neighbouring threads share
 // two rows), warps 0 and 1 clean values. Per block: S = Q K^T (M = 128, N = 128) into one of two buffers in tensor
 // memory, so that the next block's scores are computed during a block's softmax, also across segments; softmax in
-// base 2 with the running maximum raised only past a headroom of 2^64 (O is rescaled then); the weights over their
+// base 2 with the running maximum raised only past a headroom of 2^20 (O is rescaled then); the weights over their
 // scores as bf16; O += P V with P from tensor memory and V as an MN-major operand, into one of two buffers by segment.
 // Rows past R are padding and are left to whatever their rows of Q hold. A block takes the tensor cores 1024 cycles at
 // D = 128 and the softmax about as long, where its 64 KB take 2800 at the memory's rate.

@@ -8,16 +8,16 @@
 // Per tile and block: S = Q K^T (both operands in shared memory) into tensor memory, a softmax by the tile's own eight
 // warps, the weights written back as bf16 over their own scores in tensor memory, and O += P V with P read from there,
 // so that P never passes through shared memory. The tiles alternate: while one is in its softmax the tensor cores work
-// on the other. Softmax in base 2, fp32; the running maximum is raised (and O rescaled) only past a headroom of 2^64,
-// which leaves O alone in nearly every block; at d = 128 a block's weights are taken against the maximum so far while
-// its own is still being found. P is rounded to bf16, the only rounding before the output's; the row sums are taken in
-// fp32 from the unrounded weights.
+// on the other. Softmax in base 2, fp32; the running maximum is raised (and O rescaled) only past a headroom of 2^20,
+// which leaves O alone in nearly every block. A block's weights are taken against the maximum so far, at d = 128 while
+// its own is still being found, at d = 64 without it: the weights' sum shows a row that left its headroom. P is rounded
+// to bf16, the only rounding before the output's; the row sums are taken in fp32 from the unrounded weights.
 // One CTA per SM stays for all of its items: the loads of the next item and its first scores run under the last block
 // and the epilogue of the one before. Items are dealt out longest first, from a counter in the workspace (the order
 // changes no result).
 // Measured, 32/8 heads: one prompt of 16384, d = 128: 1390 us, 1.58 PFLOP/s, 82% of cuBLAS' burst rate (tensor pipe 71%
 // active; S = Q K^T takes all of shared memory's bandwidth). 12 prompts of 33 to 2500: 205 us, 1.06 PFLOP/s (a block of
-// both tiles takes 1.5 us, an item's end and start 2). 5 prompts of 1000 to 4097, d = 64: 189 us, 0.83 PFLOP/s (issue
+// both tiles takes 1.5 us, an item's end and start 2). 5 prompts of 1000 to 4097, d = 64: 180 us, 0.88 PFLOP/s (issue
 // slots 65% taken, exponentials 39%, tensor pipe 39%: the softmax's own chain).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -37,6 +37,8 @@ constexpr int kPrThreads = 640;              // warps 0-3: load, MMA, items, MMA
 constexpr int kPrSoft = 256;                 // softmax threads of a tile
 constexpr int kPrAhead = 3;                  // items that may be known ahead
 constexpr int kPrSorted = 8;                 // prompts a lane of the item warp keeps: up to 256 are dealt out sorted
+// of a thread's weights of a block and row, at most 32 of up to 2^kAtLazy: a larger sum holds a larger weight
+constexpr float kPrSumMost = 67108864.f;     // 2^26
 constexpr uint32_t kPrBox = kPrKeys * 128;   // 128 rows x 64 elements: 16 KB
 
 struct PrParams {
@@ -511,11 +513,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         float s[64];
         at_ld_s(ts, s);
-        if (kApart) {
-          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_empty[i]);
-        }
         // Apart, the weights before have been read and their products are in O only after this.
         auto p_free = [&]() {
           if (kApart && us > 0) ok = at_wait(&p_empty[i], (us - 1u) & 1u) && ok;
@@ -532,7 +529,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
         };
         if (diag) mask();
         float mx[2], alpha[2];
-        at_max(s, p.scale_log2, mx);
         auto rescale = [&]() {
           p_free();  // (not apart, S is full only after the products into O before it)
 #pragma unroll 1
@@ -544,37 +540,73 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
             at_st_o(to + 32u * h, o);
           }
         };
-        auto raised = [&]() { return __any_sync(0xFFFFFFFFu, mx[0] + nref[0] > kAtLazy || mx[1] + nref[1] > kAtLazy); };
-        if (kApart ? raised() : j == 0) {  // the first block sets the reference
-          at_raise(mx, nref, l, alpha);
-          if (kApart && j > 0) rescale();
-        }
-        // Not apart, later blocks' weights are taken against the reference so far while the maxima are being found.
         uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
-        uint32_t pk[16];
-        at_weights<0>(s, p.scale_log2, nref, ls, pk);
-        if (!kApart && j > 0 && raised()) {  // rare: take the scores and the weights again
-          at_raise(mx, nref, l, alpha);
-          rescale();
-          at_ld_s(ts, s);
-          if (diag) mask();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) ls[c] = 0ull;
-          at_weights<0>(s, p.scale_log2, nref, ls, pk);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h == 1) at_weights<1>(s, p.scale_log2, nref, ls, pk);
-          if (kApart && h == 0) p_free();
+        // half of the weights are in place: their products may start (apart, all of them start together)
+        auto give = [&](int h, const uint32_t (&pk)[16]) {
           at_st_p(tp + 32u * h, pk);
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           if (diag && h == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the cleared values
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           __syncwarp();
-          // half of the weights are in place: their products may start (apart, all of them start together)
           if (lane == 0 && (!kApart || h == 1)) mbar_arrive(&p_full[i][h]);
+        };
+        if (kApart) {
+          if (j == 0) {  // the first block sets the reference
+            at_max(s, p.scale_log2, mx);
+            at_raise(mx, nref, l, alpha);
+          }
+          // Later blocks take their weights against the reference so far; their sums show a row that left its headroom.
+          uint32_t pk[16], pk1[16];
+          at_weights<0>(s, p.scale_log2, nref, ls, pk);
+          at_weights<1>(s, p.scale_log2, nref, ls, pk1);
+          float sum[2] = {0.f, 0.f};
+          at_sums(ls, sum);
+          if (__any_sync(0xFFFFFFFFu, !(sum[0] <= kPrSumMost && sum[1] <= kPrSumMost))) {  // rare (or NaN)
+            at_ld_s(ts, s);
+            if (diag) mask();
+            at_max(s, p.scale_log2, mx);
+            at_raise(mx, nref, l, alpha);
+            if (j > 0) rescale();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ls[c] = 0ull;
+            at_weights<0>(s, p.scale_log2, nref, ls, pk);
+            at_weights<1>(s, p.scale_log2, nref, ls, pk1);
+            sum[0] = sum[1] = 0.f;
+            at_sums(ls, sum);
+          }
+          if (kApart) {
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[i]);
+            p_free();
+          }
+          l[0] += sum[0];
+          l[1] += sum[1];
+          give(0, pk);
+          give(1, pk1);
+        } else {
+          at_max(s, p.scale_log2, mx);
+          auto raised = [&]() {
+            return __any_sync(0xFFFFFFFFu, mx[0] + nref[0] > kAtLazy || mx[1] + nref[1] > kAtLazy);
+          };
+          if (j == 0) at_raise(mx, nref, l, alpha);  // the first block sets the reference
+          // Later blocks' weights are taken against the reference so far while the maxima are being found.
+          uint32_t pk[16];
+          at_weights<0>(s, p.scale_log2, nref, ls, pk);
+          if (j > 0 && raised()) {  // rare: take the scores and the weights again
+            at_raise(mx, nref, l, alpha);
+            rescale();
+            at_ld_s(ts, s);
+            if (diag) mask();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ls[c] = 0ull;
+            at_weights<0>(s, p.scale_log2, nref, ls, pk);
+          }
+          give(0, pk);
+          at_weights<1>(s, p.scale_log2, nref, ls, pk);
+          give(1, pk);
+          at_sums(ls, l);
         }
-        at_sums(ls, l);
         ok = __all_sync(0xFFFFFFFFu, ok);
       }
       if (!ok) break;

@@ -103,6 +103,25 @@ def test_the_most_heads(dtlib, Hq, Hkv):
     prompt.parity(dtlib, prompt.make([140, 300], Hq, Hkv, 64), heads=[0, 1, Hq // 2, Hq - 1])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_values_under_growing_scores(dtlib, d):
+    """Values of 10^30 under scores that grow along the sequence by less than what raises the running maximum at once:
+    the weights above the first block's maximum times the values stay finite."""
+    grow = lambda n: torch.linspace(0, 2, n, device="cuda")[:, None, None]
+    s = prompt.make([900], 4, 2, d, fused=False, spread=0.02)
+    s["q"][..., 0], s["k"][..., 0] = 4.0, (grow(900) * math.sqrt(d))[..., 0].to(BF)
+    s["v"] *= 1e30
+    prompt.parity(dtlib, s)
+    p = paged.make([1500, 300], 2, 8, 2, d, 16, mask="tree", spread=0.02)
+    p["q"][..., 0] = 4.0
+    for b in range(2):
+        n = int(p["lens"][b])
+        for i in range(-(-n // 16)):
+            p["kc"][p["table"][b, i].long(), :, :, 0] = float(grow(n)[16 * i] * math.sqrt(d))
+            p["vc"][p["table"][b, i].long()] *= 1e30
+    paged.parity(dtlib, p)
+
+
 def test_prompt_rows_past_two_to_the_31_elements(dtlib):
     n, count, Hq, Hkv, d = 5000, 108, 32, 1, 128
     total = n * count
