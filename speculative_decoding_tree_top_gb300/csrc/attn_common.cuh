@@ -121,7 +121,7 @@ __device__ __forceinline__ void at_ld_o(uint32_t taddr, float (&v)[16]) {  // 4 
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void at_st_o(uint32_t taddr, const float* v) {  // 4 groups, as pr_ld holds them
+__device__ __forceinline__ void at_st_o(uint32_t taddr, const float* v) {  // 4 groups, as at_ld_o holds them
   asm volatile(
       "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
       ::"r"(taddr),
