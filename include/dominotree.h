@@ -27,6 +27,10 @@
  *     dt_build_trees keeps its own region after the one dt_topm uses, so a workspace of
  *     dt_build_workspace_bytes(...) bytes serves both calls of a round when they are ordered on one stream. Two
  *     calls that may run concurrently need two workspaces.
+ *     dt_kv_append, dt_paged_attention, dt_prompt_attention and dt_tree_attention find nothing in a workspace but its
+ *     first 256 bytes, and leave those as they found them: one workspace of the largest size serves them all, in any
+ *     order on one stream. The other calls (dt_topm, the builders, dt_lmhead_topm) rely on more: a workspace that
+ *     another kind of call has used is initialised again before it serves one of them.
  *   - No C++ exception crosses this boundary. The calls are thread-safe for distinct workspaces.
  */
 #ifndef DOMINOTREE_H

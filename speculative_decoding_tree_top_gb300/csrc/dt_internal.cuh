@@ -8,6 +8,8 @@
 
 namespace dt {
 
+constexpr int kWsTickets = 192;  // most CTAs whose pairs dt_paged_attention may cut
+
 // Every workspace starts with this 256-byte header. It is zeroed once (dt_workspace_init); kernels leave it zeroed
 // again except for `status`, which holds the first device-side problem until dt_get_error clears it.
 struct WsHeader {
@@ -24,7 +26,8 @@ struct WsHeader {
   unsigned stat_waves;                  // waves run
   unsigned stat_expansions;             // expansions computed (the roots included)
   unsigned deal_next, deal_done;        // dt_prompt_attention: items dealt out, CTAs through (zero between calls)
-  unsigned reserved[48];
+  unsigned tickets[kWsTickets / 4];     // dt_paged_attention: by a cut pair's first CTA, a byte each: segments finished
+                                        // (zero between calls)
 };
 static_assert(sizeof(WsHeader) == 256, "workspace header is 256 bytes");
 

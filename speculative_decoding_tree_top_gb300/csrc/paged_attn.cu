@@ -47,7 +47,6 @@ struct PaParams {
   float scale_log2;                // scale * log2(e)
   float* part;                     // [grid][2][R][D] unnormalised outputs of cut segments
   float* ml;                       // [grid][2][R][2] running maximum (base 2) and sum
-  unsigned* tickets;               // [grid] by a cut pair's first CTA: segments finished; zero between calls
   unsigned short* out;             // [B][n][Hq][D] bf16
 };
 struct PaMaps {
@@ -667,9 +666,11 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
       ok = pa_sync(&s_meet, meet, lane);  // the ticket's release covers what the other warps wrote before it
       if (!ok) break;
       if (t == 128) {
-        const unsigned done = atom_add_acq_rel_gpu(p.tickets + c0, 1u) + 1u;
+        // a pair's ticket is a byte: it counts to the grid at most, and goes back to zero before it is used again
+        const int shift = 8 * (c0 & 3);
+        const unsigned done = ((atom_add_acq_rel_gpu(hdr->tickets + c0 / 4, 1u << shift) >> shift) & 0xFFu) + 1u;
         if (done == static_cast<unsigned>(c1 - c0 + 1)) {
-          p.tickets[c0] = 0u;  // ready for the next call
+          atomicSub(hdr->tickets + c0 / 4, done << shift);  // ready for the next call
           s_join[s_joins++] = PaJoin{sg.b, sg.kvh, c0, c1};
         }
       }
@@ -697,13 +698,12 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
 
 struct PaPlan {
   int grid;
-  size_t tickets, part, ml, bytes;
+  size_t part, ml, bytes;  // behind the header nothing outlives a call
 };
 inline PaPlan pa_plan(int R, int d, int sms) {
   PaPlan P{};
-  P.grid = sms;
-  P.tickets = align_up(sizeof(WsHeader));
-  P.part = align_up(P.tickets + sizeof(unsigned) * P.grid);
+  P.grid = sms < kWsTickets ? sms : kWsTickets;
+  P.part = align_up(sizeof(WsHeader));
   P.ml = align_up(P.part + sizeof(float) * 2 * P.grid * static_cast<size_t>(R) * d);
   P.bytes = align_up(P.ml + sizeof(float) * 2 * 2 * P.grid * static_cast<size_t>(R));
   return P;
@@ -770,7 +770,6 @@ extern "C" dt_status dt_paged_attention(int B, int n, int Hq, int Hkv, int d, co
   p.page_table = page_table; p.lens = lens; p.mask = mask;
   p.scale_log2 = scale * 1.4426950408889634f;
   char* ws = static_cast<char*>(workspace);
-  p.tickets = reinterpret_cast<unsigned*>(ws + P.tickets);
   p.part = reinterpret_cast<float*>(ws + P.part);
   p.ml = reinterpret_cast<float*>(ws + P.ml);
   p.out = static_cast<unsigned short*>(out);
