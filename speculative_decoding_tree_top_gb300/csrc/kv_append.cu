@@ -18,12 +18,12 @@
 
 #include <climits>
 
+#include "append_shape.cuh"
 #include "attn_common.cuh"
 
 namespace dt {
 namespace {
 
-constexpr int kAppendThreads = 256;   // at most
 constexpr int kAppendPerSm = 2048;    // threads per SM that the grid is sized to: half again what fits (48 registers)
 
 struct AppendParams {
@@ -194,19 +194,6 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendParams 
       }
     }
   }
-}
-
-// The CTA's threads: whole warps, the size whose passes over a token's heads leave the fewest threads idle.
-inline int append_threads(int heads, int items) {
-  int best = kAppendThreads, best_idle = INT_MAX;
-  for (int threads = kAppendThreads; threads >= 64; threads -= 32) {
-    const int step = threads / items, passes = (heads + step - 1) / step, idle = passes * step - heads;
-    if (idle * best < best_idle * threads || best_idle == INT_MAX) {
-      best = threads;
-      best_idle = idle;
-    }
-  }
-  return best;
 }
 
 }  // namespace
