@@ -308,7 +308,8 @@ dt_status dt_kv_append(int N, int Hq, int Hkv, int d, const void* q, int64_t q_s
  * tokens up to its own (t <= i). out[b][i][h] = sum_j softmax_j(scale * q[b][i][h] . k_j) v_j over them, query head h
  * reading key/value head h / (Hq / Hkv); a node that sees nothing gets zeros. Arithmetic as dt_tree_attention (bf16
  * products, fp32 accumulation, softmax weights rounded to bf16), the output rounded to bf16 once. Keys and values that
- * a node does not see do not reach its output, finite or not.
+ * a node does not see do not reach its output, finite or not. Values of up to 10^30 in size give finite outputs at every
+ * length (larger ones may overflow fp32 in the sums over the keys).
  *   q           [B,n,Hq,d] bf16; out [B,n,Hq,d] bf16.
  *   page_table  [B,max_pages] int32; entries past a request's last page are not read.
  *   lens        [B] int32, in n .. max_pages * page_size. lens[b] <= 0 marks an unused row of the batch: its output is
@@ -331,8 +332,8 @@ dt_status dt_paged_attention(int B, int n, int Hq, int Hkv, int d, const void* q
  *
  * Semantics: prompt b is rows cu_seqlens[b] .. cu_seqlens[b+1] - 1; its row i sees its rows 0..i:
  * out[row][h] = sum_j softmax_j(scale * q[row][h] . k_j) v_j, query head h reading key/value head h / (Hq / Hkv).
- * Arithmetic as dt_paged_attention; what a row does not see (later rows, other prompts) does not reach its output,
- * finite or not. Rows before cu_seqlens[0] and from cu_seqlens[B] on are left as they were.
+ * Arithmetic and range of values as dt_paged_attention; what a row does not see (later rows, other prompts) does not
+ * reach its output, finite or not. Rows before cu_seqlens[0] and from cu_seqlens[B] on are left as they were.
  *   q [total,Hq,d], k, v [total,Hkv,d] bf16, rows q_stride, k_stride, v_stride elements apart as in dt_kv_append;
  *   out [total,Hq,d] bf16, dense, overlapping no input.
  *   cu_seqlens  [B+1] int32, not decreasing, within 0 .. total (a prompt may be empty). Otherwise

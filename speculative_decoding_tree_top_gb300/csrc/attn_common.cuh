@@ -11,11 +11,17 @@
 namespace dt {
 namespace {
 
-// log2 headroom before a running maximum is raised: the weights stay below 2^20, which bf16 and fp32 hold with the same
-// relative rounding as weights below 1, and their products with values of up to 10^31 in size stay finite
-constexpr float kAtLazy = 20.f;
-// minus a running maximum that has seen nothing: any finite score raises it, a score of -inf has no weight under it,
-// and NaN stays
+// Weights are powers of two relative to a reference: a row's maximum as last raised, and 2^kAtShift more, so that they
+// start out at 2^-26 and a row's later keys may exceed the maximum by a headroom of 2^kAtLazy before it is raised. bf16
+// and fp32 hold such weights with the relative rounding of weights below 1. The shift makes room for the sums: of
+// 2^24 keys of weight 2^kAtMost with values of 2^100 (10^30) in size they stay finite in fp32, and products of weights
+// with values of 2^-100 are normal numbers still.
+constexpr float kAtLazy = 20.f, kAtShift = 26.f, kAtMost = kAtLazy - kAtShift;
+constexpr double kAtValueMost = 1e30;  // as the public header states it
+constexpr double kAtWeightMost = 1.0 / 64;
+static_assert(kAtMost == -6.f, "log2 of kAtWeightMost");
+// minus a reference that has seen nothing: any finite score raises it, a score of -inf has no weight under it, and NaN
+// stays
 constexpr float kAtNone = 3e38f;
 constexpr uint64_t kAtBudgetNs = 4000000000ull;
 
@@ -152,17 +158,18 @@ __device__ __forceinline__ void at_max(const float (&s)[64], float scale, float 
     mx[k2] = fmaxf(u, w) * scale;
   }
 }
-// Raises the running maxima of a warp's rows (nref: minus them) where a block's exceed them by more than the headroom;
-// alpha: what the sums and outputs so far are multiplied by.
+// Raises the references of a warp's rows (nref: minus them) where a block's maxima leave the headroom; alpha: what the
+// sums and outputs so far are multiplied by.
 __device__ __forceinline__ void at_raise(float (&mx)[2], float (&nref)[2], float (&l)[2], float (&alpha)[2]) {
 #pragma unroll
   for (int k2 = 0; k2 < 2; ++k2) {
     mx[k2] = fmaxf(mx[k2], __shfl_xor_sync(0xFFFFFFFFu, mx[k2], 1));
     mx[k2] = fmaxf(mx[k2], __shfl_xor_sync(0xFFFFFFFFu, mx[k2], 2));
-    const bool raise = mx[k2] + nref[k2] > kAtLazy;
-    alpha[k2] = raise ? at_exp2(-nref[k2] - mx[k2]) : 1.f;  // from nothing: 0
+    const bool raise = mx[k2] + nref[k2] > kAtMost;
+    const float to = -mx[k2] - kAtShift;
+    alpha[k2] = raise ? at_exp2(to - nref[k2]) : 1.f;  // from nothing: 0
     l[k2] *= alpha[k2];
-    if (raise) nref[k2] = -mx[k2];
+    if (raise) nref[k2] = to;
   }
 }
 // The weights of half a block (64 keys), rounded to bf16 pairs; their sums are taken before the rounding.

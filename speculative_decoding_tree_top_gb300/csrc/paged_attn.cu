@@ -35,6 +35,7 @@ constexpr int kPaMaxStages = 12;
 constexpr int kPaCleans = 8;      // barriers of cleaned blocks: more than the ring can hold
 constexpr uint32_t kPaBox = kPaKeys * 128;  // 128 rows x 64 elements: 16 KB
 constexpr size_t kPaSmemCap = 232448 - 5120;  // opt-in shared memory of a CTA, less the static part
+static_assert(kAtWeightMost * kAtValueMost * DT_PAGED_MAX_TOKENS < 1e38, "a request's weighted values have a sum");
 
 struct PaParams {
   int B, n, Hq, Hkv, G, R, grid, stages;
@@ -46,7 +47,7 @@ struct PaParams {
   const uint8_t* mask;             // [B][n][n] or null: causal among the n
   float scale_log2;                // scale * log2(e)
   float* part;                     // [grid][2][R][D] unnormalised outputs of cut segments
-  float* ml;                       // [grid][2][R][2] running maximum (base 2) and sum
+  float* ml;                       // [grid][2][R][2] the weights' reference (base 2) and their sum
   unsigned short* out;             // [B][n][Hq][D] bf16
 };
 struct PaMaps {
@@ -568,7 +569,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
         }
         float mx[2];
         at_max(s, p.scale_log2, mx);
-        if (__any_sync(0xFFFFFFFFu, mx[0] + nref[0] > kAtLazy || mx[1] + nref[1] > kAtLazy)) {  // rare: rescale O
+        if (__any_sync(0xFFFFFFFFu, mx[0] + nref[0] > kAtMost || mx[1] + nref[1] > kAtMost)) {  // rare: rescale O
           float alpha[2];
           at_raise(mx, nref, l, alpha);
           if (j > 0) {

@@ -8,10 +8,11 @@
 // Per tile and block: S = Q K^T (both operands in shared memory) into tensor memory, a softmax by the tile's own eight
 // warps, the weights written back as bf16 over their own scores in tensor memory, and O += P V with P read from there,
 // so that P never passes through shared memory. The tiles alternate: while one is in its softmax the tensor cores work
-// on the other. Softmax in base 2, fp32; the running maximum is raised (and O rescaled) only past a headroom of 2^20,
-// which leaves O alone in nearly every block. A block's weights are taken against the maximum so far, at d = 128 while
-// its own is still being found, at d = 64 without it: the weights' sum shows a row that left its headroom. P is rounded
-// to bf16, the only rounding before the output's; the row sums are taken in fp32 from the unrounded weights.
+// on the other. Softmax in base 2, fp32; the running maximum is raised (and O rescaled) only past a headroom of 2^20
+// (at d = 64 of up to 2^26), which leaves O alone in nearly every block. A block's weights are taken against the maximum
+// so far, at d = 128 while its own is still being found, at d = 64 without it: the weights' sum shows a row that left its
+// headroom. P is rounded to bf16, the only rounding before the output's (the tensor cores want it in the values' type);
+// the row sums are taken in fp32 from the unrounded weights.
 // One CTA per SM stays for all of its items: the loads of the next item and its first scores run under the last block
 // and the epilogue of the one before. Items are dealt out longest first, from a counter in the workspace (the order
 // changes no result).
@@ -37,8 +38,13 @@ constexpr int kPrThreads = 640;              // warps 0-3: load, MMA, items, MMA
 constexpr int kPrSoft = 256;                 // softmax threads of a tile
 constexpr int kPrAhead = 3;                  // items that may be known ahead
 constexpr int kPrSorted = 8;                 // prompts a lane of the item warp keeps: up to 256 are dealt out sorted
-// of a thread's weights of a block and row, at most 32 of up to 2^kAtLazy: a larger sum holds a larger weight
-constexpr float kPrSumMost = 67108864.f;     // 2^26
+// Of a thread's weights of a block and row, 32 at most, of up to 2^-6: a larger sum holds a larger weight. (A weight may
+// come near 1 before that.)
+constexpr float kPrSumMost = 1.f;
+static_assert(32 * kAtWeightMost <= kPrSumMost, "a sum that is taken again raises the reference");
+// the longest packed batch (2^30 rows), in blocks of 128 keys of four threads' sums, and the others' weights
+static_assert(4 * kPrSumMost * kAtValueMost * (INT_MAX / 2 / 128) < 3e38, "a row's weighted values have a sum");
+static_assert(kAtWeightMost * kAtValueMost * (INT_MAX / 2) < 3e38, "a row's weighted values have a sum");
 constexpr uint32_t kPrBox = kPrKeys * 128;   // 128 rows x 64 elements: 16 KB
 
 struct PrParams {
@@ -469,7 +475,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
       if (it.len == 0) break;
       const int nb = i ? it.n1() : it.n0();
       const int row0 = it.q0 + i * kPrTile + ra;  // row ra's token in its prompt; the other row's is 8 further
-      // minus the running maximum of the scaled scores, as last raised
+      // minus the weights' reference: the running maximum of the scaled scores, as last raised, and kAtShift
       float nref[2] = {kAtNone, kAtNone};
       float l[2] = {0.f, 0.f};                    // sums of this thread's weights
       for (int j = 0; j < nb && ok; ++j, ++us) {
@@ -587,7 +593,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
         } else {
           at_max(s, p.scale_log2, mx);
           auto raised = [&]() {
-            return __any_sync(0xFFFFFFFFu, mx[0] + nref[0] > kAtLazy || mx[1] + nref[1] > kAtLazy);
+            return __any_sync(0xFFFFFFFFu, mx[0] + nref[0] > kAtMost || mx[1] + nref[1] > kAtMost);
           };
           if (j == 0) at_raise(mx, nref, l, alpha);  // the first block sets the reference
           // Later blocks' weights are taken against the reference so far while the maxima are being found.
