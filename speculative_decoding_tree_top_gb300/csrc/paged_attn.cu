@@ -160,10 +160,9 @@ template <int D>
 __device__ __forceinline__ void pa_join_out(const PaParams& p, const PaJoin& jn, int i, const PaSum& s) {
   constexpr int kQuads = D / 4;
   const int r = i / kQuads, node = r / p.G;
-  bool none = s.den == 0.f && p.mask && p.lens[jn.b] == p.n;  // no prefix: perhaps no visible key at all
-  if (none)
-    for (int c = 0; c < p.n; ++c) none = none && p.mask[(static_cast<size_t>(jn.b) * p.n + node) * p.n + c] == 0;
-  const float inv = none ? 0.f : 1.f / s.den;
+  // a cut pair has two blocks at least, and so a prefix that every node sees
+  static_assert(kPaNodes < kPaKeys, "the nodes' own keys fill no block");
+  const float inv = 1.f / s.den;
   unsigned short* o =
       p.out + ((static_cast<size_t>(jn.b) * p.n + node) * p.Hq + jn.kvh * p.G + r % p.G) * D + 4 * (i % kQuads);
   *reinterpret_cast<uint2*>(o) =

@@ -580,12 +580,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_attn_kernel(PrParams p, 
             sum[0] = sum[1] = 0.f;
             at_sums(ls, sum);
           }
-          if (kApart) {
-            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_empty[i]);
-            p_free();
-          }
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_empty[i]);
+          p_free();
           l[0] += sum[0];
           l[1] += sum[1];
           give(0, pk);
