@@ -248,16 +248,21 @@ __device__ __forceinline__ bool at_test(uint64_t* bar, unsigned parity) {
   return done != 0;
 }
 // Waits until the loader has issued more than `e` ring entries (its count, in shared memory). A waiter that skips
-// entries calls this before it waits for entry e's phase: by then the phase before, of the other parity, is over.
+// entries calls this before it waits for entry e's phase: by then the phase before, of the other parity, is over. It may
+// have skipped a whole share (many long caches that end with a block), so the time runs from the loader's last step.
 __device__ __forceinline__ bool at_issued(const unsigned* count, unsigned e) {
   const volatile unsigned* seen = count;
-  if (*seen > e) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (*seen <= e) {
+  unsigned now = *seen;
+  if (now > e) return true;
+  uint64_t t0 = global_timer_ns();
+  while (true) {
+    const unsigned was = now;
+    now = *seen;
+    if (now > e) return true;
+    if (now != was) t0 = global_timer_ns();
     if (global_timer_ns() - t0 > kAtBudgetNs) return false;
     __nanosleep(100);
   }
-  return true;
 }
 
 }  // namespace
