@@ -281,7 +281,7 @@ dt_status dt_tree_attention(int B, int n, int L, int Hq, int Hkv, int d, const v
  *   q [N,Hq,d], k, v [N,Hkv,d] bf16, tokens q_stride, k_stride, v_stride elements apart (multiples of 8, at least a
  *               token's width: views of one fused projection's output serve). No queries: Hq = 0, q = out_q = NULL.
  *   slots       [N] int32: where each token goes. A negative slot marks a padding token: nothing of it is read or
- *               written. Slots are distinct (of two tokens that name one slot, which is kept is unspecified).
+ *               written. Slots are distinct (a row that two tokens name may end up as a mix of them).
  *   positions   [N] int32 and rope [max_pos, rot] fp32 (a position's rot / 2 cosines, then its sines), any frequency
  *               schedule; NULL when rot = 0 (nothing is rotated). A draft tree's node has the position of its depth,
  *               whatever its slot.
@@ -310,7 +310,7 @@ dt_status dt_kv_append(int N, int Hq, int Hkv, int d, const void* q, int64_t q_s
  * products, fp32 accumulation, softmax weights rounded to bf16), the output rounded to bf16 once. Keys and values that
  * a node does not see do not reach its output, finite or not. Values of up to 10^30 in size give finite outputs at every
  * length (larger ones may overflow fp32 in the sums over the keys).
- *   q           [B,n,Hq,d] bf16; out [B,n,Hq,d] bf16.
+ *   q           [B,n,Hq,d] bf16; out [B,n,Hq,d] bf16, overlapping no input.
  *   page_table  [B,max_pages] int32; entries past a request's last page are not read.
  *   lens        [B] int32, in n .. max_pages * page_size. lens[b] <= 0 marks an unused row of the batch: its output is
  *               zero. Other lengths, and pages outside the pool, set DT_ERR_INVALID_ARG in the status word; such a

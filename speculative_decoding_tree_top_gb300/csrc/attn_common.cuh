@@ -248,8 +248,8 @@ __device__ __forceinline__ bool at_test(uint64_t* bar, unsigned parity) {
   return done != 0;
 }
 // Waits until the loader has issued more than `e` ring entries (its count, in shared memory). A waiter that skips
-// entries calls this before it waits for entry e's phase: by then the phase before, of the other parity, is over. It may
-// have skipped a whole share (many long caches that end with a block), so the time runs from the loader's last step.
+// entries calls this before it waits for entry e's phase: by then the phase before, of the other parity, is over. It
+// may have skipped a whole share (many long caches that end with a block): the time runs from the loader's last step.
 __device__ __forceinline__ bool at_issued(const unsigned* count, unsigned e) {
   const volatile unsigned* seen = count;
   unsigned now = *seen;

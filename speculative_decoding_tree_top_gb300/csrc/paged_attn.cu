@@ -15,7 +15,9 @@
 // Bound by memory: the key and value rows are the bytes. Measured, 32/8 heads, d = 128: one new token for 64 requests
 // of 1 to 8191, pages of 16: 165 us, 6.5 TB/s, 96% of the copy rate (1.077 GB read from DRAM for 1.074 needed); three
 // of 100001 to 131072: 205 us, 102%; 64 trees of 16 nodes over 130 to 4099: 103 us, 82% (pairs of 2 to 33 blocks:
-// starts, ends and joins); one of 2049: 10 us, a chain of latencies.
+// starts, ends and joins); one of 2049: 10 us, a chain of latencies. d = 64: the same 64 requests 91 us with pages of
+// 64 (5.9 TB/s, 87%) and 122 with pages of 16, whose 16 copies of 2 KB a block take longer than their bytes; the three
+// long ones 111 (6.4 TB/s, 94%); the trees 69 (4.1 TB/s, 61%: starts, ends and joins cost what they do at d = 128).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

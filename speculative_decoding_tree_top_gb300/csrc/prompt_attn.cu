@@ -9,17 +9,17 @@
 // warps, the weights written back as bf16 over their own scores in tensor memory, and O += P V with P read from there,
 // so that P never passes through shared memory. The tiles alternate: while one is in its softmax the tensor cores work
 // on the other. Softmax in base 2, fp32; the running maximum is raised (and O rescaled) only past a headroom of 2^20
-// (at d = 64 of up to 2^26), which leaves O alone in nearly every block. A block's weights are taken against the maximum
-// so far, at d = 128 while its own is still being found, at d = 64 without it: the weights' sum shows a row that left its
-// headroom. P is rounded to bf16, the only rounding before the output's (the tensor cores want it in the values' type);
-// the row sums are taken in fp32 from the unrounded weights.
+// (at d = 64 of up to 2^26), which leaves O alone in nearly every block. A block's weights are taken against the
+// maximum so far, at d = 128 while its own is still being found, at d = 64 without it: the weights' sum shows a row that
+// left its headroom. P is rounded to bf16, the only rounding before the output's (the tensor cores want it in the
+// values' type); the row sums are taken in fp32 from the unrounded weights.
 // One CTA per SM stays for all of its items: the loads of the next item and its first scores run under the last block
 // and the epilogue of the one before. Items are dealt out longest first, from a counter in the workspace (the order
 // changes no result).
-// Measured, 32/8 heads: one prompt of 16384, d = 128: 1390 us, 1.58 PFLOP/s, 82% of cuBLAS' burst rate (tensor pipe 71%
+// Measured, 32/8 heads: one prompt of 16384, d = 128: 1390 us, 1.58 PFLOP/s, 82% of cuBLAS' burst rate (tensor pipe 72%
 // active; S = Q K^T takes all of shared memory's bandwidth). 12 prompts of 33 to 2500: 205 us, 1.06 PFLOP/s (a block of
 // both tiles takes 1.5 us, an item's end and start 2). 5 prompts of 1000 to 4097, d = 64: 180 us, 0.88 PFLOP/s (issue
-// slots 65% taken, exponentials 39%, tensor pipe 39%: the softmax's own chain).
+// slots 63% taken, exponentials 41%, tensor pipe 41%: the softmax's own chain).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -38,8 +38,8 @@ constexpr int kPrThreads = 640;              // warps 0-3: load, MMA, items, MMA
 constexpr int kPrSoft = 256;                 // softmax threads of a tile
 constexpr int kPrAhead = 3;                  // items that may be known ahead
 constexpr int kPrSorted = 8;                 // prompts a lane of the item warp keeps: up to 256 are dealt out sorted
-// Of a thread's weights of a block and row, 32 at most, of up to 2^-6: a larger sum holds a larger weight. (A weight may
-// come near 1 before that.)
+// Of a thread's weights of a block and row, 32 at most, of up to 2^-6: a larger sum holds a larger weight. (A weight
+// may come near 1 before that.)
 constexpr float kPrSumMost = 1.f;
 static_assert(32 * kAtWeightMost <= kPrSumMost, "a sum that is taken again raises the reference");
 // the longest packed batch (2^30 rows), in blocks of 128 keys of four threads' sums, and the others' weights
