@@ -20,6 +20,7 @@
 
 #include "append_shape.cuh"
 #include "attn_common.cuh"
+#include "rotate.cuh"
 
 namespace dt {
 namespace {
@@ -35,56 +36,6 @@ struct AppendParams {
   const float* rope;  // [max_pos][2 half]: cosines, then sines
   unsigned short *out_q, *out_k, *k_cache, *v_cache;
 };
-
-struct Eight {  // eight bf16 as fp32
-  float x[8];
-};
-__device__ __forceinline__ Eight unpack8(uint4 u) {
-  Eight e;
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    e.x[2 * i] = __uint_as_float(w[i] << 16);
-    e.x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-  return e;
-}
-__device__ __forceinline__ uint4 pack8(const Eight& e) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(e.x[2 * i], e.x[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// The cosines and sines of an item's columns, and its rotation. Half-split pairs: group A holds pairs c..c+7's first
-// elements and group B their second ones. Interleaved: each group holds four whole pairs.
-struct Turn {
-  float c[8], s[8];
-};
-__device__ __forceinline__ void turn_halves(uint4& a, uint4& b, const Turn& t) {
-  Eight x = unpack8(a), y = unpack8(b);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float u = x.x[i] * t.c[i] - y.x[i] * t.s[i], w = y.x[i] * t.c[i] + x.x[i] * t.s[i];
-    x.x[i] = u;
-    y.x[i] = w;
-  }
-  a = pack8(x);
-  b = pack8(y);
-}
-__device__ __forceinline__ void turn_pairs(uint4& a, const float* c, const float* s) {
-  Eight x = unpack8(a);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float u = x.x[2 * i] * c[i] - x.x[2 * i + 1] * s[i], w = x.x[2 * i + 1] * c[i] + x.x[2 * i] * s[i];
-    x.x[2 * i] = u;
-    x.x[2 * i + 1] = w;
-  }
-  a = pack8(x);
-}
 
 // A head's part of a token: where its item comes from and goes to.
 struct AppendHead {
@@ -116,20 +67,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendParams 
   constexpr int kItems = D / 16;                                  // items per head
   const int step = static_cast<int>(blockDim.x) / kItems;         // heads a pass of the CTA covers
   const int item = threadIdx.x % kItems, head0 = threadIdx.x / kItems;
-  // The item's two groups of eight columns. Within the rotated part of a half-split head they are a pair's two
-  // halves; otherwise two neighbouring groups (half is a multiple of 8: a group is rotated as a whole or not at all).
-  const bool halves = !p.interleaved && 8 * item < p.half;
-  int ca, cb;
-  if (p.interleaved) {
-    ca = 16 * item;
-    cb = ca + 8;
-  } else if (halves) {
-    ca = 8 * item;
-    cb = ca + p.half;
-  } else {  // the columns past rot = 2 half: items half / 8 .. kItems - 1 take 16 each
-    ca = 2 * p.half + 16 * (item - p.half / 8);
-    cb = ca + 8;
-  }
+  const TurnCols cols = turn_cols(item, p.half, p.interleaved);
+  const bool halves = cols.halves;
+  const int ca = cols.ca, cb = cols.cb;
   const int heads = p.Hq + 2 * p.Hkv;
   at_launch_order();
   // a token's slot and position are read while the token before it is on its way
@@ -148,32 +88,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendParams 
       continue;
     }
     Turn tu;
-    if (p.half) {
-      const float* row = p.rope + static_cast<size_t>(pos) * (2 * p.half);
-      auto four = [](const float* from, float* to) {
-        const float4 x = *reinterpret_cast<const float4*>(from);
-        to[0] = x.x;
-        to[1] = x.y;
-        to[2] = x.z;
-        to[3] = x.w;
-      };
-      if (p.interleaved) {
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {  // pairs 8 item + 4 g .. + 3 (half is a multiple of 8)
-          const int pr = 8 * item + 4 * g;
-          if (pr < p.half) {
-            four(row + pr, tu.c + 4 * g);
-            four(row + p.half + pr, tu.s + 4 * g);
-          }
-        }
-      } else if (halves) {
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          four(row + 8 * item + 4 * g, tu.c + 4 * g);
-          four(row + p.half + 8 * item + 4 * g, tu.s + 4 * g);
-        }
-      }
-    }
+    if (p.half) load_turn(p.rope + static_cast<size_t>(pos) * (2 * p.half), item, p.half, p.interleaved, halves, tu);
     const size_t row = static_cast<size_t>(slot / p.page_size) * p.Hkv * p.page_size + slot % p.page_size;
     for (int h = head0; h < heads; h += step) {
       const AppendHead hd = append_head<D>(p, t, h, row);

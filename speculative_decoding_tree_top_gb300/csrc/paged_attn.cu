@@ -25,32 +25,21 @@
 #include <cmath>
 
 #include "attn_common.cuh"
+#include "paged_share.cuh"
 
 namespace dt {
 namespace {
 
-constexpr int kPaRows = 128;      // query rows per pair: G n at most
-constexpr int kPaNodes = 64;      // n at most (a node's mask row is one 64-bit word)
-constexpr int kPaKeys = 128;      // keys per block
 constexpr int kPaThreads = 384;   // warps 0, 1: values kept from the tensor cores; 2: load; 3: MMA; 4-11: softmax
 constexpr int kPaMaxStages = 12;
 constexpr int kPaCleans = 8;      // barriers of cleaned blocks: more than the ring can hold
 constexpr uint32_t kPaBox = kPaKeys * 128;  // 128 rows x 64 elements: 16 KB
-constexpr size_t kPaSmemCap = 232448 - 5120;  // opt-in shared memory of a CTA, less the static part
-static_assert(kAtWeightMost * kAtValueMost * DT_PAGED_MAX_TOKENS < 1e38, "a request's weighted values have a sum");
 
-struct PaParams {
-  int B, n, Hq, Hkv, G, R, grid, stages;
-  int page_size, num_pages, max_pages;
+struct PaParams : PaWork {
+  int stages;
   uint32_t q_box;                  // one 64-element box of Q: rows rounded up to 8, x 128 bytes
   const unsigned short* v_cache;   // [num_pages][Hkv][page_size][D], re-read only for values that are not finite
-  const int32_t* page_table;       // [B][max_pages]
-  const int32_t* lens;             // [B]
-  const uint8_t* mask;             // [B][n][n] or null: causal among the n
   float scale_log2;                // scale * log2(e)
-  float* part;                     // [grid][2][R][D] unnormalised outputs of cut segments
-  float* ml;                       // [grid][2][R][2] the weights' reference (base 2) and their sum
-  unsigned short* out;             // [B][n][Hq][D] bf16
 };
 struct PaMaps {
   CUtensorMap q;     // [B][n][Hq][D], box 64 x G x n x 1
@@ -66,174 +55,6 @@ __device__ __forceinline__ bool pa_sync(uint64_t* bar, unsigned& count, int lane
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
   return __all_sync(0xFFFFFFFFu, at_wait(bar, count++ & 1u));
-}
-
-// The lengths' plan. cum[b]: units of one head of the requests before b, a request's being its 128-key blocks and one
-// more; a request whose length is not in [n, max_pages * page_size] has none (0 and below: an unused row of the batch;
-// otherwise an error).
-__device__ __forceinline__ int pa_length(const PaParams& p, int b, bool* bad) {
-  const int len = p.lens[b];
-  if (len <= 0) return 0;
-  if (len < p.n || len > static_cast<long long>(p.max_pages) * p.page_size) {
-    *bad = true;
-    return 0;
-  }
-  return len;
-}
-// CTA c's share of W units starts here; the CTA whose share holds unit x. (A 64-bit division takes half a microsecond
-// on the way to the first load; a batch's units nearly always fit 32 bits.)
-__device__ __forceinline__ long long pa_div(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
-  return a / b;
-}
-__device__ __forceinline__ long long pa_share(long long W, int grid, int c) { return pa_div(W * c, grid); }
-__device__ __forceinline__ int pa_owner(long long x, long long W, int grid) {
-  return static_cast<int>(pa_div((x + 1) * grid - 1, W));
-}
-struct PaSeg {
-  int b, kvh, nb, j0, nblk;  // blocks j0 .. j0 + nblk - 1 of the pair's nb
-  long long pair0;           // the pair's first block in the flattened order (after the pair's extra unit)
-};
-struct PaWalk {  // a CTA's segments, in order
-  int b;
-  long long x0, x, x1;
-};
-__device__ __forceinline__ PaWalk pa_walk(const PaParams& p, const int* cum, long long W, int ctas) {
-  PaWalk w{0, 0, 0, 0};
-  if (static_cast<int>(blockIdx.x) >= ctas) return w;
-  w.x0 = w.x = pa_share(W, ctas, blockIdx.x);
-  w.x1 = pa_share(W, ctas, blockIdx.x + 1);
-  int lo = 0, hi = p.B - 1;  // the last request that starts at or before x0
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (static_cast<long long>(cum[mid]) * p.Hkv <= w.x0) lo = mid;
-    else hi = mid - 1;
-  }
-  w.b = lo;
-  return w;
-}
-// The next segment, nblk 0 when there is none.
-__device__ __forceinline__ PaSeg pa_next(const PaParams& p, const int* cum, PaWalk& w) {
-  PaSeg s{};
-  while (w.x < w.x1) {
-    while (static_cast<long long>(cum[w.b + 1]) * p.Hkv <= w.x) ++w.b;
-    const int units = cum[w.b + 1] - cum[w.b];
-    const long long start = static_cast<long long>(cum[w.b]) * p.Hkv;
-    const int rel = static_cast<int>(w.x - start), kvh = rel / units, at = rel - kvh * units;  // rel < units Hkv < 2^26
-    const long long left = w.x1 - w.x;
-    const int take = left < units - at ? static_cast<int>(left) : units - at;
-    w.x += take;
-    s.nblk = at == 0 ? take - 1 : take;
-    if (s.nblk == 0) continue;  // the share ends behind the pair's extra unit
-    s.b = w.b;
-    s.kvh = kvh;
-    s.nb = units - 1;
-    s.j0 = at == 0 ? 0 : at - 1;
-    s.pair0 = start + static_cast<long long>(kvh) * units + 1;
-    break;
-  }
-  return s;
-}
-
-// A cut pair's segments are those of CTAs c0 .. c1. A CTA's slot 1 holds the segment that starts its pair, slot 0 one
-// that goes on with another CTA's.
-struct PaJoin {
-  int b, kvh, c0, c1;
-};
-// Joins them with every thread of the CTA: a thread takes four columns of a query row and runs through the segments
-// with a maximum that may rise. Many rows: several at once, so that their loads are in flight together. Few rows
-// (kAtOnce 1): as many threads a row as there are, each with every so many segments, joined in order through shared
-// memory.
-struct PaSum {
-  float4 num;
-  float m, den;
-  __device__ __forceinline__ void add(const float4& x, float mx, float d) {
-    const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.f : mn;  // nothing visible so far: 2^-inf = 0
-    const float a = exp2f(m - ref), b = exp2f(mx - ref);
-    m = mn;
-    den = den * a + b * d;
-    num.x = num.x * a + b * x.x;
-    num.y = num.y * a + b * x.y;
-    num.z = num.z * a + b * x.z;
-    num.w = num.w * a + b * x.w;
-  }
-};
-template <int D>
-__device__ __forceinline__ void pa_join_out(const PaParams& p, const PaJoin& jn, int i, const PaSum& s) {
-  constexpr int kQuads = D / 4;
-  const int r = i / kQuads, node = r / p.G;
-  // a cut pair has two blocks at least, and so a prefix that every node sees
-  static_assert(kPaNodes < kPaKeys, "the nodes' own keys fill no block");
-  const float inv = 1.f / s.den;
-  unsigned short* o =
-      p.out + ((static_cast<size_t>(jn.b) * p.n + node) * p.Hq + jn.kvh * p.G + r % p.G) * D + 4 * (i % kQuads);
-  *reinterpret_cast<uint2*>(o) =
-      make_uint2(at_pack(s.num.x * inv, s.num.y * inv), at_pack(s.num.z * inv, s.num.w * inv));
-}
-template <int D, int kAtOnce>
-__device__ __forceinline__ void pa_join(const PaParams& p, const PaJoin& jn, PaSum* red) {
-  constexpr int kQuads = D / 4, kSegments = kAtOnce == 1 ? 8 : 2;  // in flight: kAtOnce rows of kSegments segments
-  const int nseg = jn.c1 - jn.c0 + 1, total = p.R * kQuads;
-  const int groups = kAtOnce == 1 ? kPaThreads / total : 1, group = kAtOnce == 1 ? threadIdx.x / total : 0;
-  const int first = kAtOnce == 1 ? static_cast<int>(threadIdx.x) % total : static_cast<int>(threadIdx.x);
-  for (int i0 = first; i0 < total; i0 += kAtOnce * kPaThreads) {
-    PaSum s[kAtOnce];
-#pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) s[u] = PaSum{make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
-    for (int c0 = group; group < groups && c0 < nseg; c0 += kSegments * groups) {
-      float2 ml[kSegments][kAtOnce];
-      float4 x[kSegments][kAtOnce];
-#pragma unroll
-      for (int k = 0; k < kSegments; ++k) {
-        const int c = c0 + k * groups;
-        const size_t unit = 2 * static_cast<size_t>(jn.c0 + c) + (c == 0 ? 1 : 0);
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-          const int i = i0 + u * kPaThreads;
-          const size_t row = unit * p.R + i / kQuads;
-          ml[k][u] = make_float2(-INFINITY, 0.f);
-          x[k][u] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (c < nseg && i < total) {
-            ml[k][u] = __ldcg(reinterpret_cast<const float2*>(p.ml + 2 * row));
-            x[k][u] = __ldcg(reinterpret_cast<const float4*>(p.part + row * D + 4 * (i % kQuads)));
-          }
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kSegments; ++k)
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) s[u].add(x[k][u], ml[k][u].x, ml[k][u].y);
-    }
-    if constexpr (kAtOnce == 1) {
-      if (group > 0 && group < groups) red[threadIdx.x] = s[0];
-      __syncthreads();
-      if (group == 0) {
-        for (int g = 1; g < groups; ++g) {
-          const PaSum& other = red[g * total + i0];
-          s[0].add(other.num, other.m, other.den);
-        }
-        pa_join_out<D>(p, jn, i0, s[0]);
-      }
-      __syncthreads();
-      break;  // every thread had one
-    } else {
-#pragma unroll
-      for (int u = 0; u < kAtOnce; ++u)
-        if (i0 + u * kPaThreads < total) pa_join_out<D>(p, jn, i0 + u * kPaThreads, s[u]);
-    }
-  }
-}
-
-// The keys of a pair from here on are not the same for all rows (the nodes' own), or not all there (the last block's
-// rows past the request's end): blocks that reach past it are masked, and their values cleaned.
-__device__ __forceinline__ int pa_common(const PaParams& p, int len) { return p.n > 1 || p.mask ? len - p.n : len; }
-
-// Of 64 consecutive keys: all before `own` are visible, key own + c where bit c of `nodes` is set, none from `end` on.
-__device__ __forceinline__ unsigned long long pa_visible(int own, int end, unsigned long long nodes) {
-  const unsigned long long before = own >= 64 ? ~0ull : own <= 0 ? 0ull : (1ull << own) - 1ull;
-  const unsigned long long there = end >= 64 ? ~0ull : end <= 0 ? 0ull : (1ull << end) - 1ull;
-  const unsigned long long tree = own >= 64 || own <= -64 ? 0ull : own >= 0 ? nodes << own : nodes >> -own;
-  return (before | tree) & there;
 }
 
 // Roles: warp 2 loads (its lanes look the pages up and issue one page's boxes each), warp 3 issues the MMAs, the
@@ -689,26 +510,13 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
     // the ticket's thread acquired the others' partials; the barrier above passed them on
     for (int i = 0; i < s_joins; ++i) {
       PaSum* red = reinterpret_cast<PaSum*>(skv);  // the ring is empty by now
-      if (p.R * (D / 4) <= kPaThreads) pa_join<D, 1>(p, s_join[i], red);
-      else pa_join<D, 6>(p, s_join[i], red);
+      if (p.R * (D / 4) <= kPaThreads) pa_join<D, 1, kPaThreads>(p, s_join[i], red);
+      else pa_join<D, 6, kPaThreads>(p, s_join[i], red);
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   if (warp == 3) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
-}
-
-struct PaPlan {
-  int grid;
-  size_t part, ml, bytes;  // behind the header nothing outlives a call
-};
-inline PaPlan pa_plan(int R, int d, int sms) {
-  PaPlan P{};
-  P.grid = sms < kWsTickets ? sms : kWsTickets;
-  P.part = align_up(sizeof(WsHeader));
-  P.ml = align_up(P.part + sizeof(float) * 2 * P.grid * static_cast<size_t>(R) * d);
-  P.bytes = align_up(P.ml + sizeof(float) * 2 * 2 * P.grid * static_cast<size_t>(R));
-  return P;
 }
 
 template <int D>
