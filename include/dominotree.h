@@ -27,9 +27,9 @@
  *     dt_build_trees keeps its own region after the one dt_topm uses, so a workspace of
  *     dt_build_workspace_bytes(...) bytes serves both calls of a round when they are ordered on one stream. Two
  *     calls that may run concurrently need two workspaces.
- *     dt_kv_append, dt_paged_attention, dt_prompt_attention and dt_tree_attention find nothing in a workspace but its
- *     first 256 bytes, and leave those as they found them: one workspace of the largest size serves them all, in any
- *     order on one stream. The other calls (dt_topm, the builders, dt_lmhead_topm) rely on more: a workspace that
+ *     dt_page_plan, dt_kv_append, dt_kv_append8, dt_paged_attention, dt_paged_attention8, dt_prompt_attention and
+ *     dt_tree_attention find nothing in a workspace but its first 256 bytes, and leave those as they found them: one
+ *     workspace of the largest size serves them all, in any order on one stream. The other calls (dt_topm, the builders, dt_lmhead_topm) rely on more: a workspace that
  *     another kind of call has used is initialised again before it serves one of them.
  *   - No C++ exception crosses this boundary. The calls are thread-safe for distinct workspaces.
  */
@@ -54,7 +54,8 @@ typedef enum {
   DT_ERR_UNSUPPORTED = 2, /* valid, but outside the envelope the kernels are built for (limits below)    */
   DT_ERR_CUDA = 3,        /* a CUDA runtime call failed (launch, attribute query)                        */
   DT_ERR_TIMEOUT = 4,     /* device: a grid-barrier wait ran out of its time budget; the kernel returned  */
-  DT_ERR_NUMERIC = 5      /* device: a NaN was found among the logits                                    */
+  DT_ERR_NUMERIC = 5,     /* device: a NaN was found among the logits                                    */
+  DT_ERR_NO_PAGES = 6     /* device: the pool has not enough free pages for every request (dt_page_plan)  */
 } dt_status;
 
 typedef enum { DT_F32 = 0, DT_BF16 = 1 } dt_dtype;
@@ -271,6 +272,49 @@ dt_status dt_tree_attention(int B, int n, int L, int Hq, int Hkv, int d, const v
 #define DT_PAGED_MAX_TOKENS (1 << 24)     /* max_pages * page_size: a request's longest cache */
 
 /* ---------------------------------------------------------------------------------------------------------------
+ * dt_page_plan — a step's pages, slots and positions from the requests' lengths, without a round trip to the host.
+ *
+ * Request b keeps its first lens[b] tokens (what the cache holds behind them is given up: a verified tree's rejected
+ * nodes) and gets grow[b] more. With a pool it holds exactly ceil((lens[b] + grow[b]) / page_size) pages afterwards:
+ * pages it lacks are taken from the pool and entered in its row of page_table, pages it no longer needs are given back
+ * (its row's entries past them stay as they are, and mean nothing). lens[b] < 0: the request has ended, everything it
+ * holds is given back, grow[b] is not looked at.
+ * The free pages are a stack, free_pages[0 .. free_count[0] - 1]. First those given back are pushed, the last request's
+ * first and each request's from its last page; then the requests take theirs from the top in their order, each from its
+ * first missing page: what one step took and the next gives back leaves the stack as it was.
+ * The rows of the slot map, as dt_kv_append and dt_paged_attention take them:
+ *   n = 0     the requests' grow[b] new tokens, packed one request after the other (prompts);
+ *   n > 0     n rows per request, N = B n. Row i is the request's i-th new token while i < grow[b] (one token each: n = 1;
+ *             a draft tree's nodes: grow[b] = n). With `path` (dt_accept_paths: the accepted nodes in order) row i is
+ *             the j-th new token where path[b][j] = i for a j < grow[b] = accept_len[b] (the first such j): the slots at
+ *             which the accepted nodes are appended again.
+ * A row that is a token gets its slot, and its position: its index in the request, or with `depth` (dt_build_trees: a
+ * tree node's depth, from 1) lens[b] + depth[b][i] - 1. Every other row gets slot -1 and position 0.
+ *   lens, grow [B] int32;  depth, path [B,n] int32, or NULL (not both; only with n > 0);
+ *   page_table  [B,max_pages] int32, updated;
+ *   held [B], free_pages [num_pages], free_count [1] int32, updated: the pool; all NULL without one (the page table then
+ *               has every page that is needed, and is only read). A request may hold more pages than lens[b] needs.
+ *   out_lens    [B] int32 or NULL: lens[b] + grow[b];  cu_seqlens [B+1] int32 or NULL: each request's first row (n = 0:
+ *               as dt_prompt_attention takes it);
+ *   slots, positions [N] int32, or both NULL with N = 0 (pages only). n = 0: N is what the arrays hold, rows behind the
+ *               last request's are marked as no tokens.
+ *   workspace   dt_page_plan_workspace_bytes(B) bytes, initialised by dt_workspace_init.
+ * A request that cannot be served gets no tokens: out_lens[b] = 0, its rows are marked as none, its pages and held[b]
+ * stay as they are, and the status word says why. DT_ERR_NO_PAGES: the pool does not hold the pages that it needs (later
+ * requests that need pages get none either). DT_ERR_INVALID_ARG: grow[b] negative (or above n > 0), more tokens than
+ * max_pages pages hold, fewer pages held than lens[b] needs, or rows behind N; and a row whose page lies outside the
+ * pool. A pool that contradicts itself (free_count out of range, more pages given back than there is room for) sets
+ * DT_ERR_INVALID_ARG and no page moves.
+ * No array may overlap another. B <= DT_PAGED_MAX_BATCH; page sizes, pool and max_pages as dt_paged_attention.
+ * ------------------------------------------------------------------------------------------------------------- */
+size_t dt_page_plan_workspace_bytes(int B);
+dt_status dt_page_plan(int B, int n, int N, int page_size, int num_pages, int max_pages, const int32_t* lens,
+                       const int32_t* grow, const int32_t* depth, const int32_t* path, int32_t* page_table,
+                       int32_t* held, int32_t* free_pages, int32_t* free_count, int32_t* out_lens,
+                       int32_t* cu_seqlens, int32_t* slots, int32_t* positions, void* workspace,
+                       size_t workspace_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------------------------------------
  * dt_kv_append — N tokens' keys and values into the paged cache, rotated by their positions on the way.
  *
  * Rotary embedding (arXiv 2104.09864): of each head's first `rot` elements, pair i is turned by the angle whose cosine
@@ -300,6 +344,36 @@ dt_status dt_kv_append(int N, int Hq, int Hkv, int d, const void* q, int64_t q_s
                        size_t workspace_bytes, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------------------------------------------
+ * dt_kv_append8 — dt_kv_append into a cache in 8 bits: e4m3 codes with one scale for each block of tokens and head.
+ *
+ * The cache is k_cache, v_cache [num_pages,Hkv,page_size,d] uint8 (e4m3: four significant bits, largest value 448) and
+ * k_scale, v_scale [num_pages,Hkv,page_size/scale_block] fp32: an element is its code times the scale of its block of
+ * scale_block rows. Half the bytes of the bf16 cache; dt_paged_attention8 reads it.
+ * Everything as dt_kv_append (tokens, slots, rotation, queries, out_k) but for what the cache holds:
+ *   - A block's scale is 2^e with the least e in DT_SCALE_LOW .. DT_SCALE_HIGH that brings the largest finite element of
+ *     the block's rows to 448 or less. Elements (rotated keys in fp32) are divided by it and rounded once, to nearest
+ *     even: off by at most 2^-4 of their value or 2^-10 of the scale, whichever is more. What is not finite, or larger
+ *     than 448 2^DT_SCALE_HIGH, is stored as NaN and does not count for the scale.
+ *   - Tokens are appended: of a block that the call writes to, the rows below the lowest written one hold earlier tokens
+ *     and are kept (where the scale grows they are coded again: exactly, but for codes that fall below e4m3's normal
+ *     range, which are rounded to 2^-10 of the new scale); the scale does not shrink while such rows are kept. Rows
+ *     above it that the call does not write hold nothing any more. A block written from its first row starts anew,
+ *     whatever it held. A stored scale that is no power of two in range (0 in a fresh pool) says that no rows are kept.
+ *   Two calls that write to one block are ordered by the caller, as any two calls that write to one place.
+ *   workspace   dt_kv_append8_workspace_bytes(N,num_pages,page_size) bytes, initialised by dt_workspace_init.
+ * Supported beyond dt_kv_append: scale_block a power of two in DT_MIN_PAGE .. page_size. If two tokens of a call name one
+ * slot, one of them is stored.
+ * ------------------------------------------------------------------------------------------------------------- */
+#define DT_SCALE_LOW (-48)
+#define DT_SCALE_HIGH 48
+size_t dt_kv_append8_workspace_bytes(int N, int num_pages, int page_size);
+dt_status dt_kv_append8(int N, int Hq, int Hkv, int d, const void* q, int64_t q_stride, const void* k,
+                        int64_t k_stride, const void* v, int64_t v_stride, dt_dtype dtype, const int32_t* slots,
+                        const int32_t* positions, const float* rope, int max_pos, int rot, int interleaved, void* out_q,
+                        void* out_k, void* k_cache, void* v_cache, float* k_scale, float* v_scale, int num_pages,
+                        int page_size, int scale_block, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------------------------------------
  * dt_paged_attention — attention of each request's newest n tokens over its paged cache: one new token (n = 1), or a
  * draft tree's nodes in the verify pass. As dt_tree_attention, with a cache in pages and a length per request.
  *
@@ -326,6 +400,27 @@ dt_status dt_paged_attention(int B, int n, int Hq, int Hkv, int d, const void* q
                              const void* v_cache, dt_dtype dtype, int num_pages, int page_size,
                              const int32_t* page_table, int max_pages, const int32_t* lens, const uint8_t* mask,
                              float scale, void* out, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------------------------------------
+ * dt_paged_attention8 — dt_paged_attention over a cache in 8 bits with scales (dt_kv_append8).
+ *
+ * Semantics as dt_paged_attention, with k_j and v_j the codes times the scales of their blocks and heads. Any scales in
+ * 2^DT_SCALE_LOW .. 2^DT_SCALE_HIGH serve (they need not be powers of two); with others what a query that sees their
+ * block gets is unspecified. Scales of blocks of which no row is seen are not looked at.
+ * Arithmetic: a query row is brought by a power of two to 2^14 .. 2^15 and held in fp16 (exact but for elements below
+ * 2^-31 of the row's largest), codes are exact in fp16; products on the tensor cores, accumulated in fp32. A softmax weight
+ * times its value's scale is rounded to fp16, relative to the row's largest such product so far: off by 2^-11 of itself,
+ * or by 2^-31 of that largest where that is more. The output is rounded to bf16 once.
+ *   k_scale, v_scale [num_pages,Hkv,page_size/scale_block] fp32;  everything else as dt_paged_attention.
+ *   workspace   dt_paged_attention8_workspace_bytes(B,n,Hq,Hkv,d) bytes on the current device, initialised by
+ *               dt_workspace_init; serves any lengths. After DT_ERR_TIMEOUT (dt_get_error) initialise it again.
+ * ------------------------------------------------------------------------------------------------------------- */
+size_t dt_paged_attention8_workspace_bytes(int B, int n, int Hq, int Hkv, int d);
+dt_status dt_paged_attention8(int B, int n, int Hq, int Hkv, int d, const void* q, const void* k_cache,
+                              const void* v_cache, const float* k_scale, const float* v_scale, dt_dtype dtype,
+                              int num_pages, int page_size, int scale_block, const int32_t* page_table, int max_pages,
+                              const int32_t* lens, const uint8_t* mask, float scale, void* out, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------------------------------------------
  * dt_prompt_attention — causal attention over B whole prompts, packed one after the other (before the first round).

@@ -77,6 +77,7 @@ extern "C" const char* dt_status_string(dt_status s) {
     case DT_ERR_CUDA: return "CUDA runtime error";
     case DT_ERR_TIMEOUT: return "grid-barrier wait ran out of its time budget";
     case DT_ERR_NUMERIC: return "NaN among the logits";
+    case DT_ERR_NO_PAGES: return "not enough free pages";
   }
   return "unknown status";
 }

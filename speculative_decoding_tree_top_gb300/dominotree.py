@@ -26,6 +26,7 @@ class Status(enum.IntEnum):
     CUDA = 3
     TIMEOUT = 4
     NUMERIC = 5
+    NO_PAGES = 6
 
 
 F32, BF16 = 0, 1
@@ -66,9 +67,17 @@ SIGNATURES = {
     "dt_tree_attention": (_I, [_I, _I, _I, _I, _I, _I, _P, _P, _P, _I, _P, ctypes.c_float, _P, _P, _SZ, _P]),
     "dt_kv_append": (_I, [_I, _I, _I, _I, _P, _L, _P, _L, _P, _L, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _I, _I,
                           _P, _SZ, _P]),
+    "dt_page_plan_workspace_bytes": (_SZ, [_I]),
+    "dt_page_plan": (_I, [_I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "dt_kv_append8_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "dt_kv_append8": (_I, [_I, _I, _I, _I, _P, _L, _P, _L, _P, _L, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P,
+                           _I, _I, _I, _P, _SZ, _P]),
     "dt_paged_attention_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "dt_paged_attention": (_I, [_I, _I, _I, _I, _I, _P, _P, _P, _I, _I, _I, _P, _I, _P, _P, ctypes.c_float, _P, _P,
                                 _SZ, _P]),
+    "dt_paged_attention8_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "dt_paged_attention8": (_I, [_I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P, ctypes.c_float,
+                                 _P, _P, _SZ, _P]),
     "dt_prompt_attention_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "dt_prompt_attention": (_I, [_I, _I, _I, _I, _I, _P, _L, _P, _L, _P, _L, _I, _P, ctypes.c_float, _P, _P, _SZ,
                                  _P]),
@@ -261,6 +270,15 @@ def new_paged_cache(num_pages: int, Hkv: int, page_size: int, d: int, device="cu
     return tuple(torch.empty(shape, dtype=torch.bfloat16, device=device) for _ in range(2))
 
 
+def new_paged_cache8(num_pages: int, Hkv: int, page_size: int, d: int, scale_block: int = 16, device="cuda"):
+    """A paged cache in 8 bits -> (k_cache, v_cache) [num_pages,Hkv,page_size,d] float8_e4m3fn, not initialised, and
+    (k_scale, v_scale) [num_pages,Hkv,page_size/scale_block] fp32, zero (no rows yet): four tensors in that order."""
+    caches = (torch.empty((num_pages, Hkv, page_size, d), dtype=torch.float8_e4m3fn, device=device) for _ in range(2))
+    scales = (torch.zeros((num_pages, Hkv, page_size // scale_block), dtype=torch.float32, device=device)
+              for _ in range(2))
+    return (*caches, *scales)
+
+
 def _here(t: torch.Tensor, name: str) -> int:
     """The tensor's device index. The library launches on the current device: tensors of another one are refused."""
     if not t.is_cuda:
@@ -321,6 +339,88 @@ def _side(stream, device):
     return torch.cuda.stream(stream)
 
 
+def dt_page_plan_workspace_bytes(B: int) -> int:
+    return int(lib().dt_page_plan_workspace_bytes(B))
+
+
+def dt_page_plan(lens: torch.Tensor, grow: torch.Tensor, page_table: torch.Tensor, page_size: int, num_pages: int,
+                 held: Optional[torch.Tensor] = None, free_pages: Optional[torch.Tensor] = None,
+                 free_count: Optional[torch.Tensor] = None, n: int = 0, rows: int = 0,
+                 depth: Optional[torch.Tensor] = None, path: Optional[torch.Tensor] = None,
+                 out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """A step's pages, slots and positions: requests that keep lens [B] tokens and get grow [B] more (int32). The pool
+    held [B], free_pages [num_pages], free_count [1] and page_table [B,max_pages] (int32) are updated; without the pool
+    the table is only read. ``n`` rows a request, or n = 0: packed, ``rows`` of them (0: pages alone). depth, path [B,n]
+    int32 as dt_build_trees and dt_accept_paths give them -> lens [B], cu_seqlens [B+1], and where there are rows slots,
+    positions [rows]. ``out``: the tensors to write, any of lens, cu_seqlens, and both or none of slots, positions."""
+    i32 = torch.int32
+    B, = lens.shape
+    dev = _here(lens, "lens")
+    max_pages = page_table.shape[1]
+    if n > 0:
+        rows = B * n
+    if workspace is None or out is None:
+        with _side(stream, dev):
+            if out is None:
+                sizes = dict(lens=B, cu_seqlens=B + 1, **(dict(slots=rows, positions=rows) if rows else {}))
+                out = {name: torch.empty(size, dtype=i32, device=lens.device) for name, size in sizes.items()}
+            if workspace is None:
+                workspace = new_workspace(max(256, dt_page_plan_workspace_bytes(max(B, 1))), lens.device)
+    slots = out.get("slots")
+    if slots is not None:
+        if n > 0 and slots.shape != (rows,):
+            raise ValueError(f"slots must have shape {(rows,)}, not {tuple(slots.shape)}")
+        rows = slots.shape[0]
+    else:
+        rows = 0
+
+    def opt(t, name, shape):
+        return None if t is None else _on(t, name, dev, i32, shape)
+    status = lib().dt_page_plan(
+        B, n, rows, page_size, num_pages, max_pages, _on(lens, "lens", dev, i32, (B,)), _on(grow, "grow", dev, i32, (B,)),
+        opt(depth, "depth", (B, n)), opt(path, "path", (B, n)), _on(page_table, "page_table", dev, i32, (B, max_pages)),
+        opt(held, "held", (B,)), opt(free_pages, "free_pages", (num_pages,)), opt(free_count, "free_count", (1,)),
+        opt(out.get("lens"), "out lens", (B,)), opt(out.get("cu_seqlens"), "cu_seqlens", (B + 1,)),
+        opt(slots, "slots", (rows,)), opt(out.get("positions"), "positions", (rows,)), *_room(workspace, dev),
+        _raw(stream, dev))
+    if status:
+        raise DTError(status, "dt_page_plan")
+    return out
+
+
+def _append_sides(N: int, kv: tuple, dev: int, positions, rope, q, out_q, out_k) -> tuple:
+    """An append's optional arguments: (Hq, q, its row pitch, out_q), (positions, rope, max_pos, rot), out_k."""
+    Hq = max_pos = rot = q_at = q_pitch = 0
+    oq_at = ok_at = rope_at = pos_at = None
+    if q is not None:
+        Hq = q.shape[1]
+        heads = (N, Hq, kv[2])
+        q_at, q_pitch = _rows(q, "q", dev, heads)
+        oq_at = _on(out_q, "out_q", dev, torch.bfloat16, heads)
+    elif out_q is not None:
+        raise ValueError("out_q without q")
+    if out_k is not None:
+        ok_at = _on(out_k, "out_k", dev, torch.bfloat16, kv)
+    if rope is not None:
+        if positions is None:
+            raise ValueError("rope without positions")
+        max_pos, rot = table = rope.shape
+        rope_at = _on(rope, "rope", dev, torch.float32, table)
+        pos_at = _on(positions, "positions", dev, torch.int32, (N,))
+    return (Hq, q_at, q_pitch, oq_at), (pos_at, rope_at, max_pos, rot), ok_at
+
+
+def _scales(k_scale: torch.Tensor, v_scale: torch.Tensor, dev: int, cache: tuple) -> tuple:
+    """The addresses of an 8-bit cache's scales, and the rows of a page that share one."""
+    blocks = k_scale.shape[-1]
+    if blocks < 1 or cache[2] % blocks:
+        raise ValueError(f"k_scale must have shape {(cache[0], cache[1])} + (page_size / scale_block,), "
+                         f"not {tuple(k_scale.shape)}")
+    shape = (cache[0], cache[1], blocks)
+    f32 = torch.float32
+    return (_on(k_scale, "k_scale", dev, f32, shape), _on(v_scale, "v_scale", dev, f32, shape)), cache[2] // blocks
+
+
 def dt_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, slots: torch.Tensor,
                  positions: Optional[torch.Tensor] = None, rope: Optional[torch.Tensor] = None,
                  interleaved: bool = False, q: Optional[torch.Tensor] = None, out_q: Optional[torch.Tensor] = None,
@@ -338,23 +438,8 @@ def dt_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
                 workspace = new_workspace(256, k.device)
             if q is not None and out_q is None:
                 out_q = torch.empty(q.shape, dtype=bf, device=k.device)
-    Hq = max_pos = rot = q_at = q_pitch = 0
-    oq_at = ok_at = rope_at = pos_at = None
-    if q is not None:
-        Hq = q.shape[1]
-        heads = (N, Hq, d)
-        q_at, q_pitch = _rows(q, "q", dev, heads)
-        oq_at = _on(out_q, "out_q", dev, bf, heads)
-    elif out_q is not None:
-        raise ValueError("out_q without q")
-    if out_k is not None:
-        ok_at = _on(out_k, "out_k", dev, bf, kv)
-    if rope is not None:
-        if positions is None:
-            raise ValueError("rope without positions")
-        max_pos, rot = table = rope.shape
-        rope_at = _on(rope, "rope", dev, torch.float32, table)
-        pos_at = _on(positions, "positions", dev, i32, (N,))
+    (Hq, q_at, q_pitch, oq_at), (pos_at, rope_at, max_pos, rot), ok_at = _append_sides(
+        N, kv, dev, positions, rope, q, out_q, out_k)
     k_at, k_pitch = _rows(k, "k", dev, kv)
     v_at, v_pitch = _rows(v, "v", dev, kv)
     if pool_heads != Hkv or pool_d != d:
@@ -365,6 +450,43 @@ def dt_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
         _on(v_cache, "v_cache", dev, bf, cache), num_pages, page_size, *_room(workspace, dev), _raw(stream, dev))
     if status:
         raise DTError(status, "dt_kv_append")
+    return out_q
+
+
+def dt_kv_append8_workspace_bytes(N: int, num_pages: int, page_size: int) -> int:
+    return int(lib().dt_kv_append8_workspace_bytes(N, num_pages, page_size))
+
+
+def dt_kv_append8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                  k_scale: torch.Tensor, v_scale: torch.Tensor, slots: torch.Tensor,
+                  positions: Optional[torch.Tensor] = None, rope: Optional[torch.Tensor] = None,
+                  interleaved: bool = False, q: Optional[torch.Tensor] = None, out_q: Optional[torch.Tensor] = None,
+                  out_k: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """``dt_kv_append`` into a cache in 8 bits (``new_paged_cache8``): k_cache, v_cache [num_pages,Hkv,page_size,d]
+    float8_e4m3fn, k_scale, v_scale [num_pages,Hkv,page_size/scale_block] fp32."""
+    N, Hkv, d = kv = k.shape
+    dev, bf, i32, f8 = _here(k, "k"), torch.bfloat16, torch.int32, torch.float8_e4m3fn
+    num_pages, pool_heads, page_size, pool_d = cache = k_cache.shape
+    if workspace is None or (q is not None and out_q is None):
+        with _side(stream, dev):
+            if workspace is None:
+                workspace = new_workspace(dt_kv_append8_workspace_bytes(N, num_pages, page_size), k.device)
+            if q is not None and out_q is None:
+                out_q = torch.empty(q.shape, dtype=bf, device=k.device)
+    (Hq, q_at, q_pitch, oq_at), (pos_at, rope_at, max_pos, rot), ok_at = _append_sides(
+        N, kv, dev, positions, rope, q, out_q, out_k)
+    k_at, k_pitch = _rows(k, "k", dev, kv)
+    v_at, v_pitch = _rows(v, "v", dev, kv)
+    if pool_heads != Hkv or pool_d != d:
+        raise ValueError(f"k_cache must have shape {(num_pages, Hkv, page_size, d)}, not {tuple(cache)}")
+    scales, block = _scales(k_scale, v_scale, dev, cache)
+    status = lib().dt_kv_append8(
+        N, Hq, Hkv, d, q_at, q_pitch, k_at, k_pitch, v_at, v_pitch, BF16, _on(slots, "slots", dev, i32, (N,)),
+        pos_at, rope_at, max_pos, rot, 1 if interleaved else 0, oq_at, ok_at, _on(k_cache, "k_cache", dev, f8, cache),
+        _on(v_cache, "v_cache", dev, f8, cache), *scales, num_pages, page_size, block, *_room(workspace, dev),
+        _raw(stream, dev))
+    if status:
+        raise DTError(status, "dt_kv_append8")
     return out_q
 
 
@@ -399,6 +521,42 @@ def dt_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
         _on(out, "out", dev, bf, shape), *_room(workspace, dev), _raw(stream, dev))
     if status:
         raise DTError(status, "dt_paged_attention")
+    return out
+
+
+def dt_paged_attention8_workspace_bytes(B: int, n: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(lib().dt_paged_attention8_workspace_bytes(B, n, Hq, Hkv, d))
+
+
+def dt_paged_attention8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                        v_scale: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor, scale: float,
+                        mask: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None):
+    """``dt_paged_attention`` over a cache in 8 bits (``new_paged_cache8``, ``dt_kv_append8``): q [B,n,Hq,d] bf16,
+    k_cache, v_cache [num_pages,Hkv,page_size,d] float8_e4m3fn, k_scale, v_scale [num_pages,Hkv,page_size/scale_block]
+    fp32 -> out [B,n,Hq,d] bf16."""
+    B, n, Hq, d = shape = q.shape
+    dev, bf, f8 = _here(q, "q"), torch.bfloat16, torch.float8_e4m3fn
+    num_pages, Hkv, page_size, _ = cache = k_cache.shape
+    max_pages = page_table.shape[1]
+    if workspace is None or out is None:
+        with _side(stream, dev):
+            if out is None:
+                out = torch.empty(shape, dtype=bf, device=q.device)
+            if workspace is None:
+                workspace = new_workspace(dt_paged_attention8_workspace_bytes(B, n, Hq, Hkv, d), q.device)
+    if cache[3] != d:
+        raise ValueError(f"k_cache must have shape {(num_pages, Hkv, page_size, d)}, not {tuple(cache)}")
+    scales, block = _scales(k_scale, v_scale, dev, cache)
+    status = lib().dt_paged_attention8(
+        B, n, Hq, Hkv, d, _on(q, "q", dev, bf, shape), _on(k_cache, "k_cache", dev, f8, cache),
+        _on(v_cache, "v_cache", dev, f8, cache), *scales, BF16, num_pages, page_size, block,
+        _on(page_table, "page_table", dev, torch.int32, (B, max_pages)), max_pages,
+        _on(lens, "lens", dev, torch.int32, (B,)),
+        _on(mask, "mask", dev, torch.uint8, (B, n, n)) if mask is not None else None, scale,
+        _on(out, "out", dev, bf, shape), *_room(workspace, dev), _raw(stream, dev))
+    if status:
+        raise DTError(status, "dt_paged_attention8")
     return out
 
 
