@@ -50,13 +50,6 @@ __device__ __forceinline__ bool nonfinite_bf16x2(uint32_t w) {
   return (w & 0x7F800000u) == 0x7F800000u || (w & 0x7F80u) == 0x7F80u;
 }
 
-// The softmax warps meet (a barrier whose wait is bounded); `count` is the meetings so far, the same in every warp.
-__device__ __forceinline__ bool pa_sync(uint64_t* bar, unsigned& count, int lane) {
-  __syncwarp();
-  if (lane == 0) mbar_arrive(bar);
-  return __all_sync(0xFFFFFFFFu, at_wait(bar, count++ & 1u));
-}
-
 // Roles: warp 2 loads (its lanes look the pages up and issue one page's boxes each), warp 3 issues the MMAs, the
 // softmax warps own 16 query rows each (row r = node G + head, tensor memory lane r; four neighbouring threads share
 // two rows), warps 0 and 1 clean values. Per block: S = Q K^T (M = 128, N = 128) into one of two buffers in tensor

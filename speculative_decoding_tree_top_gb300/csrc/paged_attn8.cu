@@ -1,4 +1,16 @@
 // dt_paged_attention8 — attention of each request's newest tokens over its paged cache in 8 bits with scales.
+//
+// For request b, node i and query head h: out = softmax(scale q.k_j) v_j over the visible keys j, where k_j and v_j are
+// e4m3 codes times the scales ks_j and vs_j of their block of rows. The scales stay outside the products:
+//     score_j = ks_j (q . code_j),  out = sum_j (p_j vs_j) code_j / sum_j p_j.
+//
+// GB300 design. As in the bf16 kernel the R = G n query rows that share a key/value head read each cached row once, and
+// the 128-key blocks of all pairs are split evenly over the CTAs. What bounds it is memory, at half the bytes a block; so
+// the codes must become tensor-core operands without passing through shared memory a second time. Keys and values are the
+// left operands, in tensor memory: S^T = K Q^T (a lane a key) and O^T = V^T W (a lane a column), and the warps that turn
+// codes into fp16 (exactly) write them straight there. The few query rows are N, so a product costs little when R is
+// small, and a softmax thread owns a key: its scales are two registers, and a row's maximum is looked for only when some
+// weight leaves the headroom.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -12,83 +24,847 @@
 namespace dt {
 namespace {
 
+constexpr int kP8MaxStages = 16;
+constexpr size_t kPa8SmemCap = 232448 - 8192;  // opt-in shared memory of a CTA, less the static part
+// Weights times their values' scales are fp16: a row's largest starts out at 2^kP8Start and may grow to 2^kP8Most before
+// the reference is raised. fp16 goes up to 2^16 and holds subnormal numbers in steps of 2^-24.
+constexpr float kP8Start = 6.f, kP8Most = 14.f;
+constexpr float kP8LeastScale = -64.f;  // log2: smaller scales of values do not pull the reference further down
+
 struct Pa8Params : PaWork {
-  int block;                        // rows of a page that share a scale
-  const unsigned short* q;
-  const unsigned char *k_cache, *v_cache;
+  int stages, block;                // block: rows of a page that share a scale
+  const unsigned short* q;          // [B][n][Hq][D]
+  const unsigned char* v_cache;     // re-read only for codes that are NaN
   const float *k_scale, *v_scale;   // [num_pages][Hkv][page_size / block]
-  float scale;
+  float scale_log2;                 // scale * log2(e)
+};
+struct Pa8Maps {
+  CUtensorMap k, v;  // [num_pages * Hkv][page_size][D], boxes of min(page_size, 128) rows
 };
 
-__device__ __forceinline__ float code_value(unsigned char c) {
-  uint32_t two;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"(static_cast<uint16_t>(c)));
-  return __low2float(*reinterpret_cast<const __half2*>(&two));
+// Loads and stores of tensor memory with a row (lane) per thread: column c of the thread's lane is v[c]. Each load waits for
+// itself.
+__device__ __forceinline__ void p8_ld16(uint32_t taddr, float* v) {  // 16 columns
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void p8_ld32(uint32_t taddr, float* v) {  // 32 columns
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void p8_st16(uint32_t taddr, const float* v) {  // 16 columns
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+        "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void p8_st_k(uint32_t taddr, const uint32_t* v) {  // 32 columns of two fp16
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+        "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
+        "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+// 16 lanes x 64 columns: in each group of 4 columns thread l holds column l % 4 of lanes l / 4 and l / 4 + 8.
+__device__ __forceinline__ void p8_st_v(uint32_t taddr, const uint32_t* v) {  // 64 columns of two fp16
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+        "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
+        "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
 }
 
-// One query row a CTA, 128 keys at a time: a thread a key for the scores, a thread a column for the sums.
-template <int D>
-__global__ void __launch_bounds__(128) paged_attn8_kernel(Pa8Params p, WsHeader* hdr) {
-  __shared__ float s_q[D], s_p[128], s_red[4];
-  __shared__ size_t s_row[128];
-  at_launch_order();
-  const int t = threadIdx.x;
-  const int h = blockIdx.x % p.Hq, node = blockIdx.x / p.Hq % p.n, b = blockIdx.x / p.Hq / p.n, kvh = h / p.G;
-  unsigned short* out = p.out + ((static_cast<size_t>(b) * p.n + node) * p.Hq + h) * D;
-  bool bad = false;
-  const int len = pa_length(p, b, &bad);
-  if (bad && t == 0) record_error(hdr, DT_ERR_INVALID_ARG);
-  if (t < D) s_q[t] = __uint_as_float(static_cast<uint32_t>(p.q[out - p.out + t]) << 16);
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (int k0 = 0; k0 < len; k0 += 128) {
-    const int key = k0 + t;
-    bool seen = key < len;
-    if (seen && key >= len - p.n) {
-      const int c = key - (len - p.n);
-      seen = p.mask ? p.mask[(static_cast<size_t>(b) * p.n + node) * p.n + c] != 0 : c <= node;
+__device__ __forceinline__ uint32_t p8_two(uint32_t codes) {  // the two e4m3 codes in the low half
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
+  return r;
+}
+__device__ __forceinline__ uint32_t p8_pack(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float p8_log2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Whether any thread of the group says so; everyone of the group comes here, by whole warps.
+__device__ __forceinline__ bool p8_any(int id, bool x) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x)), "r"(id)
+      : "memory");
+  return r != 0u;
+}
+__device__ __forceinline__ void p8_meet(int id) {
+  __syncwarp();
+  asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
+}
+// The warp's largest value of x; NaN counts for nothing.
+__device__ __forceinline__ float p8_warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The warp's sums of R values a lane: lane x returns that of value x / (32 / R).
+template <int R>
+__device__ __forceinline__ float p8_warp_sums(float (&v)[R], int lane) {
+#pragma unroll
+  for (int w = R / 2, h = 16; w >= 1; w /= 2, h /= 2) {
+    const bool up = (lane & h) != 0;
+#pragma unroll
+    for (int i = 0; i < w; ++i) {
+      const float got = __shfl_xor_sync(0xFFFFFFFFu, up ? v[i] : v[i + w], h);
+      v[i] = (up ? v[i + w] : v[i]) + got;
     }
-    float s = -INFINITY;
-    __syncthreads();
-    if (seen) {
-      int page = p.page_table[static_cast<size_t>(b) * p.max_pages + key / p.page_size];
-      if (page < 0 || page >= p.num_pages) {
-        record_error(hdr, DT_ERR_INVALID_ARG);
-        page = 0;
-      }
-      const int row = key % p.page_size;
-      const size_t plane = static_cast<size_t>(page) * p.Hkv + kvh, at = plane * p.page_size + row;
-      const size_t sc = plane * (p.page_size / p.block) + row / p.block;
-      s = 0.f;
-      for (int e = 0; e < D; ++e) s += s_q[e] * code_value(p.k_cache[at * D + e]);
-      s *= p.k_scale[sc] * p.scale * 1.4426950408889634f;
-      s_row[t] = at;
-    }
-    float mx = s;
-    for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
-    if (t % 32 == 0) s_red[t / 32] = mx;
-    __syncthreads();
-    mx = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
-    const float now = fmaxf(m, mx), ref = now == -INFINITY ? 0.f : now, a = exp2f(m - ref);
-    m = now;
-    const float w = seen ? exp2f(s - ref) : 0.f;
-    float sum = w;
-    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
-    __syncthreads();
-    if (t % 32 == 0) s_red[t / 32] = sum;
-    s_p[t] = seen ? w : -1.f;
-    __syncthreads();
-    l = l * a + (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
-    o *= a;
-    if (t < D)
-      for (int j = 0; j < 128; ++j)
-        if (!(s_p[j] < 0.f)) {
-          const size_t at = s_row[j], plane = at / p.page_size;
-          const float vs = p.v_scale[plane * (p.page_size / p.block) + at % p.page_size / p.block];
-          o += s_p[j] * vs * code_value(p.v_cache[at * D + t]);
-        }
   }
-  const bool none = l == 0.f && m == -INFINITY;
-  if (t < D) out[t] = static_cast<unsigned short>(at_pack(none ? 0.f : o / l, 0.f));
+#pragma unroll
+  for (int h = 16 / R; h >= 1; h /= 2) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], h);
+  return v[0];
+}
+// Where 16-byte piece c of row r of a block lies in its ring entry.
+template <int D>
+__device__ __forceinline__ uint32_t p8_piece(int r, int c) {
+  return D == 128 ? static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4))
+                  : static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+// The shape of one instance: N columns of query rows (R rounded up).
+template <int D, int N>
+struct P8 {
+  static constexpr int kGroups = N <= 32 ? 1 : 2;        // softmax groups of four warps
+  static constexpr int kThreads = 384 + 128 * kGroups;   // warps 0: load, 1: MMA, 2-3: queries, 4-7: keys, 8-11: values
+  static constexpr int kMine = N / kGroups;              // a softmax thread's query rows
+  static constexpr int kStep = kMine < 32 ? kMine : 32;  // taken at once
+  static constexpr int kSteps = kMine / kStep;
+  static constexpr int kOps = N <= 64 ? 2 : 1;           // buffers of keys, of values, of outputs, of weights
+  static constexpr uint32_t kEntry = kPaKeys * D;        // a ring entry: a block's keys or values
+  static constexpr uint32_t kQ = N * D * 2;              // a buffer of queries
+  static constexpr int kAtom = N < 64 ? N : 64;          // query rows in a row of the weights
+  static constexpr uint32_t kRowW = kAtom * 2;
+  static constexpr uint32_t kW = kPaKeys * N * 2;        // a buffer of weights
+  // tensor memory
+  static constexpr uint32_t kS = 0, kO = 2 * N, kK = kO + kOps * N, kV = kK + kOps * (D / 2);
+  static_assert(kV + kOps * 64 <= 512, "tensor memory");
+  static constexpr size_t kFixed = 1024 + 2 * kQ + kOps * kW + 4 * kPaKeys * sizeof(float2);
+};
+
+// Roles. Load: pages to the ring, as in the bf16 kernel. Queries: a segment's rows, each brought by a power of two to
+// 2^14 .. 2^15 and rounded to fp16, with the factor that undoes it; the nodes' mask, by keys. Keys: lane = key, its row's
+// codes to fp16 in tensor memory; its two scales, loaded two blocks ahead, for the softmax. Values: lane = column, two
+// keys a register: a transposing load of pairs of columns, a byte shuffle. Softmax: lane = key. MMA: the scores run one
+// block ahead of the outputs, through the segments.
+template <int D, int N>
+__global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8Params p, const __grid_constant__ Pa8Maps maps,
+                                                                            WsHeader* hdr) {
+  using C = P8<D, N>;
+  constexpr int kThreads = C::kThreads, kMine = C::kMine, kStep = C::kStep, kOps = C::kOps;
+  extern __shared__ float4 smem_f4[];
+  unsigned char* sq =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_f4) + 1023) & ~uintptr_t(1023));
+  unsigned char* sw = sq + 2 * C::kQ;
+  unsigned char* skv = sw + kOps * C::kW;
+  float2* s_scales = reinterpret_cast<float2*>(skv + p.stages * C::kEntry);  // [4][kPaKeys]: a key's, its value's
+  int* cum = reinterpret_cast<int*>(s_scales + 4 * kPaKeys);                 // [B + 1]
+  int* lens = cum + p.B + 1;                                                 // [B]
+  __shared__ uint64_t kv_full[kP8MaxStages], kv_empty[kP8MaxStages];
+  __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  __shared__ uint64_t s_full[2], w_full[2], o_done[2], q_full[2], o_free[2], s_meet;
+  __shared__ uint32_t s_tmem;
+  __shared__ unsigned s_kv_issued;
+  __shared__ int s_warp[kThreads / 32];
+  __shared__ int s_bad, s_joins;
+  __shared__ PaJoin s_join[2];
+  __shared__ __align__(16) float s_factor[2][N], s_nref[N], s_alpha[N], s_red[4][N];
+  __shared__ unsigned long long s_sees[2][kPaNodes];  // bit i: node i sees the key of node c
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const unsigned stages = static_cast<unsigned>(p.stages);
+  if (t == 0) {
+    for (unsigned i = 0; i < stages; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], 4);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 4);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&w_full[i], 4 * C::kGroups);
+      mbar_init(&o_done[i], 1);
+      mbar_init(&q_full[i], 2);
+      mbar_init(&o_free[i], 4 * C::kGroups);
+    }
+    mbar_init(&s_meet, 4 * C::kGroups);
+    mbar_fence_init();
+    s_kv_issued = 0u;
+    s_bad = s_joins = 0;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                 "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == 0 && lane < 2)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &maps.k : &maps.v) : "memory");
+  // rows of queries that there are not: zero, with a factor of zero
+  for (int i = t; i < static_cast<int>(2 * C::kQ / 16); i += kThreads)
+    if (static_cast<int>(i * 16 / 128) % N >= p.R) reinterpret_cast<uint4*>(sq)[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = t; i < 2 * N; i += kThreads) s_factor[i / N][i % N] = 0.f;
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  at_launch_order();
+  // the plan: block counts scanned over the requests; rows of requests without blocks are zero
+  int carry = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    const int b = b0 + t;
+    bool bad = false;
+    const int len = b < p.B ? pa_length(p, b, &bad) : 0;
+    if (bad && blockIdx.x == 0) record_error(hdr, DT_ERR_INVALID_ARG);
+    int total;
+    const int units = len > 0 ? (len + kPaKeys - 1) / kPaKeys + 1 : 0;
+    const int before = block_exclusive_scan<kThreads / 32>(units, &total, s_warp);
+    if (b < p.B) {
+      cum[b] = carry + before;
+      lens[b] = len;
+    }
+    carry += total;
+  }
+  if (t == 0) cum[p.B] = carry;
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = s_tmem;
+  const long long W = static_cast<long long>(carry) * p.Hkv;
+  for (int b = blockIdx.x; b < p.B; b += p.grid)
+    if (cum[b + 1] == cum[b]) {
+      uint4* o = reinterpret_cast<uint4*>(p.out + static_cast<size_t>(b) * p.n * p.Hq * D);
+      for (int i = t; i < p.n * p.Hq * (D / 8); i += kThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  bool ok = true;
+  const int ctas = W < p.grid ? static_cast<int>(W) : p.grid;  // that take a share: a block each at least
+  PaWalk w = pa_walk(p, cum, W, ctas);
+
+  if (warp == 0) {  // load: the whole warp, one page's box a lane
+    unsigned st = 0, par = 1u, e = 0;  // ring entry, the parity of its last release, entries so far
+    const int box_rows = p.page_size < kPaKeys ? p.page_size : kPaKeys;
+    const int per_block = kPaKeys / box_rows;  // pages a block spans (1 when a page holds whole blocks)
+    while (ok) {
+      const PaSeg sg = pa_next(p, cum, w);
+      if (sg.nblk == 0) break;
+      const int used = (lens[sg.b] + p.page_size - 1) / p.page_size;  // pages the request holds
+      const int32_t* table = p.page_table + static_cast<size_t>(sg.b) * p.max_pages;
+      // page ids, 32 at a time and one window ahead
+      int win = static_cast<int>(static_cast<long long>(sg.j0) * kPaKeys / p.page_size) / 32;
+      int cur = 32 * win + lane < used ? table[32 * win + lane] : 0;
+      int nxt = 32 * (win + 1) + lane < used ? table[32 * (win + 1) + lane] : 0;
+      for (int j = 0; j < sg.nblk && ok; ++j) {
+        const int key = (sg.j0 + j) * kPaKeys, first = key / p.page_size, row = key % p.page_size;
+        if (first / 32 != win) {
+          ++win;
+          cur = nxt;
+          nxt = 32 * (win + 1) + lane < used ? table[32 * (win + 1) + lane] : 0;
+        }
+        const int pages = used - first < per_block ? used - first : per_block;
+        int page = __shfl_sync(0xFFFFFFFFu, cur, (first + lane) & 31);
+        if (lane < pages && (page < 0 || page >= p.num_pages)) {
+          record_error(hdr, DT_ERR_INVALID_ARG);
+          page = 0;
+        }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {  // the keys, then the values
+          if (ok && e >= stages) ok = __all_sync(0xFFFFFFFFu, at_wait(&kv_empty[st], par));
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(&kv_full[st], static_cast<uint32_t>(pages * box_rows * D));
+          __syncwarp();
+          if (lane < pages)
+            tma_load_3d(skv + st * C::kEntry + lane * box_rows * D, kv ? &maps.v : &maps.k, 0, row,
+                        page * p.Hkv + sg.kvh, &kv_full[st]);
+          ++e;
+          if (lane == 0) s_kv_issued = e;
+          if (++st == stages) {
+            st = 0;
+            par ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (elect_one()) {  // MMA
+      const uint32_t id_s = umma_idesc_f16(N), id_o = umma_idesc_f16(N) | (1u << 16);  // O: the weights MN-major
+      const uint64_t dq = umma_desc_sw128(smem_u32(sq));
+      const uint64_t dw = umma_desc_mn(smem_u32(sw), C::kRowW, kPaKeys * 128);
+      auto wait = [&](uint64_t* bar, unsigned parity) {
+        const bool done = at_wait(bar, parity);
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        return done;
+      };
+      PaWalk ws = w;
+      PaSeg ss{};
+      int js = 0, sis = -1;
+      unsigned gs = 0;
+      auto scores = [&]() {  // of the next block, if there is one
+        if (js == ss.nblk) {
+          ss = pa_next(p, cum, ws);
+          js = 0;
+          if (ss.nblk == 0) return true;
+          ++sis;
+          if (!wait(&q_full[sis & 1], static_cast<unsigned>(sis >> 1) & 1u)) return false;
+        }
+        const unsigned kb = gs % kOps;
+        if (!wait(&k_full[kb], (gs / kOps) & 1u)) return false;
+        const uint64_t q0 = dq + static_cast<uint64_t>((sis & 1) * (C::kQ >> 4));
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_f16_ts(tmem + C::kS + (gs & 1u) * N, tmem + C::kK + kb * (D / 2) + 8u * kk,
+                      q0 + (((kk >> 2) * N * 128u + (kk & 3) * 32u) >> 4), id_s, kk > 0 ? 1u : 0u);
+        umma_commit(&k_empty[kb]);
+        umma_commit(&s_full[gs & 1u]);
+        ++js;
+        ++gs;
+        return true;
+      };
+      unsigned g = 0;
+      ok = scores();
+      for (int si = 0; ok; ++si) {
+        const PaSeg sg = pa_next(p, cum, w);
+        if (sg.nblk == 0) break;
+        const unsigned ob = static_cast<unsigned>(si) % kOps;
+        for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
+          // its buffer was freed by block g - 1's softmax (waited for below, one block ago)
+          ok = scores();
+          if (ok && j == 0 && si >= kOps) {  // the segment that had the buffer before has been read
+            const int was = si - kOps;
+            ok = wait(&o_free[was & 1], static_cast<unsigned>(was >> 1) & 1u);
+          }
+          const unsigned vb = g % kOps;
+          if (ok) ok = wait(&v_full[vb], (g / kOps) & 1u);
+          if (ok) ok = wait(&w_full[g & 1u], (g >> 1) & 1u);
+          if (!ok) break;
+#pragma unroll
+          for (int kk = 0; kk < kPaKeys / 16; ++kk)
+            umma_f16_ts(tmem + C::kO + ob * N, tmem + C::kV + vb * 64u + 8u * kk,
+                        dw + ((vb * C::kW + kk * 16u * C::kRowW) >> 4), id_o, (j > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&v_empty[vb]);
+          umma_commit(&o_done[g & 1u]);
+        }
+      }
+    }
+  } else if (warp < 4) {  // queries
+    const int who = warp - 2;
+    for (int si = 0; ok; ++si) {
+      const PaSeg sg = pa_next(p, cum, w);
+      if (sg.nblk == 0) break;
+      const unsigned qb = static_cast<unsigned>(si) & 1u;
+      // the segment that had the buffer before is over: its factors and its mask are not read any more
+      if (si >= 2) ok = __all_sync(0xFFFFFFFFu, at_wait(&o_free[qb], static_cast<unsigned>((si >> 1) - 1) & 1u));
+      if (!ok) break;
+      const int c = 32 * who + lane;
+      if (c < p.n) {
+        unsigned long long bits = ~0ull << c;
+        if (p.mask) {
+          const uint8_t* col = p.mask + static_cast<size_t>(sg.b) * p.n * p.n + c;
+          bits = 0ull;
+#pragma unroll 8
+          for (int i = 0; i < p.n; ++i) bits |= static_cast<unsigned long long>(col[static_cast<size_t>(i) * p.n] != 0) << i;
+        }
+        s_sees[qb][c] = bits;
+      }
+      unsigned char* qd = sq + qb * C::kQ;
+      constexpr int kEach = D / 32, kAtOnce = 8;  // a lane's elements of a row; rows in flight
+      for (int r0 = who; r0 < p.R; r0 += 2 * kAtOnce) {
+        uint32_t x[kAtOnce][kEach / 2];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int r = r0 + 2 * u;
+          if (r < p.R) {
+            const unsigned short* src =
+                p.q + ((static_cast<size_t>(sg.b) * p.n + r / p.G) * p.Hq + sg.kvh * p.G + r % p.G) * D + kEach * lane;
+            if constexpr (D == 128) {
+              const uint2 y = *reinterpret_cast<const uint2*>(src);
+              x[u][0] = y.x;
+              x[u][kEach / 2 - 1] = y.y;
+            } else {
+              x[u][0] = *reinterpret_cast<const uint32_t*>(src);
+            }
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int r = r0 + 2 * u;
+          if (r >= p.R) break;
+          float f[kEach];
+          unsigned most = 0u;  // the bits of the largest finite element
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) {
+            f[i] = __uint_as_float(i & 1 ? x[u][i / 2] & 0xFFFF0000u : x[u][i / 2] << 16);
+            const unsigned m = __float_as_uint(f[i]) & 0x7FFFFFFFu;
+            if (m < 0x7F800000u && m > most) most = m;
+          }
+          most = __reduce_max_sync(0xFFFFFFFFu, most);
+          int up = 14 - (static_cast<int>(most >> 23) - 127);
+          if (up > 100) up = 100;  // (nothing is lost: such a row's scores are zero whatever the keys are)
+          const float by = __uint_as_float(static_cast<unsigned>(up + 127) << 23);
+          uint32_t h[kEach / 2];
+#pragma unroll
+          for (int i = 0; i < kEach / 2; ++i) h[i] = p8_pack(f[2 * i] * by, f[2 * i + 1] * by);
+          if constexpr (D == 128) {
+            unsigned char* at = qd + (lane >> 4) * (N * 128) + r * 128 + ((((lane & 15) >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8;
+            *reinterpret_cast<uint2*>(at) = make_uint2(h[0], h[kEach / 2 - 1]);
+          } else {
+            *reinterpret_cast<uint32_t*>(qd + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) = h[0];
+          }
+          if (lane == 0) s_factor[qb][r] = p.scale_log2 * __uint_as_float(static_cast<unsigned>(127 - up) << 23);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads Q through the async proxy
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[qb]);
+    }
+  } else if (warp < 8) {  // keys
+    const int row = 32 * (warp & 3) + lane;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    unsigned g = 0;
+    for (;ok;) {
+      const PaSeg sg = pa_next(p, cum, w);
+      if (sg.nblk == 0) break;
+      const int len = lens[sg.b], spp = p.page_size / p.block;
+      const int32_t* table = p.page_table + static_cast<size_t>(sg.b) * p.max_pages;
+      // a key's page id is read two blocks ahead of its use, its scales one
+      auto page_of = [&](int j) {
+        const int key = (sg.j0 + j) * kPaKeys + row;
+        return j < sg.nblk && key < len ? table[key / p.page_size] : -1;
+      };
+      auto scales_of = [&](int j, int page) {
+        const int key = (sg.j0 + j) * kPaKeys + row;
+        if (page < 0 || page >= p.num_pages) return make_float2(0.f, 0.f);  // no key (or reported by the load)
+        const size_t at = (static_cast<size_t>(page) * p.Hkv + sg.kvh) * spp + key % p.page_size / p.block;
+        return make_float2(p.k_scale[at], p.v_scale[at]);
+      };
+      float2 here = scales_of(0, page_of(0));
+      int next_page = page_of(1);
+      for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
+        const float2 next = j + 1 < sg.nblk ? scales_of(j + 1, next_page) : make_float2(0.f, 0.f);
+        next_page = page_of(j + 2);
+        const unsigned e = 2u * g, at = e % stages, kb = g % kOps;
+        ok = __all_sync(0xFFFFFFFFu, at_wait(&kv_full[at], (e / stages) & 1u));
+        if (!ok) break;
+        const uint32_t src = smem_u32(skv + at * C::kEntry);
+        uint32_t r[D / 2];
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t x[4];
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                       : "r"(src + p8_piece<D>(row, c)));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            r[8 * c + 2 * i] = p8_two(x[i]);
+            r[8 * c + 2 * i + 1] = p8_two(x[i] >> 16);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kv_empty[at]);
+        if (g >= kOps) {
+          ok = __all_sync(0xFFFFFFFFu, at_wait(&k_empty[kb], (g / kOps - 1) & 1u));
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        }
+        s_scales[(g & 3u) * kPaKeys + row] = here;  // the softmax of block g - 4 is through: its scores' buffer was reused
+        const uint32_t to = tmem + lanes + C::kK + kb * (D / 2);
+        p8_st_k(to, r);
+        if constexpr (D == 128) p8_st_k(to + 32u, r + 32);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_full[kb]);
+        here = next;
+      }
+    }
+  } else if (warp < 12) {  // values
+    constexpr int kParts = D / 64;  // pieces of 16 columns a warp has
+    const int part0 = (warp & 3) * kParts;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const int ldrow = lane;  // of 32 keys: matrix lane / 8, row lane % 8
+    unsigned g = 0;
+    for (int si = 0; ok; ++si) {
+      const PaSeg sg = pa_next(p, cum, w);
+      if (sg.nblk == 0) break;
+      const int len = lens[sg.b], common = pa_common(p, len);
+      for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
+        const unsigned e = 2u * g + 1u, at = e % stages, vb = g % kOps;
+        const int kbase = (sg.j0 + j) * kPaKeys;
+        ok = __all_sync(0xFFFFFFFFu, at_wait(&kv_full[at], (e / stages) & 1u));
+        if (!ok) break;
+        const uint32_t src = smem_u32(skv + at * C::kEntry);
+        bool found = false;
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) {
+          uint32_t r[32];
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            uint32_t x[4];
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                         : "r"(src + p8_piece<D>(32 * kk + ldrow, part0 + h))
+                         : "memory");
+            if (kbase + kPaKeys > common) {
+              // A weight of zero does not hide a NaN from the tensor cores. Rows past the request's end are cleared; a NaN
+              // among the nodes' codes is cleared here and given to the rows that see it at the end.
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                const int key = kbase + 32 * kk + 8 * m + 2 * (lane & 3);
+                if (key + 1 >= len) x[m] &= key >= len ? 0u : 0xFFFFu;
+                const uint32_t nodes = (key >= common ? 0xFFFFu : 0u) | (key + 1 >= common ? 0xFFFF0000u : 0u);
+                const uint32_t nan = __vcmpeq4(x[m] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) & nodes;
+                if (nan) {
+                  x[m] &= ~nan;
+                  found = true;
+                }
+              }
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const uint32_t y = __byte_perm(x[m], 0u, 0x3120);  // two keys of a column, then of the next
+              r[2 * (4 * kk + m)] = p8_two(y);
+              r[2 * (4 * kk + m) + 1] = p8_two(y >> 16);
+            }
+          }
+          if (h == kParts - 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&kv_empty[at]);
+          }
+          if (h == 0 && g >= kOps) {
+            ok = __all_sync(0xFFFFFFFFu, at_wait(&v_empty[vb], (g / kOps - 1) & 1u));
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          }
+          p8_st_v(tmem + lanes + (static_cast<uint32_t>(16 * h) << 16) + C::kV + vb * 64u, r);
+        }
+        if (!ok) break;
+        if (found) atomicMax(&s_bad, si + 1);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_full[vb]);
+      }
+    }
+  } else {  // softmax
+    const int group = (warp - 12) >> 2, quad = warp & 3, row = 32 * quad + lane;  // the thread's key of a block
+    const int bar = 1 + group, first = group * kMine, mine = t - (384 + 128 * group);
+    const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+    // the column that the thread's lane of the outputs is, and the pair of columns that it writes
+    const int column = D / 4 * quad + 16 * (lane >> 4) + 2 * (lane & 7) + ((lane >> 3) & 1);
+    const bool has_column = D == 128 || lane < 16;
+    unsigned g = 0, meet = 0;
+    bool failed = false;  // a wait ran out; the group leaves together, at its next meeting
+    for (int si = 0; ok; ++si) {
+      const PaSeg sg = pa_next(p, cum, w);
+      if (sg.nblk == 0) break;
+      const unsigned qb = static_cast<unsigned>(si) & 1u;
+      const uint32_t to = tmem + lanes + C::kO + (static_cast<unsigned>(si) % kOps) * N + first;
+      const int len = lens[sg.b], pre = len - p.n, common = pa_common(p, len);
+      constexpr int kSums = kMine <= 32 ? kMine : kMine / 32;
+      float l[kSums];
+#pragma unroll
+      for (int i = 0; i < kSums; ++i) l[i] = 0.f;
+      if (mine < kMine) s_nref[first + mine] = kAtNone;
+      p8_meet(bar);
+      for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
+        const uint32_t ts = tmem + lanes + C::kS + (g & 1u) * N + first;
+        if (!at_wait(&s_full[g & 1u], (g >> 1) & 1u)) failed = true;
+        __syncwarp();
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const float2 scales = s_scales[(g & 3u) * kPaKeys + row];
+        const float log_vs = fmaxf(p8_log2(fabsf(scales.y)), kP8LeastScale);
+        const int key = (sg.j0 + j) * kPaKeys + row;
+        const bool masked = (sg.j0 + j + 1) * kPaKeys > common;
+        unsigned long long sees = ~0ull;  // bit i: row first + i sees the key
+        if (masked && key >= pre) {
+          sees = 0ull;
+          if (key < len) {
+            const unsigned long long nodes = s_sees[qb][key - pre];
+            int node = first / p.G, rem = first % p.G;
+            for (int i = 0; i < kMine; ++i) {
+              sees |= ((nodes >> (node & 63)) & 1ull) << i;
+              if (++rem == p.G) {
+                rem = 0;
+                ++node;
+              }
+            }
+          }
+        }
+        const float value_scale = sees == 0ull ? 0.f : scales.y;
+        __syncwarp();
+        // kStep scores from the step's first row on, scaled, against the reference
+        float x[kStep];
+        auto load = [&](int step, bool against) {
+          if constexpr (kStep == 16) p8_ld16(ts, x);
+          else p8_ld32(ts + 32u * step, x);
+          const float* factor = &s_factor[qb][first + kStep * step];
+          const float* nref = &s_nref[first + kStep * step];
+#pragma unroll
+          for (int i = 0; i < kStep; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(factor + i);
+            float4 n4 = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (against) n4 = *reinterpret_cast<const float4*>(nref + i);
+            x[i] = fmaf(x[i], f.x * scales.x, n4.x);
+            x[i + 1] = fmaf(x[i + 1], f.y * scales.x, n4.y);
+            x[i + 2] = fmaf(x[i + 2], f.z * scales.x, n4.z);
+            x[i + 3] = fmaf(x[i + 3], f.w * scales.x, n4.w);
+          }
+          if (masked) {
+            const unsigned bits = static_cast<unsigned>(sees >> (kStep * step));
+#pragma unroll
+            for (int i = 0; i < kStep; ++i)
+              if (!((bits >> i) & 1u)) x[i] = -INFINITY;
+          }
+        };
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int step = 0; step < C::kSteps; ++step) {
+          load(step, true);
+#pragma unroll
+          for (int i = 0; i < kStep; i += 2) top = at_max3(top, x[i], x[i + 1]);
+        }
+        if (p8_any(bar, top + log_vs > kP8Most || failed)) {  // rare: raise references
+          if (p8_any(bar, failed)) {
+            ok = false;
+            break;
+          }
+#pragma unroll 1
+          for (int step = 0; step < C::kSteps; ++step) {
+            load(step, false);
+            float keep = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kStep; ++i) {
+              const float m = p8_warp_max(x[i] + log_vs);
+              if (lane == i) keep = m;
+            }
+            if (lane < kStep) s_red[quad][first + kStep * step + lane] = keep;
+          }
+          p8_meet(bar);
+          if (mine < kMine) {
+            const int r = first + mine;
+            const float m = fmaxf(fmaxf(s_red[0][r], s_red[1][r]), fmaxf(s_red[2][r], s_red[3][r]));
+            const float was = s_nref[r];
+            const bool raise = m + was > kP8Most;
+            const float now = kP8Start - m;
+            s_alpha[r] = raise ? at_exp2(now - was) : 1.f;  // from nothing: 0
+            if (raise) s_nref[r] = now;
+          }
+          p8_meet(bar);
+          if constexpr (kMine <= 32) {
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) l[i] *= s_alpha[first + i];
+          } else {
+#pragma unroll
+            for (int i = 0; i < kSums; ++i) l[i] *= s_alpha[first + 32 * i + lane];
+          }
+          if (j > 0) {
+            if (!at_wait(&o_done[(g - 1u) & 1u], ((g - 1u) >> 1) & 1u)) failed = true;
+            __syncwarp();
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll 1
+            for (int i0 = 0; i0 < kMine; i0 += 16) {
+              float o[16];
+              p8_ld16(to + i0, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= s_alpha[first + i0 + i];
+              p8_st16(to + i0, o);
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          }
+          if constexpr (C::kSteps == 1) load(0, true);
+        }
+        const unsigned wb = g % kOps;
+        if (g >= kOps) {  // the product that read the buffer before is done
+          const unsigned was = g - kOps;
+          if (!at_wait(&o_done[was & 1u], (was >> 1) & 1u)) failed = true;
+          __syncwarp();
+        }
+        unsigned char* wrow = sw + wb * C::kW + row * C::kRowW;
+#pragma unroll
+        for (int step = 0; step < C::kSteps; ++step) {
+          if constexpr (C::kSteps > 1) load(step, true);
+          float sums[kStep];
+          uint32_t h[kStep / 2];
+#pragma unroll
+          for (int i = 0; i < kStep; i += 2) {
+            const float a = at_exp2(x[i]), b = at_exp2(x[i + 1]);
+            if constexpr (kMine <= 32) {
+              l[i] += a;
+              l[i + 1] += b;
+            } else {
+              sums[i] = a;
+              sums[i + 1] = b;
+            }
+            h[i / 2] = p8_pack(a * value_scale, b * value_scale);
+          }
+          if constexpr (kMine > 32) l[step] += p8_warp_sums(sums, lane);
+#pragma unroll
+          for (int c = 0; c < kStep / 8; ++c) {
+            const int r = first + kStep * step + 8 * c, atom = r / C::kAtom, piece = r % C::kAtom / 8;
+            const int turn = C::kRowW == 128 ? row & 7 : C::kRowW == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
+            *reinterpret_cast<uint4*>(wrow + atom * (kPaKeys * 128) + ((piece ^ turn) << 4)) =
+                make_uint4(h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads the weights through the async proxy
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&w_full[g & 1u]);
+      }
+      if (!ok) break;
+      // the segment's outputs
+      if (!at_wait(&o_done[(g - 1u) & 1u], ((g - 1u) >> 1) & 1u)) failed = true;
+      ok = !p8_any(bar, failed);
+      if (!ok) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      // the sums over the keys: by warps, then over the four
+      if constexpr (kMine <= 32) {
+        const float sum = p8_warp_sums(l, lane);
+        if (lane % (32 / kMine) == 0) s_red[quad][first + lane / (32 / kMine)] = sum;
+      } else {
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) s_red[quad][first + 32 * i + lane] = l[i];
+      }
+      p8_meet(bar);
+      const bool whole = sg.nblk == sg.nb;
+      const size_t unit = 2 * static_cast<size_t>(blockIdx.x) + (sg.j0 == 0 ? 1 : 0);
+      if (mine < kMine) {
+        const int r = first + mine;
+        const float sum = (s_red[0][r] + s_red[1][r]) + (s_red[2][r] + s_red[3][r]);
+        float inv = 1.f / sum;
+        if (sum == 0.f && pre == 0 && r < p.R) {  // no visible key at all: zero; visible keys of weight 0 alone: NaN
+          bool any = false;
+          for (int c = 0; c < p.n; ++c) any = any || ((s_sees[qb][c] >> (r / p.G)) & 1ull);
+          if (!any) inv = 0.f;
+        }
+        s_alpha[r] = whole ? inv : 1.f;
+        if (!whole && r < p.R) {
+          const float nref = s_nref[r];
+          *reinterpret_cast<float2*>(p.ml + 2 * (unit * p.R + r)) = make_float2(nref == kAtNone ? -INFINITY : -nref, sum);
+        }
+      }
+      p8_meet(bar);
+      const bool bad = *reinterpret_cast<volatile int*>(&s_bad) > si;  // (a later segment's mark counts too: only slower)
+#pragma unroll 1
+      for (int i0 = 0; i0 < kMine; i0 += 16) {
+        float o[16];
+        __syncwarp();
+        p8_ld16(to + i0, o);
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        if (first + i0 >= p.R) continue;
+        if (bad && has_column) {  // rare: NaN among the nodes' codes
+          for (int c = 0; c < p.n; ++c) {
+            const int key = pre + c;
+            if (key < sg.j0 * kPaKeys || key >= (sg.j0 + sg.nblk) * kPaKeys) continue;
+            const int page = p.page_table[static_cast<size_t>(sg.b) * p.max_pages + key / p.page_size];
+            if (page < 0 || page >= p.num_pages) continue;
+            const unsigned char code =
+                p.v_cache[((static_cast<size_t>(page) * p.Hkv + sg.kvh) * p.page_size + key % p.page_size) * D + column];
+            if ((code & 0x7Fu) != 0x7Fu) continue;
+            const unsigned long long nodes = s_sees[qb][c];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if ((nodes >> (((first + i0 + i) / p.G) & 63)) & 1ull) o[i] = NAN;
+          }
+        }
+        // lanes 8 apart hold neighbouring columns: one of them takes both of a row, the other those of the next row
+        const bool odd = (lane & 8) != 0;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const int r = first + i0 + i + (odd ? 1 : 0);
+          const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? o[i] : o[i + 1], 8);
+          const float lo = odd ? got : o[i], hi = odd ? o[i + 1] : got, by = s_alpha[first + i0 + i + (odd ? 1 : 0)];
+          if (r >= p.R || !has_column) continue;
+          const int at = column & ~1;
+          if (whole) {
+            *reinterpret_cast<uint32_t*>(
+                p.out + ((static_cast<size_t>(sg.b) * p.n + r / p.G) * p.Hq + sg.kvh * p.G + r % p.G) * D + at) =
+                at_pack(lo * by, hi * by);
+          } else {
+            *reinterpret_cast<float2*>(p.part + (unit * p.R + r) * D + at) = make_float2(lo, hi);
+          }
+        }
+      }
+      p8_meet(bar);  // everyone is through with the segment's factors, mask and outputs
+      if (lane == 0) mbar_arrive(&o_free[qb]);
+      if (whole) continue;
+      // the pair's last segment to finish joins them all, once the CTA is through its share
+      const int c0 = pa_owner(sg.pair0, W, ctas), c1 = pa_owner(sg.pair0 + sg.nb - 1, W, ctas);
+      bool met = pa_sync(&s_meet, meet, lane);  // the ticket's release covers what the other warps wrote before it
+      ok = !p8_any(bar, !met);
+      if (!ok) break;
+      if (t == 384) {
+        // a pair's ticket is a byte: it counts to the grid at most, and goes back to zero before it is used again
+        const int shift = 8 * (c0 & 3);
+        const unsigned done = ((atom_add_acq_rel_gpu(hdr->tickets + c0 / 4, 1u << shift) >> shift) & 0xFFu) + 1u;
+        if (done == static_cast<unsigned>(c1 - c0 + 1)) {
+          atomicSub(hdr->tickets + c0 / 4, done << shift);  // ready for the next call
+          s_join[s_joins++] = PaJoin{sg.b, sg.kvh, c0, c1};
+        }
+      }
+    }
+  }
+  ok = __syncthreads_and(ok);
+  if (!ok && t == 0) {
+    record_error(hdr, DT_ERR_TIMEOUT);
+    // copies issued must land before the CTA leaves: wait for the last of each entry too (bounded)
+    const unsigned from = s_kv_issued > stages ? s_kv_issued - stages : 0u;
+    for (unsigned e = from; e < s_kv_issued; ++e) mbar_wait(&kv_full[e % stages], (e / stages) & 1u, kAtBudgetNs);
+  }
+  if (ok) {
+    // the ticket's thread acquired the others' partials; the barrier above passed them on
+    for (int i = 0; i < s_joins; ++i) {
+      PaSum* red = reinterpret_cast<PaSum*>(skv);  // the ring is empty by now
+      if (p.R * (D / 4) <= kThreads) pa_join<D, 1, kThreads>(p, s_join[i], red);
+      else pa_join<D, 4, kThreads>(p, s_join[i], red);
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+template <int D, int N>
+dt_status pa8_launch(Pa8Params& p, const Pa8Maps& maps, WsHeader* hdr, cudaStream_t stream) {
+  using C = P8<D, N>;
+  const size_t fixed = C::kFixed + align_up(sizeof(int) * (2 * p.B + 1), 16);
+  const int fit = static_cast<int>((kPa8SmemCap - fixed) / C::kEntry);
+  p.stages = fit > kP8MaxStages ? kP8MaxStages : fit;
+  const size_t smem = fixed + static_cast<size_t>(p.stages) * C::kEntry;
+  if (ensure_dynamic_smem(reinterpret_cast<const void*>(paged_attn8_kernel<D, N>), kPa8SmemCap) != cudaSuccess)
+    return DT_ERR_CUDA;
+  return at_launch(paged_attn8_kernel<D, N>, p.grid, C::kThreads, smem, stream, p, maps, hdr);
+}
+template <int D>
+dt_status pa8_pick(Pa8Params& p, const Pa8Maps& maps, WsHeader* hdr, cudaStream_t stream) {
+  if (p.R <= 16) return pa8_launch<D, 16>(p, maps, hdr, stream);
+  if (p.R <= 32) return pa8_launch<D, 32>(p, maps, hdr, stream);
+  if (p.R <= 64) return pa8_launch<D, 64>(p, maps, hdr, stream);
+  return pa8_launch<D, 128>(p, maps, hdr, stream);
 }
 
 }  // namespace
@@ -140,12 +916,20 @@ extern "C" dt_status dt_paged_attention8(int B, int n, int Hq, int Hkv, int d, c
   p.B = B; p.n = n; p.Hq = Hq; p.Hkv = Hkv; p.G = G; p.R = G * n; p.grid = P.grid;
   p.page_size = page_size; p.num_pages = num_pages; p.max_pages = max_pages; p.block = scale_block;
   p.q = static_cast<const unsigned short*>(q);
-  p.k_cache = static_cast<const unsigned char*>(k_cache);
   p.v_cache = static_cast<const unsigned char*>(v_cache);
   p.k_scale = k_scale; p.v_scale = v_scale;
-  p.page_table = page_table; p.lens = lens; p.mask = mask; p.scale = scale;
+  p.page_table = page_table; p.lens = lens; p.mask = mask;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  char* ws = static_cast<char*>(workspace);
+  p.part = reinterpret_cast<float*>(ws + P.part);
+  p.ml = reinterpret_cast<float*>(ws + P.ml);
   p.out = static_cast<unsigned short*>(out);
-  WsHeader* hdr = static_cast<WsHeader*>(workspace);
-  return d == 64 ? at_launch(paged_attn8_kernel<64>, B * n * Hq, 128, 0, stream, p, hdr)
-                 : at_launch(paged_attn8_kernel<128>, B * n * Hq, 128, 0, stream, p, hdr);
+  Pa8Maps maps{};
+  const uint64_t planes = static_cast<uint64_t>(num_pages) * static_cast<uint64_t>(Hkv);
+  const uint32_t box = page_size < kPaKeys ? static_cast<uint32_t>(page_size) : kPaKeys;
+  if (!encode_u8_rows(&maps.k, k_cache, static_cast<uint64_t>(d), static_cast<uint64_t>(page_size), planes, box) ||
+      !encode_u8_rows(&maps.v, v_cache, static_cast<uint64_t>(d), static_cast<uint64_t>(page_size), planes, box))
+    return DT_ERR_CUDA;
+  WsHeader* hdr = reinterpret_cast<WsHeader*>(ws);
+  return d == 64 ? pa8_pick<64>(p, maps, hdr, stream) : pa8_pick<128>(p, maps, hdr, stream);
 }

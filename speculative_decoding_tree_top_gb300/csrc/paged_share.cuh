@@ -99,6 +99,13 @@ __device__ __forceinline__ PaSeg pa_next(const PaWork& p, const int* cum, PaWalk
   return s;
 }
 
+// The softmax warps meet (a barrier whose wait is bounded); `count` is the meetings so far, the same in every warp.
+__device__ __forceinline__ bool pa_sync(uint64_t* bar, unsigned& count, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+  return __all_sync(0xFFFFFFFFu, at_wait(bar, count++ & 1u));
+}
+
 // A cut pair's segments are those of CTAs c0 .. c1. A CTA's slot 1 holds the segment that starts its pair, slot 0 one
 // that goes on with another CTA's.
 struct PaJoin {

@@ -40,6 +40,16 @@ __device__ __forceinline__ void umma_f16(uint32_t tmem_d, uint64_t da, uint64_t 
                "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
                ::"r"(tmem_d), "l"(da), "l"(db), "r"(idesc), "r"(acc) : "memory");
 }
+__device__ __forceinline__ uint32_t umma_idesc_f16(int n, int m = 128) {  // f16 x f16 -> fp32, both K-major
+  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+// MN-major tile of one swizzle atom's width: rows of `row_bytes` (32, 64 or 128, swizzled over that width) hold row_bytes / 2
+// elements of N, eight K rows per atom; `mn_stride` bytes to the next atom along N, when there is one.
+__device__ __forceinline__ uint64_t umma_desc_mn(uint32_t saddr, uint32_t row_bytes, uint32_t mn_stride) {
+  const uint64_t mode = row_bytes == 128 ? 2 : row_bytes == 64 ? 4 : 6;
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((mn_stride >> 4) & 0x3FFFu) << 16) |
+         (static_cast<uint64_t>((8 * row_bytes) >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (mode << 61);
+}
 // One lane of a warp that is together. Code behind a branch on it keeps the operands of tcgen05.mma in uniform registers;
 // behind a branch on a lane's number they are moved there for every instruction (alone on an SM, a product with both
 // operands in shared memory issues every 40 cycles instead of 46, one with the left operand in tensor memory every 32
@@ -178,6 +188,21 @@ inline bool encode_bf16_atoms(CUtensorMap* m, const void* ptr, uint64_t cols, ui
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), gdim, gstride, box, estride,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Planes of `rows` rows of `cols` (64 or 128) bytes (dense), read in boxes of whole rows, `box_rows` of one plane, swizzled
+// over the row's width.
+inline bool encode_u8_rows(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t planes,
+                           uint32_t box_rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (!encode) return false;
+  const cuuint64_t gdim[3] = {cols, rows, planes};
+  const cuuint64_t gstride[2] = {cols, cols * rows};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(cols), box_rows, 1};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), gdim, gstride, box, estride,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // A 4-D bf16 tensor map over a dense [d3][d2][d1][d0] array (d0 innermost), read in boxes of b0 x b1 x b2 x 1 with
