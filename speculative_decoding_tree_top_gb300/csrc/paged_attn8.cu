@@ -32,10 +32,11 @@ constexpr float kP8Start = 6.f, kP8Most = 14.f;
 constexpr float kP8LeastScale = -64.f;  // log2: smaller scales of values do not pull the reference further down
 
 struct Pa8Params : PaWork {
-  int stages, block;                // block: rows of a page that share a scale
+  int stages;
+  int page_shift, block_shift;      // log2 of the rows of a page, and of those that share a scale
   const unsigned short* q;          // [B][n][Hq][D]
   const unsigned char* v_cache;     // re-read only for codes that are NaN
-  const float *k_scale, *v_scale;   // [num_pages][Hkv][page_size / block]
+  const float *k_scale, *v_scale;   // [num_pages][Hkv][page_size >> block_shift]
   float scale_log2;                 // scale * log2(e)
 };
 struct Pa8Maps {
@@ -100,6 +101,11 @@ __device__ __forceinline__ uint32_t p8_pack(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+__device__ __forceinline__ uint64_t p8_mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 __device__ __forceinline__ float p8_log2(float x) {
   float y;
@@ -272,14 +278,14 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
     while (ok) {
       const PaSeg sg = pa_next(p, cum, w);
       if (sg.nblk == 0) break;
-      const int used = (lens[sg.b] + p.page_size - 1) / p.page_size;  // pages the request holds
+      const int used = (lens[sg.b] + p.page_size - 1) >> p.page_shift;  // pages the request holds
       const int32_t* table = p.page_table + static_cast<size_t>(sg.b) * p.max_pages;
       // page ids, 32 at a time and one window ahead
-      int win = static_cast<int>(static_cast<long long>(sg.j0) * kPaKeys / p.page_size) / 32;
+      int win = ((sg.j0 * kPaKeys) >> p.page_shift) / 32;
       int cur = 32 * win + lane < used ? table[32 * win + lane] : 0;
       int nxt = 32 * (win + 1) + lane < used ? table[32 * (win + 1) + lane] : 0;
       for (int j = 0; j < sg.nblk && ok; ++j) {
-        const int key = (sg.j0 + j) * kPaKeys, first = key / p.page_size, row = key % p.page_size;
+        const int key = (sg.j0 + j) * kPaKeys, first = key >> p.page_shift, row = key & (p.page_size - 1);
         if (first / 32 != win) {
           ++win;
           cur = nxt;
@@ -444,21 +450,22 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
   } else if (warp < 8) {  // keys
     const int row = 32 * (warp & 3) + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    unsigned g = 0;
-    for (;ok;) {
+    unsigned g = 0, at = 0, par = 0;  // its entries are every other one
+    while (ok) {
       const PaSeg sg = pa_next(p, cum, w);
       if (sg.nblk == 0) break;
-      const int len = lens[sg.b], spp = p.page_size / p.block;
+      const int len = lens[sg.b], per_page = p.page_shift - p.block_shift;  // log2 of the scales of a page and head
       const int32_t* table = p.page_table + static_cast<size_t>(sg.b) * p.max_pages;
       // a key's page id is read two blocks ahead of its use, its scales one
       auto page_of = [&](int j) {
         const int key = (sg.j0 + j) * kPaKeys + row;
-        return j < sg.nblk && key < len ? table[key / p.page_size] : -1;
+        return j < sg.nblk && key < len ? table[key >> p.page_shift] : -1;
       };
       auto scales_of = [&](int j, int page) {
         const int key = (sg.j0 + j) * kPaKeys + row;
         if (page < 0 || page >= p.num_pages) return make_float2(0.f, 0.f);  // no key (or reported by the load)
-        const size_t at = (static_cast<size_t>(page) * p.Hkv + sg.kvh) * spp + key % p.page_size / p.block;
+        const size_t at = ((static_cast<size_t>(page) * p.Hkv + sg.kvh) << per_page) +
+                          ((key & (p.page_size - 1)) >> p.block_shift);
         return make_float2(p.k_scale[at], p.v_scale[at]);
       };
       float2 here = scales_of(0, page_of(0));
@@ -466,59 +473,93 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
       for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
         const float2 next = j + 1 < sg.nblk ? scales_of(j + 1, next_page) : make_float2(0.f, 0.f);
         next_page = page_of(j + 2);
-        const unsigned e = 2u * g, at = e % stages, kb = g % kOps;
-        ok = __all_sync(0xFFFFFFFFu, at_wait(&kv_full[at], (e / stages) & 1u));
+        const unsigned kb = g % kOps;
+        ok = __all_sync(0xFFFFFFFFu, at_wait(&kv_full[at], par));
         if (!ok) break;
-        const uint32_t src = smem_u32(skv + at * C::kEntry);
-        uint32_t r[D / 2];
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t x[4];
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                       : "r"(src + p8_piece<D>(row, c)));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            r[8 * c + 2 * i] = p8_two(x[i]);
-            r[8 * c + 2 * i + 1] = p8_two(x[i] >> 16);
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&kv_empty[at]);
         if (g >= kOps) {
           ok = __all_sync(0xFFFFFFFFu, at_wait(&k_empty[kb], (g / kOps - 1) & 1u));
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         }
         s_scales[(g & 3u) * kPaKeys + row] = here;  // the softmax of block g - 4 is through: its scores' buffer was reused
-        const uint32_t to = tmem + lanes + C::kK + kb * (D / 2);
-        p8_st_k(to, r);
-        if constexpr (D == 128) p8_st_k(to + 32u, r + 32);
+        const uint32_t src = smem_u32(skv + at * C::kEntry), to = tmem + lanes + C::kK + kb * (D / 2);
+#pragma unroll 1  // (code that fits the instruction cache beside the other roles')
+        for (int half = 0; half < D / 64; ++half) {
+          uint32_t r[32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                         : "r"(src + p8_piece<D>(row, 4 * half + c)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              r[8 * c + 2 * i] = p8_two(x[i]);
+              r[8 * c + 2 * i + 1] = p8_two(x[i] >> 16);
+            }
+          }
+          p8_st_k(to + 32u * half, r);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kv_empty[at]);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&k_full[kb]);
         here = next;
+        at += 2;
+        if (at >= stages) {
+          at -= stages;
+          par ^= 1u;
+        }
       }
     }
   } else if (warp < 12) {  // values
     constexpr int kParts = D / 64;  // pieces of 16 columns a warp has
     const int part0 = (warp & 3) * kParts;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const int ldrow = lane;  // of 32 keys: matrix lane / 8, row lane % 8
-    unsigned g = 0;
+    unsigned g = 0, at = 1, par = 0;
     for (int si = 0; ok; ++si) {
       const PaSeg sg = pa_next(p, cum, w);
       if (sg.nblk == 0) break;
       const int len = lens[sg.b], common = pa_common(p, len);
       for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
-        const unsigned e = 2u * g + 1u, at = e % stages, vb = g % kOps;
+        const unsigned vb = g % kOps;
         const int kbase = (sg.j0 + j) * kPaKeys;
-        ok = __all_sync(0xFFFFFFFFu, at_wait(&kv_full[at], (e / stages) & 1u));
+        ok = __all_sync(0xFFFFFFFFu, at_wait(&kv_full[at], par));
         if (!ok) break;
         const uint32_t src = smem_u32(skv + at * C::kEntry);
-        bool found = false;
-#pragma unroll
+        if (__builtin_expect(kbase + kPaKeys > common, 0)) {
+          // A weight of zero does not hide a NaN from the tensor cores. Rows past the request's end are cleared; a NaN
+          // among the nodes' codes is cleared here and given to the rows that see it at the end.
+          bool found = false;
+#pragma unroll 1
+          for (int i = lane; i < kPaKeys * kParts; i += 32) {
+            const int key = kbase + i / kParts;
+            if (key < common) continue;
+            uint4* piece = reinterpret_cast<uint4*>(skv + at * C::kEntry + p8_piece<D>(i / kParts, part0 + i % kParts));
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (key < len) {
+              x = *piece;
+              const uint4 nan = make_uint4(
+                  __vcmpeq4(x.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu), __vcmpeq4(x.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu),
+                  __vcmpeq4(x.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu), __vcmpeq4(x.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu));
+              if ((nan.x | nan.y | nan.z | nan.w) == 0u) continue;
+              found = true;
+              x = make_uint4(x.x & ~nan.x, x.y & ~nan.y, x.z & ~nan.z, x.w & ~nan.w);
+            }
+            *piece = x;
+          }
+          if (found) atomicMax(&s_bad, si + 1);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the entry's next copy
+          __syncwarp();
+        }
+        if (g >= kOps) {
+          ok = __all_sync(0xFFFFFFFFu, at_wait(&v_empty[vb], (g / kOps - 1) & 1u));
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        }
+#pragma unroll 1
         for (int h = 0; h < kParts; ++h) {
           uint32_t r[32];
 #pragma unroll
@@ -526,23 +567,8 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
             uint32_t x[4];
             asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                          : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                         : "r"(src + p8_piece<D>(32 * kk + ldrow, part0 + h))
+                         : "r"(src + p8_piece<D>(32 * kk + lane, part0 + h))
                          : "memory");
-            if (kbase + kPaKeys > common) {
-              // A weight of zero does not hide a NaN from the tensor cores. Rows past the request's end are cleared; a NaN
-              // among the nodes' codes is cleared here and given to the rows that see it at the end.
-#pragma unroll
-              for (int m = 0; m < 4; ++m) {
-                const int key = kbase + 32 * kk + 8 * m + 2 * (lane & 3);
-                if (key + 1 >= len) x[m] &= key >= len ? 0u : 0xFFFFu;
-                const uint32_t nodes = (key >= common ? 0xFFFFu : 0u) | (key + 1 >= common ? 0xFFFF0000u : 0u);
-                const uint32_t nan = __vcmpeq4(x[m] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) & nodes;
-                if (nan) {
-                  x[m] &= ~nan;
-                  found = true;
-                }
-              }
-            }
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
               const uint32_t y = __byte_perm(x[m], 0u, 0x3120);  // two keys of a column, then of the next
@@ -550,23 +576,19 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
               r[2 * (4 * kk + m) + 1] = p8_two(y >> 16);
             }
           }
-          if (h == kParts - 1) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&kv_empty[at]);
-          }
-          if (h == 0 && g >= kOps) {
-            ok = __all_sync(0xFFFFFFFFu, at_wait(&v_empty[vb], (g / kOps - 1) & 1u));
-            if (!ok) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          }
           p8_st_v(tmem + lanes + (static_cast<uint32_t>(16 * h) << 16) + C::kV + vb * 64u, r);
         }
-        if (!ok) break;
-        if (found) atomicMax(&s_bad, si + 1);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kv_empty[at]);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&v_full[vb]);
+        at += 2;
+        if (at >= stages) {
+          at -= stages;
+          par ^= 1u;
+        }
       }
     }
   } else {  // softmax
@@ -600,7 +622,7 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
         const int key = (sg.j0 + j) * kPaKeys + row;
         const bool masked = (sg.j0 + j + 1) * kPaKeys > common;
         unsigned long long sees = ~0ull;  // bit i: row first + i sees the key
-        if (masked && key >= pre) {
+        if (__builtin_expect(masked && key >= pre, 0)) {
           sees = 0ull;
           if (key < len) {
             const unsigned long long nodes = s_sees[qb][key - pre];
@@ -623,17 +645,18 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
           else p8_ld32(ts + 32u * step, x);
           const float* factor = &s_factor[qb][first + kStep * step];
           const float* nref = &s_nref[first + kStep * step];
+          const uint64_t ks = at_pair(scales.x, scales.x);
 #pragma unroll
           for (int i = 0; i < kStep; i += 4) {
             const float4 f = *reinterpret_cast<const float4*>(factor + i);
             float4 n4 = make_float4(0.f, 0.f, 0.f, 0.f);
             if (against) n4 = *reinterpret_cast<const float4*>(nref + i);
-            x[i] = fmaf(x[i], f.x * scales.x, n4.x);
-            x[i + 1] = fmaf(x[i + 1], f.y * scales.x, n4.y);
-            x[i + 2] = fmaf(x[i + 2], f.z * scales.x, n4.z);
-            x[i + 3] = fmaf(x[i + 3], f.w * scales.x, n4.w);
+            at_unpair(at_fma2(at_pair(x[i], x[i + 1]), p8_mul2(at_pair(f.x, f.y), ks), at_pair(n4.x, n4.y)), x[i],
+                      x[i + 1]);
+            at_unpair(at_fma2(at_pair(x[i + 2], x[i + 3]), p8_mul2(at_pair(f.z, f.w), ks), at_pair(n4.z, n4.w)), x[i + 2],
+                      x[i + 3]);
           }
-          if (masked) {
+          if (__builtin_expect(masked, 0)) {
             const unsigned bits = static_cast<unsigned>(sees >> (kStep * step));
 #pragma unroll
             for (int i = 0; i < kStep; ++i)
@@ -647,7 +670,7 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
 #pragma unroll
           for (int i = 0; i < kStep; i += 2) top = at_max3(top, x[i], x[i + 1]);
         }
-        if (p8_any(bar, top + log_vs > kP8Most || failed)) {  // rare: raise references
+        if (__builtin_expect(p8_any(bar, top + log_vs > kP8Most || failed), 0)) {  // rare: raise references
           if (p8_any(bar, failed)) {
             ok = false;
             break;
@@ -709,17 +732,18 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
           if constexpr (C::kSteps > 1) load(step, true);
           float sums[kStep];
           uint32_t h[kStep / 2];
+          const uint64_t vs = at_pair(value_scale, value_scale);
 #pragma unroll
           for (int i = 0; i < kStep; i += 2) {
-            const float a = at_exp2(x[i]), b = at_exp2(x[i + 1]);
+            float a = at_exp2(x[i]), b = at_exp2(x[i + 1]);
             if constexpr (kMine <= 32) {
-              l[i] += a;
-              l[i + 1] += b;
+              at_unpair(at_add2(at_pair(l[i], l[i + 1]), at_pair(a, b)), l[i], l[i + 1]);
             } else {
               sums[i] = a;
               sums[i + 1] = b;
             }
-            h[i / 2] = p8_pack(a * value_scale, b * value_scale);
+            at_unpair(p8_mul2(at_pair(a, b), vs), a, b);
+            h[i / 2] = p8_pack(a, b);
           }
           if constexpr (kMine > 32) l[step] += p8_warp_sums(sums, lane);
 #pragma unroll
@@ -914,7 +938,9 @@ extern "C" dt_status dt_paged_attention8(int B, int n, int Hq, int Hkv, int d, c
   if (workspace_bytes < P.bytes) return DT_ERR_INVALID_ARG;
   Pa8Params p{};
   p.B = B; p.n = n; p.Hq = Hq; p.Hkv = Hkv; p.G = G; p.R = G * n; p.grid = P.grid;
-  p.page_size = page_size; p.num_pages = num_pages; p.max_pages = max_pages; p.block = scale_block;
+  p.page_size = page_size; p.num_pages = num_pages; p.max_pages = max_pages;
+  while ((1 << p.page_shift) < page_size) ++p.page_shift;
+  while ((1 << p.block_shift) < scale_block) ++p.block_shift;
   p.q = static_cast<const unsigned short*>(q);
   p.v_cache = static_cast<const unsigned char*>(v_cache);
   p.k_scale = k_scale; p.v_scale = v_scale;
