@@ -407,10 +407,11 @@ dt_status dt_paged_attention(int B, int n, int Hq, int Hkv, int d, const void* q
  * Semantics as dt_paged_attention, with k_j and v_j the codes times the scales of their blocks and heads. Any scales in
  * 2^DT_SCALE_LOW .. 2^DT_SCALE_HIGH serve (they need not be powers of two); with others what a query that sees their
  * block gets is unspecified. Scales of blocks of which no row is seen are not looked at.
- * Arithmetic: a query row is brought by a power of two to 2^14 .. 2^15 and held in fp16 (exact but for elements below
- * 2^-31 of the row's largest), codes are exact in fp16; products on the tensor cores, accumulated in fp32. A softmax weight
- * times its value's scale is rounded to fp16, relative to the row's largest such product so far: off by 2^-11 of itself,
- * or by 2^-31 of that largest where that is more. The output is rounded to bf16 once.
+ * Arithmetic: a query row is brought by a power of two to at most 448 and held in two e4m3 terms (exact but for elements
+ * below 2^-9 of the row's largest, which are off by at most 2^-17 of it); codes enter the products as they are; products
+ * on the tensor cores, accumulated in fp32. A softmax weight times its value's scale is rounded to fp16, relative to the
+ * row's largest such product so far: off by 2^-11 of itself, or by 2^-31 of that largest where that is more. The output is
+ * rounded to bf16 once.
  *   k_scale, v_scale [num_pages,Hkv,page_size/scale_block] fp32;  everything else as dt_paged_attention.
  *   workspace   dt_paged_attention8_workspace_bytes(B,n,Hq,Hkv,d) bytes on the current device, initialised by
  *               dt_workspace_init; serves any lengths. After DT_ERR_TIMEOUT (dt_get_error) initialise it again.

@@ -5,12 +5,17 @@
 //     score_j = ks_j (q . code_j),  out = sum_j (p_j vs_j) code_j / sum_j p_j.
 //
 // GB300 design. As in the bf16 kernel the R = G n query rows that share a key/value head read each cached row once, and
-// the 128-key blocks of all pairs are split evenly over the CTAs. What bounds it is memory, at half the bytes a block; so
-// the codes must become tensor-core operands without passing through shared memory a second time. Keys and values are the
-// left operands, in tensor memory: S^T = K Q^T (a lane a key) and O^T = V^T W (a lane a column), and the warps that turn
-// codes into fp16 (exactly) write them straight there. The few query rows are N, so a product costs little when R is
-// small, and a softmax thread owns a key: its scales are two registers, and a row's maximum is looked for only when some
-// weight leaves the headroom.
+// the 128-key blocks of all pairs are split evenly over the CTAs. What bounds it is memory, at half the bytes a block, so
+// little may be done to a code on its way. Keys and values are the left operands: S^T = K Q^T (a lane a key) and
+// O^T = V^T W (a lane a column), so that the few query rows are N and a product costs little when R is small.
+//   Keys go to the tensor cores as the e4m3 they are, from the ring that TMA fills. The queries then are e4m3 too: two
+// terms, q = q1 + q2, which hold the eight significant bits of a bf16 between them (what q1 rounds away is at most eight
+// steps of the eighth bit: four bits), so each key is multiplied twice, and once less is read than with a conversion.
+//   Weights are not so kind: they need a wide range below their largest. They stay fp16, and values are brought to fp16
+// (exactly) on the way from the ring to tensor memory: a transposing load of pairs of columns, a byte shuffle, one
+// conversion for two codes.
+//   A softmax thread owns a key: its scales are two registers, and a row's maximum is looked for only when some weight
+// leaves the headroom.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -24,8 +29,13 @@
 namespace dt {
 namespace {
 
-constexpr int kP8MaxStages = 16;
-constexpr size_t kPa8SmemCap = 232448 - 8192;  // opt-in shared memory of a CTA, less the static part
+constexpr int kP8MaxStages = 24;
+constexpr int kP8VStages = 4;
+// Blocks whose scales are there: the load runs at most half a ring ahead of the keys that the tensor cores have read, and
+// those two blocks ahead of the softmax.
+constexpr int kP8Scales = 16;
+static_assert(kP8MaxStages / 2 + 2 <= kP8Scales, "scales are not overwritten before they are read");
+constexpr size_t kPa8SmemCap = 232448 - 9216;  // opt-in shared memory of a CTA, less the static part
 // Weights times their values' scales are fp16: a row's largest starts out at 2^kP8Start and may grow to 2^kP8Most before
 // the reference is raised. fp16 goes up to 2^16 and holds subnormal numbers in steps of 2^-24.
 constexpr float kP8Start = 6.f, kP8Most = 14.f;
@@ -72,15 +82,6 @@ __device__ __forceinline__ void p8_st16(uint32_t taddr, const float* v) {  // 16
         "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
       : "memory");
 }
-__device__ __forceinline__ void p8_st_k(uint32_t taddr, const uint32_t* v) {  // 32 columns of two fp16
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
-        "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
-        "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-      : "memory");
-}
 // 16 lanes x 64 columns: in each group of 4 columns thread l holds column l % 4 of lanes l / 4 and l / 4 + 8.
 __device__ __forceinline__ void p8_st_v(uint32_t taddr, const uint32_t* v) {  // 64 columns of two fp16
   asm volatile(
@@ -97,6 +98,11 @@ __device__ __forceinline__ uint32_t p8_two(uint32_t codes) {  // the two e4m3 co
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
   return r;
 }
+__device__ __forceinline__ uint32_t p8_code2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ uint32_t p8_pack(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -111,6 +117,11 @@ __device__ __forceinline__ float p8_log2(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// As at_wait, with the long way in one place: code that every role repeats crowds the instruction cache.
+__device__ __noinline__ bool p8_wait_long(uint64_t* bar, unsigned parity) { return at_wait(bar, parity); }
+__device__ __forceinline__ bool p8_wait(uint64_t* bar, unsigned parity) {
+  return mbar_try_wait(bar, parity) || p8_wait_long(bar, parity);
 }
 // Whether any thread of the group says so; everyone of the group comes here, by whole warps.
 __device__ __forceinline__ bool p8_any(int id, bool x) {
@@ -159,63 +170,68 @@ __device__ __forceinline__ uint32_t p8_piece(int r, int c) {
 // The shape of one instance: N columns of query rows (R rounded up).
 template <int D, int N>
 struct P8 {
-  static constexpr int kGroups = N <= 32 ? 1 : 2;        // softmax groups of four warps
-  static constexpr int kThreads = 384 + 128 * kGroups;   // warps 0: load, 1: MMA, 2-3: queries, 4-7: keys, 8-11: values
+  static constexpr int kThreads = 512;
+  static constexpr int kGroups = N <= 32 ? 1 : 2;        // softmax groups of four warps, the last ones
+  static constexpr int kSets = 3 - kGroups;              // sets of four warps for the values: they take blocks in turn
+  static constexpr int kSoftmax = 16 - 4 * kGroups;      // warps 0: load, 1: MMA, 2-3: queries, 4 on: values, then softmax
   static constexpr int kMine = N / kGroups;              // a softmax thread's query rows
   static constexpr int kStep = kMine < 32 ? kMine : 32;  // taken at once
   static constexpr int kSteps = kMine / kStep;
-  static constexpr int kOps = N <= 64 ? 2 : 1;           // buffers of keys, of values, of outputs, of weights
+  static constexpr int kVs = N <= 64 ? kP8VStages : 2;   // buffers of values
+  static constexpr int kOs = N <= 64 ? 2 : 1;            // buffers of outputs
   static constexpr uint32_t kEntry = kPaKeys * D;        // a ring entry: a block's keys or values
-  static constexpr uint32_t kQ = N * D * 2;              // a buffer of queries
+  static constexpr uint32_t kTerm = N * D;               // one term of the queries
+  static constexpr uint32_t kQ = 2 * kTerm;              // a buffer of queries
   static constexpr int kAtom = N < 64 ? N : 64;          // query rows in a row of the weights
   static constexpr uint32_t kRowW = kAtom * 2;
   static constexpr uint32_t kW = kPaKeys * N * 2;        // a buffer of weights
   // tensor memory
-  static constexpr uint32_t kS = 0, kO = 2 * N, kK = kO + kOps * N, kV = kK + kOps * (D / 2);
-  static_assert(kV + kOps * 64 <= 512, "tensor memory");
-  static constexpr size_t kFixed = 1024 + 2 * kQ + kOps * kW + 4 * kPaKeys * sizeof(float2);
+  static constexpr uint32_t kS = 0, kO = 2 * N, kV = kO + kOs * N;
+  static_assert(kV + kVs * 64 <= 512, "tensor memory");
+  static constexpr size_t kFixed = 1024 + 2 * kQ + 2 * kW;
 };
 
-// Roles. Load: pages to the ring, as in the bf16 kernel. Queries: a segment's rows, each brought by a power of two to
-// 2^14 .. 2^15 and rounded to fp16, with the factor that undoes it; the nodes' mask, by keys. Keys: lane = key, its row's
-// codes to fp16 in tensor memory; its two scales, loaded two blocks ahead, for the softmax. Values: lane = column, two
-// keys a register: a transposing load of pairs of columns, a byte shuffle. Softmax: lane = key. MMA: the scores run one
-// block ahead of the outputs, through the segments.
+// Roles. Load: pages to the ring, as in the bf16 kernel, and their scales. Queries: a segment's rows, each brought by a power of two to at
+// most 448 and split in two, with the factor that undoes it; the nodes' mask, by keys. Values: lane = column, two keys a
+// register. Softmax: lane = key; its scales come with the keys (loaded by the softmax itself a block ahead they are late:
+// a block takes less than a load). MMA: the scores run one block ahead of the outputs, through the segments.
 template <int D, int N>
 __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8Params p, const __grid_constant__ Pa8Maps maps,
                                                                             WsHeader* hdr) {
   using C = P8<D, N>;
-  constexpr int kThreads = C::kThreads, kMine = C::kMine, kStep = C::kStep, kOps = C::kOps;
+  constexpr int kThreads = C::kThreads, kMine = C::kMine, kStep = C::kStep, kVs = C::kVs, kOs = C::kOs;
   extern __shared__ float4 smem_f4[];
   unsigned char* sq =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_f4) + 1023) & ~uintptr_t(1023));
   unsigned char* sw = sq + 2 * C::kQ;
-  unsigned char* skv = sw + kOps * C::kW;
-  float2* s_scales = reinterpret_cast<float2*>(skv + p.stages * C::kEntry);  // [4][kPaKeys]: a key's, its value's
-  int* cum = reinterpret_cast<int*>(s_scales + 4 * kPaKeys);                 // [B + 1]
-  int* lens = cum + p.B + 1;                                                 // [B]
+  unsigned char* skv = sw + 2 * C::kW;
+  int* cum = reinterpret_cast<int*>(skv + p.stages * C::kEntry);  // [B + 1]
+  int* lens = cum + p.B + 1;                                      // [B]
   __shared__ uint64_t kv_full[kP8MaxStages], kv_empty[kP8MaxStages];
-  __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  __shared__ uint64_t v_full[kVs], v_empty[kVs];
   __shared__ uint64_t s_full[2], w_full[2], o_done[2], q_full[2], o_free[2], s_meet;
   __shared__ uint32_t s_tmem;
   __shared__ unsigned s_kv_issued;
   __shared__ int s_warp[kThreads / 32];
   __shared__ int s_bad, s_joins;
   __shared__ PaJoin s_join[2];
+  __shared__ float s_scales[kP8Scales][2][kPaKeys / DT_MIN_PAGE];  // of a block's keys, then of its values
   __shared__ __align__(16) float s_factor[2][N], s_nref[N], s_alpha[N], s_red[4][N];
   __shared__ unsigned long long s_sees[2][kPaNodes];  // bit i: node i sees the key of node c
+  __shared__ int s_at[N];                             // a query row's place in a request's outputs
+  __shared__ unsigned char s_node[N];                 // its node
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const unsigned stages = static_cast<unsigned>(p.stages);
   if (t == 0) {
     for (unsigned i = 0; i < stages; ++i) {
-      mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 4);
+      mbar_init(&kv_full[i], i % 2 == 0 ? 33 : 1);  // keys: and each lane's copy of a scale
+      mbar_init(&kv_empty[i], i % 2 == 0 ? 1 : 4);  // keys: by the tensor cores; values: by four warps
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], 4);
-      mbar_init(&k_empty[i], 1);
+    for (int i = 0; i < kVs; ++i) {
       mbar_init(&v_full[i], 4);
       mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&w_full[i], 4 * C::kGroups);
       mbar_init(&o_done[i], 1);
@@ -236,7 +252,11 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
     asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &maps.k : &maps.v) : "memory");
   // rows of queries that there are not: zero, with a factor of zero
   for (int i = t; i < static_cast<int>(2 * C::kQ / 16); i += kThreads)
-    if (static_cast<int>(i * 16 / 128) % N >= p.R) reinterpret_cast<uint4*>(sq)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (static_cast<int>(i * 16 / D) % N >= p.R) reinterpret_cast<uint4*>(sq)[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (int r = t; r < N; r += kThreads) {
+    s_node[r] = static_cast<unsigned char>(r / p.G < kPaNodes ? r / p.G : kPaNodes - 1);
+    s_at[r] = (r / p.G * p.Hq + r % p.G) * D;
+  }
   for (int i = t; i < 2 * N; i += kThreads) s_factor[i / N][i % N] = 0.f;
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   at_launch_order();
@@ -275,6 +295,8 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
     unsigned st = 0, par = 1u, e = 0;  // ring entry, the parity of its last release, entries so far
     const int box_rows = p.page_size < kPaKeys ? p.page_size : kPaKeys;
     const int per_block = kPaKeys / box_rows;  // pages a block spans (1 when a page holds whole blocks)
+    const int per_scale = p.block_shift < 7 ? kPaKeys >> p.block_shift : 1;  // scales a block has
+    unsigned g = 0;
     while (ok) {
       const PaSeg sg = pa_next(p, cum, w);
       if (sg.nblk == 0) break;
@@ -297,12 +319,28 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
           record_error(hdr, DT_ERR_INVALID_ARG);
           page = 0;
         }
+        // the block's scales: lanes 0-15 the keys', the others the values'
+        const int at = row + ((lane & 15) << p.block_shift), from = __shfl_sync(0xFFFFFFFFu, page, at >> p.page_shift);
+        const bool scaled = (lane & 15) < per_scale && (at >> p.page_shift) < pages;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {  // the keys, then the values
-          if (ok && e >= stages) ok = __all_sync(0xFFFFFFFFu, at_wait(&kv_empty[st], par));
+          if (ok && e >= stages) ok = __all_sync(0xFFFFFFFFu, p8_wait(&kv_empty[st], par));
           if (!ok) break;
           if (lane == 0) mbar_expect_tx(&kv_full[st], static_cast<uint32_t>(pages * box_rows * D));
           __syncwarp();
+          if (kv == 0) {
+            if (scaled) {
+              const float* src = (lane < 16 ? p.k_scale : p.v_scale) +
+                                 ((static_cast<size_t>(from) * p.Hkv + sg.kvh) << (p.page_shift - p.block_shift)) +
+                                 ((at & (p.page_size - 1)) >> p.block_shift);
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                               smem_u32(&s_scales[g % kP8Scales][lane >> 4][lane & 15])),
+                           "l"(src)
+                           : "memory");
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&kv_full[st])) : "memory");
+            ++g;
+          }
           if (lane < pages)
             tma_load_3d(skv + st * C::kEntry + lane * box_rows * D, kv ? &maps.v : &maps.k, 0, row,
                         page * p.Hkv + sg.kvh, &kv_full[st]);
@@ -317,18 +355,19 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
     }
   } else if (warp == 1) {
     if (elect_one()) {  // MMA
-      const uint32_t id_s = umma_idesc_f16(N), id_o = umma_idesc_f16(N) | (1u << 16);  // O: the weights MN-major
-      const uint64_t dq = umma_desc_sw128(smem_u32(sq));
+      // the same bits for e4m3 and for fp16; O: the weights MN-major
+      const uint32_t id_s = umma_idesc_f16(N), id_o = umma_idesc_f16(N) | (1u << 16);
+      const uint64_t dq = umma_desc_rows(smem_u32(sq), D), dk = umma_desc_rows(smem_u32(skv), D);
       const uint64_t dw = umma_desc_mn(smem_u32(sw), C::kRowW, kPaKeys * 128);
       auto wait = [&](uint64_t* bar, unsigned parity) {
-        const bool done = at_wait(bar, parity);
+        const bool done = p8_wait(bar, parity);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         return done;
       };
       PaWalk ws = w;
       PaSeg ss{};
       int js = 0, sis = -1;
-      unsigned gs = 0;
+      unsigned gs = 0, st = 0, par = 0;  // the ring entry of the next keys: every other one
       auto scores = [&]() {  // of the next block, if there is one
         if (js == ss.nblk) {
           ss = pa_next(p, cum, ws);
@@ -337,14 +376,20 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
           ++sis;
           if (!wait(&q_full[sis & 1], static_cast<unsigned>(sis >> 1) & 1u)) return false;
         }
-        const unsigned kb = gs % kOps;
-        if (!wait(&k_full[kb], (gs / kOps) & 1u)) return false;
-        const uint64_t q0 = dq + static_cast<uint64_t>((sis & 1) * (C::kQ >> 4));
+        if (!wait(&kv_full[st], par)) return false;
+        const uint64_t q0 = dq + static_cast<uint64_t>((sis & 1) * (C::kQ >> 4)), k0 = dk + st * (C::kEntry >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_f16_ts(tmem + C::kS + (gs & 1u) * N, tmem + C::kK + kb * (D / 2) + 8u * kk,
-                      q0 + (((kk >> 2) * N * 128u + (kk & 3) * 32u) >> 4), id_s, kk > 0 ? 1u : 0u);
-        umma_commit(&k_empty[kb]);
+        for (int term = 0; term < 2; ++term)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)
+            umma_f8(tmem + C::kS + (gs & 1u) * N, k0 + 2u * kk, q0 + ((term * C::kTerm) >> 4) + 2u * kk, id_s,
+                    term + kk > 0 ? 1u : 0u);
+        umma_commit(&kv_empty[st]);
+        st += 2;
+        if (st == stages) {
+          st = 0;
+          par ^= 1u;
+        }
         umma_commit(&s_full[gs & 1u]);
         ++js;
         ++gs;
@@ -355,22 +400,22 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
       for (int si = 0; ok; ++si) {
         const PaSeg sg = pa_next(p, cum, w);
         if (sg.nblk == 0) break;
-        const unsigned ob = static_cast<unsigned>(si) % kOps;
+        const unsigned ob = static_cast<unsigned>(si) % kOs;
         for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
           // its buffer was freed by block g - 1's softmax (waited for below, one block ago)
           ok = scores();
-          if (ok && j == 0 && si >= kOps) {  // the segment that had the buffer before has been read
-            const int was = si - kOps;
+          if (ok && j == 0 && si >= kOs) {  // the segment that had the buffer before has been read
+            const int was = si - kOs;
             ok = wait(&o_free[was & 1], static_cast<unsigned>(was >> 1) & 1u);
           }
-          const unsigned vb = g % kOps;
-          if (ok) ok = wait(&v_full[vb], (g / kOps) & 1u);
+          const unsigned vb = g % kVs;
+          if (ok) ok = wait(&v_full[vb], (g / kVs) & 1u);
           if (ok) ok = wait(&w_full[g & 1u], (g >> 1) & 1u);
           if (!ok) break;
 #pragma unroll
           for (int kk = 0; kk < kPaKeys / 16; ++kk)
             umma_f16_ts(tmem + C::kO + ob * N, tmem + C::kV + vb * 64u + 8u * kk,
-                        dw + ((vb * C::kW + kk * 16u * C::kRowW) >> 4), id_o, (j > 0 || kk > 0) ? 1u : 0u);
+                        dw + (((g & 1u) * C::kW + kk * 16u * C::kRowW) >> 4), id_o, (j > 0 || kk > 0) ? 1u : 0u);
           umma_commit(&v_empty[vb]);
           umma_commit(&o_done[g & 1u]);
         }
@@ -383,7 +428,7 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
       if (sg.nblk == 0) break;
       const unsigned qb = static_cast<unsigned>(si) & 1u;
       // the segment that had the buffer before is over: its factors and its mask are not read any more
-      if (si >= 2) ok = __all_sync(0xFFFFFFFFu, at_wait(&o_free[qb], static_cast<unsigned>((si >> 1) - 1) & 1u));
+      if (si >= 2) ok = __all_sync(0xFFFFFFFFu, p8_wait(&o_free[qb], static_cast<unsigned>((si >> 1) - 1) & 1u));
       if (!ok) break;
       const int c = 32 * who + lane;
       if (c < p.n) {
@@ -397,136 +442,85 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
         s_sees[qb][c] = bits;
       }
       unsigned char* qd = sq + qb * C::kQ;
-      constexpr int kEach = D / 32, kAtOnce = 8;  // a lane's elements of a row; rows in flight
-      for (int r0 = who; r0 < p.R; r0 += 2 * kAtOnce) {
-        uint32_t x[kAtOnce][kEach / 2];
+      constexpr int kLanes = D / 4, kAcross = 32 / kLanes, kAtOnce = 8;  // lanes a row, rows a step, steps in flight
+      const int sub = lane % kLanes;
+      const unsigned short* src = p.q + (static_cast<size_t>(sg.b) * p.n * p.Hq + sg.kvh * p.G) * D + 4 * sub;
+#pragma unroll 1
+      for (int r0 = who * kAcross; r0 < p.R; r0 += 2 * kAcross * kAtOnce) {
+        uint2 x[kAtOnce];
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
-          const int r = r0 + 2 * u;
-          if (r < p.R) {
-            const unsigned short* src =
-                p.q + ((static_cast<size_t>(sg.b) * p.n + r / p.G) * p.Hq + sg.kvh * p.G + r % p.G) * D + kEach * lane;
-            if constexpr (D == 128) {
-              const uint2 y = *reinterpret_cast<const uint2*>(src);
-              x[u][0] = y.x;
-              x[u][kEach / 2 - 1] = y.y;
-            } else {
-              x[u][0] = *reinterpret_cast<const uint32_t*>(src);
-            }
-          }
+          const int r = r0 + 2 * kAcross * u + lane / kLanes;
+          x[u] = r < p.R ? *reinterpret_cast<const uint2*>(src + s_at[r]) : make_uint2(0u, 0u);
         }
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
-          const int r = r0 + 2 * u;
-          if (r >= p.R) break;
-          float f[kEach];
-          unsigned most = 0u;  // the bits of the largest finite element
+          const int r = r0 + 2 * kAcross * u + lane / kLanes;
+          if (r0 + 2 * kAcross * u >= p.R) break;
+          float f[4] = {__uint_as_float(x[u].x << 16), __uint_as_float(x[u].x & 0xFFFF0000u),
+                        __uint_as_float(x[u].y << 16), __uint_as_float(x[u].y & 0xFFFF0000u)};
+          unsigned most = 0u;  // the bits of the row's largest finite element
 #pragma unroll
-          for (int i = 0; i < kEach; ++i) {
-            f[i] = __uint_as_float(i & 1 ? x[u][i / 2] & 0xFFFF0000u : x[u][i / 2] << 16);
+          for (int i = 0; i < 4; ++i) {
             const unsigned m = __float_as_uint(f[i]) & 0x7FFFFFFFu;
             if (m < 0x7F800000u && m > most) most = m;
           }
-          most = __reduce_max_sync(0xFFFFFFFFu, most);
-          int up = 14 - (static_cast<int>(most >> 23) - 127);
+#pragma unroll
+          for (int h = kLanes / 2; h > 0; h >>= 1) {
+            const unsigned other = __shfl_xor_sync(0xFFFFFFFFu, most, h);
+            most = other > most ? other : most;
+          }
+          // the largest power of two that leaves it at 448 = 1.75 2^8 or less
+          int up = ((most & 0x7FFFFFu) > 0x600000u ? 7 : 8) - (static_cast<int>(most >> 23) - 127);
           if (up > 100) up = 100;  // (nothing is lost: such a row's scores are zero whatever the keys are)
           const float by = __uint_as_float(static_cast<unsigned>(up + 127) << 23);
-          uint32_t h[kEach / 2];
+          uint32_t q1 = 0u, q2 = 0u;
 #pragma unroll
-          for (int i = 0; i < kEach / 2; ++i) h[i] = p8_pack(f[2 * i] * by, f[2 * i + 1] * by);
-          if constexpr (D == 128) {
-            unsigned char* at = qd + (lane >> 4) * (N * 128) + r * 128 + ((((lane & 15) >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8;
-            *reinterpret_cast<uint2*>(at) = make_uint2(h[0], h[kEach / 2 - 1]);
-          } else {
-            *reinterpret_cast<uint32_t*>(qd + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) = h[0];
+          for (int i = 0; i < 4; i += 2) {
+            const float a = f[i] * by, b = f[i + 1] * by;
+            const float a1 = fabsf(a) <= 448.f ? a : NAN, b1 = fabsf(b) <= 448.f ? b : NAN;
+            const uint32_t c = p8_code2(a1, b1), two = p8_two(c);
+            const float2 got = __half22float2(*reinterpret_cast<const __half2*>(&two));
+            q1 |= c << (8 * i);
+            q2 |= p8_code2(a1 - got.x, b1 - got.y) << (8 * i);
           }
-          if (lane == 0) s_factor[qb][r] = p.scale_log2 * __uint_as_float(static_cast<unsigned>(127 - up) << 23);
+          if (r < p.R) {
+            unsigned char* at = qd + p8_piece<D>(r, sub >> 2) + (sub & 3) * 4;
+            *reinterpret_cast<uint32_t*>(at) = q1;
+            *reinterpret_cast<uint32_t*>(at + C::kTerm) = q2;
+            if (sub == 0) s_factor[qb][r] = p.scale_log2 * __uint_as_float(static_cast<unsigned>(127 - up) << 23);
+          }
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads Q through the async proxy
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[qb]);
     }
-  } else if (warp < 8) {  // keys
-    const int row = 32 * (warp & 3) + lane;
-    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    unsigned g = 0, at = 0, par = 0;  // its entries are every other one
-    while (ok) {
-      const PaSeg sg = pa_next(p, cum, w);
-      if (sg.nblk == 0) break;
-      const int len = lens[sg.b], per_page = p.page_shift - p.block_shift;  // log2 of the scales of a page and head
-      const int32_t* table = p.page_table + static_cast<size_t>(sg.b) * p.max_pages;
-      // a key's page id is read two blocks ahead of its use, its scales one
-      auto page_of = [&](int j) {
-        const int key = (sg.j0 + j) * kPaKeys + row;
-        return j < sg.nblk && key < len ? table[key >> p.page_shift] : -1;
-      };
-      auto scales_of = [&](int j, int page) {
-        const int key = (sg.j0 + j) * kPaKeys + row;
-        if (page < 0 || page >= p.num_pages) return make_float2(0.f, 0.f);  // no key (or reported by the load)
-        const size_t at = ((static_cast<size_t>(page) * p.Hkv + sg.kvh) << per_page) +
-                          ((key & (p.page_size - 1)) >> p.block_shift);
-        return make_float2(p.k_scale[at], p.v_scale[at]);
-      };
-      float2 here = scales_of(0, page_of(0));
-      int next_page = page_of(1);
-      for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
-        const float2 next = j + 1 < sg.nblk ? scales_of(j + 1, next_page) : make_float2(0.f, 0.f);
-        next_page = page_of(j + 2);
-        const unsigned kb = g % kOps;
-        ok = __all_sync(0xFFFFFFFFu, at_wait(&kv_full[at], par));
-        if (!ok) break;
-        if (g >= kOps) {
-          ok = __all_sync(0xFFFFFFFFu, at_wait(&k_empty[kb], (g / kOps - 1) & 1u));
-          if (!ok) break;
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        }
-        s_scales[(g & 3u) * kPaKeys + row] = here;  // the softmax of block g - 4 is through: its scores' buffer was reused
-        const uint32_t src = smem_u32(skv + at * C::kEntry), to = tmem + lanes + C::kK + kb * (D / 2);
-#pragma unroll 1  // (code that fits the instruction cache beside the other roles')
-        for (int half = 0; half < D / 64; ++half) {
-          uint32_t r[32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t x[4];
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                         : "r"(src + p8_piece<D>(row, 4 * half + c)));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              r[8 * c + 2 * i] = p8_two(x[i]);
-              r[8 * c + 2 * i + 1] = p8_two(x[i] >> 16);
-            }
-          }
-          p8_st_k(to + 32u * half, r);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&kv_empty[at]);
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&k_full[kb]);
-        here = next;
-        at += 2;
-        if (at >= stages) {
-          at -= stages;
-          par ^= 1u;
-        }
-      }
-    }
-  } else if (warp < 12) {  // values
+  } else if (warp < C::kSoftmax) {  // values
     constexpr int kParts = D / 64;  // pieces of 16 columns a warp has
     const int part0 = (warp & 3) * kParts;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const unsigned set = static_cast<unsigned>(warp - 4) >> 2;
     unsigned g = 0, at = 1, par = 0;
+    auto advance = [&] {
+      at += 2;
+      if (at > stages) {
+        at = 1;
+        par ^= 1u;
+      }
+    };
     for (int si = 0; ok; ++si) {
       const PaSeg sg = pa_next(p, cum, w);
       if (sg.nblk == 0) break;
       const int len = lens[sg.b], common = pa_common(p, len);
       for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
-        const unsigned vb = g % kOps;
+        if (g % C::kSets != set) {
+          advance();
+          continue;
+        }
+        const unsigned vb = g % kVs;
         const int kbase = (sg.j0 + j) * kPaKeys;
-        ok = __all_sync(0xFFFFFFFFu, at_wait(&kv_full[at], par));
+        ok = __all_sync(0xFFFFFFFFu, p8_wait(&kv_full[at], par));
         if (!ok) break;
         const uint32_t src = smem_u32(skv + at * C::kEntry);
         if (__builtin_expect(kbase + kPaKeys > common, 0)) {
@@ -554,8 +548,8 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the entry's next copy
           __syncwarp();
         }
-        if (g >= kOps) {
-          ok = __all_sync(0xFFFFFFFFu, at_wait(&v_empty[vb], (g / kOps - 1) & 1u));
+        if (g >= kVs) {
+          ok = __all_sync(0xFFFFFFFFu, p8_wait(&v_empty[vb], (g / kVs - 1) & 1u));
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         }
@@ -584,27 +578,24 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&v_full[vb]);
-        at += 2;
-        if (at >= stages) {
-          at -= stages;
-          par ^= 1u;
-        }
+        advance();
       }
     }
   } else {  // softmax
-    const int group = (warp - 12) >> 2, quad = warp & 3, row = 32 * quad + lane;  // the thread's key of a block
-    const int bar = 1 + group, first = group * kMine, mine = t - (384 + 128 * group);
+    const int group = (warp - C::kSoftmax) >> 2, quad = warp & 3, row = 32 * quad + lane;  // the thread's key of a block
+    const int bar = 1 + group, first = group * kMine, mine = t - (32 * C::kSoftmax + 128 * group);
     const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
     // the column that the thread's lane of the outputs is, and the pair of columns that it writes
     const int column = D / 4 * quad + 16 * (lane >> 4) + 2 * (lane & 7) + ((lane >> 3) & 1);
     const bool has_column = D == 128 || lane < 16;
+    const int my_scale = p.block_shift < 7 ? row >> p.block_shift : 0;
     unsigned g = 0, meet = 0;
     bool failed = false;  // a wait ran out; the group leaves together, at its next meeting
     for (int si = 0; ok; ++si) {
       const PaSeg sg = pa_next(p, cum, w);
       if (sg.nblk == 0) break;
       const unsigned qb = static_cast<unsigned>(si) & 1u;
-      const uint32_t to = tmem + lanes + C::kO + (static_cast<unsigned>(si) % kOps) * N + first;
+      const uint32_t to = tmem + lanes + C::kO + (static_cast<unsigned>(si) % kOs) * N + first;
       const int len = lens[sg.b], pre = len - p.n, common = pa_common(p, len);
       constexpr int kSums = kMine <= 32 ? kMine : kMine / 32;
       float l[kSums];
@@ -614,10 +605,11 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
       p8_meet(bar);
       for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
         const uint32_t ts = tmem + lanes + C::kS + (g & 1u) * N + first;
-        if (!at_wait(&s_full[g & 1u], (g >> 1) & 1u)) failed = true;
+        if (!p8_wait(&s_full[g & 1u], (g >> 1) & 1u)) failed = true;
         __syncwarp();
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const float2 scales = s_scales[(g & 3u) * kPaKeys + row];
+        const float2 scales =
+            make_float2(s_scales[g % kP8Scales][0][my_scale], s_scales[g % kP8Scales][1][my_scale]);
         const float log_vs = fmaxf(p8_log2(fabsf(scales.y)), kP8LeastScale);
         const int key = (sg.j0 + j) * kPaKeys + row;
         const bool masked = (sg.j0 + j + 1) * kPaKeys > common;
@@ -626,14 +618,8 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
           sees = 0ull;
           if (key < len) {
             const unsigned long long nodes = s_sees[qb][key - pre];
-            int node = first / p.G, rem = first % p.G;
-            for (int i = 0; i < kMine; ++i) {
-              sees |= ((nodes >> (node & 63)) & 1ull) << i;
-              if (++rem == p.G) {
-                rem = 0;
-                ++node;
-              }
-            }
+#pragma unroll 4
+            for (int i = 0; i < kMine; ++i) sees |= ((nodes >> s_node[first + i]) & 1ull) << i;
           }
         }
         const float value_scale = sees == 0ull ? 0.f : scales.y;
@@ -663,14 +649,17 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
               if (!((bits >> i) & 1u)) x[i] = -INFINITY;
           }
         };
-        float top = -INFINITY;
 #pragma unroll 1
-        for (int step = 0; step < C::kSteps; ++step) {
-          load(step, true);
+        for (bool raised = false;; raised = true) {
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int step = 0; step < C::kSteps; ++step) {
+            load(step, true);
 #pragma unroll
-          for (int i = 0; i < kStep; i += 2) top = at_max3(top, x[i], x[i + 1]);
-        }
-        if (__builtin_expect(p8_any(bar, top + log_vs > kP8Most || failed), 0)) {  // rare: raise references
+            for (int i = 0; i < kStep; i += 2) top = at_max3(top, x[i], x[i + 1]);
+          }
+          if (raised || __builtin_expect(!p8_any(bar, top + log_vs > kP8Most || failed), 1)) break;
+          // rare: raise references
           if (p8_any(bar, failed)) {
             ok = false;
             break;
@@ -705,7 +694,7 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
             for (int i = 0; i < kSums; ++i) l[i] *= s_alpha[first + 32 * i + lane];
           }
           if (j > 0) {
-            if (!at_wait(&o_done[(g - 1u) & 1u], ((g - 1u) >> 1) & 1u)) failed = true;
+            if (!p8_wait(&o_done[(g - 1u) & 1u], ((g - 1u) >> 1) & 1u)) failed = true;
             __syncwarp();
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll 1
@@ -718,15 +707,13 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
             }
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           }
-          if constexpr (C::kSteps == 1) load(0, true);
         }
-        const unsigned wb = g % kOps;
-        if (g >= kOps) {  // the product that read the buffer before is done
-          const unsigned was = g - kOps;
-          if (!at_wait(&o_done[was & 1u], (was >> 1) & 1u)) failed = true;
+        if (!ok) break;
+        if (g >= 2u) {  // the product that read the buffer before is done
+          if (!p8_wait(&o_done[g & 1u], ((g - 2u) >> 1) & 1u)) failed = true;
           __syncwarp();
         }
-        unsigned char* wrow = sw + wb * C::kW + row * C::kRowW;
+        unsigned char* wrow = sw + (g & 1u) * C::kW + row * C::kRowW;
 #pragma unroll
         for (int step = 0; step < C::kSteps; ++step) {
           if constexpr (C::kSteps > 1) load(step, true);
@@ -761,7 +748,7 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
       }
       if (!ok) break;
       // the segment's outputs
-      if (!at_wait(&o_done[(g - 1u) & 1u], ((g - 1u) >> 1) & 1u)) failed = true;
+      if (!p8_wait(&o_done[(g - 1u) & 1u], ((g - 1u) >> 1) & 1u)) failed = true;
       ok = !p8_any(bar, failed);
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -782,7 +769,7 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
         float inv = 1.f / sum;
         if (sum == 0.f && pre == 0 && r < p.R) {  // no visible key at all: zero; visible keys of weight 0 alone: NaN
           bool any = false;
-          for (int c = 0; c < p.n; ++c) any = any || ((s_sees[qb][c] >> (r / p.G)) & 1ull);
+          for (int c = 0; c < p.n; ++c) any = any || ((s_sees[qb][c] >> s_node[r]) & 1ull);
           if (!any) inv = 0.f;
         }
         s_alpha[r] = whole ? inv : 1.f;
@@ -792,6 +779,7 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
         }
       }
       p8_meet(bar);
+      unsigned short* out = p.out + (static_cast<size_t>(sg.b) * p.n * p.Hq + sg.kvh * p.G) * D;
       const bool bad = *reinterpret_cast<volatile int*>(&s_bad) > si;  // (a later segment's mark counts too: only slower)
 #pragma unroll 1
       for (int i0 = 0; i0 < kMine; i0 += 16) {
@@ -812,7 +800,7 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
             const unsigned long long nodes = s_sees[qb][c];
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              if ((nodes >> (((first + i0 + i) / p.G) & 63)) & 1ull) o[i] = NAN;
+              if ((nodes >> s_node[first + i0 + i]) & 1ull) o[i] = NAN;
           }
         }
         // lanes 8 apart hold neighbouring columns: one of them takes both of a row, the other those of the next row
@@ -825,9 +813,7 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
           if (r >= p.R || !has_column) continue;
           const int at = column & ~1;
           if (whole) {
-            *reinterpret_cast<uint32_t*>(
-                p.out + ((static_cast<size_t>(sg.b) * p.n + r / p.G) * p.Hq + sg.kvh * p.G + r % p.G) * D + at) =
-                at_pack(lo * by, hi * by);
+            *reinterpret_cast<uint32_t*>(out + s_at[r] + at) = at_pack(lo * by, hi * by);
           } else {
             *reinterpret_cast<float2*>(p.part + (unit * p.R + r) * D + at) = make_float2(lo, hi);
           }
@@ -841,7 +827,7 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
       bool met = pa_sync(&s_meet, meet, lane);  // the ticket's release covers what the other warps wrote before it
       ok = !p8_any(bar, !met);
       if (!ok) break;
-      if (t == 384) {
+      if (t == 32 * C::kSoftmax) {
         // a pair's ticket is a byte: it counts to the grid at most, and goes back to zero before it is used again
         const int shift = 8 * (c0 & 3);
         const unsigned done = ((atom_add_acq_rel_gpu(hdr->tickets + c0 / 4, 1u << shift) >> shift) & 0xFFu) + 1u;
@@ -877,7 +863,8 @@ dt_status pa8_launch(Pa8Params& p, const Pa8Maps& maps, WsHeader* hdr, cudaStrea
   using C = P8<D, N>;
   const size_t fixed = C::kFixed + align_up(sizeof(int) * (2 * p.B + 1), 16);
   const int fit = static_cast<int>((kPa8SmemCap - fixed) / C::kEntry);
-  p.stages = fit > kP8MaxStages ? kP8MaxStages : fit;
+  // a multiple of four: a slot then always holds keys or always values, and always the same set's
+  p.stages = (fit > kP8MaxStages ? kP8MaxStages : fit) & ~3;
   const size_t smem = fixed + static_cast<size_t>(p.stages) * C::kEntry;
   if (ensure_dynamic_smem(reinterpret_cast<const void*>(paged_attn8_kernel<D, N>), kPa8SmemCap) != cudaSuccess)
     return DT_ERR_CUDA;

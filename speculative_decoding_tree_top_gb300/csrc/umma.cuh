@@ -43,6 +43,12 @@ __device__ __forceinline__ void umma_f16(uint32_t tmem_d, uint64_t da, uint64_t 
 __device__ __forceinline__ uint32_t umma_idesc_f16(int n, int m = 128) {  // f16 x f16 -> fp32, both K-major
   return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
+// K-major tile of dense rows of 64 or 128 bytes, swizzled over that width.
+__device__ __forceinline__ uint64_t umma_desc_rows(uint32_t saddr, uint32_t row_bytes) {
+  const uint64_t mode = row_bytes == 128 ? 2 : 4;
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
+         (static_cast<uint64_t>((8 * row_bytes) >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (mode << 61);
+}
 // MN-major tile of one swizzle atom's width: rows of `row_bytes` (32, 64 or 128, swizzled over that width) hold row_bytes / 2
 // elements of N, eight K rows per atom; `mn_stride` bytes to the next atom along N, when there is one.
 __device__ __forceinline__ uint64_t umma_desc_mn(uint32_t saddr, uint32_t row_bytes, uint32_t mn_stride) {
@@ -65,6 +71,12 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, ui
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
                ::"r"(tmem_d), "r"(tmem_a), "l"(db), "r"(idesc), "r"(acc) : "memory");
+}
+// e4m3 x e4m3 -> fp32, both operands in shared memory.
+__device__ __forceinline__ void umma_f8(uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t acc) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
+               ::"r"(tmem_d), "l"(da), "l"(db), "r"(idesc), "r"(acc) : "memory");
 }
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))

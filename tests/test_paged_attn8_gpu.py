@@ -4,9 +4,11 @@ that no request uses hold NaN codes, their blocks NaN scales, unused table entri
 The bound, element by element (attention_ref derives its like for bf16). A rounding is off by at most half a step: 2^-11
 of the value in fp16, 2^-8 in bf16, 2^-23 for an fp32 step of the tensor cores, which may cut. With p_j the softmax
 weights, w_j = p_j times the scale of value j, c_j its code, A = sum_j p_j |v_j|, T keys:
-- an element of q is off by 2^-25 after its row was brought to 2^14 or more: 2^-39 of the row's largest; a score is d
-  products: off by e = scale ((d + 4) 2^-23 sum |q||k| + 2^-39 max|q| sum |k|), a weight by the factor e + 2^-21 (the
-  approximate exponential), and so is the sum that divides: 2 (e + 2^-21) A;
+- a row of q is brought to more than 224 and at most 448 and split into two e4m3 terms. The first is off by at most eight
+  steps of the element's eighth bit; that is four bits, so the second is exact unless it falls below e4m3's normal range:
+  off by 2^-10 then, which is 2^-17 of the row's largest. A score is d products twice: off by e = scale ((2 d + 4) 2^-23
+  sum |q||k| + 2^-17 max|q| sum |k|), a weight by the factor e + 2^-21 (the approximate exponential), and so is the sum
+  that divides: 2 (e + 2^-21) A;
 - w_j to fp16, products in fp32 before it: (2^-11 + 2^-22) A, and where it is a subnormal number 2^-31 of the largest w
   that is seen (which starts out at 2^6, where a step is 2^-24 at least): 2^-31 max w sum |c_j|;
 - the sums over T keys in fp32: 2 T 2^-23 A; the output's rounding to bf16: 2^-8 |out|."""
@@ -67,8 +69,8 @@ def attend8(q, k, v, vs, seen, scale):
     p = torch.where(total > 0, p / total, torch.zeros_like(p))
     out, A = p @ v, p @ v.abs()
     d, T = q.shape[1], k.shape[0]
-    e = scale * ((d + 4) * 2.0 ** -23 * (q.abs() @ k.abs().t()) +
-                 2.0 ** -39 * q.abs().amax(1, keepdim=True) * k.abs().sum(1)).mul(seen).amax(1, keepdim=True)
+    e = scale * ((2 * d + 4) * 2.0 ** -23 * (q.abs() @ k.abs().t()) +
+                 2.0 ** -17 * q.abs().amax(1, keepdim=True) * k.abs().sum(1)).mul(seen).amax(1, keepdim=True)
     floor = 2.0 ** -31 * (p * vs).amax(1, keepdim=True) * (seen.double() @ (v.abs() / vs[:, None]))
     return out, A * (2 * (e + 2.0 ** -21) + 2.0 ** -11 + 2.0 ** -22 + 2 * T * 2.0 ** -23) + floor + 2.0 ** -8 * out.abs()
 
