@@ -30,12 +30,11 @@ namespace dt {
 namespace {
 
 constexpr int kP8MaxStages = 24;
-constexpr int kP8VStages = 4;
 // Blocks whose scales are there: the load runs at most half a ring ahead of the keys that the tensor cores have read, and
-// those two blocks ahead of the softmax.
-constexpr int kP8Scales = 16;
-static_assert(kP8MaxStages / 2 + 2 <= kP8Scales, "scales are not overwritten before they are read");
-constexpr size_t kPa8SmemCap = 232448 - 9216;  // opt-in shared memory of a CTA, less the static part
+// those two steps of up to two blocks ahead of the softmax.
+constexpr int kP8Scales = 32;
+static_assert(kP8MaxStages / 2 + 4 <= kP8Scales, "scales are not overwritten before they are read");
+constexpr size_t kPa8SmemCap = 232448 - 11264;  // opt-in shared memory of a CTA, less the static part
 // Weights times their values' scales are fp16: a row's largest starts out at 2^kP8Start and may grow to 2^kP8Most before
 // the reference is raised. fp16 goes up to 2^16 and holds subnormal numbers in steps of 2^-24.
 constexpr float kP8Start = 6.f, kP8Most = 14.f;
@@ -53,9 +52,32 @@ struct Pa8Maps {
   CUtensorMap k, v;  // [num_pages * Hkv][page_size][D], boxes of min(page_size, 128) rows
 };
 
-// Loads and stores of tensor memory with a row (lane) per thread: column c of the thread's lane is v[c]. Each load waits for
-// itself.
-__device__ __forceinline__ void p8_ld16(uint32_t taddr, float* v) {  // 16 columns
+// Loads and stores of n columns of tensor memory with a row (lane) per thread: column c of the thread's lane is v[c]. Each
+// load waits for itself.
+template <int n>
+__device__ __forceinline__ void p8_ld(uint32_t taddr, float* v);
+template <int n>
+__device__ __forceinline__ void p8_st(uint32_t taddr, const float* v);
+template <>
+__device__ __forceinline__ void p8_ld<4>(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+      : "r"(taddr)
+      : "memory");
+}
+template <>
+__device__ __forceinline__ void p8_ld<8>(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+      : "r"(taddr)
+      : "memory");
+}
+template <>
+__device__ __forceinline__ void p8_ld<16>(uint32_t taddr, float* v) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
@@ -64,9 +86,26 @@ __device__ __forceinline__ void p8_ld16(uint32_t taddr, float* v) {  // 16 colum
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void p8_ld32(uint32_t taddr, float* v) {  // 32 columns
+template <>
+__device__ __forceinline__ void p8_st<8>(uint32_t taddr, const float* v) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+      : "memory");
+}
+template <>
+__device__ __forceinline__ void p8_st<16>(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+        "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+template <>
+__device__ __forceinline__ void p8_ld<32>(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%1"
+      "7,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
         "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
@@ -75,11 +114,15 @@ __device__ __forceinline__ void p8_ld32(uint32_t taddr, float* v) {  // 32 colum
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void p8_st16(uint32_t taddr, const float* v) {  // 16 columns
+template <>
+__device__ __forceinline__ void p8_st<32>(uint32_t taddr, const float* v) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%"
+      "17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
         "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
-        "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+        "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]),
+        "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]),
+        "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
       : "memory");
 }
 // 16 lanes x 64 columns: in each group of 4 columns thread l holds column l % 4 of lanes l / 4 and l / 4 + 8.
@@ -118,25 +161,58 @@ __device__ __forceinline__ float p8_log2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// As at_wait, with the long way in one place: code that every role repeats crowds the instruction cache.
-__device__ __noinline__ bool p8_wait_long(uint64_t* bar, unsigned parity) { return at_wait(bar, parity); }
-__device__ __forceinline__ bool p8_wait(uint64_t* bar, unsigned parity) {
-  return mbar_try_wait(bar, parity) || p8_wait_long(bar, parity);
+// Waits. try_wait holds a warp for some fifty cycles only, so a warp that waits is a warp that polls, and takes issue slots
+// and instruction fetches from those that work. The roles that run ahead (load, queries, values) rest between their looks;
+// the others poll in as few instructions as there can be. The long way stands in one place each.
+__device__ __noinline__ bool p8_poll(uint64_t* bar, unsigned parity) {
+  const uint64_t t0 = global_timer_ns();
+  do {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
+        "LOOK:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+        "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 1000;\n\t@q bra LOOK;\n"
+        "DONE:\n\tselp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (done) return true;
+  } while (global_timer_ns() - t0 <= kAtBudgetNs);
+  return false;
 }
-// Whether any thread of the group says so; everyone of the group comes here, by whole warps.
+__device__ __noinline__ bool p8_nap(uint64_t* bar, unsigned parity) {
+  const uint64_t t0 = global_timer_ns();
+  do {
+#pragma unroll 1
+    for (int i = 0; i < 1000; ++i) {
+      __nanosleep(64);
+      if (mbar_try_wait(bar, parity)) return true;
+    }
+  } while (global_timer_ns() - t0 <= kAtBudgetNs);
+  return false;
+}
+__device__ __forceinline__ bool p8_wait(uint64_t* bar, unsigned parity) {
+  return mbar_try_wait(bar, parity) || p8_poll(bar, parity);
+}
+__device__ __forceinline__ bool p8_rest(uint64_t* bar, unsigned parity) {
+  return mbar_try_wait(bar, parity) || p8_nap(bar, parity);
+}
+// Whether any of a group's threads says so; all of them come here, by whole warps.
+template <int kThreads>
 __device__ __forceinline__ bool p8_any(int id, bool x) {
   uint32_t r;
   __syncwarp();
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n}"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n}"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(x)), "r"(id)
+      : "r"(static_cast<uint32_t>(x)), "r"(id), "n"(kThreads)
       : "memory");
   return r != 0u;
 }
+template <int kThreads>
 __device__ __forceinline__ void p8_meet(int id) {
   __syncwarp();
-  asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
 }
 // The warp's largest value of x; NaN counts for nothing.
 __device__ __forceinline__ float p8_warp_max(float x) {
@@ -167,17 +243,23 @@ __device__ __forceinline__ uint32_t p8_piece(int r, int c) {
                   : static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-// The shape of one instance: N columns of query rows (R rounded up).
-template <int D, int N>
+// The shape of one instance: N columns of query rows (R rounded up), of which a softmax thread has M for its key.
+// Measured, M rows a thread against twice as many: TODO
+template <int D, int N, int M, int kPar_, int kSets_, int kStep_>
 struct P8 {
-  static constexpr int kThreads = 512;
-  static constexpr int kGroups = N <= 32 ? 1 : 2;        // softmax groups of four warps, the last ones
-  static constexpr int kSets = 3 - kGroups;              // sets of four warps for the values: they take blocks in turn
-  static constexpr int kSoftmax = 16 - 4 * kGroups;      // warps 0: load, 1: MMA, 2-3: queries, 4 on: values, then softmax
-  static constexpr int kMine = N / kGroups;              // a softmax thread's query rows
-  static constexpr int kStep = kMine < 32 ? kMine : 32;  // taken at once
-  static constexpr int kSteps = kMine / kStep;
-  static constexpr int kVs = N <= 64 ? kP8VStages : 2;   // buffers of values
+  static constexpr int kPar = kPar_;                     // blocks of a step: the softmax takes them at once
+  static constexpr int kRowGroups = N > 16 ? N / M : 1;  // groups of four softmax warps share a block's rows
+  static constexpr int kGroups = kPar * kRowGroups;
+  static constexpr int kMeet = 128 * kPar;               // softmax threads that have the same rows
+  static constexpr int kSets = kSets_;                   // sets of four warps for the values: they take blocks in turn
+  static constexpr int kSoftmax = 4 + 4 * kSets;         // warps 0, 2: load, 1: MMA, 3: queries, 4 on: values, then softmax
+  static constexpr int kThreads = 32 * kSoftmax + 128 * kGroups;
+  static constexpr int kStep = kStep_;                   // rows taken at once
+  static constexpr int kSteps = M / kStep;
+  static constexpr int kSums = kSteps > 1 ? kSteps : M;  // a thread's sums: of its keys and a row each, or of its warp's
+  static constexpr bool kKeep = M <= 8;                  // registers for the rows' factors and references
+  static constexpr int kOut = M / kPar < 16 ? M / kPar : 16;  // rows of outputs that a thread takes at once
+  static constexpr int kVs = N <= 64 ? 4 : 2;            // buffers of values
   static constexpr int kOs = N <= 64 ? 2 : 1;            // buffers of outputs
   static constexpr uint32_t kEntry = kPaKeys * D;        // a ring entry: a block's keys or values
   static constexpr uint32_t kTerm = N * D;               // one term of the queries
@@ -186,37 +268,39 @@ struct P8 {
   static constexpr uint32_t kRowW = kAtom * 2;
   static constexpr uint32_t kW = kPaKeys * N * 2;        // a buffer of weights
   // tensor memory
-  static constexpr uint32_t kS = 0, kO = 2 * N, kV = kO + kOs * N;
+  static constexpr uint32_t kS = 0, kO = 2 * kPar * N, kV = kO + kOs * N;
   static_assert(kV + kVs * 64 <= 512, "tensor memory");
-  static constexpr size_t kFixed = 1024 + 2 * kQ + 2 * kW;
+  static constexpr size_t kFixed = 1024 + 2 * kQ + 2 * kPar * kW;
 };
 
-// Roles. Load: pages to the ring, as in the bf16 kernel, and their scales. Queries: a segment's rows, each brought by a power of two to at
-// most 448 and split in two, with the factor that undoes it; the nodes' mask, by keys. Values: lane = column, two keys a
-// register. Softmax: lane = key; its scales come with the keys (loaded by the softmax itself a block ahead they are late:
-// a block takes less than a load). MMA: the scores run one block ahead of the outputs, through the segments.
-template <int D, int N>
-__global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8Params p, const __grid_constant__ Pa8Maps maps,
-                                                                            WsHeader* hdr) {
-  using C = P8<D, N>;
-  constexpr int kThreads = C::kThreads, kMine = C::kMine, kStep = C::kStep, kVs = C::kVs, kOs = C::kOs;
+// Roles. Load: pages to the ring, as in the bf16 kernel, and their scales, keys and values by a warp each (a
+// box takes its warp about a hundred cycles to issue). Queries: a segment's rows, each brought by a
+// power of two to at most 448 and split in two, with the factor that undoes it; the nodes' mask, by keys. Values: lane =
+// column, two keys a register. Softmax: lane = key; its scales come with the keys (loaded by the softmax itself a block
+// ahead they are late: a block takes less than a load). MMA: the scores run one step ahead of the outputs, through the
+// segments.
+template <int D, int N, int M, int kPar_, int kSets_, int kStep_>
+__global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 1)
+    paged_attn8_kernel(Pa8Params p, const __grid_constant__ Pa8Maps maps, WsHeader* hdr) {
+  using C = P8<D, N, M, kPar_, kSets_, kStep_>;
+  constexpr int kThreads = C::kThreads, kPar = C::kPar, kMeet = C::kMeet, kStep = C::kStep, kVs = C::kVs, kOs = C::kOs;
   extern __shared__ float4 smem_f4[];
   unsigned char* sq =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_f4) + 1023) & ~uintptr_t(1023));
   unsigned char* sw = sq + 2 * C::kQ;
-  unsigned char* skv = sw + 2 * C::kW;
+  unsigned char* skv = sw + 2 * kPar * C::kW;
   int* cum = reinterpret_cast<int*>(skv + p.stages * C::kEntry);  // [B + 1]
   int* lens = cum + p.B + 1;                                      // [B]
   __shared__ uint64_t kv_full[kP8MaxStages], kv_empty[kP8MaxStages];
   __shared__ uint64_t v_full[kVs], v_empty[kVs];
   __shared__ uint64_t s_full[2], w_full[2], o_done[2], q_full[2], o_free[2], s_meet;
   __shared__ uint32_t s_tmem;
-  __shared__ unsigned s_kv_issued;
+  __shared__ unsigned s_issued[2];  // ring entries of keys, of values
   __shared__ int s_warp[kThreads / 32];
   __shared__ int s_bad, s_joins;
   __shared__ PaJoin s_join[2];
   __shared__ float s_scales[kP8Scales][2][kPaKeys / DT_MIN_PAGE];  // of a block's keys, then of its values
-  __shared__ __align__(16) float s_factor[2][N], s_nref[N], s_alpha[N], s_red[4][N];
+  __shared__ __align__(16) float s_factor[2][N], s_nref[N], s_alpha[N], s_red[4 * kPar][N];
   __shared__ unsigned long long s_sees[2][kPaNodes];  // bit i: node i sees the key of node c
   __shared__ int s_at[N];                             // a query row's place in a request's outputs
   __shared__ unsigned char s_node[N];                 // its node
@@ -235,12 +319,12 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
       mbar_init(&s_full[i], 1);
       mbar_init(&w_full[i], 4 * C::kGroups);
       mbar_init(&o_done[i], 1);
-      mbar_init(&q_full[i], 2);
+      mbar_init(&q_full[i], 1);
       mbar_init(&o_free[i], 4 * C::kGroups);
     }
     mbar_init(&s_meet, 4 * C::kGroups);
     mbar_fence_init();
-    s_kv_issued = 0u;
+    s_issued[0] = s_issued[1] = 0u;
     s_bad = s_joins = 0;
   }
   if (warp == 1) {
@@ -253,6 +337,9 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
   // rows of queries that there are not: zero, with a factor of zero
   for (int i = t; i < static_cast<int>(2 * C::kQ / 16); i += kThreads)
     if (static_cast<int>(i * 16 / D) % N >= p.R) reinterpret_cast<uint4*>(sq)[i] = make_uint4(0u, 0u, 0u, 0u);
+  // and the weights of rows that no softmax thread has
+  for (int i = t; i < static_cast<int>(2 * kPar * C::kW / 16); i += kThreads)
+    reinterpret_cast<uint4*>(sw)[i] = make_uint4(0u, 0u, 0u, 0u);
   for (int r = t; r < N; r += kThreads) {
     s_node[r] = static_cast<unsigned char>(r / p.G < kPaNodes ? r / p.G : kPaNodes - 1);
     s_at[r] = (r / p.G * p.Hq + r % p.G) * D;
@@ -291,12 +378,13 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
   const int ctas = W < p.grid ? static_cast<int>(W) : p.grid;  // that take a share: a block each at least
   PaWalk w = pa_walk(p, cum, W, ctas);
 
-  if (warp == 0) {  // load: the whole warp, one page's box a lane
-    unsigned st = 0, par = 1u, e = 0;  // ring entry, the parity of its last release, entries so far
+  if (warp == 0 || warp == 2) {  // load: the keys, the values; the whole warp, one page's box a lane
+    const int kv = warp >> 1;
+    const CUtensorMap* map = kv ? &maps.v : &maps.k;
+    unsigned st = kv, par = 1u, g = 0;  // ring entry, the parity of its last release, entries so far
     const int box_rows = p.page_size < kPaKeys ? p.page_size : kPaKeys;
     const int per_block = kPaKeys / box_rows;  // pages a block spans (1 when a page holds whole blocks)
     const int per_scale = p.block_shift < 7 ? kPaKeys >> p.block_shift : 1;  // scales a block has
-    unsigned g = 0;
     while (ok) {
       const PaSeg sg = pa_next(p, cum, w);
       if (sg.nblk == 0) break;
@@ -306,7 +394,7 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
       int win = ((sg.j0 * kPaKeys) >> p.page_shift) / 32;
       int cur = 32 * win + lane < used ? table[32 * win + lane] : 0;
       int nxt = 32 * (win + 1) + lane < used ? table[32 * (win + 1) + lane] : 0;
-      for (int j = 0; j < sg.nblk && ok; ++j) {
+      for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
         const int key = (sg.j0 + j) * kPaKeys, first = key >> p.page_shift, row = key & (p.page_size - 1);
         if (first / 32 != win) {
           ++win;
@@ -319,37 +407,30 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
           record_error(hdr, DT_ERR_INVALID_ARG);
           page = 0;
         }
-        // the block's scales: lanes 0-15 the keys', the others the values'
-        const int at = row + ((lane & 15) << p.block_shift), from = __shfl_sync(0xFFFFFFFFu, page, at >> p.page_shift);
-        const bool scaled = (lane & 15) < per_scale && (at >> p.page_shift) < pages;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {  // the keys, then the values
-          if (ok && e >= stages) ok = __all_sync(0xFFFFFFFFu, p8_wait(&kv_empty[st], par));
-          if (!ok) break;
-          if (lane == 0) mbar_expect_tx(&kv_full[st], static_cast<uint32_t>(pages * box_rows * D));
-          __syncwarp();
-          if (kv == 0) {
-            if (scaled) {
-              const float* src = (lane < 16 ? p.k_scale : p.v_scale) +
-                                 ((static_cast<size_t>(from) * p.Hkv + sg.kvh) << (p.page_shift - p.block_shift)) +
-                                 ((at & (p.page_size - 1)) >> p.block_shift);
-              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
-                               smem_u32(&s_scales[g % kP8Scales][lane >> 4][lane & 15])),
-                           "l"(src)
-                           : "memory");
-            }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&kv_full[st])) : "memory");
-            ++g;
-          }
-          if (lane < pages)
-            tma_load_3d(skv + st * C::kEntry + lane * box_rows * D, kv ? &maps.v : &maps.k, 0, row,
-                        page * p.Hkv + sg.kvh, &kv_full[st]);
-          ++e;
-          if (lane == 0) s_kv_issued = e;
-          if (++st == stages) {
-            st = 0;
-            par ^= 1u;
-          }
+        const int plane = page * p.Hkv + sg.kvh;  // num_pages Hkv < 2^31
+        // the block's scales come with its keys, the values' too: the softmax needs both, and waits for no value. Lanes
+        // 0-15 the keys', the others the values'
+        const int at = row + ((lane & 15) << p.block_shift), from = __shfl_sync(0xFFFFFFFFu, plane, at >> p.page_shift);
+        if (2 * g >= stages) ok = __all_sync(0xFFFFFFFFu, p8_rest(&kv_empty[st], par));
+        if (!ok) break;
+        if (lane == 0) mbar_expect_tx(&kv_full[st], static_cast<uint32_t>(pages * box_rows * D));
+        __syncwarp();
+        if (lane < pages)
+          tma_load_3d(skv + st * C::kEntry + lane * box_rows * D, map, 0, row, plane, &kv_full[st]);
+        if (kv == 0 && (lane & 15) < per_scale && (at >> p.page_shift) < pages) {
+          const float* src = (lane < 16 ? p.k_scale : p.v_scale) + (static_cast<size_t>(from) << (p.page_shift - p.block_shift)) +
+                             ((at & (p.page_size - 1)) >> p.block_shift);
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(
+                           &s_scales[g % kP8Scales][lane >> 4][lane & 15])),
+                       "l"(src)
+                       : "memory");
+        }
+        if (kv == 0) asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&kv_full[st])) : "memory");
+        if (lane == 0) s_issued[kv] = g + 1u;
+        st += 2;
+        if (st >= stages) {
+          st = kv;
+          par ^= 1u;
         }
       }
     }
@@ -368,70 +449,78 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
       PaSeg ss{};
       int js = 0, sis = -1;
       unsigned gs = 0, st = 0, par = 0;  // the ring entry of the next keys: every other one
-      auto scores = [&]() {  // of the next block, if there is one
-        if (js == ss.nblk) {
+      auto scores = [&]() {  // of the next step, if there is one
+        if (js >= ss.nblk) {
           ss = pa_next(p, cum, ws);
           js = 0;
           if (ss.nblk == 0) return true;
           ++sis;
           if (!wait(&q_full[sis & 1], static_cast<unsigned>(sis >> 1) & 1u)) return false;
         }
-        if (!wait(&kv_full[st], par)) return false;
-        const uint64_t q0 = dq + static_cast<uint64_t>((sis & 1) * (C::kQ >> 4)), k0 = dk + st * (C::kEntry >> 4);
+        const uint64_t q0 = dq + static_cast<uint64_t>((sis & 1) * (C::kQ >> 4));
+#pragma unroll 1
+        for (int u = 0; u < kPar && js + u < ss.nblk; ++u) {
+          if (!wait(&kv_full[st], par)) return false;
+          const uint64_t k0 = dk + st * (C::kEntry >> 4);
+          const uint32_t to = tmem + C::kS + ((gs & 1u) * kPar + u) * N;
 #pragma unroll
-        for (int term = 0; term < 2; ++term)
+          for (int term = 0; term < 2; ++term)
 #pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk)
-            umma_f8(tmem + C::kS + (gs & 1u) * N, k0 + 2u * kk, q0 + ((term * C::kTerm) >> 4) + 2u * kk, id_s,
-                    term + kk > 0 ? 1u : 0u);
-        umma_commit(&kv_empty[st]);
-        st += 2;
-        if (st == stages) {
-          st = 0;
-          par ^= 1u;
+            for (int kk = 0; kk < D / 32; ++kk)
+              umma_f8(to, k0 + 2u * kk, q0 + ((term * C::kTerm) >> 4) + 2u * kk, id_s, term + kk > 0 ? 1u : 0u);
+          umma_commit(&kv_empty[st]);
+          st += 2;
+          if (st == stages) {
+            st = 0;
+            par ^= 1u;
+          }
         }
         umma_commit(&s_full[gs & 1u]);
-        ++js;
+        js += kPar;
         ++gs;
         return true;
       };
-      unsigned g = 0;
+      unsigned g = 0, step = 0;  // blocks and steps so far
       ok = scores();
       for (int si = 0; ok; ++si) {
         const PaSeg sg = pa_next(p, cum, w);
         if (sg.nblk == 0) break;
         const unsigned ob = static_cast<unsigned>(si) % kOs;
-        for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
-          // its buffer was freed by block g - 1's softmax (waited for below, one block ago)
+        for (int j = 0; j < sg.nblk && ok; j += kPar, ++step) {
+          // their buffers were freed by the softmax of the step before (waited for below, one step ago)
           ok = scores();
           if (ok && j == 0 && si >= kOs) {  // the segment that had the buffer before has been read
             const int was = si - kOs;
             ok = wait(&o_free[was & 1], static_cast<unsigned>(was >> 1) & 1u);
           }
-          const unsigned vb = g % kVs;
-          if (ok) ok = wait(&v_full[vb], (g / kVs) & 1u);
-          if (ok) ok = wait(&w_full[g & 1u], (g >> 1) & 1u);
-          if (!ok) break;
+          if (ok) ok = wait(&w_full[step & 1u], (step >> 1) & 1u);
+#pragma unroll 1
+          for (int u = 0; u < kPar && j + u < sg.nblk && ok; ++u, ++g) {
+            const unsigned vb = g % kVs;
+            ok = wait(&v_full[vb], (g / kVs) & 1u);
+            if (!ok) break;
+            const uint64_t w0 = dw + ((((step & 1u) * kPar + u) * C::kW) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kPaKeys / 16; ++kk)
-            umma_f16_ts(tmem + C::kO + ob * N, tmem + C::kV + vb * 64u + 8u * kk,
-                        dw + (((g & 1u) * C::kW + kk * 16u * C::kRowW) >> 4), id_o, (j > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(&v_empty[vb]);
-          umma_commit(&o_done[g & 1u]);
+            for (int kk = 0; kk < kPaKeys / 16; ++kk)
+              umma_f16_ts(tmem + C::kO + ob * N, tmem + C::kV + vb * 64u + 8u * kk, w0 + ((kk * 16u * C::kRowW) >> 4), id_o,
+                          (j + u > 0 || kk > 0) ? 1u : 0u);
+            umma_commit(&v_empty[vb]);
+          }
+          if (!ok) break;
+          umma_commit(&o_done[step & 1u]);
         }
       }
     }
   } else if (warp < 4) {  // queries
-    const int who = warp - 2;
     for (int si = 0; ok; ++si) {
       const PaSeg sg = pa_next(p, cum, w);
       if (sg.nblk == 0) break;
       const unsigned qb = static_cast<unsigned>(si) & 1u;
       // the segment that had the buffer before is over: its factors and its mask are not read any more
-      if (si >= 2) ok = __all_sync(0xFFFFFFFFu, p8_wait(&o_free[qb], static_cast<unsigned>((si >> 1) - 1) & 1u));
+      if (si >= 2) ok = __all_sync(0xFFFFFFFFu, p8_rest(&o_free[qb], static_cast<unsigned>((si >> 1) - 1) & 1u));
       if (!ok) break;
-      const int c = 32 * who + lane;
-      if (c < p.n) {
+#pragma unroll 1
+      for (int c = lane; c < p.n; c += 32) {
         unsigned long long bits = ~0ull << c;
         if (p.mask) {
           const uint8_t* col = p.mask + static_cast<size_t>(sg.b) * p.n * p.n + c;
@@ -442,52 +531,63 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
         s_sees[qb][c] = bits;
       }
       unsigned char* qd = sq + qb * C::kQ;
-      constexpr int kLanes = D / 4, kAcross = 32 / kLanes, kAtOnce = 8;  // lanes a row, rows a step, steps in flight
-      const int sub = lane % kLanes;
-      const unsigned short* src = p.q + (static_cast<size_t>(sg.b) * p.n * p.Hq + sg.kvh * p.G) * D + 4 * sub;
+      // eight lanes a row, D / 8 elements each; four rows a step, several steps' loads in flight
+      constexpr int kEach = D / 8, kAtOnce = 4;
+      const int sub = lane & 7;
+      const unsigned short* src = p.q + (static_cast<size_t>(sg.b) * p.n * p.Hq + sg.kvh * p.G) * D + kEach * sub;
 #pragma unroll 1
-      for (int r0 = who * kAcross; r0 < p.R; r0 += 2 * kAcross * kAtOnce) {
-        uint2 x[kAtOnce];
+      for (int r0 = 0; r0 < p.R; r0 += 4 * kAtOnce) {
+        uint4 x[kAtOnce][kEach / 8];
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
-          const int r = r0 + 2 * kAcross * u + lane / kLanes;
-          x[u] = r < p.R ? *reinterpret_cast<const uint2*>(src + s_at[r]) : make_uint2(0u, 0u);
+          const int r = r0 + 4 * u + (lane >> 3);
+#pragma unroll
+          for (int i = 0; i < kEach / 8; ++i)
+            x[u][i] = r < p.R ? *reinterpret_cast<const uint4*>(src + s_at[r] + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
-          const int r = r0 + 2 * kAcross * u + lane / kLanes;
-          if (r0 + 2 * kAcross * u >= p.R) break;
-          float f[4] = {__uint_as_float(x[u].x << 16), __uint_as_float(x[u].x & 0xFFFF0000u),
-                        __uint_as_float(x[u].y << 16), __uint_as_float(x[u].y & 0xFFFF0000u)};
-          unsigned most = 0u;  // the bits of the row's largest finite element
+          if (r0 + 4 * u >= p.R) break;
+          const int r = r0 + 4 * u + (lane >> 3);
+          const uint32_t* bits = reinterpret_cast<const uint32_t*>(x[u]);
+          unsigned most = 0u;  // the bits of the row's largest finite element, as a bf16
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const unsigned m = __float_as_uint(f[i]) & 0x7FFFFFFFu;
-            if (m < 0x7F800000u && m > most) most = m;
+          for (int i = 0; i < kEach / 2; ++i) {
+            const unsigned lo = bits[i] & 0x7FFFu, hi = (bits[i] >> 16) & 0x7FFFu;
+            if (lo < 0x7F80u && lo > most) most = lo;
+            if (hi < 0x7F80u && hi > most) most = hi;
           }
 #pragma unroll
-          for (int h = kLanes / 2; h > 0; h >>= 1) {
+          for (int h = 4; h > 0; h >>= 1) {
             const unsigned other = __shfl_xor_sync(0xFFFFFFFFu, most, h);
             most = other > most ? other : most;
           }
           // the largest power of two that leaves it at 448 = 1.75 2^8 or less
-          int up = ((most & 0x7FFFFFu) > 0x600000u ? 7 : 8) - (static_cast<int>(most >> 23) - 127);
+          int up = ((most & 0x7Fu) > 0x60u ? 7 : 8) - (static_cast<int>(most >> 7) - 127);
           if (up > 100) up = 100;  // (nothing is lost: such a row's scores are zero whatever the keys are)
           const float by = __uint_as_float(static_cast<unsigned>(up + 127) << 23);
-          uint32_t q1 = 0u, q2 = 0u;
+          uint32_t q1[kEach / 4], q2[kEach / 4];
 #pragma unroll
-          for (int i = 0; i < 4; i += 2) {
-            const float a = f[i] * by, b = f[i + 1] * by;
+          for (int i = 0; i < kEach / 4; ++i) q1[i] = q2[i] = 0u;
+#pragma unroll
+          for (int i = 0; i < kEach / 2; ++i) {
+            const float a = __uint_as_float(bits[i] << 16) * by, b = __uint_as_float(bits[i] & 0xFFFF0000u) * by;
             const float a1 = fabsf(a) <= 448.f ? a : NAN, b1 = fabsf(b) <= 448.f ? b : NAN;
             const uint32_t c = p8_code2(a1, b1), two = p8_two(c);
             const float2 got = __half22float2(*reinterpret_cast<const __half2*>(&two));
-            q1 |= c << (8 * i);
-            q2 |= p8_code2(a1 - got.x, b1 - got.y) << (8 * i);
+            q1[i / 2] |= c << (16 * (i & 1));
+            q2[i / 2] |= p8_code2(a1 - got.x, b1 - got.y) << (16 * (i & 1));
           }
           if (r < p.R) {
-            unsigned char* at = qd + p8_piece<D>(r, sub >> 2) + (sub & 3) * 4;
-            *reinterpret_cast<uint32_t*>(at) = q1;
-            *reinterpret_cast<uint32_t*>(at + C::kTerm) = q2;
+            if constexpr (D == 128) {
+              unsigned char* at = qd + p8_piece<D>(r, sub);
+              *reinterpret_cast<uint4*>(at) = make_uint4(q1[0], q1[1], q1[kEach / 4 - 2], q1[kEach / 4 - 1]);
+              *reinterpret_cast<uint4*>(at + C::kTerm) = make_uint4(q2[0], q2[1], q2[kEach / 4 - 2], q2[kEach / 4 - 1]);
+            } else {
+              unsigned char* at = qd + p8_piece<D>(r, sub >> 1) + 8 * (sub & 1);
+              *reinterpret_cast<uint2*>(at) = make_uint2(q1[0], q1[1]);
+              *reinterpret_cast<uint2*>(at + C::kTerm) = make_uint2(q2[0], q2[1]);
+            }
             if (sub == 0) s_factor[qb][r] = p.scale_log2 * __uint_as_float(static_cast<unsigned>(127 - up) << 23);
           }
         }
@@ -520,7 +620,7 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
         }
         const unsigned vb = g % kVs;
         const int kbase = (sg.j0 + j) * kPaKeys;
-        ok = __all_sync(0xFFFFFFFFu, p8_wait(&kv_full[at], par));
+        ok = __all_sync(0xFFFFFFFFu, p8_rest(&kv_full[at], par));
         if (!ok) break;
         const uint32_t src = smem_u32(skv + at * C::kEntry);
         if (__builtin_expect(kbase + kPaKeys > common, 0)) {
@@ -549,7 +649,7 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
           __syncwarp();
         }
         if (g >= kVs) {
-          ok = __all_sync(0xFFFFFFFFu, p8_wait(&v_empty[vb], (g / kVs - 1) & 1u));
+          ok = __all_sync(0xFFFFFFFFu, p8_rest(&v_empty[vb], (g / kVs - 1) & 1u));
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         }
@@ -583,33 +683,43 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
     }
   } else {  // softmax
     const int group = (warp - C::kSoftmax) >> 2, quad = warp & 3, row = 32 * quad + lane;  // the thread's key of a block
-    const int bar = 1 + group, first = group * kMine, mine = t - (32 * C::kSoftmax + 128 * group);
+    const int part = group / C::kRowGroups, first = group % C::kRowGroups * M;  // its block of a step, its first row
+    const int bar = 1 + group % C::kRowGroups, mine = 128 * part + row, four = 4 * part + quad;
     const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
     // the column that the thread's lane of the outputs is, and the pair of columns that it writes
     const int column = D / 4 * quad + 16 * (lane >> 4) + 2 * (lane & 7) + ((lane >> 3) & 1);
     const bool has_column = D == 128 || lane < 16;
     const int my_scale = p.block_shift < 7 ? row >> p.block_shift : 0;
-    unsigned g = 0, meet = 0;
-    bool failed = false;  // a wait ran out; the group leaves together, at its next meeting
+    unsigned g = part, step = 0, meet = 0;  // the thread's block, and the steps so far
+    bool failed = false;                    // a wait ran out; those with the same rows leave together, at their next meeting
     for (int si = 0; ok; ++si) {
       const PaSeg sg = pa_next(p, cum, w);
       if (sg.nblk == 0) break;
       const unsigned qb = static_cast<unsigned>(si) & 1u;
       const uint32_t to = tmem + lanes + C::kO + (static_cast<unsigned>(si) % kOs) * N + first;
       const int len = lens[sg.b], pre = len - p.n, common = pa_common(p, len);
-      constexpr int kSums = kMine <= 32 ? kMine : kMine / 32;
-      float l[kSums];
+      float l[C::kSums], factors[C::kKeep ? M : 4], nrefs[C::kKeep ? M : 4];
 #pragma unroll
-      for (int i = 0; i < kSums; ++i) l[i] = 0.f;
-      if (mine < kMine) s_nref[first + mine] = kAtNone;
-      p8_meet(bar);
-      for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
-        const uint32_t ts = tmem + lanes + C::kS + (g & 1u) * N + first;
-        if (!p8_wait(&s_full[g & 1u], (g >> 1) & 1u)) failed = true;
+      for (int i = 0; i < C::kSums; ++i) l[i] = 0.f;
+      if (mine < M) s_nref[first + mine] = kAtNone;
+      p8_meet<kMeet>(bar);
+      for (int j = part; j - part < sg.nblk && ok; j += kPar, g += kPar, ++step) {
+        const bool there = j < sg.nblk;  // the step's last block may be missing
+        const uint32_t ts = tmem + lanes + C::kS + ((step & 1u) * kPar + part) * N + first;
+        if (!p8_wait(&s_full[step & 1u], (step >> 1) & 1u)) failed = true;
         __syncwarp();
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const float2 scales =
-            make_float2(s_scales[g % kP8Scales][0][my_scale], s_scales[g % kP8Scales][1][my_scale]);
+        if constexpr (C::kKeep) {
+          if (j < kPar) {
+#pragma unroll
+            for (int i = 0; i < M; i += 4) {
+              *reinterpret_cast<float4*>(factors + i) = *reinterpret_cast<const float4*>(&s_factor[qb][first + i]);
+              nrefs[i] = nrefs[i + 1] = nrefs[i + 2] = nrefs[i + 3] = kAtNone;
+            }
+          }
+        }
+        float2 scales = make_float2(0.f, 0.f);
+        if (there) scales = make_float2(s_scales[g % kP8Scales][0][my_scale], s_scales[g % kP8Scales][1][my_scale]);
         const float log_vs = fmaxf(p8_log2(fabsf(scales.y)), kP8LeastScale);
         const int key = (sg.j0 + j) * kPaKeys + row;
         const bool masked = (sg.j0 + j + 1) * kPaKeys > common;
@@ -619,31 +729,33 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
           if (key < len) {
             const unsigned long long nodes = s_sees[qb][key - pre];
 #pragma unroll 4
-            for (int i = 0; i < kMine; ++i) sees |= ((nodes >> s_node[first + i]) & 1ull) << i;
+            for (int i = 0; i < M; ++i) sees |= ((nodes >> s_node[first + i]) & 1ull) << i;
           }
         }
         const float value_scale = sees == 0ull ? 0.f : scales.y;
         __syncwarp();
-        // kStep scores from the step's first row on, scaled, against the reference
+        // kStep scores from row `r` of the thread's on, scaled, against the reference
         float x[kStep];
-        auto load = [&](int step, bool against) {
-          if constexpr (kStep == 16) p8_ld16(ts, x);
-          else p8_ld32(ts + 32u * step, x);
-          const float* factor = &s_factor[qb][first + kStep * step];
-          const float* nref = &s_nref[first + kStep * step];
+        auto load = [&](int r, bool against) {
+          p8_ld<kStep>(ts + r, x);
           const uint64_t ks = at_pair(scales.x, scales.x);
 #pragma unroll
           for (int i = 0; i < kStep; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(factor + i);
-            float4 n4 = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (against) n4 = *reinterpret_cast<const float4*>(nref + i);
+            float4 f, n4 = make_float4(0.f, 0.f, 0.f, 0.f);
+            if constexpr (C::kKeep) {
+              f = make_float4(factors[i], factors[i + 1], factors[i + 2], factors[i + 3]);
+              if (against) n4 = make_float4(nrefs[i], nrefs[i + 1], nrefs[i + 2], nrefs[i + 3]);
+            } else {
+              f = *reinterpret_cast<const float4*>(&s_factor[qb][first + r + i]);
+              if (against) n4 = *reinterpret_cast<const float4*>(&s_nref[first + r + i]);
+            }
             at_unpair(at_fma2(at_pair(x[i], x[i + 1]), p8_mul2(at_pair(f.x, f.y), ks), at_pair(n4.x, n4.y)), x[i],
                       x[i + 1]);
             at_unpair(at_fma2(at_pair(x[i + 2], x[i + 3]), p8_mul2(at_pair(f.z, f.w), ks), at_pair(n4.z, n4.w)), x[i + 2],
                       x[i + 3]);
           }
           if (__builtin_expect(masked, 0)) {
-            const unsigned bits = static_cast<unsigned>(sees >> (kStep * step));
+            const unsigned bits = static_cast<unsigned>(sees >> r);
 #pragma unroll
             for (int i = 0; i < kStep; ++i)
               if (!((bits >> i) & 1u)) x[i] = -INFINITY;
@@ -652,120 +764,136 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
 #pragma unroll 1
         for (bool raised = false;; raised = true) {
           float top = -INFINITY;
+          if (there) {
 #pragma unroll 1
-          for (int step = 0; step < C::kSteps; ++step) {
-            load(step, true);
+            for (int r = 0; r < M; r += kStep) {
+              load(r, true);
 #pragma unroll
-            for (int i = 0; i < kStep; i += 2) top = at_max3(top, x[i], x[i + 1]);
+              for (int i = 0; i < kStep; i += 2) top = at_max3(top, x[i], x[i + 1]);
+            }
           }
-          if (raised || __builtin_expect(!p8_any(bar, top + log_vs > kP8Most || failed), 1)) break;
+          if (raised || __builtin_expect(!p8_any<kMeet>(bar, top + log_vs > kP8Most || failed), 1)) break;
           // rare: raise references
-          if (p8_any(bar, failed)) {
+          if (p8_any<kMeet>(bar, failed)) {
             ok = false;
             break;
           }
 #pragma unroll 1
-          for (int step = 0; step < C::kSteps; ++step) {
-            load(step, false);
+          for (int r = 0; r < M; r += kStep) {
             float keep = -INFINITY;
+            if (there) {
+              load(r, false);
 #pragma unroll
-            for (int i = 0; i < kStep; ++i) {
-              const float m = p8_warp_max(x[i] + log_vs);
-              if (lane == i) keep = m;
+              for (int i = 0; i < kStep; ++i) {
+                const float m = p8_warp_max(x[i] + log_vs);
+                if (lane == i) keep = m;
+              }
             }
-            if (lane < kStep) s_red[quad][first + kStep * step + lane] = keep;
+            if (lane < kStep) s_red[four][first + r + lane] = keep;
           }
-          p8_meet(bar);
-          if (mine < kMine) {
+          p8_meet<kMeet>(bar);
+          if (mine < M) {
             const int r = first + mine;
-            const float m = fmaxf(fmaxf(s_red[0][r], s_red[1][r]), fmaxf(s_red[2][r], s_red[3][r]));
+            float m = s_red[0][r];
+#pragma unroll
+            for (int i = 1; i < 4 * kPar; ++i) m = fmaxf(m, s_red[i][r]);
             const float was = s_nref[r];
             const bool raise = m + was > kP8Most;
             const float now = kP8Start - m;
             s_alpha[r] = raise ? at_exp2(now - was) : 1.f;  // from nothing: 0
             if (raise) s_nref[r] = now;
           }
-          p8_meet(bar);
-          if constexpr (kMine <= 32) {
+          p8_meet<kMeet>(bar);
+          if constexpr (C::kSteps == 1) {
 #pragma unroll
-            for (int i = 0; i < kMine; ++i) l[i] *= s_alpha[first + i];
+            for (int i = 0; i < M; ++i) l[i] *= s_alpha[first + i];
           } else {
 #pragma unroll
-            for (int i = 0; i < kSums; ++i) l[i] *= s_alpha[first + 32 * i + lane];
+            for (int i = 0; i < C::kSums; ++i) l[i] *= s_alpha[first + kStep * i + lane / (32 / kStep)];
           }
-          if (j > 0) {
-            if (!p8_wait(&o_done[(g - 1u) & 1u], ((g - 1u) >> 1) & 1u)) failed = true;
+          if constexpr (C::kKeep) {
+#pragma unroll
+            for (int i = 0; i < M; ++i) nrefs[i] = s_nref[first + i];
+          }
+          if (part == 0 && j > 0) {
+            if (!p8_wait(&o_done[(step - 1u) & 1u], ((step - 1u) >> 1) & 1u)) failed = true;
             __syncwarp();
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll 1
-            for (int i0 = 0; i0 < kMine; i0 += 16) {
-              float o[16];
-              p8_ld16(to + i0, o);
+            for (int r = 0; r < M; r += kStep) {
+              float o[kStep];
+              p8_ld<kStep>(to + r, o);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= s_alpha[first + i0 + i];
-              p8_st16(to + i0, o);
+              for (int i = 0; i < kStep; ++i) o[i] *= s_alpha[first + r + i];
+              p8_st<kStep>(to + r, o);
             }
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           }
         }
         if (!ok) break;
-        if (g >= 2u) {  // the product that read the buffer before is done
-          if (!p8_wait(&o_done[g & 1u], ((g - 2u) >> 1) & 1u)) failed = true;
+        if (step >= 2u) {  // the product that read the buffer before is done
+          if (!p8_wait(&o_done[step & 1u], ((step - 2u) >> 1) & 1u)) failed = true;
           __syncwarp();
         }
-        unsigned char* wrow = sw + (g & 1u) * C::kW + row * C::kRowW;
-#pragma unroll
-        for (int step = 0; step < C::kSteps; ++step) {
-          if constexpr (C::kSteps > 1) load(step, true);
-          float sums[kStep];
-          uint32_t h[kStep / 2];
+        if (there) {
+          unsigned char* wrow = sw + ((step & 1u) * kPar + part) * C::kW + row * C::kRowW;
+          const int turn = C::kRowW == 128 ? row & 7 : C::kRowW == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
           const uint64_t vs = at_pair(value_scale, value_scale);
 #pragma unroll
-          for (int i = 0; i < kStep; i += 2) {
-            float a = at_exp2(x[i]), b = at_exp2(x[i + 1]);
-            if constexpr (kMine <= 32) {
-              at_unpair(at_add2(at_pair(l[i], l[i + 1]), at_pair(a, b)), l[i], l[i + 1]);
-            } else {
-              sums[i] = a;
-              sums[i + 1] = b;
-            }
-            at_unpair(p8_mul2(at_pair(a, b), vs), a, b);
-            h[i / 2] = p8_pack(a, b);
-          }
-          if constexpr (kMine > 32) l[step] += p8_warp_sums(sums, lane);
+          for (int r = 0; r < M; r += kStep) {
+            if constexpr (C::kSteps > 1) load(r, true);
+            float sums[kStep];
+            uint32_t h[kStep / 2];
 #pragma unroll
-          for (int c = 0; c < kStep / 8; ++c) {
-            const int r = first + kStep * step + 8 * c, atom = r / C::kAtom, piece = r % C::kAtom / 8;
-            const int turn = C::kRowW == 128 ? row & 7 : C::kRowW == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
-            *reinterpret_cast<uint4*>(wrow + atom * (kPaKeys * 128) + ((piece ^ turn) << 4)) =
-                make_uint4(h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]);
+            for (int i = 0; i < kStep; i += 2) {
+              float a = at_exp2(x[i]), b = at_exp2(x[i + 1]);
+              if constexpr (C::kSteps == 1) {
+                at_unpair(at_add2(at_pair(l[i], l[i + 1]), at_pair(a, b)), l[i], l[i + 1]);
+              } else {
+                sums[i] = a;
+                sums[i + 1] = b;
+              }
+              at_unpair(p8_mul2(at_pair(a, b), vs), a, b);
+              h[i / 2] = p8_pack(a, b);
+            }
+            if constexpr (C::kSteps > 1) l[r / kStep] += p8_warp_sums(sums, lane);
+#pragma unroll
+            for (int c = 0; c < kStep / 8; ++c) {
+              const int at = first + r + 8 * c, atom = at / C::kAtom, piece = at % C::kAtom / 8;
+              *reinterpret_cast<uint4*>(wrow + atom * (kPaKeys * 128) + ((piece ^ turn) << 4)) =
+                  make_uint4(h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]);
+            }
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads the weights through the async proxy
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(&w_full[g & 1u]);
+        if (lane == 0) mbar_arrive(&w_full[step & 1u]);
       }
       if (!ok) break;
+      g -= kPar * ((sg.nblk + kPar - 1) / kPar) - sg.nblk;  // the blocks of the last step that were not there
       // the segment's outputs
-      if (!p8_wait(&o_done[(g - 1u) & 1u], ((g - 1u) >> 1) & 1u)) failed = true;
-      ok = !p8_any(bar, failed);
+      if (!p8_wait(&o_done[(step - 1u) & 1u], ((step - 1u) >> 1) & 1u)) failed = true;
+      ok = !p8_any<kMeet>(bar, failed);
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      // the sums over the keys: by warps, then over the four
-      if constexpr (kMine <= 32) {
+      // the sums over the keys: by warps, then over the warps
+      if constexpr (C::kSteps == 1) {
         const float sum = p8_warp_sums(l, lane);
-        if (lane % (32 / kMine) == 0) s_red[quad][first + lane / (32 / kMine)] = sum;
+        if (lane % (32 / M) == 0) s_red[four][first + lane / (32 / M)] = sum;
       } else {
 #pragma unroll
-        for (int i = 0; i < kSums; ++i) s_red[quad][first + 32 * i + lane] = l[i];
+        for (int i = 0; i < C::kSums; ++i)
+          if (lane % (32 / kStep) == 0) s_red[four][first + kStep * i + lane / (32 / kStep)] = l[i];
       }
-      p8_meet(bar);
+      p8_meet<kMeet>(bar);
       const bool whole = sg.nblk == sg.nb;
       const size_t unit = 2 * static_cast<size_t>(blockIdx.x) + (sg.j0 == 0 ? 1 : 0);
-      if (mine < kMine) {
+      if (mine < M) {
         const int r = first + mine;
-        const float sum = (s_red[0][r] + s_red[1][r]) + (s_red[2][r] + s_red[3][r]);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4 * kPar; ++i) sum += s_red[i][r];
         float inv = 1.f / sum;
         if (sum == 0.f && pre == 0 && r < p.R) {  // no visible key at all: zero; visible keys of weight 0 alone: NaN
           bool any = false;
@@ -778,54 +906,53 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
           *reinterpret_cast<float2*>(p.ml + 2 * (unit * p.R + r)) = make_float2(nref == kAtNone ? -INFINITY : -nref, sum);
         }
       }
-      p8_meet(bar);
-      unsigned short* out = p.out + (static_cast<size_t>(sg.b) * p.n * p.Hq + sg.kvh * p.G) * D;
+      p8_meet<kMeet>(bar);
+      unsigned short* out = p.out + (static_cast<size_t>(sg.b) * p.n * p.Hq + sg.kvh * p.G) * D + (column & ~1);
+      float* partial = p.part + unit * p.R * D + (column & ~1);
       const bool bad = *reinterpret_cast<volatile int*>(&s_bad) > si;  // (a later segment's mark counts too: only slower)
+      constexpr int kOut = C::kOut;
+      const int from = M / kPar * part;
 #pragma unroll 1
-      for (int i0 = 0; i0 < kMine; i0 += 16) {
-        float o[16];
+      for (int i0 = from; i0 < from + M / kPar; i0 += kOut) {
+        float o[kOut];
         __syncwarp();
-        p8_ld16(to + i0, o);
+        p8_ld<kOut>(to + i0, o);
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         if (first + i0 >= p.R) continue;
-        if (bad && has_column) {  // rare: NaN among the nodes' codes
+        if (__builtin_expect(bad && has_column, 0)) {  // rare: NaN among the nodes' codes
+#pragma unroll 1
           for (int c = 0; c < p.n; ++c) {
             const int key = pre + c;
             if (key < sg.j0 * kPaKeys || key >= (sg.j0 + sg.nblk) * kPaKeys) continue;
-            const int page = p.page_table[static_cast<size_t>(sg.b) * p.max_pages + key / p.page_size];
+            const int page = p.page_table[static_cast<size_t>(sg.b) * p.max_pages + (key >> p.page_shift)];
             if (page < 0 || page >= p.num_pages) continue;
-            const unsigned char code =
-                p.v_cache[((static_cast<size_t>(page) * p.Hkv + sg.kvh) * p.page_size + key % p.page_size) * D + column];
-            if ((code & 0x7Fu) != 0x7Fu) continue;
+            const size_t at = (static_cast<size_t>(page) * p.Hkv + sg.kvh) * p.page_size + (key & (p.page_size - 1));
+            if ((p.v_cache[at * D + column] & 0x7Fu) != 0x7Fu) continue;
             const unsigned long long nodes = s_sees[qb][c];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
+            for (int i = 0; i < kOut; ++i)
               if ((nodes >> s_node[first + i0 + i]) & 1ull) o[i] = NAN;
           }
         }
         // lanes 8 apart hold neighbouring columns: one of them takes both of a row, the other those of the next row
         const bool odd = (lane & 8) != 0;
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
+        for (int i = 0; i < kOut; i += 2) {
           const int r = first + i0 + i + (odd ? 1 : 0);
           const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? o[i] : o[i + 1], 8);
-          const float lo = odd ? got : o[i], hi = odd ? o[i + 1] : got, by = s_alpha[first + i0 + i + (odd ? 1 : 0)];
+          const float lo = odd ? got : o[i], hi = odd ? o[i + 1] : got, by = s_alpha[r];
           if (r >= p.R || !has_column) continue;
-          const int at = column & ~1;
-          if (whole) {
-            *reinterpret_cast<uint32_t*>(out + s_at[r] + at) = at_pack(lo * by, hi * by);
-          } else {
-            *reinterpret_cast<float2*>(p.part + (unit * p.R + r) * D + at) = make_float2(lo, hi);
-          }
+          if (whole) *reinterpret_cast<uint32_t*>(out + s_at[r]) = at_pack(lo * by, hi * by);
+          else *reinterpret_cast<float2*>(partial + r * D) = make_float2(lo, hi);
         }
       }
-      p8_meet(bar);  // everyone is through with the segment's factors, mask and outputs
+      p8_meet<kMeet>(bar);  // everyone is through with the segment's factors, mask and outputs
       if (lane == 0) mbar_arrive(&o_free[qb]);
       if (whole) continue;
       // the pair's last segment to finish joins them all, once the CTA is through its share
       const int c0 = pa_owner(sg.pair0, W, ctas), c1 = pa_owner(sg.pair0 + sg.nb - 1, W, ctas);
-      bool met = pa_sync(&s_meet, meet, lane);  // the ticket's release covers what the other warps wrote before it
-      ok = !p8_any(bar, !met);
+      const bool met = pa_sync(&s_meet, meet, lane);  // the ticket's release covers what the other warps wrote before it
+      ok = !p8_any<kMeet>(bar, !met);
       if (!ok) break;
       if (t == 32 * C::kSoftmax) {
         // a pair's ticket is a byte: it counts to the grid at most, and goes back to zero before it is used again
@@ -842,15 +969,16 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
   if (!ok && t == 0) {
     record_error(hdr, DT_ERR_TIMEOUT);
     // copies issued must land before the CTA leaves: wait for the last of each entry too (bounded)
-    const unsigned from = s_kv_issued > stages ? s_kv_issued - stages : 0u;
-    for (unsigned e = from; e < s_kv_issued; ++e) mbar_wait(&kv_full[e % stages], (e / stages) & 1u, kAtBudgetNs);
+    for (unsigned kv = 0; kv < 2; ++kv)
+      for (unsigned i = s_issued[kv] > stages / 2 ? s_issued[kv] - stages / 2 : 0u; i < s_issued[kv]; ++i)
+        mbar_wait(&kv_full[(2 * i + kv) % stages], ((2 * i + kv) / stages) & 1u, kAtBudgetNs);
   }
   if (ok) {
     // the ticket's thread acquired the others' partials; the barrier above passed them on
     for (int i = 0; i < s_joins; ++i) {
       PaSum* red = reinterpret_cast<PaSum*>(skv);  // the ring is empty by now
       if (p.R * (D / 4) <= kThreads) pa_join<D, 1, kThreads>(p, s_join[i], red);
-      else pa_join<D, 4, kThreads>(p, s_join[i], red);
+      else pa_join<D, kThreads <= 640 ? 4 : 2, kThreads>(p, s_join[i], red);
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -858,24 +986,40 @@ __global__ void __launch_bounds__(P8<D, N>::kThreads, 1) paged_attn8_kernel(Pa8P
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
-template <int D, int N>
+template <int D, int N, int M, int kPar_, int kSets_, int kStep_>
 dt_status pa8_launch(Pa8Params& p, const Pa8Maps& maps, WsHeader* hdr, cudaStream_t stream) {
-  using C = P8<D, N>;
+  using C = P8<D, N, M, kPar_, kSets_, kStep_>;
   const size_t fixed = C::kFixed + align_up(sizeof(int) * (2 * p.B + 1), 16);
   const int fit = static_cast<int>((kPa8SmemCap - fixed) / C::kEntry);
   // a multiple of four: a slot then always holds keys or always values, and always the same set's
   p.stages = (fit > kP8MaxStages ? kP8MaxStages : fit) & ~3;
   const size_t smem = fixed + static_cast<size_t>(p.stages) * C::kEntry;
-  if (ensure_dynamic_smem(reinterpret_cast<const void*>(paged_attn8_kernel<D, N>), kPa8SmemCap) != cudaSuccess)
+  if (ensure_dynamic_smem(reinterpret_cast<const void*>(paged_attn8_kernel<D, N, M, kPar_, kSets_, kStep_>), kPa8SmemCap) != cudaSuccess)
     return DT_ERR_CUDA;
-  return at_launch(paged_attn8_kernel<D, N>, p.grid, C::kThreads, smem, stream, p, maps, hdr);
+  return at_launch(paged_attn8_kernel<D, N, M, kPar_, kSets_, kStep_>, p.grid, C::kThreads, smem, stream, p, maps, hdr);
 }
 template <int D>
 dt_status pa8_pick(Pa8Params& p, const Pa8Maps& maps, WsHeader* hdr, cudaStream_t stream) {
-  if (p.R <= 16) return pa8_launch<D, 16>(p, maps, hdr, stream);
-  if (p.R <= 32) return pa8_launch<D, 32>(p, maps, hdr, stream);
-  if (p.R <= 64) return pa8_launch<D, 64>(p, maps, hdr, stream);
-  return pa8_launch<D, 128>(p, maps, hdr, stream);
+#ifndef V8
+#define V8 8, 2, 1, 8
+#endif
+#ifndef V16
+#define V16 16, 2, 1, 16
+#endif
+#ifndef V32
+#define V32 32, 2, 1, 32
+#endif
+#ifndef V64
+#define V64 32, 1, 1, 32
+#endif
+#ifndef V128
+#define V128 64, 1, 1, 32
+#endif
+  if (p.R <= 8) return pa8_launch<D, 16, V8>(p, maps, hdr, stream);
+  if (p.R <= 16) return pa8_launch<D, 16, V16>(p, maps, hdr, stream);
+  if (p.R <= 32) return pa8_launch<D, 32, V32>(p, maps, hdr, stream);
+  if (p.R <= 64) return pa8_launch<D, 64, V64>(p, maps, hdr, stream);
+  return pa8_launch<D, 128, V128>(p, maps, hdr, stream);
 }
 
 }  // namespace
