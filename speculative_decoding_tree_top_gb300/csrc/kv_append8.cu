@@ -6,9 +6,10 @@
 // change of exponents, exactly but for codes that leave e4m3's normal range.
 //
 // The tokens of one block have to be seen together. A block is worked on where its lowest written row's token is (its
-// leader): `who` holds the token of each of its rows, found by a look at all slots of the call when those are few, and
-// otherwise through an index from slots to tokens that a launch before fills. An entry of the index counts if the token
-// that it names has that slot, so the index needs no clearing, and what an earlier call left there does no harm.
+// leader), by a warp a head and side; `who` holds the token of each of its rows. It is found by a look at all slots of the
+// call when those are few. Otherwise a launch before fills an index from slots to tokens, and a row's token is looked for
+// first where it is when tokens are in order, then in the index. An entry of the index counts if the token that it names
+// has that slot, so the index needs no clearing, and what an earlier call left there does no harm.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -22,13 +23,16 @@ namespace {
 
 constexpr int kA8Threads = 256;
 constexpr int kA8Warps = kA8Threads / 32;
+constexpr int kA8PerSm = 5;      // CTAs: 48 registers a thread
 constexpr int kA8Scan = 2048;    // up to so many tokens every CTA looks at all slots
-constexpr int kA8Chunk = 16;     // tokens of a CTA that uses the index
-constexpr int kE4m3Most = 448;
+constexpr int kA8Chunk = 16;     // tokens that a CTA looks after, at most
+constexpr int kA8Tile = 16;      // rows that a warp holds
+constexpr size_t kA8Smem = kA8Warps * kA8Tile * 128 * 2 + kA8Chunk * DT_MAX_PAGE * sizeof(int2);  // at most
 constexpr int kScaleLow = DT_SCALE_LOW, kScaleHigh = DT_SCALE_HIGH;
 
 struct Append8Params {
-  int N, Hq, Hkv, max_pos, half, interleaved, page_size, block;  // half = rot / 2
+  int N, Hq, Hkv, max_pos, half, interleaved;                    // half = rot / 2
+  int page_shift, block_shift;                                   // log2 of a page's rows, of a block's
   int chunk, chunks;                                             // tokens a key/value CTA looks after; such CTAs
   long long slots_end;                                           // num_pages * page_size
   const unsigned short *q, *k, *v;
@@ -61,47 +65,58 @@ __global__ void __launch_bounds__(kA8Threads) append8_index_kernel(Append8Params
   if (slot >= 0) p.index[slot] = t;
 }
 
-// An item of 16 columns of one row in fp32, rotated. (No contraction: the largest element decides a scale, and should
-// not depend on how a compiler pairs products and sums.)
-struct Item {
-  Eight a, b;
+// Eight columns of one row in fp32, rotated: two groups of four, a half-split head's the two halves of four pairs. (No
+// contraction: the largest element decides a scale, and should not depend on how a compiler pairs products and sums.)
+struct Cols {
+  int a, b;     // the groups' first columns
+  int pair;     // the first of their pairs, -1: not rotated
 };
+__device__ __forceinline__ Cols a8_cols(int item, int half, int interleaved) {
+  if (interleaved || 4 * item >= half) {  // eight columns in a row; half is a multiple of 8, so they turn together
+    const int at = interleaved ? 8 * item : 2 * half + 8 * (item - half / 4);
+    return Cols{at, at + 4, interleaved && at < 2 * half ? 4 * item : -1};
+  }
+  return Cols{4 * item, 4 * item + half, 4 * item};
+}
 __device__ __forceinline__ void a8_turn(float& a, float& b, float c, float s) {
   const float u = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s)), w = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
   a = u;
   b = w;
 }
-__device__ __forceinline__ Item a8_item(const Append8Params& p, const unsigned short* src, const TurnCols& cols,
-                                        int item, int pos, bool turned) {
-  Item x;
-  x.a = unpack8(*reinterpret_cast<const uint4*>(src + cols.ca));
-  x.b = unpack8(*reinterpret_cast<const uint4*>(src + cols.cb));
-  if (turned) {
-    Turn tu;
-    load_turn(p.rope + static_cast<size_t>(pos) * (2 * p.half), item, p.half, p.interleaved, cols.halves, tu);
-    if (cols.halves) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) a8_turn(x.a.x[i], x.b.x[i], tu.c[i], tu.s[i]);
-    } else if (p.interleaved) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (cols.ca < 2 * p.half) a8_turn(x.a.x[2 * i], x.a.x[2 * i + 1], tu.c[i], tu.s[i]);
-        if (cols.cb < 2 * p.half) a8_turn(x.b.x[2 * i], x.b.x[2 * i + 1], tu.c[4 + i], tu.s[4 + i]);
-      }
+__device__ __forceinline__ Eight a8_item(const Append8Params& p, uint2 a, uint2 b, const Cols& cols, int pos) {
+  Eight x = unpack8(make_uint4(a.x, a.y, b.x, b.y));
+  if (cols.pair >= 0) {
+    const float* row = p.rope + static_cast<size_t>(pos) * (2 * p.half) + cols.pair;
+    const float4 c = *reinterpret_cast<const float4*>(row), s = *reinterpret_cast<const float4*>(row + p.half);
+    if (p.interleaved) {
+      a8_turn(x.x[0], x.x[1], c.x, s.x);
+      a8_turn(x.x[2], x.x[3], c.y, s.y);
+      a8_turn(x.x[4], x.x[5], c.z, s.z);
+      a8_turn(x.x[6], x.x[7], c.w, s.w);
+    } else {
+      a8_turn(x.x[0], x.x[4], c.x, s.x);
+      a8_turn(x.x[1], x.x[5], c.y, s.y);
+      a8_turn(x.x[2], x.x[6], c.z, s.z);
+      a8_turn(x.x[3], x.x[7], c.w, s.w);
     }
   }
   return x;
 }
 
-// The bits of the largest |x| that a scale serves: they order as the values do. What is larger, infinite or no number is
-// stored as NaN and leaves the block's scale alone.
-constexpr unsigned kMostBits = (static_cast<unsigned>(kScaleHigh + 8 + 127) << 23) | 0x600000u;  // 448 2^kScaleHigh
-__device__ __forceinline__ unsigned a8_most(const Eight& e, unsigned most) {
+// The largest size that a scale serves, 448 2^kScaleHigh. What is larger, infinite or no number is stored as NaN and leaves
+// the block's scale alone.
+constexpr unsigned kMostBits = (static_cast<unsigned>(kScaleHigh + 8 + 127) << 23) | 0x600000u;
+// The largest |x|, infinite ones among them.
+__device__ __forceinline__ float a8_most(const Eight& e, float most) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const unsigned u = __float_as_uint(e.x[i]) & 0x7FFFFFFFu;
-    if (u <= kMostBits && u > most) most = u;
-  }
+  for (int i = 0; i < 8; i += 2) most = at_max3(most, fabsf(e.x[i]), fabsf(e.x[i + 1]));
+  return most;
+}
+// The largest that a scale serves.
+__device__ __forceinline__ float a8_most_served(const Eight& e, float most) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (fabsf(e.x[i]) <= __uint_as_float(kMostBits)) most = fmaxf(most, fabsf(e.x[i]));
   return most;
 }
 // The least e within the limits with most <= 448 2^e.
@@ -118,20 +133,19 @@ __device__ __forceinline__ int a8_exponent_of(float scale) {
   return (u & 0x7FFFFFu) == 0u && e >= kScaleLow && e <= kScaleHigh ? e : kScaleLow - 1;
 }
 __device__ __forceinline__ uint32_t a8_code2(float lo, float hi) {
-  // what is not finite, or too large for the largest scale, is stored as NaN
-  if (!(fabsf(lo) <= static_cast<float>(kE4m3Most))) lo = NAN;
-  if (!(fabsf(hi) <= static_cast<float>(kE4m3Most))) hi = NAN;
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ uint2 a8_code8(const Eight& e, float inv) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = a8_code2(e.x[2 * i] * inv, e.x[2 * i + 1] * inv);
-  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+__device__ __forceinline__ uint32_t a8_code4(const float* x, float inv) {
+  return a8_code2(x[0] * inv, x[1] * inv) | a8_code2(x[2] * inv, x[3] * inv) << 16;
 }
-// Four codes under a scale 2^up times as large.
+__device__ __forceinline__ void a8_drop(Eight& e) {  // what no scale serves
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (!(fabsf(e.x[i]) <= __uint_as_float(kMostBits))) e.x[i] = NAN;
+}
+// Four codes under a scale 1 / down times as large.
 __device__ __forceinline__ uint32_t a8_again(uint32_t codes, float down) {
   uint32_t out = 0u;
 #pragma unroll
@@ -144,106 +158,183 @@ __device__ __forceinline__ uint32_t a8_again(uint32_t codes, float down) {
   return out;
 }
 
-// One head's keys or values of a block, by a warp: D / 16 lanes a row.
+// One head's keys or values of a block, by a warp: D / 8 lanes a row. kA8Tile rows at a time come to shared memory as they
+// are and are read from there twice, for the scale and for the codes (kept in registers, they were either few loads in
+// flight or spilled); a block of more rows is gone through twice.
 template <int D>
-__device__ __forceinline__ void a8_block(const Append8Params& p, const int* who, int low, int first_slot, int head,
-                                         bool is_k) {
-  constexpr int kItems = D / 16, kRows = 32 / kItems;
+__device__ __forceinline__ void a8_block(const Append8Params& p, const int2* who, int low, int first_slot, int head,
+                                         bool is_k, unsigned char* tile) {
+  constexpr int kItems = D / 8, kRows = 32 / kItems;
   const int lane = threadIdx.x & 31, item = lane % kItems, row0 = lane / kItems;
-  const bool turned = is_k && p.half > 0;
-  const TurnCols cols = turned ? turn_cols(item, p.half, p.interleaved) : TurnCols{16 * item, 16 * item + 8, false};
+  const Cols cols = is_k && p.half > 0 ? a8_cols(item, p.half, p.interleaved) : Cols{8 * item, 8 * item + 4, -1};
   const unsigned short* src = (is_k ? p.k : p.v) + head * D;
   const long long stride = is_k ? p.k_stride : p.v_stride;
-  unsigned short* dense = is_k ? p.out_k : nullptr;
-  const int page = first_slot / p.page_size, row_at = first_slot % p.page_size;
+  const int page = first_slot >> p.page_shift, row_at = first_slot & ((1 << p.page_shift) - 1);
   const size_t plane = static_cast<size_t>(page) * p.Hkv + head;
-  unsigned char* cache = (is_k ? p.k_cache : p.v_cache) + (plane * p.page_size + row_at) * D;
-  float* scale = (is_k ? p.k_scale : p.v_scale) + plane * (p.page_size / p.block) + row_at / p.block;
-  const int from = low / kRows * kRows;
-  unsigned most = 0u;
-  for (int r = from + row0; r < p.block; r += kRows) {
-    const int t = who[r];
-    if (t == INT_MAX) continue;
-    const Item x = a8_item(p, src + t * stride, cols, item, turned ? p.positions[t] : 0, turned);
-    most = a8_most(x.b, a8_most(x.a, most));
+  unsigned char* cache = (is_k ? p.k_cache : p.v_cache) + ((plane << p.page_shift) + row_at) * D;
+  float* scale = (is_k ? p.k_scale : p.v_scale) + (plane << (p.page_shift - p.block_shift)) + (row_at >> p.block_shift);
+  const int block = 1 << p.block_shift, from = low & ~(kA8Tile - 1);
+  auto load = [&](int r0) {
+    const uint32_t to = smem_u32(tile) + (row0 * D + 8 * item) * 2;
+#pragma unroll
+    for (int u = 0; u < kA8Tile; u += kRows) {
+      const int r = r0 + u + row0, t = r < block ? who[r].x : INT_MAX;
+      if (t != INT_MAX)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + u * D * 2),
+                     "l"(src + t * stride + 8 * item)
+                     : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+  };
+  auto item_of = [&](int u, int pos) {  // of the tile's row u + row0
+    const unsigned short* at = reinterpret_cast<const unsigned short*>(tile) + (u + row0) * D;
+    return a8_item(p, *reinterpret_cast<const uint2*>(at + cols.a), *reinterpret_cast<const uint2*>(at + cols.b), cols, pos);
+  };
+  const float was_scale = low > 0 ? *scale : 0.f;
+  float most = 0.f;
+  bool odd = false;  // something that no scale serves
+  unsigned bits;
+#pragma unroll 1
+  while (true) {
+#pragma unroll 1
+    for (int r0 = from; r0 < block; r0 += kA8Tile) {
+      if (!odd || block > kA8Tile) load(r0);
+#pragma unroll 2
+      for (int u = 0; u < kA8Tile; u += kRows) {
+        const int r = r0 + u + row0;
+        const int2 w = r < block ? who[r] : make_int2(INT_MAX, 0);
+        if (w.x == INT_MAX) continue;
+        const Eight x = item_of(u, w.y);
+        most = odd ? a8_most_served(x, most) : a8_most(x, most);
+      }
+      if (block > kA8Tile) __syncwarp();  // the tile is read before the next one comes
+    }
+    bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
+    if (odd || bits <= kMostBits) break;
+    odd = true;  // rare: once more, without what is not served
+    most = 0.f;
   }
-  most = __reduce_max_sync(0xFFFFFFFFu, most);
-  int e = a8_exponent(most);
-  const int was = low > 0 ? a8_exponent_of(*scale) : kScaleLow - 1;
+  int e = a8_exponent(bits);
+  const int was = low > 0 ? a8_exponent_of(was_scale) : kScaleLow - 1;
   if (was > e) e = was;
   __syncwarp();  // every lane has read the scale
   if (lane == 0) *scale = a8_pow2(e);
   if (was >= kScaleLow && e > was) {  // the rows that are there already
     const float down = a8_pow2(was - e);
     for (int r = row0; r < low; r += kRows) {
-      uint4* at = reinterpret_cast<uint4*>(cache + r * D + 16 * item);
-      const uint4 c = *at;
-      *at = make_uint4(a8_again(c.x, down), a8_again(c.y, down), a8_again(c.z, down), a8_again(c.w, down));
+      uint2* at = reinterpret_cast<uint2*>(cache + r * D + 8 * item);
+      const uint2 c = *at;
+      *at = make_uint2(a8_again(c.x, down), a8_again(c.y, down));
     }
   }
   const float inv = a8_pow2(-e);
-  for (int r = from + row0; r < p.block; r += kRows) {
-    const int t = who[r];
-    if (t == INT_MAX) continue;
-    const Item x = a8_item(p, src + t * stride, cols, item, turned ? p.positions[t] : 0, turned);
-    *reinterpret_cast<uint2*>(cache + r * D + cols.ca) = a8_code8(x.a, inv);
-    *reinterpret_cast<uint2*>(cache + r * D + cols.cb) = a8_code8(x.b, inv);
-    if (dense) {
-      unsigned short* o = dense + (static_cast<size_t>(t) * p.Hkv + head) * D;
-      *reinterpret_cast<uint4*>(o + cols.ca) = pack8(x.a);
-      *reinterpret_cast<uint4*>(o + cols.cb) = pack8(x.b);
+  unsigned short* dense = is_k && p.out_k ? p.out_k + head * D : nullptr;
+#pragma unroll 1
+  for (int r0 = from; r0 < block; r0 += kA8Tile) {
+    if (block > kA8Tile) load(r0);
+#pragma unroll 2
+    for (int u = 0; u < kA8Tile; u += kRows) {
+      const int r = r0 + u + row0;
+      const int2 w = r < block ? who[r] : make_int2(INT_MAX, 0);
+      if (w.x == INT_MAX) continue;
+      Eight x = item_of(u, w.y);
+      if (dense) {
+        unsigned short* o = dense + static_cast<size_t>(w.x) * p.Hkv * D;
+        const uint4 y = pack8(x);
+        *reinterpret_cast<uint2*>(o + cols.a) = make_uint2(y.x, y.y);
+        *reinterpret_cast<uint2*>(o + cols.b) = make_uint2(y.z, y.w);
+      }
+      if (odd) a8_drop(x);
+      *reinterpret_cast<uint32_t*>(cache + r * D + cols.a) = a8_code4(x.x, inv);
+      *reinterpret_cast<uint32_t*>(cache + r * D + cols.b) = a8_code4(x.x + 4, inv);
     }
+    __syncwarp();  // the tile is read before the next one comes
   }
 }
 
-// CTAs 0 .. chunks - 1: the keys and values of the blocks whose leaders are among the CTA's tokens. The others: queries.
+// CTAs 0 .. chunks - 1: the keys and values of the blocks whose leaders are among the CTA's tokens. The others: queries, a
+// token at a time, each thread in the same columns of its heads (as dt_kv_append).
 template <int D>
-__global__ void __launch_bounds__(kA8Threads) kv_append8_kernel(Append8Params p, WsHeader* hdr) {
-  extern __shared__ int s_who[];  // [chunk][block]: the token of each row, INT_MAX for none
-  __shared__ int s_low[kA8Chunk], s_first[kA8Chunk];
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+__global__ void __launch_bounds__(kA8Threads, kA8PerSm) kv_append8_kernel(Append8Params p, WsHeader* hdr) {
+  extern __shared__ __align__(16) unsigned char s_tiles[];  // a tile a warp
+  // [chunk][block]: the token of each row, INT_MAX for none, and its position
+  int2* s_who = reinterpret_cast<int2*>(s_tiles + kA8Warps * kA8Tile * D * 2);
+  __shared__ int s_low[kA8Chunk], s_first[kA8Chunk], s_lead[kA8Chunk];
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, block = 1 << p.block_shift;
   at_launch_order();
   if (static_cast<int>(blockIdx.x) >= p.chunks) {
     constexpr int kItems = D / 16;
     const int item = t % kItems, head0 = t / kItems, step = kA8Threads / kItems;
     const TurnCols cols = p.half ? turn_cols(item, p.half, p.interleaved) : TurnCols{16 * item, 16 * item + 8, false};
-    for (long long token = blockIdx.x - p.chunks; token < p.N; token += gridDim.x - p.chunks) {
-      bool bad = false;
-      if (a8_slot(p, static_cast<int>(token), &bad) < 0) continue;
+    const int stride = gridDim.x - p.chunks;
+    int token = blockIdx.x - p.chunks;
+    int slot_next = token < p.N ? p.slots[token] : -1, pos_next = p.half && token < p.N ? p.positions[token] : 0;
+    for (; token < p.N; token += stride) {
+      const int slot = slot_next, pos = pos_next;
+      const long long after = static_cast<long long>(token) + stride;
+      if (after < p.N) {
+        slot_next = p.slots[after];
+        if (p.half) pos_next = p.positions[after];
+      }
+      if (slot < 0 || slot >= p.slots_end || (p.half && (pos < 0 || pos >= p.max_pos))) continue;
+      Turn tu;
+      if (p.half)
+        load_turn(p.rope + static_cast<size_t>(pos) * (2 * p.half), item, p.half, p.interleaved, cols.halves, tu);
       for (int h = head0; h < p.Hq; h += step) {
-        const Item x = a8_item(p, p.q + token * p.q_stride + h * D, cols, item, p.half ? p.positions[token] : 0,
-                               p.half > 0);
-        unsigned short* o = p.out_q + (token * p.Hq + h) * D;
-        *reinterpret_cast<uint4*>(o + cols.ca) = pack8(x.a);
-        *reinterpret_cast<uint4*>(o + cols.cb) = pack8(x.b);
+        const unsigned short* src = p.q + token * p.q_stride + h * D;
+        uint4 a = *reinterpret_cast<const uint4*>(src + cols.ca), b = *reinterpret_cast<const uint4*>(src + cols.cb);
+        if (cols.halves) {
+          turn_halves(a, b, tu);
+        } else if (p.half && p.interleaved) {  // a group past rot is copied: its bits stay as they are
+          if (cols.ca < 2 * p.half) turn_pairs(a, tu.c, tu.s);
+          if (cols.cb < 2 * p.half) turn_pairs(b, tu.c + 4, tu.s + 4);
+        }
+        unsigned short* o = p.out_q + (static_cast<size_t>(token) * p.Hq + h) * D;
+        *reinterpret_cast<uint4*>(o + cols.ca) = a;
+        *reinterpret_cast<uint4*>(o + cols.cb) = b;
       }
     }
     return;
   }
-  for (int i = t; i < p.chunk * p.block; i += kA8Threads) s_who[i] = INT_MAX;
-  __syncthreads();
+  for (int i = t; i < p.chunk << p.block_shift; i += kA8Threads) s_who[i] = make_int2(INT_MAX, 0);
   const int token0 = blockIdx.x * p.chunk;
-  for (int c = warp; c < p.chunk; c += kA8Warps) {  // a warp a token
+  if (t < p.chunk) {
     bool bad = false;
-    const int token = token0 + c, slot = token < p.N ? a8_slot(p, token, &bad) : -1;
-    if (bad && lane == 0) record_error(hdr, DT_ERR_INVALID_ARG);
-    if (lane == 0) {
-      s_low[c] = p.block;
-      s_first[c] = slot < 0 ? -1 : slot / p.block * p.block;
-    }
+    const int token = token0 + t, slot = token < p.N ? a8_slot(p, token, &bad) : -1;
+    if (bad) record_error(hdr, DT_ERR_INVALID_ARG);
+    s_low[t] = block;
+    s_lead[t] = -1;
+    s_first[t] = slot < 0 ? -1 : slot;
   }
   __syncthreads();
   if (p.index) {
     for (int c = warp; c < p.chunk; c += kA8Warps) {
-      const int first = s_first[c];
-      if (first < 0) continue;
-      for (int r = lane; r < p.block; r += 32) {
-        const int u = p.index[first + r];
-        bool bad = false;
-        if (u >= 0 && u < p.N && a8_slot(p, u, &bad) == first + r) {
-          s_who[c * p.block + r] = u;
-          atomicMin(&s_low[c], r);
+      const int slot = s_first[c];
+      if (slot < 0) continue;
+      const int first = slot & ~(block - 1), token = token0 + c;
+      int low = block, lead = -1;
+      for (int r = lane; r < block; r += 32) {
+        // the row's token where tokens are in order, else by the index
+        const int named = p.index[first + r], near = token + first + r - slot;
+        int u = near;
+        bool bad = false, there = near >= 0 && near < p.N && a8_slot(p, near, &bad) == first + r;
+        if (!there) {
+          u = named;
+          there = u >= 0 && u < p.N && a8_slot(p, u, &bad) == first + r;
         }
+        if (there) {
+          s_who[(c << p.block_shift) + r] = make_int2(u, p.half ? p.positions[u] : 0);
+          if (r < low) {
+            low = r;
+            lead = named;  // of two tokens with one slot the index names one
+          }
+        }
+      }
+      const int lowest = __reduce_min_sync(0xFFFFFFFFu, low);
+      if (low == lowest && low < block) {
+        s_low[c] = low;
+        s_lead[c] = lead;
       }
     }
   } else {
@@ -251,19 +342,25 @@ __global__ void __launch_bounds__(kA8Threads) kv_append8_kernel(Append8Params p,
       bool bad = false;
       const int slot = a8_slot(p, u, &bad);
       if (slot < 0) continue;
+#pragma unroll 1
       for (int c = 0; c < p.chunk; ++c)
-        if (s_first[c] >= 0 && slot / p.block * p.block == s_first[c]) {
-          atomicMin(&s_who[c * p.block + slot % p.block], u);
-          atomicMin(&s_low[c], slot % p.block);
+        if (s_first[c] >= 0 && (slot ^ s_first[c]) >> p.block_shift == 0) {
+          const int r = slot & (block - 1);
+          atomicMin(&s_who[(c << p.block_shift) + r].x, u);
+          atomicMin(&s_low[c], r);
         }
     }
+    __syncthreads();
+    for (int i = t; i < p.chunk << p.block_shift; i += kA8Threads)
+      if (p.half && s_who[i].x != INT_MAX) s_who[i].y = p.positions[s_who[i].x];
+    if (t < p.chunk && s_low[t] < block) s_lead[t] = s_who[(t << p.block_shift) + s_low[t]].x;
   }
   __syncthreads();
-  for (int i = warp; i < p.chunk * 2 * p.Hkv; i += kA8Warps) {
-    const int c = i / (2 * p.Hkv), part = i % (2 * p.Hkv);
-    if (s_first[c] < 0 || s_low[c] >= p.block) continue;
-    if (s_who[c * p.block + s_low[c]] != token0 + c) continue;  // another token leads
-    a8_block<D>(p, s_who + c * p.block, s_low[c], s_first[c], part >> 1, (part & 1) == 0);
+  for (int c = 0; c < p.chunk; ++c) {
+    if (s_lead[c] != token0 + c) continue;  // another token leads
+    for (int part = warp; part < 2 * p.Hkv; part += kA8Warps)
+      a8_block<D>(p, s_who + (c << p.block_shift), s_low[c], s_first[c] & ~(block - 1), part >> 1, (part & 1) == 0,
+                  s_tiles + warp * kA8Tile * D * 2);
   }
 }
 
@@ -323,7 +420,8 @@ extern "C" dt_status dt_kv_append8(int N, int Hq, int Hkv, int d, const void* q,
   if (current_device_info(&di) != cudaSuccess) return DT_ERR_CUDA;
   Append8Params p{};
   p.N = N; p.Hq = Hq; p.Hkv = Hkv; p.max_pos = max_pos; p.half = rot / 2; p.interleaved = interleaved;
-  p.page_size = page_size; p.block = scale_block;
+  while ((1 << p.page_shift) < page_size) ++p.page_shift;
+  while ((1 << p.block_shift) < scale_block) ++p.block_shift;
   p.slots_end = static_cast<long long>(num_pages) * page_size;
   p.q = static_cast<const unsigned short*>(q);
   p.k = static_cast<const unsigned short*>(k);
@@ -337,15 +435,20 @@ extern "C" dt_status dt_kv_append8(int N, int Hq, int Hkv, int d, const void* q,
   p.k_scale = k_scale; p.v_scale = v_scale;
   const bool indexed = N > kA8Scan;
   p.index = indexed ? reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + align_up(sizeof(WsHeader))) : nullptr;
-  p.chunk = indexed ? kA8Chunk : 1;
+  // as many CTAs as there is room for, but no more tokens than a CTA looks after
+  const int each = N / (kA8PerSm * di.sms) + 1;
+  p.chunk = each < kA8Chunk ? each : kA8Chunk;
   p.chunks = (N + p.chunk - 1) / p.chunk;
   WsHeader* hdr = static_cast<WsHeader*>(workspace);
   if (indexed) {
     const dt_status s = at_launch(append8_index_kernel, (N + kA8Threads - 1) / kA8Threads, kA8Threads, 0, stream, p);
     if (s != DT_OK) return s;
   }
-  const int cap = 16 * di.sms, grid = p.chunks + (Hq > 0 ? (N < cap ? N : cap) : 0);
-  const size_t smem = sizeof(int) * static_cast<size_t>(p.chunk) * scale_block;
+  const int cap = 8 * di.sms, grid = p.chunks + (Hq > 0 ? (N < cap ? N : cap) : 0);
+  const size_t smem = sizeof(int2) * static_cast<size_t>(p.chunk) * scale_block + kA8Warps * kA8Tile * static_cast<size_t>(d) * 2;
+  const void* fn = d == 64 ? reinterpret_cast<const void*>(kv_append8_kernel<64>)
+                           : reinterpret_cast<const void*>(kv_append8_kernel<128>);
+  if (ensure_dynamic_smem(fn, kA8Smem) != cudaSuccess) return DT_ERR_CUDA;
   return d == 64 ? at_launch(kv_append8_kernel<64>, grid, kA8Threads, smem, stream, p, hdr)
                  : at_launch(kv_append8_kernel<128>, grid, kA8Threads, smem, stream, p, hdr);
 }
