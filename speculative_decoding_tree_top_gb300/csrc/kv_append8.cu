@@ -26,8 +26,8 @@ constexpr int kA8Warps = kA8Threads / 32;
 constexpr int kA8PerSm = 5;      // CTAs: 48 registers a thread
 constexpr int kA8Scan = 2048;    // up to so many tokens every CTA looks at all slots
 constexpr int kA8Chunk = 16;     // tokens that a CTA looks after, at most
-constexpr int kA8Tile = 16;      // rows that a warp holds
-constexpr size_t kA8Smem = kA8Warps * kA8Tile * 128 * 2 + kA8Chunk * DT_MAX_PAGE * sizeof(int2);  // at most
+constexpr int kA8TileBytes = 4096;  // of rows as they come, for each warp
+constexpr size_t kA8Smem = kA8Warps * kA8TileBytes + kA8Chunk * DT_MAX_PAGE * sizeof(int2);  // at most
 constexpr int kScaleLow = DT_SCALE_LOW, kScaleHigh = DT_SCALE_HIGH;
 
 struct Append8Params {
@@ -158,13 +158,13 @@ __device__ __forceinline__ uint32_t a8_again(uint32_t codes, float down) {
   return out;
 }
 
-// One head's keys or values of a block, by a warp: D / 8 lanes a row. kA8Tile rows at a time come to shared memory as they
-// are and are read from there twice, for the scale and for the codes (kept in registers, they were either few loads in
+// One head's keys or values of a block, by a warp: D / 8 lanes a row. A tile of rows at a time comes to shared memory as they
+// are and is read from there twice, for the scale and for the codes (kept in registers, they were either few loads in
 // flight or spilled); a block of more rows is gone through twice.
 template <int D>
 __device__ __forceinline__ void a8_block(const Append8Params& p, const int2* who, int low, int first_slot, int head,
                                          bool is_k, unsigned char* tile) {
-  constexpr int kItems = D / 8, kRows = 32 / kItems;
+  constexpr int kItems = D / 8, kRows = 32 / kItems, kTile = kA8TileBytes / (2 * D);
   const int lane = threadIdx.x & 31, item = lane % kItems, row0 = lane / kItems;
   const Cols cols = is_k && p.half > 0 ? a8_cols(item, p.half, p.interleaved) : Cols{8 * item, 8 * item + 4, -1};
   const unsigned short* src = (is_k ? p.k : p.v) + head * D;
@@ -173,11 +173,11 @@ __device__ __forceinline__ void a8_block(const Append8Params& p, const int2* who
   const size_t plane = static_cast<size_t>(page) * p.Hkv + head;
   unsigned char* cache = (is_k ? p.k_cache : p.v_cache) + ((plane << p.page_shift) + row_at) * D;
   float* scale = (is_k ? p.k_scale : p.v_scale) + (plane << (p.page_shift - p.block_shift)) + (row_at >> p.block_shift);
-  const int block = 1 << p.block_shift, from = low & ~(kA8Tile - 1);
+  const int block = 1 << p.block_shift, from = low & ~(kTile - 1);
   auto load = [&](int r0) {
     const uint32_t to = smem_u32(tile) + (row0 * D + 8 * item) * 2;
 #pragma unroll
-    for (int u = 0; u < kA8Tile; u += kRows) {
+    for (int u = 0; u < kTile; u += kRows) {
       const int r = r0 + u + row0, t = r < block ? who[r].x : INT_MAX;
       if (t != INT_MAX)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + u * D * 2),
@@ -198,17 +198,17 @@ __device__ __forceinline__ void a8_block(const Append8Params& p, const int2* who
 #pragma unroll 1
   while (true) {
 #pragma unroll 1
-    for (int r0 = from; r0 < block; r0 += kA8Tile) {
-      if (!odd || block > kA8Tile) load(r0);
+    for (int r0 = from; r0 < block; r0 += kTile) {
+      if (!odd || block > kTile) load(r0);
 #pragma unroll 2
-      for (int u = 0; u < kA8Tile; u += kRows) {
+      for (int u = 0; u < kTile; u += kRows) {
         const int r = r0 + u + row0;
         const int2 w = r < block ? who[r] : make_int2(INT_MAX, 0);
         if (w.x == INT_MAX) continue;
         const Eight x = item_of(u, w.y);
         most = odd ? a8_most_served(x, most) : a8_most(x, most);
       }
-      if (block > kA8Tile) __syncwarp();  // the tile is read before the next one comes
+      if (block > kTile) __syncwarp();  // the tile is read before the next one comes
     }
     bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
     if (odd || bits <= kMostBits) break;
@@ -231,10 +231,10 @@ __device__ __forceinline__ void a8_block(const Append8Params& p, const int2* who
   const float inv = a8_pow2(-e);
   unsigned short* dense = is_k && p.out_k ? p.out_k + head * D : nullptr;
 #pragma unroll 1
-  for (int r0 = from; r0 < block; r0 += kA8Tile) {
-    if (block > kA8Tile) load(r0);
+  for (int r0 = from; r0 < block; r0 += kTile) {
+    if (block > kTile) load(r0);
 #pragma unroll 2
-    for (int u = 0; u < kA8Tile; u += kRows) {
+    for (int u = 0; u < kTile; u += kRows) {
       const int r = r0 + u + row0;
       const int2 w = r < block ? who[r] : make_int2(INT_MAX, 0);
       if (w.x == INT_MAX) continue;
@@ -253,26 +253,29 @@ __device__ __forceinline__ void a8_block(const Append8Params& p, const int2* who
   }
 }
 
-// CTAs 0 .. chunks - 1: the keys and values of the blocks whose leaders are among the CTA's tokens. The others: queries, a
-// token at a time, each thread in the same columns of its heads (as dt_kv_append).
+// CTAs 0 .. 2 chunks - 1: the keys (the even ones) or the values of the blocks whose leaders are among the CTA's tokens.
+// The others: queries, a token or several at a time, each thread in the same columns of its heads (as dt_kv_append).
 template <int D>
 __global__ void __launch_bounds__(kA8Threads, kA8PerSm) kv_append8_kernel(Append8Params p, WsHeader* hdr) {
   extern __shared__ __align__(16) unsigned char s_tiles[];  // a tile a warp
   // [chunk][block]: the token of each row, INT_MAX for none, and its position
-  int2* s_who = reinterpret_cast<int2*>(s_tiles + kA8Warps * kA8Tile * D * 2);
+  int2* s_who = reinterpret_cast<int2*>(s_tiles + kA8Warps * kA8TileBytes);
   __shared__ int s_low[kA8Chunk], s_first[kA8Chunk], s_lead[kA8Chunk];
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, block = 1 << p.block_shift;
   at_launch_order();
-  if (static_cast<int>(blockIdx.x) >= p.chunks) {
-    constexpr int kItems = D / 16;
-    const int item = t % kItems, head0 = t / kItems, step = kA8Threads / kItems;
+  if (static_cast<int>(blockIdx.x) >= 2 * p.chunks) {
+    constexpr int kItems = D / 16, kStep = kA8Threads / kItems;
+    const int item = t % kItems, tokens = p.Hq < kStep ? kStep / p.Hq : 1;
+    const int mine = t / kItems / p.Hq;  // of the tokens of a pass
+    if (mine >= tokens && p.Hq < kStep) return;
+    const int head0 = p.Hq < kStep ? t / kItems % p.Hq : t / kItems;
     const TurnCols cols = p.half ? turn_cols(item, p.half, p.interleaved) : TurnCols{16 * item, 16 * item + 8, false};
-    const int stride = gridDim.x - p.chunks;
-    int token = blockIdx.x - p.chunks;
+    const long long stride = static_cast<long long>(gridDim.x - 2 * p.chunks) * tokens;
+    long long token = static_cast<long long>(blockIdx.x - 2 * p.chunks) * tokens + (p.Hq < kStep ? mine : 0);
     int slot_next = token < p.N ? p.slots[token] : -1, pos_next = p.half && token < p.N ? p.positions[token] : 0;
     for (; token < p.N; token += stride) {
       const int slot = slot_next, pos = pos_next;
-      const long long after = static_cast<long long>(token) + stride;
+      const long long after = token + stride;
       if (after < p.N) {
         slot_next = p.slots[after];
         if (p.half) pos_next = p.positions[after];
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__(kA8Threads, kA8PerSm) kv_append8_kernel(Append
       Turn tu;
       if (p.half)
         load_turn(p.rope + static_cast<size_t>(pos) * (2 * p.half), item, p.half, p.interleaved, cols.halves, tu);
-      for (int h = head0; h < p.Hq; h += step) {
+      for (int h = head0; h < p.Hq; h += kStep) {
         const unsigned short* src = p.q + token * p.q_stride + h * D;
         uint4 a = *reinterpret_cast<const uint4*>(src + cols.ca), b = *reinterpret_cast<const uint4*>(src + cols.cb);
         if (cols.halves) {
@@ -297,8 +300,16 @@ __global__ void __launch_bounds__(kA8Threads, kA8PerSm) kv_append8_kernel(Append
     }
     return;
   }
+  const int token0 = (blockIdx.x >> 1) * p.chunk;
+  const bool is_k = (blockIdx.x & 1) == 0;
+  // a look at all slots: under way before it is known what for
+  constexpr int kLooks = kA8Scan / kA8Threads;
+  int look[kLooks];
+  if (!p.index) {
+#pragma unroll
+    for (int i = 0; i < kLooks; ++i) look[i] = t + i * kA8Threads < p.N ? p.slots[t + i * kA8Threads] : -1;
+  }
   for (int i = t; i < p.chunk << p.block_shift; i += kA8Threads) s_who[i] = make_int2(INT_MAX, 0);
-  const int token0 = blockIdx.x * p.chunk;
   if (t < p.chunk) {
     bool bad = false;
     const int token = token0 + t, slot = token < p.N ? a8_slot(p, token, &bad) : -1;
@@ -338,14 +349,14 @@ __global__ void __launch_bounds__(kA8Threads, kA8PerSm) kv_append8_kernel(Append
       }
     }
   } else {
-    for (int u = t; u < p.N; u += kA8Threads) {
-      bool bad = false;
-      const int slot = a8_slot(p, u, &bad);
-      if (slot < 0) continue;
+#pragma unroll
+    for (int i = 0; i < kLooks; ++i) {
+      const int slot = look[i], u = t + i * kA8Threads;
 #pragma unroll 1
       for (int c = 0; c < p.chunk; ++c)
-        if (s_first[c] >= 0 && (slot ^ s_first[c]) >> p.block_shift == 0) {
-          const int r = slot & (block - 1);
+        if (s_first[c] >= 0 && ((slot ^ s_first[c]) >> p.block_shift) == 0) {  // (a negative slot differs in its sign)
+          const int pos = p.half ? p.positions[u] : 0, r = slot & (block - 1);
+          if (p.half && (pos < 0 || pos >= p.max_pos)) continue;
           atomicMin(&s_who[(c << p.block_shift) + r].x, u);
           atomicMin(&s_low[c], r);
         }
@@ -358,9 +369,9 @@ __global__ void __launch_bounds__(kA8Threads, kA8PerSm) kv_append8_kernel(Append
   __syncthreads();
   for (int c = 0; c < p.chunk; ++c) {
     if (s_lead[c] != token0 + c) continue;  // another token leads
-    for (int part = warp; part < 2 * p.Hkv; part += kA8Warps)
-      a8_block<D>(p, s_who + (c << p.block_shift), s_low[c], s_first[c] & ~(block - 1), part >> 1, (part & 1) == 0,
-                  s_tiles + warp * kA8Tile * D * 2);
+    for (int head = warp; head < p.Hkv; head += kA8Warps)
+      a8_block<D>(p, s_who + (c << p.block_shift), s_low[c], s_first[c] & ~(block - 1), head, is_k,
+                  s_tiles + warp * kA8TileBytes);
   }
 }
 
@@ -436,7 +447,7 @@ extern "C" dt_status dt_kv_append8(int N, int Hq, int Hkv, int d, const void* q,
   const bool indexed = N > kA8Scan;
   p.index = indexed ? reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + align_up(sizeof(WsHeader))) : nullptr;
   // as many CTAs as there is room for, but no more tokens than a CTA looks after
-  const int each = N / (kA8PerSm * di.sms) + 1;
+  const int each = 2 * N / (kA8PerSm * di.sms) + 1;
   p.chunk = each < kA8Chunk ? each : kA8Chunk;
   p.chunks = (N + p.chunk - 1) / p.chunk;
   WsHeader* hdr = static_cast<WsHeader*>(workspace);
@@ -444,8 +455,8 @@ extern "C" dt_status dt_kv_append8(int N, int Hq, int Hkv, int d, const void* q,
     const dt_status s = at_launch(append8_index_kernel, (N + kA8Threads - 1) / kA8Threads, kA8Threads, 0, stream, p);
     if (s != DT_OK) return s;
   }
-  const int cap = 8 * di.sms, grid = p.chunks + (Hq > 0 ? (N < cap ? N : cap) : 0);
-  const size_t smem = sizeof(int2) * static_cast<size_t>(p.chunk) * scale_block + kA8Warps * kA8Tile * static_cast<size_t>(d) * 2;
+  const int cap = 8 * di.sms, grid = 2 * p.chunks + (Hq > 0 ? (N < cap ? N : cap) : 0);
+  const size_t smem = sizeof(int2) * static_cast<size_t>(p.chunk) * scale_block + kA8Warps * kA8TileBytes;
   const void* fn = d == 64 ? reinterpret_cast<const void*>(kv_append8_kernel<64>)
                            : reinterpret_cast<const void*>(kv_append8_kernel<128>);
   if (ensure_dynamic_smem(fn, kA8Smem) != cudaSuccess) return DT_ERR_CUDA;
