@@ -27,13 +27,14 @@ constexpr int kA8PerSm = 5;      // CTAs: 48 registers a thread
 constexpr int kA8Scan = 2048;    // up to so many tokens every CTA looks at all slots
 constexpr int kA8Chunk = 16;     // tokens that a CTA looks after, at most
 constexpr int kA8TileBytes = 4096;  // of rows as they come, for each warp
-constexpr size_t kA8Smem = kA8Warps * kA8TileBytes + kA8Chunk * DT_MAX_PAGE * sizeof(int2);  // at most
+constexpr size_t kA8Smem = kA8Warps * kA8TileBytes + kA8Chunk * DT_MAX_PAGE * sizeof(int2) +
+                          2 * kA8TileBytes;  // at most
 constexpr int kScaleLow = DT_SCALE_LOW, kScaleHigh = DT_SCALE_HIGH;
 
 struct Append8Params {
   int N, Hq, Hkv, max_pos, half, interleaved;                    // half = rot / 2
   int page_shift, block_shift;                                   // log2 of a page's rows, of a block's
-  int chunk, chunks;                                             // tokens a key/value CTA looks after; such CTAs
+  int chunk, kv_ctas, q_ctas;                                    // tokens a key/value CTA looks after; CTAs of each kind
   long long slots_end;                                           // num_pages * page_size
   const unsigned short *q, *k, *v;
   long long q_stride, k_stride, v_stride;  // elements between tokens
@@ -65,8 +66,8 @@ __global__ void __launch_bounds__(kA8Threads) append8_index_kernel(Append8Params
   if (slot >= 0) p.index[slot] = t;
 }
 
-// Eight columns of one row in fp32, rotated: two groups of four, a half-split head's the two halves of four pairs. (No
-// contraction: the largest element decides a scale, and should not depend on how a compiler pairs products and sums.)
+// Eight columns of one row in fp32, rotated: two groups of four, a half-split head's the two halves of four pairs. The
+// products and sums are paired as written here, not as a compiler likes: the largest element decides a scale.
 struct Cols {
   int a, b;     // the groups' first columns
   int pair;     // the first of their pairs, -1: not rotated
@@ -78,29 +79,31 @@ __device__ __forceinline__ Cols a8_cols(int item, int half, int interleaved) {
   }
   return Cols{4 * item, 4 * item + half, 4 * item};
 }
-__device__ __forceinline__ void a8_turn(float& a, float& b, float c, float s) {
-  const float u = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s)), w = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
-  a = u;
-  b = w;
+__device__ __forceinline__ uint64_t a8_mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
-__device__ __forceinline__ Eight a8_item(const Append8Params& p, uint2 a, uint2 b, const Cols& cols, int pos) {
-  Eight x = unpack8(make_uint4(a.x, a.y, b.x, b.y));
-  if (cols.pair >= 0) {
-    const float* row = p.rope + static_cast<size_t>(pos) * (2 * p.half) + cols.pair;
-    const float4 c = *reinterpret_cast<const float4*>(row), s = *reinterpret_cast<const float4*>(row + p.half);
-    if (p.interleaved) {
-      a8_turn(x.x[0], x.x[1], c.x, s.x);
-      a8_turn(x.x[2], x.x[3], c.y, s.y);
-      a8_turn(x.x[4], x.x[5], c.z, s.z);
-      a8_turn(x.x[6], x.x[7], c.w, s.w);
-    } else {
-      a8_turn(x.x[0], x.x[4], c.x, s.x);
-      a8_turn(x.x[1], x.x[5], c.y, s.y);
-      a8_turn(x.x[2], x.x[6], c.z, s.z);
-      a8_turn(x.x[3], x.x[7], c.w, s.w);
-    }
+// Two pairs: (a, b) -> (a c - b s, b c + a s), each a product and a fused one.
+__device__ __forceinline__ void a8_turn2(float& a0, float& a1, float& b0, float& b1, float c0, float c1, float s0,
+                                         float s1) {
+  const uint64_t a = at_pair(a0, a1), b = at_pair(b0, b1), c = at_pair(c0, c1);
+  at_unpair(at_fma2(b, at_pair(-s0, -s1), a8_mul2(a, c)), a0, a1);
+  at_unpair(at_fma2(a, at_pair(s0, s1), a8_mul2(b, c)), b0, b1);
+}
+__device__ __forceinline__ void a8_rotate(Eight& x, const float4& c, const float4& s, bool interleaved) {
+  if (interleaved) {
+    a8_turn2(x.x[0], x.x[2], x.x[1], x.x[3], c.x, c.y, s.x, s.y);
+    a8_turn2(x.x[4], x.x[6], x.x[5], x.x[7], c.z, c.w, s.z, s.w);
+  } else {
+    a8_turn2(x.x[0], x.x[1], x.x[4], x.x[5], c.x, c.y, s.x, s.y);
+    a8_turn2(x.x[2], x.x[3], x.x[6], x.x[7], c.z, c.w, s.z, s.w);
   }
-  return x;
+}
+__device__ __forceinline__ float4 a8_shared4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+  return v;
 }
 
 // The largest size that a scale serves, 448 2^kScaleHigh. What is larger, infinite or no number is stored as NaN and leaves
@@ -138,7 +141,11 @@ __device__ __forceinline__ uint32_t a8_code2(float lo, float hi) {
   return r;
 }
 __device__ __forceinline__ uint32_t a8_code4(const float* x, float inv) {
-  return a8_code2(x[0] * inv, x[1] * inv) | a8_code2(x[2] * inv, x[3] * inv) << 16;
+  const uint64_t by = at_pair(inv, inv);
+  float a, b, c, d;
+  at_unpair(a8_mul2(at_pair(x[0], x[1]), by), a, b);
+  at_unpair(a8_mul2(at_pair(x[2], x[3]), by), c, d);
+  return a8_code2(a, b) | a8_code2(c, d) << 16;
 }
 __device__ __forceinline__ void a8_drop(Eight& e) {  // what no scale serves
 #pragma unroll
@@ -162,34 +169,65 @@ __device__ __forceinline__ uint32_t a8_again(uint32_t codes, float down) {
 // are and is read from there twice, for the scale and for the codes (kept in registers, they were either few loads in
 // flight or spilled); a block of more rows is gone through twice.
 template <int D>
-__device__ __forceinline__ void a8_block(const Append8Params& p, const int2* who, int low, int first_slot, int head,
-                                         bool is_k, unsigned char* tile) {
-  constexpr int kItems = D / 8, kRows = 32 / kItems, kTile = kA8TileBytes / (2 * D);
-  const int lane = threadIdx.x & 31, item = lane % kItems, row0 = lane / kItems;
-  const Cols cols = is_k && p.half > 0 ? a8_cols(item, p.half, p.interleaved) : Cols{8 * item, 8 * item + 4, -1};
-  const unsigned short* src = (is_k ? p.k : p.v) + head * D;
+struct A8 {
+  static constexpr int kItems = D / 8, kRows = 32 / kItems, kTile = kA8TileBytes / (2 * D);
+};
+// A head's rows of a block, from r0 on, to the warp's tile.
+template <int D>
+__device__ __forceinline__ void a8_load(const Append8Params& p, const int2* who, int r0, int head, bool is_k,
+                                        unsigned char* tile) {
+  constexpr int kItems = A8<D>::kItems, kRows = A8<D>::kRows;
+  const int lane = threadIdx.x & 31, item = lane % kItems, row0 = lane / kItems, block = 1 << p.block_shift;
+  const unsigned short* src = (is_k ? p.k : p.v) + head * D + 8 * item;
   const long long stride = is_k ? p.k_stride : p.v_stride;
+  const uint32_t to = smem_u32(tile) + (row0 * D + 8 * item) * 2;
+#pragma unroll
+  for (int u = 0; u < A8<D>::kTile; u += kRows) {
+    const int r = r0 + u + row0, t = r < block ? who[r].x : INT_MAX;
+    if (t != INT_MAX)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + u * D * 2), "l"(src + t * stride) : "memory");
+  }
+}
+// kKind: values (or keys that are not rotated) 0; keys whose rows' parts of the rotation's table are in shared memory at
+// `turns`, row by row, and whose first tile is there if `loaded`: 1; keys that read the table: 2.
+template <int D, int kKind>
+__device__ __forceinline__ void a8_block(const Append8Params& p, const int2* who, int low, int first_slot, int head,
+                                         bool is_k, unsigned char* tile, uint32_t turns, bool loaded) {
+  constexpr int kItems = A8<D>::kItems, kRows = A8<D>::kRows, kTile = A8<D>::kTile;
+  const int lane = threadIdx.x & 31, item = lane % kItems, row0 = lane / kItems;
+  const Cols cols = kKind ? a8_cols(item, p.half, p.interleaved) : Cols{8 * item, 8 * item + 4, -1};
+  const bool turned = kKind && cols.pair >= 0;
   const int page = first_slot >> p.page_shift, row_at = first_slot & ((1 << p.page_shift) - 1);
   const size_t plane = static_cast<size_t>(page) * p.Hkv + head;
   unsigned char* cache = (is_k ? p.k_cache : p.v_cache) + ((plane << p.page_shift) + row_at) * D;
   float* scale = (is_k ? p.k_scale : p.v_scale) + (plane << (p.page_shift - p.block_shift)) + (row_at >> p.block_shift);
-  const int block = 1 << p.block_shift, from = low & ~(kTile - 1);
+  const int block = 1 << p.block_shift, from = low & ~(kTile - 1), rot = 2 * p.half;
+  const unsigned short* own = reinterpret_cast<const unsigned short*>(tile) + row0 * D;  // the lane's first row of a tile
+  const int rows = block < kTile ? block : kTile;
   auto load = [&](int r0) {
-    const uint32_t to = smem_u32(tile) + (row0 * D + 8 * item) * 2;
-#pragma unroll
-    for (int u = 0; u < kTile; u += kRows) {
-      const int r = r0 + u + row0, t = r < block ? who[r].x : INT_MAX;
-      if (t != INT_MAX)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + u * D * 2),
-                     "l"(src + t * stride + 8 * item)
-                     : "memory");
-    }
+    a8_load<D>(p, who, r0, head, is_k, tile);
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
   };
   auto item_of = [&](int u, int pos) {  // of the tile's row u + row0
-    const unsigned short* at = reinterpret_cast<const unsigned short*>(tile) + (u + row0) * D;
-    return a8_item(p, *reinterpret_cast<const uint2*>(at + cols.a), *reinterpret_cast<const uint2*>(at + cols.b), cols, pos);
+    Eight x;
+    if constexpr (kKind == 0) {
+      x = unpack8(*reinterpret_cast<const uint4*>(own + u * D + 8 * item));
+    } else {
+      const uint2 a = *reinterpret_cast<const uint2*>(own + u * D + cols.a);
+      const uint2 b = *reinterpret_cast<const uint2*>(own + u * D + cols.b);
+      x = unpack8(make_uint4(a.x, a.y, b.x, b.y));
+      if (turned) {
+        if constexpr (kKind == 1) {
+          const uint32_t at = turns + ((u + row0) * rot + cols.pair) * 4;
+          a8_rotate(x, a8_shared4(at), a8_shared4(at + 2 * rot), p.interleaved);
+        } else {
+          const float* at = p.rope + static_cast<size_t>(pos) * rot + cols.pair;
+          a8_rotate(x, *reinterpret_cast<const float4*>(at), *reinterpret_cast<const float4*>(at + p.half), p.interleaved);
+        }
+      }
+    }
+    return x;
   };
   const float was_scale = low > 0 ? *scale : 0.f;
   float most = 0.f;
@@ -199,14 +237,15 @@ __device__ __forceinline__ void a8_block(const Append8Params& p, const int2* who
   while (true) {
 #pragma unroll 1
     for (int r0 = from; r0 < block; r0 += kTile) {
-      if (!odd || block > kTile) load(r0);
-#pragma unroll 2
-      for (int u = 0; u < kTile; u += kRows) {
-        const int r = r0 + u + row0;
-        const int2 w = r < block ? who[r] : make_int2(INT_MAX, 0);
-        if (w.x == INT_MAX) continue;
-        const Eight x = item_of(u, w.y);
-        most = odd ? a8_most_served(x, most) : a8_most(x, most);
+      if ((!odd && !loaded) || block > kTile) load(r0);
+      const int2* w = who + r0 + row0;
+#pragma unroll 4
+      for (int u = 0; u < rows; u += kRows) {
+        const int2 token = w[u];
+        if (token.x == INT_MAX) continue;
+        const Eight x = item_of(u, token.y);
+        if (__builtin_expect(odd, 0)) most = a8_most_served(x, most);
+        else most = a8_most(x, most);
       }
       if (block > kTile) __syncwarp();  // the tile is read before the next one comes
     }
@@ -233,28 +272,34 @@ __device__ __forceinline__ void a8_block(const Append8Params& p, const int2* who
 #pragma unroll 1
   for (int r0 = from; r0 < block; r0 += kTile) {
     if (block > kTile) load(r0);
-#pragma unroll 2
-    for (int u = 0; u < kTile; u += kRows) {
-      const int r = r0 + u + row0;
-      const int2 w = r < block ? who[r] : make_int2(INT_MAX, 0);
-      if (w.x == INT_MAX) continue;
-      Eight x = item_of(u, w.y);
+    const int2* w = who + r0 + row0;
+    unsigned char* to = cache + (r0 + row0) * D;
+#pragma unroll 4
+    for (int u = 0; u < rows; u += kRows) {
+      const int2 token = w[u];
+      if (token.x == INT_MAX) continue;
+      Eight x = item_of(u, token.y);
       if (dense) {
-        unsigned short* o = dense + static_cast<size_t>(w.x) * p.Hkv * D;
+        unsigned short* o = dense + static_cast<size_t>(token.x) * (p.Hkv * D);
         const uint4 y = pack8(x);
         *reinterpret_cast<uint2*>(o + cols.a) = make_uint2(y.x, y.y);
         *reinterpret_cast<uint2*>(o + cols.b) = make_uint2(y.z, y.w);
       }
-      if (odd) a8_drop(x);
-      *reinterpret_cast<uint32_t*>(cache + r * D + cols.a) = a8_code4(x.x, inv);
-      *reinterpret_cast<uint32_t*>(cache + r * D + cols.b) = a8_code4(x.x + 4, inv);
+      if (__builtin_expect(odd, 0)) a8_drop(x);
+      if constexpr (kKind == 0) {
+        *reinterpret_cast<uint2*>(to + u * D + 8 * item) = make_uint2(a8_code4(x.x, inv), a8_code4(x.x + 4, inv));
+      } else {
+        *reinterpret_cast<uint32_t*>(to + u * D + cols.a) = a8_code4(x.x, inv);
+        *reinterpret_cast<uint32_t*>(to + u * D + cols.b) = a8_code4(x.x + 4, inv);
+      }
     }
     __syncwarp();  // the tile is read before the next one comes
   }
 }
 
-// CTAs 0 .. 2 chunks - 1: the keys (the even ones) or the values of the blocks whose leaders are among the CTA's tokens.
-// The others: queries, a token or several at a time, each thread in the same columns of its heads (as dt_kv_append).
+// Two kinds of CTAs, in turn, so that they share the SMs: those of keys and values compute while those of queries wait for
+// memory. Keys (the even ones of their kind) or values: of the blocks whose leaders are among the CTA's tokens. Queries: a
+// token or several at a time, each thread in the same columns of its heads (as dt_kv_append).
 template <int D>
 __global__ void __launch_bounds__(kA8Threads, kA8PerSm) kv_append8_kernel(Append8Params p, WsHeader* hdr) {
   extern __shared__ __align__(16) unsigned char s_tiles[];  // a tile a warp
@@ -263,15 +308,18 @@ __global__ void __launch_bounds__(kA8Threads, kA8PerSm) kv_append8_kernel(Append
   __shared__ int s_low[kA8Chunk], s_first[kA8Chunk], s_lead[kA8Chunk];
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, block = 1 << p.block_shift;
   at_launch_order();
-  if (static_cast<int>(blockIdx.x) >= 2 * p.chunks) {
+  const int both = 2 * (p.kv_ctas < p.q_ctas ? p.kv_ctas : p.q_ctas), b = blockIdx.x;
+  const bool queries = b < both ? (b & 1) != 0 : p.q_ctas > p.kv_ctas;
+  const int cta = b < both ? b >> 1 : b - both / 2;  // among its kind
+  if (queries) {
     constexpr int kItems = D / 16, kStep = kA8Threads / kItems;
     const int item = t % kItems, tokens = p.Hq < kStep ? kStep / p.Hq : 1;
     const int mine = t / kItems / p.Hq;  // of the tokens of a pass
     if (mine >= tokens && p.Hq < kStep) return;
     const int head0 = p.Hq < kStep ? t / kItems % p.Hq : t / kItems;
     const TurnCols cols = p.half ? turn_cols(item, p.half, p.interleaved) : TurnCols{16 * item, 16 * item + 8, false};
-    const long long stride = static_cast<long long>(gridDim.x - 2 * p.chunks) * tokens;
-    long long token = static_cast<long long>(blockIdx.x - 2 * p.chunks) * tokens + (p.Hq < kStep ? mine : 0);
+    const long long stride = static_cast<long long>(p.q_ctas) * tokens;
+    long long token = static_cast<long long>(cta) * tokens + (p.Hq < kStep ? mine : 0);
     int slot_next = token < p.N ? p.slots[token] : -1, pos_next = p.half && token < p.N ? p.positions[token] : 0;
     for (; token < p.N; token += stride) {
       const int slot = slot_next, pos = pos_next;
@@ -300,8 +348,8 @@ __global__ void __launch_bounds__(kA8Threads, kA8PerSm) kv_append8_kernel(Append
     }
     return;
   }
-  const int token0 = (blockIdx.x >> 1) * p.chunk;
-  const bool is_k = (blockIdx.x & 1) == 0;
+  const int token0 = (cta >> 1) * p.chunk;
+  const bool is_k = (cta & 1) == 0;
   // a look at all slots: under way before it is known what for
   constexpr int kLooks = kA8Scan / kA8Threads;
   int look[kLooks];
@@ -314,9 +362,12 @@ __global__ void __launch_bounds__(kA8Threads, kA8PerSm) kv_append8_kernel(Append
     bool bad = false;
     const int token = token0 + t, slot = token < p.N ? a8_slot(p, token, &bad) : -1;
     if (bad) record_error(hdr, DT_ERR_INVALID_ARG);
+    // the token before it in the row before it: it does not lead, as most do not
+    bool other = false;
+    const bool follows = token > 0 && token < p.N && (slot & (block - 1)) > 0 && a8_slot(p, token - 1, &other) == slot - 1;
     s_low[t] = block;
     s_lead[t] = -1;
-    s_first[t] = slot < 0 ? -1 : slot;
+    s_first[t] = slot < 0 || follows ? -1 : slot;
   }
   __syncthreads();
   if (p.index) {
@@ -367,11 +418,34 @@ __global__ void __launch_bounds__(kA8Threads, kA8PerSm) kv_append8_kernel(Append
     if (t < p.chunk && s_low[t] < block) s_lead[t] = s_who[(t << p.block_shift) + s_low[t]].x;
   }
   __syncthreads();
+  float* s_turns = reinterpret_cast<float*>(s_who + (p.chunk << p.block_shift));
+  unsigned char* tile = s_tiles + warp * kA8TileBytes;
+  // blocks of one tile: the rows' part of the rotation's table comes once for all heads
+  const bool staged = is_k && p.half > 0 && block <= A8<D>::kTile;
   for (int c = 0; c < p.chunk; ++c) {
     if (s_lead[c] != token0 + c) continue;  // another token leads
-    for (int head = warp; head < p.Hkv; head += kA8Warps)
-      a8_block<D>(p, s_who + (c << p.block_shift), s_low[c], s_first[c] & ~(block - 1), head, is_k,
-                  s_tiles + warp * kA8TileBytes);
+    const int2* who = s_who + (c << p.block_shift);
+    const int low = s_low[c], first = s_first[c] & ~(block - 1);
+    if (staged) {
+      __syncthreads();  // the block before is done
+      if (warp < p.Hkv) a8_load<D>(p, who, low & ~(A8<D>::kTile - 1), warp, true, tile);
+      const int quads = p.half / 2;  // 16-byte pieces of a position's row
+      for (int i = t; i < quads << p.block_shift; i += kA8Threads) {
+        const int r = i / quads, q = i - r * quads;
+        if (who[r].x != INT_MAX)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(s_turns + r * 2 * p.half + 4 * q)),
+                       "l"(p.rope + static_cast<size_t>(who[r].y) * (2 * p.half) + 4 * q)
+                       : "memory");
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncthreads();
+    }
+    const uint32_t turns = smem_u32(s_turns);
+    for (int head = warp; head < p.Hkv; head += kA8Warps) {
+      if (staged) a8_block<D, 1>(p, who, low, first, head, true, tile, turns, head == warp);
+      else if (is_k && p.half > 0) a8_block<D, 2>(p, who, low, first, head, true, tile, 0u, false);
+      else a8_block<D, 0>(p, who, low, first, head, is_k, tile, 0u, false);
+    }
   }
 }
 
@@ -449,14 +523,16 @@ extern "C" dt_status dt_kv_append8(int N, int Hq, int Hkv, int d, const void* q,
   // as many CTAs as there is room for, but no more tokens than a CTA looks after
   const int each = 2 * N / (kA8PerSm * di.sms) + 1;
   p.chunk = each < kA8Chunk ? each : kA8Chunk;
-  p.chunks = (N + p.chunk - 1) / p.chunk;
+  p.kv_ctas = 2 * ((N + p.chunk - 1) / p.chunk);
+  const int cap = 8 * di.sms > N / 8 ? 8 * di.sms : N / 8;
+  p.q_ctas = Hq == 0 ? 0 : N < cap ? N : cap;
   WsHeader* hdr = static_cast<WsHeader*>(workspace);
   if (indexed) {
     const dt_status s = at_launch(append8_index_kernel, (N + kA8Threads - 1) / kA8Threads, kA8Threads, 0, stream, p);
     if (s != DT_OK) return s;
   }
-  const int cap = 8 * di.sms, grid = 2 * p.chunks + (Hq > 0 ? (N < cap ? N : cap) : 0);
-  const size_t smem = sizeof(int2) * static_cast<size_t>(p.chunk) * scale_block + kA8Warps * kA8TileBytes;
+  const int grid = p.kv_ctas + p.q_ctas;
+  const size_t smem = sizeof(int2) * static_cast<size_t>(p.chunk) * scale_block + kA8Warps * kA8TileBytes + 2 * kA8TileBytes;
   const void* fn = d == 64 ? reinterpret_cast<const void*>(kv_append8_kernel<64>)
                            : reinterpret_cast<const void*>(kv_append8_kernel<128>);
   if (ensure_dynamic_smem(fn, kA8Smem) != cudaSuccess) return DT_ERR_CUDA;
