@@ -254,6 +254,8 @@ struct P8 {
   static constexpr int kSets = kSets_;                   // sets of four warps for the values: they take blocks in turn
   static constexpr int kSoftmax = 4 + 4 * kSets;         // warps 0, 2: load, 1: MMA, 3: queries, 4 on: values, then softmax
   static constexpr int kThreads = 32 * kSoftmax + 128 * kGroups;
+  // few rows: a warp for the queries; many: the warps of the values, before a segment's first
+  static constexpr int kQWarps = N <= 16 ? 1 : 4 * kSets;
   static constexpr int kStep = kStep_;                   // rows taken at once
   static constexpr int kSteps = M / kStep;
   static constexpr int kSums = kSteps > 1 ? kSteps : M;  // a thread's sums: of its keys and a row each, or of its warp's
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
       mbar_init(&s_full[i], 1);
       mbar_init(&w_full[i], 4 * C::kGroups);
       mbar_init(&o_done[i], 1);
-      mbar_init(&q_full[i], 1);
+      mbar_init(&q_full[i], C::kQWarps);
       mbar_init(&o_free[i], 4 * C::kGroups);
     }
     mbar_init(&s_meet, 4 * C::kGroups);
@@ -377,6 +379,90 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
   bool ok = true;
   const int ctas = W < p.grid ? static_cast<int>(W) : p.grid;  // that take a share: a block each at least
   PaWalk w = pa_walk(p, cum, W, ctas);
+
+  // A segment's queries and its mask, by kQWarps warps.
+  auto queries = [&](const PaSeg& sg, int si, int who) {
+    const unsigned qb = static_cast<unsigned>(si) & 1u;
+      // the segment that had the buffer before is over: its factors and its mask are not read any more
+      if (si >= 2) ok = __all_sync(0xFFFFFFFFu, p8_rest(&o_free[qb], static_cast<unsigned>((si >> 1) - 1) & 1u));
+    if (!ok) return;
+#pragma unroll 1
+      for (int c = 32 * who + lane; c < p.n; c += 32 * C::kQWarps) {
+        unsigned long long bits = ~0ull << c;
+        if (p.mask) {
+          const uint8_t* col = p.mask + static_cast<size_t>(sg.b) * p.n * p.n + c;
+          bits = 0ull;
+#pragma unroll 8
+          for (int i = 0; i < p.n; ++i) bits |= static_cast<unsigned long long>(col[static_cast<size_t>(i) * p.n] != 0) << i;
+        }
+        s_sees[qb][c] = bits;
+      }
+      unsigned char* qd = sq + qb * C::kQ;
+      // eight lanes a row, D / 8 elements each; four rows a step, several steps' loads in flight
+      constexpr int kEach = D / 8, kAtOnce = 4;
+      const int sub = lane & 7;
+      const unsigned short* src = p.q + (static_cast<size_t>(sg.b) * p.n * p.Hq + sg.kvh * p.G) * D + kEach * sub;
+#pragma unroll 1
+      for (int r0 = 4 * kAtOnce * who; r0 < p.R; r0 += 4 * kAtOnce * C::kQWarps) {
+        uint4 x[kAtOnce][kEach / 8];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int r = r0 + 4 * u + (lane >> 3);
+#pragma unroll
+          for (int i = 0; i < kEach / 8; ++i)
+            x[u][i] = r < p.R ? *reinterpret_cast<const uint4*>(src + s_at[r] + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          if (r0 + 4 * u >= p.R) break;
+          const int r = r0 + 4 * u + (lane >> 3);
+          const uint32_t* bits = reinterpret_cast<const uint32_t*>(x[u]);
+          unsigned most = 0u;  // the bits of the row's largest finite element, as a bf16
+#pragma unroll
+          for (int i = 0; i < kEach / 2; ++i) {
+            const unsigned lo = bits[i] & 0x7FFFu, hi = (bits[i] >> 16) & 0x7FFFu;
+            if (lo < 0x7F80u && lo > most) most = lo;
+            if (hi < 0x7F80u && hi > most) most = hi;
+          }
+#pragma unroll
+          for (int h = 4; h > 0; h >>= 1) {
+            const unsigned other = __shfl_xor_sync(0xFFFFFFFFu, most, h);
+            most = other > most ? other : most;
+          }
+          // the largest power of two that leaves it at 448 = 1.75 2^8 or less
+          int up = ((most & 0x7Fu) > 0x60u ? 7 : 8) - (static_cast<int>(most >> 7) - 127);
+          if (up > 100) up = 100;  // (nothing is lost: such a row's scores are zero whatever the keys are)
+          const float by = __uint_as_float(static_cast<unsigned>(up + 127) << 23);
+          uint32_t q1[kEach / 4], q2[kEach / 4];
+#pragma unroll
+          for (int i = 0; i < kEach / 4; ++i) q1[i] = q2[i] = 0u;
+#pragma unroll
+          for (int i = 0; i < kEach / 2; ++i) {
+            const float a = __uint_as_float(bits[i] << 16) * by, b = __uint_as_float(bits[i] & 0xFFFF0000u) * by;
+            const float a1 = fabsf(a) <= 448.f ? a : NAN, b1 = fabsf(b) <= 448.f ? b : NAN;
+            const uint32_t c = p8_code2(a1, b1), two = p8_two(c);
+            const float2 got = __half22float2(*reinterpret_cast<const __half2*>(&two));
+            q1[i / 2] |= c << (16 * (i & 1));
+            q2[i / 2] |= p8_code2(a1 - got.x, b1 - got.y) << (16 * (i & 1));
+          }
+          if (r < p.R) {
+            if constexpr (D == 128) {
+              unsigned char* at = qd + p8_piece<D>(r, sub);
+              *reinterpret_cast<uint4*>(at) = make_uint4(q1[0], q1[1], q1[kEach / 4 - 2], q1[kEach / 4 - 1]);
+              *reinterpret_cast<uint4*>(at + C::kTerm) = make_uint4(q2[0], q2[1], q2[kEach / 4 - 2], q2[kEach / 4 - 1]);
+            } else {
+              unsigned char* at = qd + p8_piece<D>(r, sub >> 1) + 8 * (sub & 1);
+              *reinterpret_cast<uint2*>(at) = make_uint2(q1[0], q1[1]);
+              *reinterpret_cast<uint2*>(at + C::kTerm) = make_uint2(q2[0], q2[1]);
+            }
+            if (sub == 0) s_factor[qb][r] = p.scale_log2 * __uint_as_float(static_cast<unsigned>(127 - up) << 23);
+          }
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads Q through the async proxy
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[qb]);
+  };
 
   if (warp == 0 || warp == 2) {  // load: the keys, the values; the whole warp, one page's box a lane
     const int kv = warp >> 1;
@@ -487,8 +573,10 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
         if (sg.nblk == 0) break;
         const unsigned ob = static_cast<unsigned>(si) % kOs;
         for (int j = 0; j < sg.nblk && ok; j += kPar, ++step) {
-          // their buffers were freed by the softmax of the step before (waited for below, one step ago)
-          ok = scores();
+          // their buffers were freed by the softmax of the step before (waited for below, one step ago); the next segment's
+          // wait for its queries, and this one's outputs do not wait for them
+          const bool early = js < ss.nblk;
+          if (early) ok = scores();
           if (ok && j == 0 && si >= kOs) {  // the segment that had the buffer before has been read
             const int was = si - kOs;
             ok = wait(&o_free[was & 1], static_cast<unsigned>(was >> 1) & 1u);
@@ -508,94 +596,17 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
           }
           if (!ok) break;
           umma_commit(&o_done[step & 1u]);
+          if (!early) ok = scores();
         }
       }
     }
   } else if (warp < 4) {  // queries
-    for (int si = 0; ok; ++si) {
-      const PaSeg sg = pa_next(p, cum, w);
-      if (sg.nblk == 0) break;
-      const unsigned qb = static_cast<unsigned>(si) & 1u;
-      // the segment that had the buffer before is over: its factors and its mask are not read any more
-      if (si >= 2) ok = __all_sync(0xFFFFFFFFu, p8_rest(&o_free[qb], static_cast<unsigned>((si >> 1) - 1) & 1u));
-      if (!ok) break;
-#pragma unroll 1
-      for (int c = lane; c < p.n; c += 32) {
-        unsigned long long bits = ~0ull << c;
-        if (p.mask) {
-          const uint8_t* col = p.mask + static_cast<size_t>(sg.b) * p.n * p.n + c;
-          bits = 0ull;
-#pragma unroll 8
-          for (int i = 0; i < p.n; ++i) bits |= static_cast<unsigned long long>(col[static_cast<size_t>(i) * p.n] != 0) << i;
-        }
-        s_sees[qb][c] = bits;
+    if constexpr (C::kQWarps == 1)
+      for (int si = 0; ok; ++si) {
+        const PaSeg sg = pa_next(p, cum, w);
+        if (sg.nblk == 0) break;
+        queries(sg, si, 0);
       }
-      unsigned char* qd = sq + qb * C::kQ;
-      // eight lanes a row, D / 8 elements each; four rows a step, several steps' loads in flight
-      constexpr int kEach = D / 8, kAtOnce = 4;
-      const int sub = lane & 7;
-      const unsigned short* src = p.q + (static_cast<size_t>(sg.b) * p.n * p.Hq + sg.kvh * p.G) * D + kEach * sub;
-#pragma unroll 1
-      for (int r0 = 0; r0 < p.R; r0 += 4 * kAtOnce) {
-        uint4 x[kAtOnce][kEach / 8];
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-          const int r = r0 + 4 * u + (lane >> 3);
-#pragma unroll
-          for (int i = 0; i < kEach / 8; ++i)
-            x[u][i] = r < p.R ? *reinterpret_cast<const uint4*>(src + s_at[r] + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-          if (r0 + 4 * u >= p.R) break;
-          const int r = r0 + 4 * u + (lane >> 3);
-          const uint32_t* bits = reinterpret_cast<const uint32_t*>(x[u]);
-          unsigned most = 0u;  // the bits of the row's largest finite element, as a bf16
-#pragma unroll
-          for (int i = 0; i < kEach / 2; ++i) {
-            const unsigned lo = bits[i] & 0x7FFFu, hi = (bits[i] >> 16) & 0x7FFFu;
-            if (lo < 0x7F80u && lo > most) most = lo;
-            if (hi < 0x7F80u && hi > most) most = hi;
-          }
-#pragma unroll
-          for (int h = 4; h > 0; h >>= 1) {
-            const unsigned other = __shfl_xor_sync(0xFFFFFFFFu, most, h);
-            most = other > most ? other : most;
-          }
-          // the largest power of two that leaves it at 448 = 1.75 2^8 or less
-          int up = ((most & 0x7Fu) > 0x60u ? 7 : 8) - (static_cast<int>(most >> 7) - 127);
-          if (up > 100) up = 100;  // (nothing is lost: such a row's scores are zero whatever the keys are)
-          const float by = __uint_as_float(static_cast<unsigned>(up + 127) << 23);
-          uint32_t q1[kEach / 4], q2[kEach / 4];
-#pragma unroll
-          for (int i = 0; i < kEach / 4; ++i) q1[i] = q2[i] = 0u;
-#pragma unroll
-          for (int i = 0; i < kEach / 2; ++i) {
-            const float a = __uint_as_float(bits[i] << 16) * by, b = __uint_as_float(bits[i] & 0xFFFF0000u) * by;
-            const float a1 = fabsf(a) <= 448.f ? a : NAN, b1 = fabsf(b) <= 448.f ? b : NAN;
-            const uint32_t c = p8_code2(a1, b1), two = p8_two(c);
-            const float2 got = __half22float2(*reinterpret_cast<const __half2*>(&two));
-            q1[i / 2] |= c << (16 * (i & 1));
-            q2[i / 2] |= p8_code2(a1 - got.x, b1 - got.y) << (16 * (i & 1));
-          }
-          if (r < p.R) {
-            if constexpr (D == 128) {
-              unsigned char* at = qd + p8_piece<D>(r, sub);
-              *reinterpret_cast<uint4*>(at) = make_uint4(q1[0], q1[1], q1[kEach / 4 - 2], q1[kEach / 4 - 1]);
-              *reinterpret_cast<uint4*>(at + C::kTerm) = make_uint4(q2[0], q2[1], q2[kEach / 4 - 2], q2[kEach / 4 - 1]);
-            } else {
-              unsigned char* at = qd + p8_piece<D>(r, sub >> 1) + 8 * (sub & 1);
-              *reinterpret_cast<uint2*>(at) = make_uint2(q1[0], q1[1]);
-              *reinterpret_cast<uint2*>(at + C::kTerm) = make_uint2(q2[0], q2[1]);
-            }
-            if (sub == 0) s_factor[qb][r] = p.scale_log2 * __uint_as_float(static_cast<unsigned>(127 - up) << 23);
-          }
-        }
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads Q through the async proxy
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[qb]);
-    }
   } else if (warp < C::kSoftmax) {  // values
     constexpr int kParts = D / 64;  // pieces of 16 columns a warp has
     const int part0 = (warp & 3) * kParts;
@@ -613,6 +624,10 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
       const PaSeg sg = pa_next(p, cum, w);
       if (sg.nblk == 0) break;
       const int len = lens[sg.b], common = pa_common(p, len);
+      if constexpr (C::kQWarps > 1) {
+        queries(sg, si, warp - 4);
+        if (!ok) break;
+      }
       for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
         if (g % C::kSets != set) {
           advance();
