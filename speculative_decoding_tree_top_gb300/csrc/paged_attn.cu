@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) paged_attn_kernel(PaParams p, c
     const int len = b < p.B ? pa_length(p, b, &bad) : 0;
     if (bad && blockIdx.x == 0) record_error(hdr, DT_ERR_INVALID_ARG);
     int total;
-    const int units = len > 0 ? (len + kPaKeys - 1) / kPaKeys + 1 : 0;
+    const int units = len > 0 ? (len + kPaKeys - 1) / kPaKeys + p.extra : 0;
     const int before = block_exclusive_scan<kPaThreads / 32>(units, &total, s_warp);
     if (b < p.B) {
       cum[b] = carry + before;
@@ -567,7 +567,7 @@ extern "C" dt_status dt_paged_attention(int B, int n, int Hq, int Hkv, int d, co
   const PaPlan P = pa_plan(G * n, d, di.sms);
   if (workspace_bytes < P.bytes) return DT_ERR_INVALID_ARG;
   PaParams p{};
-  p.B = B; p.n = n; p.Hq = Hq; p.Hkv = Hkv; p.G = G; p.R = G * n; p.grid = P.grid;
+  p.B = B; p.n = n; p.Hq = Hq; p.Hkv = Hkv; p.G = G; p.R = G * n; p.grid = P.grid; p.extra = 1;
   p.page_size = page_size; p.num_pages = num_pages; p.max_pages = max_pages;
   p.v_cache = static_cast<const unsigned short*>(v_cache);
   p.page_table = page_table; p.lens = lens; p.mask = mask;

@@ -35,6 +35,7 @@ constexpr int kP8MaxStages = 24;
 constexpr int kP8Scales = 32;
 static_assert(kP8MaxStages / 2 + 4 <= kP8Scales, "scales are not overwritten before they are read");
 constexpr size_t kPa8SmemCap = 232448 - 11264;  // opt-in shared memory of a CTA, less the static part
+constexpr int kP8Extra = 4;       // what a pair's start and end cost, in blocks
 // Weights times their values' scales are fp16: a row's largest starts out at 2^kP8Start and may grow to 2^kP8Most before
 // the reference is raised. fp16 goes up to 2^16 and holds subnormal numbers in steps of 2^-24.
 constexpr float kP8Start = 6.f, kP8Most = 14.f;
@@ -43,6 +44,7 @@ constexpr float kP8LeastScale = -64.f;  // log2: smaller scales of values do not
 struct Pa8Params : PaWork {
   int stages;
   int page_shift, block_shift;      // log2 of the rows of a page, and of those that share a scale
+  int third;                        // whether a third warp copies boxes
   const unsigned short* q;          // [B][n][Hq][D]
   const unsigned char* v_cache;     // re-read only for codes that are NaN
   const float *k_scale, *v_scale;   // [num_pages][Hkv][page_size >> block_shift]
@@ -197,6 +199,28 @@ __device__ __forceinline__ bool p8_wait(uint64_t* bar, unsigned parity) {
 __device__ __forceinline__ bool p8_rest(uint64_t* bar, unsigned parity) {
   return mbar_try_wait(bar, parity) || p8_nap(bar, parity);
 }
+// Of a block's pages, so many are copied by the loads of the keys and of the values, the rest of both by a third warp.
+__device__ __forceinline__ int p8_own_pages(int per_block) { return per_block - (per_block + 1) / 3; }
+// Entries announced to the third warp, and its wait for more than `g` of them (each has been found empty, and expects all
+// of its bytes, by then).
+__device__ __forceinline__ void p8_issue(unsigned* count, unsigned now) {
+  asm volatile("st.release.cta.shared.u32 [%0], %1;" ::"r"(smem_u32(count)), "r"(now) : "memory");
+}
+__device__ __forceinline__ bool p8_issued(const unsigned* count, unsigned g) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (unsigned i = 0;; ++i) {
+    unsigned now;
+    asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(now) : "r"(smem_u32(count)) : "memory");
+    if (now > g) return true;
+    if ((i & 1023u) == 0u) {
+      const uint64_t t = global_timer_ns();
+      if (i == 0u) t0 = t;
+      if (t - t0 > kAtBudgetNs) return false;
+    }
+    __nanosleep(32);
+  }
+}
 // Whether any of a group's threads says so; all of them come here, by whole warps.
 template <int kThreads>
 __device__ __forceinline__ bool p8_any(int id, bool x) {
@@ -252,16 +276,16 @@ struct P8 {
   static constexpr int kGroups = kPar * kRowGroups;
   static constexpr int kMeet = 128 * kPar;               // softmax threads that have the same rows
   static constexpr int kSets = kSets_;                   // sets of four warps for the values: they take blocks in turn
-  static constexpr int kSoftmax = 4 + 4 * kSets;         // warps 0, 2: load, 1: MMA, 3: queries, 4 on: values, then softmax
+  static constexpr int kSoftmax = 4 + 4 * kSets;         // warps 0, 2, 3: load, 1: MMA, 4 on: values, then softmax
   static constexpr int kThreads = 32 * kSoftmax + 128 * kGroups;
-  // few rows: a warp for the queries; many: the warps of the values, before a segment's first
-  static constexpr int kQWarps = N <= 16 ? 1 : 4 * kSets;
+  static constexpr bool kOwnQ = N <= 16;                 // a warp of its own for the queries, unless it is wanted for boxes
   static constexpr int kStep = kStep_;                   // rows taken at once
   static constexpr int kSteps = M / kStep;
   static constexpr int kSums = kSteps > 1 ? kSteps : M;  // a thread's sums: of its keys and a row each, or of its warp's
   static constexpr bool kKeep = M <= 8;                  // registers for the rows' factors and references
   static constexpr int kOut = M / kPar < 16 ? M / kPar : 16;  // rows of outputs that a thread takes at once
-  static constexpr int kVs = N <= 64 ? 4 : 2;            // buffers of values
+  static constexpr int kWs = N * kPar <= 64 ? 2 : 1;     // steps whose weights have buffers
+  static constexpr int kVs = N * kPar <= 64 ? 4 : 2;     // buffers of values
   static constexpr int kOs = N <= 64 ? 2 : 1;            // buffers of outputs
   static constexpr uint32_t kEntry = kPaKeys * D;        // a ring entry: a block's keys or values
   static constexpr uint32_t kTerm = N * D;               // one term of the queries
@@ -272,12 +296,11 @@ struct P8 {
   // tensor memory
   static constexpr uint32_t kS = 0, kO = 2 * kPar * N, kV = kO + kOs * N;
   static_assert(kV + kVs * 64 <= 512, "tensor memory");
-  static constexpr size_t kFixed = 1024 + 2 * kQ + 2 * kPar * kW;
+  static constexpr size_t kFixed = 1024 + 2 * kQ + kWs * kPar * kW;
 };
 
-// Roles. Load: pages to the ring, as in the bf16 kernel, and their scales, keys and values by a warp each (a
-// box takes its warp about a hundred cycles to issue). Queries: a segment's rows, each brought by a
-// power of two to at most 448 and split in two, with the factor that undoes it; the nodes' mask, by keys. Values: lane =
+// Roles. Load: pages to the ring, as in the bf16 kernel, and their scales, keys and values by a warp each, and a
+// third where a block spans pages (a box takes its warp about a hundred cycles to issue). Values: lane =
 // column, two keys a register. Softmax: lane = key; its scales come with the keys (loaded by the softmax itself a block
 // ahead they are late: a block takes less than a load). MMA: the scores run one step ahead of the outputs, through the
 // segments.
@@ -290,7 +313,7 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
   unsigned char* sq =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_f4) + 1023) & ~uintptr_t(1023));
   unsigned char* sw = sq + 2 * C::kQ;
-  unsigned char* skv = sw + 2 * kPar * C::kW;
+  unsigned char* skv = sw + C::kWs * kPar * C::kW;
   int* cum = reinterpret_cast<int*>(skv + p.stages * C::kEntry);  // [B + 1]
   int* lens = cum + p.B + 1;                                      // [B]
   __shared__ uint64_t kv_full[kP8MaxStages], kv_empty[kP8MaxStages];
@@ -321,7 +344,7 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
       mbar_init(&s_full[i], 1);
       mbar_init(&w_full[i], 4 * C::kGroups);
       mbar_init(&o_done[i], 1);
-      mbar_init(&q_full[i], C::kQWarps);
+      mbar_init(&q_full[i], C::kOwnQ && p.third == 0 ? 1 : 4 * C::kSets);
       mbar_init(&o_free[i], 4 * C::kGroups);
     }
     mbar_init(&s_meet, 4 * C::kGroups);
@@ -340,7 +363,7 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
   for (int i = t; i < static_cast<int>(2 * C::kQ / 16); i += kThreads)
     if (static_cast<int>(i * 16 / D) % N >= p.R) reinterpret_cast<uint4*>(sq)[i] = make_uint4(0u, 0u, 0u, 0u);
   // and the weights of rows that no softmax thread has
-  for (int i = t; i < static_cast<int>(2 * kPar * C::kW / 16); i += kThreads)
+  for (int i = t; i < static_cast<int>(C::kWs * kPar * C::kW / 16); i += kThreads)
     reinterpret_cast<uint4*>(sw)[i] = make_uint4(0u, 0u, 0u, 0u);
   for (int r = t; r < N; r += kThreads) {
     s_node[r] = static_cast<unsigned char>(r / p.G < kPaNodes ? r / p.G : kPaNodes - 1);
@@ -357,7 +380,7 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
     const int len = b < p.B ? pa_length(p, b, &bad) : 0;
     if (bad && blockIdx.x == 0) record_error(hdr, DT_ERR_INVALID_ARG);
     int total;
-    const int units = len > 0 ? (len + kPaKeys - 1) / kPaKeys + 1 : 0;
+    const int units = len > 0 ? (len + kPaKeys - 1) / kPaKeys + p.extra : 0;
     const int before = block_exclusive_scan<kThreads / 32>(units, &total, s_warp);
     if (b < p.B) {
       cum[b] = carry + before;
@@ -380,14 +403,16 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
   const int ctas = W < p.grid ? static_cast<int>(W) : p.grid;  // that take a share: a block each at least
   PaWalk w = pa_walk(p, cum, W, ctas);
 
-  // A segment's queries and its mask, by kQWarps warps.
-  auto queries = [&](const PaSeg& sg, int si, int who) {
+  // A segment's queries and its mask, by `of` warps.
+  const bool third = C::kOwnQ && p.third != 0;  // warp 3 copies boxes
+  const int own_pages = third ? p8_own_pages(kPaKeys >> p.page_shift) : kPaKeys;
+  auto queries = [&](const PaSeg& sg, int si, int who, int of) {
     const unsigned qb = static_cast<unsigned>(si) & 1u;
       // the segment that had the buffer before is over: its factors and its mask are not read any more
       if (si >= 2) ok = __all_sync(0xFFFFFFFFu, p8_rest(&o_free[qb], static_cast<unsigned>((si >> 1) - 1) & 1u));
     if (!ok) return;
 #pragma unroll 1
-      for (int c = 32 * who + lane; c < p.n; c += 32 * C::kQWarps) {
+      for (int c = 32 * who + lane; c < p.n; c += 32 * of) {
         unsigned long long bits = ~0ull << c;
         if (p.mask) {
           const uint8_t* col = p.mask + static_cast<size_t>(sg.b) * p.n * p.n + c;
@@ -403,7 +428,7 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
       const int sub = lane & 7;
       const unsigned short* src = p.q + (static_cast<size_t>(sg.b) * p.n * p.Hq + sg.kvh * p.G) * D + kEach * sub;
 #pragma unroll 1
-      for (int r0 = 4 * kAtOnce * who; r0 < p.R; r0 += 4 * kAtOnce * C::kQWarps) {
+      for (int r0 = 4 * kAtOnce * who; r0 < p.R; r0 += 4 * kAtOnce * of) {
         uint4 x[kAtOnce][kEach / 8];
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
@@ -499,9 +524,12 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
         const int at = row + ((lane & 15) << p.block_shift), from = __shfl_sync(0xFFFFFFFFu, plane, at >> p.page_shift);
         if (2 * g >= stages) ok = __all_sync(0xFFFFFFFFu, p8_rest(&kv_empty[st], par));
         if (!ok) break;
-        if (lane == 0) mbar_expect_tx(&kv_full[st], static_cast<uint32_t>(pages * box_rows * D));
+        if (lane == 0) {
+          mbar_expect_tx(&kv_full[st], static_cast<uint32_t>(pages * box_rows * D));
+          p8_issue(&s_issued[kv], g + 1u);
+        }
         __syncwarp();
-        if (lane < pages)
+        if (lane < pages && lane < own_pages)
           tma_load_3d(skv + st * C::kEntry + lane * box_rows * D, map, 0, row, plane, &kv_full[st]);
         if (kv == 0 && (lane & 15) < per_scale && (at >> p.page_shift) < pages) {
           const float* src = (lane < 16 ? p.k_scale : p.v_scale) + (static_cast<size_t>(from) << (p.page_shift - p.block_shift)) +
@@ -512,7 +540,6 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
                        : "memory");
         }
         if (kv == 0) asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&kv_full[st])) : "memory");
-        if (lane == 0) s_issued[kv] = g + 1u;
         st += 2;
         if (st >= stages) {
           st = kv;
@@ -587,7 +614,7 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
             const unsigned vb = g % kVs;
             ok = wait(&v_full[vb], (g / kVs) & 1u);
             if (!ok) break;
-            const uint64_t w0 = dw + ((((step & 1u) * kPar + u) * C::kW) >> 4);
+            const uint64_t w0 = dw + (((step % C::kWs * kPar + u) * C::kW) >> 4);
 #pragma unroll
             for (int kk = 0; kk < kPaKeys / 16; ++kk)
               umma_f16_ts(tmem + C::kO + ob * N, tmem + C::kV + vb * 64u + 8u * kk, w0 + ((kk * 16u * C::kRowW) >> 4), id_o,
@@ -600,13 +627,44 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
         }
       }
     }
-  } else if (warp < 4) {  // queries
-    if constexpr (C::kQWarps == 1)
-      for (int si = 0; ok; ++si) {
-        const PaSeg sg = pa_next(p, cum, w);
-        if (sg.nblk == 0) break;
-        queries(sg, si, 0);
+  } else if (warp == 3) {  // queries; or the other boxes of blocks that span many pages, once the load has announced them
+    const int box_rows = p.page_size < kPaKeys ? p.page_size : kPaKeys;
+    const int per_block = kPaKeys / box_rows;
+    unsigned st = 0, g = 0;
+    for (int si = 0; ok && C::kOwnQ; ++si) {
+      const PaSeg sg = pa_next(p, cum, w);
+      if (sg.nblk == 0) break;
+      if (!third) {
+        queries(sg, si, 0, 1);
+        continue;
       }
+      const int used = (lens[sg.b] + p.page_size - 1) >> p.page_shift;
+      const int32_t* table = p.page_table + static_cast<size_t>(sg.b) * p.max_pages;
+      int win = ((sg.j0 * kPaKeys) >> p.page_shift) / 32;
+      int cur = 32 * win + lane < used ? table[32 * win + lane] : 0;
+      int nxt = 32 * (win + 1) + lane < used ? table[32 * (win + 1) + lane] : 0;
+      for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
+        const int first = ((sg.j0 + j) * kPaKeys) >> p.page_shift;
+        if (first / 32 != win) {
+          ++win;
+          cur = nxt;
+          nxt = 32 * (win + 1) + lane < used ? table[32 * (win + 1) + lane] : 0;
+        }
+        const int pages = used - first < per_block ? used - first : per_block;
+        int page = __shfl_sync(0xFFFFFFFFu, cur, (first + lane) & 31);
+        if (page < 0 || page >= p.num_pages) page = 0;  // (reported by the load)
+        const int plane = page * p.Hkv + sg.kvh;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          ok = ok && __all_sync(0xFFFFFFFFu, p8_issued(&s_issued[kv], g));
+          if (ok && lane >= own_pages && lane < pages)
+            tma_load_3d(skv + (st + kv) * C::kEntry + lane * box_rows * D, kv ? &maps.v : &maps.k, 0, 0, plane,
+                        &kv_full[st + kv]);
+        }
+        st += 2;
+        if (st >= stages) st = 0;
+      }
+    }
   } else if (warp < C::kSoftmax) {  // values
     constexpr int kParts = D / 64;  // pieces of 16 columns a warp has
     const int part0 = (warp & 3) * kParts;
@@ -624,8 +682,8 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
       const PaSeg sg = pa_next(p, cum, w);
       if (sg.nblk == 0) break;
       const int len = lens[sg.b], common = pa_common(p, len);
-      if constexpr (C::kQWarps > 1) {
-        queries(sg, si, warp - 4);
+      if (!C::kOwnQ || third) {
+        queries(sg, si, warp - 4, 4 * C::kSets);
         if (!ok) break;
       }
       for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
@@ -846,12 +904,12 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
           }
         }
         if (!ok) break;
-        if (step >= 2u) {  // the product that read the buffer before is done
-          if (!p8_wait(&o_done[step & 1u], ((step - 2u) >> 1) & 1u)) failed = true;
+        if (step >= C::kWs) {  // the product that read the buffer before is done
+          if (!p8_wait(&o_done[(step - C::kWs) & 1u], ((step - C::kWs) >> 1) & 1u)) failed = true;
           __syncwarp();
         }
         if (there) {
-          unsigned char* wrow = sw + ((step & 1u) * kPar + part) * C::kW + row * C::kRowW;
+          unsigned char* wrow = sw + (step % C::kWs * kPar + part) * C::kW + row * C::kRowW;
           const int turn = C::kRowW == 128 ? row & 7 : C::kRowW == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
           const uint64_t vs = at_pair(value_scale, value_scale);
 #pragma unroll
@@ -1022,13 +1080,13 @@ dt_status pa8_pick(Pa8Params& p, const Pa8Maps& maps, WsHeader* hdr, cudaStream_
 #define V16 16, 2, 1, 16
 #endif
 #ifndef V32
-#define V32 32, 2, 1, 32
+#define V32 16, 1, 1, 16
 #endif
 #ifndef V64
 #define V64 32, 1, 1, 32
 #endif
 #ifndef V128
-#define V128 64, 1, 1, 32
+#define V128 32, 1, 1, 16
 #endif
   if (p.R <= 8) return pa8_launch<D, 16, V8>(p, maps, hdr, stream);
   if (p.R <= 16) return pa8_launch<D, 16, V16>(p, maps, hdr, stream);
@@ -1084,9 +1142,11 @@ extern "C" dt_status dt_paged_attention8(int B, int n, int Hq, int Hkv, int d, c
   if (workspace_bytes < P.bytes) return DT_ERR_INVALID_ARG;
   Pa8Params p{};
   p.B = B; p.n = n; p.Hq = Hq; p.Hkv = Hkv; p.G = G; p.R = G * n; p.grid = P.grid;
+  p.extra = kP8Extra;
   p.page_size = page_size; p.num_pages = num_pages; p.max_pages = max_pages;
   while ((1 << p.page_shift) < page_size) ++p.page_shift;
   while ((1 << p.block_shift) < scale_block) ++p.block_shift;
+  p.third = page_size <= 16 ? 1 : 0;
   p.q = static_cast<const unsigned short*>(q);
   p.v_cache = static_cast<const unsigned char*>(v_cache);
   p.k_scale = k_scale; p.v_scale = v_scale;

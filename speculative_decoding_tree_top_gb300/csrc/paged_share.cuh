@@ -1,6 +1,6 @@
 // How the attention kernels over a paged cache share their work among the CTAs, and how cut pairs are joined.
 //
-// The 128-key blocks of all (request, key/value head) pairs, laid end to end with a unit more for each pair, are split
+// The 128-key blocks of all (request, key/value head) pairs, laid end to end with some units more for each pair, are split
 // evenly over the CTAs. A CTA's run inside one pair is a segment; a segment that covers its pair writes the output, the
 // others leave (O, m, l) in the CTA's two partial slots, and the CTA that finishes a cut pair last joins its segments in
 // slot order.
@@ -23,6 +23,7 @@ static_assert(kAtWeightMost * kAtValueMost * DT_PAGED_MAX_TOKENS < 1e38, "a requ
 
 struct PaWork {
   int B, n, Hq, Hkv, G, R, grid;
+  int extra;                       // units of a pair before those of its blocks: what its start and end cost, in blocks
   int page_size, num_pages, max_pages;
   const int32_t* page_table;       // [B][max_pages]
   const int32_t* lens;             // [B]
@@ -32,7 +33,7 @@ struct PaWork {
   unsigned short* out;             // [B][n][Hq][D] bf16
 };
 
-// The lengths' plan. cum[b]: units of one head of the requests before b, a request's being its 128-key blocks and one
+// The lengths' plan. cum[b]: units of one head of the requests before b, a request's being its 128-key blocks and `extra`
 // more; a request whose length is not in [n, max_pages * page_size] has none (0 and below: an unused row of the batch;
 // otherwise an error).
 __device__ __forceinline__ int pa_length(const PaWork& p, int b, bool* bad) {
@@ -56,7 +57,7 @@ __device__ __forceinline__ int pa_owner(long long x, long long W, int grid) {
 }
 struct PaSeg {
   int b, kvh, nb, j0, nblk;  // blocks j0 .. j0 + nblk - 1 of the pair's nb
-  long long pair0;           // the pair's first block in the flattened order (after the pair's extra unit)
+  long long pair0;           // the pair's first block in the flattened order (after the pair's extra units)
 };
 struct PaWalk {  // a CTA's segments, in order
   int b;
@@ -87,13 +88,14 @@ __device__ __forceinline__ PaSeg pa_next(const PaWork& p, const int* cum, PaWalk
     const long long left = w.x1 - w.x;
     const int take = left < units - at ? static_cast<int>(left) : units - at;
     w.x += take;
-    s.nblk = at == 0 ? take - 1 : take;
-    if (s.nblk == 0) continue;  // the share ends behind the pair's extra unit
+    const int skip = at >= p.extra ? 0 : p.extra - at < take ? p.extra - at : take;
+    s.nblk = take - skip;
+    if (s.nblk == 0) continue;  // the share ends among the pair's extra units
     s.b = w.b;
     s.kvh = kvh;
-    s.nb = units - 1;
-    s.j0 = at == 0 ? 0 : at - 1;
-    s.pair0 = start + static_cast<long long>(kvh) * units + 1;
+    s.nb = units - p.extra;
+    s.j0 = at >= p.extra ? at - p.extra : 0;
+    s.pair0 = start + static_cast<long long>(kvh) * units + p.extra;
     break;
   }
   return s;
