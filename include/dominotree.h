@@ -298,7 +298,7 @@ dt_status dt_tree_attention(int B, int n, int L, int Hq, int Hkv, int d, const v
  *               as dt_prompt_attention takes it);
  *   slots, positions [N] int32, or both NULL with N = 0 (pages only). n = 0: N is what the arrays hold, rows behind the
  *               last request's are marked as no tokens.
- *   workspace   dt_page_plan_workspace_bytes(B) bytes, initialised by dt_workspace_init.
+ *   workspace   dt_page_plan_workspace_bytes(B) bytes (the status word), initialised by dt_workspace_init.
  * A request that cannot be served gets no tokens: out_lens[b] = 0, its rows are marked as none, its pages and held[b]
  * stay as they are, and the status word says why. DT_ERR_NO_PAGES: the pool does not hold the pages that it needs (later
  * requests that need pages get none either). DT_ERR_INVALID_ARG: grow[b] negative (or above n > 0), more tokens than

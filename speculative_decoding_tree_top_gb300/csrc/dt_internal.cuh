@@ -25,7 +25,8 @@ struct WsHeader {
   unsigned long long stat_gather_bytes; // correction-row bytes the launch gathered (rows x H x element size)
   unsigned stat_waves;                  // waves run
   unsigned stat_expansions;             // expansions computed (the roots included)
-  unsigned deal_next, deal_done;        // dt_prompt_attention: items dealt out, CTAs through (zero between calls)
+  unsigned deal_next, deal_done;        // dt_prompt_attention: items dealt out, CTAs through (zero between calls);
+                                        // dt_page_plan: CTAs through
   unsigned tickets[kWsTickets / 4];     // dt_paged_attention: by a cut pair's first CTA, a byte each: segments finished
                                         // (zero between calls)
 };

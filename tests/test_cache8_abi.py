@@ -21,7 +21,7 @@ def test_plan_rejects_bad_arguments(dtlib):
                 dict(held=None, free=None), dict(lens=None), dict(grow=None), dict(table=None), dict(lens=A + 2),
                 dict(grow=A + 1), dict(n=5, N=20, depth=A + 2), dict(n=5, N=20, path=A + 2), dict(table=A + 2),
                 dict(held=A + 2), dict(free=A + 1), dict(count=A + 2), dict(out=A + 2), dict(cu=A + 1),
-                dict(slots=A + 2), dict(pos=A + 2), dict(ws=None), dict(ws=A + 8), dict(wsb=256)]:
+                dict(slots=A + 2), dict(pos=A + 2), dict(ws=None), dict(ws=A + 8), dict(wsb=128)]:
         assert call(**bad) == INVALID, bad
     for big in [dict(B=2049), dict(N=(1 << 31) - 1), dict(page=4), dict(page=512), dict(page=24),
                 dict(pages=1 << 28), dict(width=1 << 21)]:
