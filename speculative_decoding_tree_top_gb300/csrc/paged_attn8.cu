@@ -807,6 +807,7 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
         }
         const float value_scale = sees == 0ull ? 0.f : scales.y;
         __syncwarp();
+        const bool fresh = j < kPar;  // a segment's first step: there are no references yet
         // kStep scores from row `r` of the thread's on, scaled, against the reference
         float x[kStep];
         auto load = [&](int r, bool against) {
@@ -836,17 +837,19 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
         };
 #pragma unroll 1
         for (bool raised = false;; raised = true) {
-          float top = -INFINITY;
-          if (there) {
+          if (!fresh) {
+            float top = -INFINITY;
+            if (there) {
 #pragma unroll 1
-            for (int r = 0; r < M; r += kStep) {
-              load(r, true);
+              for (int r = 0; r < M; r += kStep) {
+                load(r, true);
 #pragma unroll
-              for (int i = 0; i < kStep; i += 2) top = at_max3(top, x[i], x[i + 1]);
+                for (int i = 0; i < kStep; i += 2) top = at_max3(top, x[i], x[i + 1]);
+              }
             }
+            if (raised || __builtin_expect(!p8_any<kMeet>(bar, top + log_vs > kP8Most || failed), 1)) break;
           }
-          if (raised || __builtin_expect(!p8_any<kMeet>(bar, top + log_vs > kP8Most || failed), 1)) break;
-          // rare: raise references
+          // a segment's first step, and rarely later: raise references
           if (p8_any<kMeet>(bar, failed)) {
             ok = false;
             break;
@@ -901,6 +904,12 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
               p8_st<kStep>(to + r, o);
             }
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          }
+          if constexpr (C::kSteps > 1) break;  // the scores are loaded again for the weights
+          if (fresh) {
+#pragma unroll
+            for (int i = 0; i < kStep; ++i) x[i] += C::kKeep ? nrefs[i] : s_nref[first + i];
+            break;
           }
         }
         if (!ok) break;
