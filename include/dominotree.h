@@ -410,7 +410,7 @@ dt_status dt_paged_attention(int B, int n, int Hq, int Hkv, int d, const void* q
  * Arithmetic: a query row is brought by a power of two to at most 448 and held in two e4m3 terms (exact but for elements
  * below 2^-9 of the row's largest, which are off by at most 2^-17 of it); codes enter the products as they are; products
  * on the tensor cores, accumulated in fp32. A softmax weight times its value's scale is rounded to fp16, relative to the
- * row's largest such product so far: off by 2^-11 of itself, or by 2^-31 of that largest where that is more. The output is
+ * row's largest such product so far: off by 2^-11 of itself, or by 2^-29 of that largest where that is more. The output is
  * rounded to bf16 once.
  *   k_scale, v_scale [num_pages,Hkv,page_size/scale_block] fp32;  everything else as dt_paged_attention.
  *   workspace   dt_paged_attention8_workspace_bytes(B,n,Hq,Hkv,d) bytes on the current device, initialised by

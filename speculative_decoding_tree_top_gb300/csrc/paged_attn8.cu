@@ -38,7 +38,7 @@ constexpr size_t kPa8SmemCap = 232448 - 11264;  // opt-in shared memory of a CTA
 constexpr int kP8Extra = 4;       // what a pair's start and end cost, in blocks
 // Weights times their values' scales are fp16: a row's largest starts out at 2^kP8Start and may grow to 2^kP8Most before
 // the reference is raised. fp16 goes up to 2^16 and holds subnormal numbers in steps of 2^-24.
-constexpr float kP8Start = 6.f, kP8Most = 14.f;
+constexpr float kP8Start = 4.f, kP8Most = 15.f;
 constexpr float kP8LeastScale = -64.f;  // log2: smaller scales of values do not pull the reference further down
 
 struct Pa8Params : PaWork {
@@ -881,8 +881,16 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
           }
           p8_meet<kMeet>(bar);
           if constexpr (C::kSteps == 1) {
+            if (!fresh) {
 #pragma unroll
-            for (int i = 0; i < M; ++i) l[i] *= s_alpha[first + i];
+              for (int i = 0; i < M; i += 4) {
+                const float4 a = *reinterpret_cast<const float4*>(&s_alpha[first + i]);
+                l[i] *= a.x;
+                l[i + 1] *= a.y;
+                l[i + 2] *= a.z;
+                l[i + 3] *= a.w;
+              }
+            }
           } else {
 #pragma unroll
             for (int i = 0; i < C::kSums; ++i) l[i] *= s_alpha[first + kStep * i + lane / (32 / kStep)];
@@ -900,7 +908,13 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
               float o[kStep];
               p8_ld<kStep>(to + r, o);
 #pragma unroll
-              for (int i = 0; i < kStep; ++i) o[i] *= s_alpha[first + r + i];
+              for (int i = 0; i < kStep; i += 4) {
+                const float4 a = *reinterpret_cast<const float4*>(&s_alpha[first + r + i]);
+                o[i] *= a.x;
+                o[i + 1] *= a.y;
+                o[i + 2] *= a.z;
+                o[i + 3] *= a.w;
+              }
               p8_st<kStep>(to + r, o);
             }
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -908,7 +922,13 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
           if constexpr (C::kSteps > 1) break;  // the scores are loaded again for the weights
           if (fresh) {
 #pragma unroll
-            for (int i = 0; i < kStep; ++i) x[i] += C::kKeep ? nrefs[i] : s_nref[first + i];
+            for (int i = 0; i < kStep; i += 4) {
+              const float4 n4 = *reinterpret_cast<const float4*>(&s_nref[first + i]);
+              x[i] += n4.x;
+              x[i + 1] += n4.y;
+              x[i + 2] += n4.z;
+              x[i + 3] += n4.w;
+            }
             break;
           }
         }

@@ -9,8 +9,8 @@ weights, w_j = p_j times the scale of value j, c_j its code, A = sum_j p_j |v_j|
   off by 2^-10 then, which is 2^-17 of the row's largest. A score is d products twice: off by e = scale ((2 d + 4) 2^-23
   sum |q||k| + 2^-17 max|q| sum |k|), a weight by the factor e + 2^-21 (the approximate exponential), and so is the sum
   that divides: 2 (e + 2^-21) A;
-- w_j to fp16, products in fp32 before it: (2^-11 + 2^-22) A, and where it is a subnormal number 2^-31 of the largest w
-  that is seen (which starts out at 2^6, where a step is 2^-24 at least): 2^-31 max w sum |c_j|;
+- w_j to fp16, products in fp32 before it: (2^-11 + 2^-22) A, and where it is a subnormal number, half a step of 2^-24, the
+  largest w that is seen being 2^4 at least: 2^-29 max w sum |c_j|;
 - the sums over T keys in fp32: 2 T 2^-23 A; the output's rounding to bf16: 2^-8 |out|."""
 import math
 
@@ -71,7 +71,7 @@ def attend8(q, k, v, vs, seen, scale):
     d, T = q.shape[1], k.shape[0]
     e = scale * ((2 * d + 4) * 2.0 ** -23 * (q.abs() @ k.abs().t()) +
                  2.0 ** -17 * q.abs().amax(1, keepdim=True) * k.abs().sum(1)).mul(seen).amax(1, keepdim=True)
-    floor = 2.0 ** -31 * (p * vs).amax(1, keepdim=True) * (seen.double() @ (v.abs() / vs[:, None]))
+    floor = 2.0 ** -29 * (p * vs).amax(1, keepdim=True) * (seen.double() @ (v.abs() / vs[:, None]))
     return out, A * (2 * (e + 2.0 ** -21) + 2.0 ** -11 + 2.0 ** -22 + 2 * T * 2.0 ** -23) + floor + 2.0 ** -8 * out.abs()
 
 
