@@ -284,7 +284,7 @@ struct P8 {
   static constexpr int kSums = kSteps > 1 ? kSteps : M;  // a thread's sums: of its keys and a row each, or of its warp's
   static constexpr bool kKeep = M <= 8;                  // registers for the rows' factors and references
   static constexpr int kOut = M / kPar < 16 ? M / kPar : 16;  // rows of outputs that a thread takes at once
-  static constexpr int kWs = N * kPar <= 64 ? 2 : 1;     // steps whose weights have buffers
+  static constexpr int kWs = 2;                          // steps whose weights have buffers
   static constexpr int kVs = N * kPar <= 64 ? 4 : 2;     // buffers of values
   static constexpr int kOs = N <= 64 ? 2 : 1;            // buffers of outputs
   static constexpr uint32_t kEntry = kPaKeys * D;        // a ring entry: a block's keys or values
@@ -678,15 +678,18 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
         par ^= 1u;
       }
     };
-    for (int si = 0; ok; ++si) {
-      const PaSeg sg = pa_next(p, cum, w);
-      if (sg.nblk == 0) break;
+    // queries, where they are these warps': a segment ahead, when the first buffers are full and nothing else is to do
+    const bool ours = !C::kOwnQ || third;
+    PaSeg sg = pa_next(p, cum, w), next{};
+    if (ours && sg.nblk) queries(sg, 0, warp - 4, 4 * C::kSets);
+    for (int si = 0; ok && sg.nblk; sg = next, ++si) {
       const int len = lens[sg.b], common = pa_common(p, len);
-      if (!C::kOwnQ || third) {
-        queries(sg, si, warp - 4, 4 * C::kSets);
-        if (!ok) break;
-      }
       for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
+        if (j == (sg.nblk > kVs ? kVs : sg.nblk - 1)) {
+          next = pa_next(p, cum, w);
+          if (ours && next.nblk) queries(next, si + 1, warp - 4, 4 * C::kSets);
+          if (!ok) break;
+        }
         if (g % C::kSets != set) {
           advance();
           continue;
@@ -774,8 +777,6 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
       float l[C::kSums], factors[C::kKeep ? M : 4], nrefs[C::kKeep ? M : 4];
 #pragma unroll
       for (int i = 0; i < C::kSums; ++i) l[i] = 0.f;
-      if (mine < M) s_nref[first + mine] = kAtNone;
-      p8_meet<kMeet>(bar);
       for (int j = part; j - part < sg.nblk && ok; j += kPar, g += kPar, ++step) {
         const bool there = j < sg.nblk;  // the step's last block may be missing
         const uint32_t ts = tmem + lanes + C::kS + ((step & 1u) * kPar + part) * N + first;
@@ -850,7 +851,7 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
             if (raised || __builtin_expect(!p8_any<kMeet>(bar, top + log_vs > kP8Most || failed), 1)) break;
           }
           // a segment's first step, and rarely later: raise references
-          if (p8_any<kMeet>(bar, failed)) {
+          if (!fresh && p8_any<kMeet>(bar, failed)) {
             ok = false;
             break;
           }
@@ -873,11 +874,11 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
             float m = s_red[0][r];
 #pragma unroll
             for (int i = 1; i < 4 * kPar; ++i) m = fmaxf(m, s_red[i][r]);
-            const float was = s_nref[r];
+            const float was = fresh ? kAtNone : s_nref[r];
             const bool raise = m + was > kP8Most;
-            const float now = kP8Start - m;
+            const float now = raise ? kP8Start - m : was;
             s_alpha[r] = raise ? at_exp2(now - was) : 1.f;  // from nothing: 0
-            if (raise) s_nref[r] = now;
+            s_nref[r] = now;
           }
           p8_meet<kMeet>(bar);
           if constexpr (C::kSteps == 1) {
@@ -974,12 +975,7 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
       }
       if (!ok) break;
       g -= kPar * ((sg.nblk + kPar - 1) / kPar) - sg.nblk;  // the blocks of the last step that were not there
-      // the segment's outputs
-      if (!p8_wait(&o_done[(step - 1u) & 1u], ((step - 1u) >> 1) & 1u)) failed = true;
-      ok = !p8_any<kMeet>(bar, failed);
-      if (!ok) break;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      // the sums over the keys: by warps, then over the warps
+      // the sums over the keys, while the last product runs: by warps, then over the warps
       if constexpr (C::kSteps == 1) {
         const float sum = p8_warp_sums(l, lane);
         if (lane % (32 / M) == 0) s_red[four][first + lane / (32 / M)] = sum;
@@ -988,7 +984,8 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
         for (int i = 0; i < C::kSums; ++i)
           if (lane % (32 / kStep) == 0) s_red[four][first + kStep * i + lane / (32 / kStep)] = l[i];
       }
-      p8_meet<kMeet>(bar);
+      ok = !p8_any<kMeet>(bar, failed);
+      if (!ok) break;
       const bool whole = sg.nblk == sg.nb;
       const size_t unit = 2 * static_cast<size_t>(blockIdx.x) + (sg.j0 == 0 ? 1 : 0);
       if (mine < M) {
@@ -1008,7 +1005,10 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
           *reinterpret_cast<float2*>(p.ml + 2 * (unit * p.R + r)) = make_float2(nref == kAtNone ? -INFINITY : -nref, sum);
         }
       }
-      p8_meet<kMeet>(bar);
+      if (!p8_wait(&o_done[(step - 1u) & 1u], ((step - 1u) >> 1) & 1u)) failed = true;
+      ok = !p8_any<kMeet>(bar, failed);
+      if (!ok) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       unsigned short* out = p.out + (static_cast<size_t>(sg.b) * p.n * p.Hq + sg.kvh * p.G) * D + (column & ~1);
       float* partial = p.part + unit * p.R * D + (column & ~1);
       const bool bad = *reinterpret_cast<volatile int*>(&s_bad) > si;  // (a later segment's mark counts too: only slower)
@@ -1048,8 +1048,9 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
           else *reinterpret_cast<float2*>(partial + r * D) = make_float2(lo, hi);
         }
       }
-      p8_meet<kMeet>(bar);  // everyone is through with the segment's factors, mask and outputs
-      if (lane == 0) mbar_arrive(&o_free[qb]);
+      // (what the next segment's raise writes is behind its first meeting, and that behind this)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_free[qb]);  // through with the segment's factors, mask and outputs
       if (whole) continue;
       // the pair's last segment to finish joins them all, once the CTA is through its share
       const int c0 = pa_owner(sg.pair0, W, ctas), c1 = pa_owner(sg.pair0 + sg.nb - 1, W, ctas);
@@ -1093,8 +1094,8 @@ dt_status pa8_launch(Pa8Params& p, const Pa8Maps& maps, WsHeader* hdr, cudaStrea
   using C = P8<D, N, M, kPar_, kSets_, kStep_>;
   const size_t fixed = C::kFixed + align_up(sizeof(int) * (2 * p.B + 1), 16);
   const int fit = static_cast<int>((kPa8SmemCap - fixed) / C::kEntry);
-  // a multiple of four: a slot then always holds keys or always values, and always the same set's
-  p.stages = (fit > kP8MaxStages ? kP8MaxStages : fit) & ~3;
+  // an even number: a slot then always holds keys or always values
+  p.stages = (fit > kP8MaxStages ? kP8MaxStages : fit) & ~1;
   const size_t smem = fixed + static_cast<size_t>(p.stages) * C::kEntry;
   if (ensure_dynamic_smem(reinterpret_cast<const void*>(paged_attn8_kernel<D, N, M, kPar_, kSets_, kStep_>), kPa8SmemCap) != cudaSuccess)
     return DT_ERR_CUDA;
@@ -1109,10 +1110,10 @@ dt_status pa8_pick(Pa8Params& p, const Pa8Maps& maps, WsHeader* hdr, cudaStream_
 #define V16 16, 2, 1, 16
 #endif
 #ifndef V32
-#define V32 16, 1, 1, 16
+#define V32 16, 2, 1, 8
 #endif
 #ifndef V64
-#define V64 32, 1, 1, 32
+#define V64 32, 2, 1, 16
 #endif
 #ifndef V128
 #define V128 32, 1, 1, 16
