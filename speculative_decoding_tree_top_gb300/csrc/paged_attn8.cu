@@ -103,30 +103,6 @@ __device__ __forceinline__ void p8_st<16>(uint32_t taddr, const float* v) {
         "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
       : "memory");
 }
-template <>
-__device__ __forceinline__ void p8_ld<32>(uint32_t taddr, float* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%1"
-      "7,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
-        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
-        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
-        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-      : "r"(taddr)
-      : "memory");
-}
-template <>
-__device__ __forceinline__ void p8_st<32>(uint32_t taddr, const float* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%"
-      "17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
-        "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]),
-        "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]),
-        "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
-      : "memory");
-}
 // 16 lanes x 64 columns: in each group of 4 columns thread l holds column l % 4 of lanes l / 4 and l / 4 + 8.
 __device__ __forceinline__ void p8_st_v(uint32_t taddr, const uint32_t* v) {  // 64 columns of two fp16
   asm volatile(
@@ -142,6 +118,11 @@ __device__ __forceinline__ uint32_t p8_two(uint32_t codes) {  // the two e4m3 co
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
   return r;
+}
+__device__ __forceinline__ void p8_four(uint32_t codes, uint32_t& lo, uint32_t& hi) {  // those of both halves
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
 }
 __device__ __forceinline__ uint32_t p8_code2(float lo, float hi) {
   uint16_t r;
@@ -267,21 +248,22 @@ __device__ __forceinline__ uint32_t p8_piece(int r, int c) {
                   : static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-// The shape of one instance: N columns of query rows (R rounded up), of which a softmax thread has M for its key.
-// Measured, M rows a thread against twice as many: TODO
-template <int D, int N, int M, int kPar_, int kSets_, int kStep_>
+// The shape of one instance: N columns of query rows (R rounded up), of which a softmax thread has M for its key, kStep at
+// a time, in each of its blocks: kPar blocks are a step.
+template <int D, int N, int M, int kPar_, int kStep_>
 struct P8 {
   static constexpr int kPar = kPar_;                     // blocks of a step: the softmax takes them at once
   static constexpr int kRowGroups = N > 16 ? N / M : 1;  // groups of four softmax warps share a block's rows
   static constexpr int kGroups = kPar * kRowGroups;
   static constexpr int kMeet = 128 * kPar;               // softmax threads that have the same rows
-  static constexpr int kSets = kSets_;                   // sets of four warps for the values: they take blocks in turn
-  static constexpr int kSoftmax = 4 + 4 * kSets;         // warps 0, 2, 3: load, 1: MMA, 4 on: values, then softmax
+  static constexpr int kSoftmax = 8;                     // warps 0, 2, 3: load, 1: MMA, 4-7: values, then softmax
   static constexpr int kThreads = 32 * kSoftmax + 128 * kGroups;
   static constexpr bool kOwnQ = N <= 16;                 // a warp of its own for the queries, unless it is wanted for boxes
   static constexpr int kStep = kStep_;                   // rows taken at once
   static constexpr int kSteps = M / kStep;
-  static constexpr int kSums = kSteps > 1 ? kSteps : M;  // a thread's sums: of its keys and a row each, or of its warp's
+  // a thread's sums: of its key and a row each, or, without the registers for so many, of its warp's keys
+  static constexpr bool kWarpSums = M > 16;
+  static constexpr int kSums = kWarpSums ? kSteps : M;
   static constexpr bool kKeep = M <= 8;                  // registers for the rows' factors and references
   static constexpr int kOut = M / kPar < 16 ? M / kPar : 16;  // rows of outputs that a thread takes at once
   static constexpr int kWs = 2;                          // steps whose weights have buffers
@@ -299,15 +281,16 @@ struct P8 {
   static constexpr size_t kFixed = 1024 + 2 * kQ + kWs * kPar * kW;
 };
 
-// Roles. Load: pages to the ring, as in the bf16 kernel, and their scales, keys and values by a warp each, and a
-// third where a block spans pages (a box takes its warp about a hundred cycles to issue). Values: lane =
+// Roles. Load: pages to the ring, as in the bf16 kernel, and their scales, keys and values by a warp each, and some of
+// both by a third where a block spans many pages (a box takes its warp about a hundred cycles to issue). Values: lane =
 // column, two keys a register. Softmax: lane = key; its scales come with the keys (loaded by the softmax itself a block
 // ahead they are late: a block takes less than a load). MMA: the scores run one step ahead of the outputs, through the
-// segments.
-template <int D, int N, int M, int kPar_, int kSets_, int kStep_>
-__global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 1)
+// segments. Queries: by the third warp of loads where there are few rows and it is not wanted for boxes, else by the
+// warps of the values, a segment ahead.
+template <int D, int N, int M, int kPar_, int kStep_>
+__global__ void __launch_bounds__(P8<D, N, M, kPar_, kStep_>::kThreads, 1)
     paged_attn8_kernel(Pa8Params p, const __grid_constant__ Pa8Maps maps, WsHeader* hdr) {
-  using C = P8<D, N, M, kPar_, kSets_, kStep_>;
+  using C = P8<D, N, M, kPar_, kStep_>;
   constexpr int kThreads = C::kThreads, kPar = C::kPar, kMeet = C::kMeet, kStep = C::kStep, kVs = C::kVs, kOs = C::kOs;
   extern __shared__ float4 smem_f4[];
   unsigned char* sq =
@@ -344,7 +327,7 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
       mbar_init(&s_full[i], 1);
       mbar_init(&w_full[i], 4 * C::kGroups);
       mbar_init(&o_done[i], 1);
-      mbar_init(&q_full[i], C::kOwnQ && p.third == 0 ? 1 : 4 * C::kSets);
+      mbar_init(&q_full[i], C::kOwnQ && p.third == 0 ? 1 : 4);
       mbar_init(&o_free[i], 4 * C::kGroups);
     }
     mbar_init(&s_meet, 4 * C::kGroups);
@@ -408,85 +391,85 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
   const int own_pages = third ? p8_own_pages(kPaKeys >> p.page_shift) : kPaKeys;
   auto queries = [&](const PaSeg& sg, int si, int who, int of) {
     const unsigned qb = static_cast<unsigned>(si) & 1u;
-      // the segment that had the buffer before is over: its factors and its mask are not read any more
-      if (si >= 2) ok = __all_sync(0xFFFFFFFFu, p8_rest(&o_free[qb], static_cast<unsigned>((si >> 1) - 1) & 1u));
+    // the segment that had the buffer before is over: its factors and its mask are not read any more
+    if (si >= 2) ok = __all_sync(0xFFFFFFFFu, p8_rest(&o_free[qb], static_cast<unsigned>((si >> 1) - 1) & 1u));
     if (!ok) return;
 #pragma unroll 1
-      for (int c = 32 * who + lane; c < p.n; c += 32 * of) {
-        unsigned long long bits = ~0ull << c;
-        if (p.mask) {
-          const uint8_t* col = p.mask + static_cast<size_t>(sg.b) * p.n * p.n + c;
-          bits = 0ull;
+    for (int c = 32 * who + lane; c < p.n; c += 32 * of) {
+      unsigned long long bits = ~0ull << c;
+      if (p.mask) {
+        const uint8_t* col = p.mask + static_cast<size_t>(sg.b) * p.n * p.n + c;
+        bits = 0ull;
 #pragma unroll 8
-          for (int i = 0; i < p.n; ++i) bits |= static_cast<unsigned long long>(col[static_cast<size_t>(i) * p.n] != 0) << i;
-        }
-        s_sees[qb][c] = bits;
+        for (int i = 0; i < p.n; ++i) bits |= static_cast<unsigned long long>(col[static_cast<size_t>(i) * p.n] != 0) << i;
       }
-      unsigned char* qd = sq + qb * C::kQ;
-      // eight lanes a row, D / 8 elements each; four rows a step, several steps' loads in flight
-      constexpr int kEach = D / 8, kAtOnce = 4;
-      const int sub = lane & 7;
-      const unsigned short* src = p.q + (static_cast<size_t>(sg.b) * p.n * p.Hq + sg.kvh * p.G) * D + kEach * sub;
+      s_sees[qb][c] = bits;
+    }
+    unsigned char* qd = sq + qb * C::kQ;
+    // eight lanes a row, D / 8 elements each; four rows a step, several steps' loads in flight
+    constexpr int kEach = D / 8, kAtOnce = 4;
+    const int sub = lane & 7;
+    const unsigned short* src = p.q + (static_cast<size_t>(sg.b) * p.n * p.Hq + sg.kvh * p.G) * D + kEach * sub;
 #pragma unroll 1
-      for (int r0 = 4 * kAtOnce * who; r0 < p.R; r0 += 4 * kAtOnce * of) {
-        uint4 x[kAtOnce][kEach / 8];
+    for (int r0 = 4 * kAtOnce * who; r0 < p.R; r0 += 4 * kAtOnce * of) {
+      uint4 x[kAtOnce][kEach / 8];
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-          const int r = r0 + 4 * u + (lane >> 3);
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int r = r0 + 4 * u + (lane >> 3);
 #pragma unroll
-          for (int i = 0; i < kEach / 8; ++i)
-            x[u][i] = r < p.R ? *reinterpret_cast<const uint4*>(src + s_at[r] + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < kEach / 8; ++i)
+          x[u][i] = r < p.R ? *reinterpret_cast<const uint4*>(src + s_at[r] + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        if (r0 + 4 * u >= p.R) break;
+        const int r = r0 + 4 * u + (lane >> 3);
+        const uint32_t* bits = reinterpret_cast<const uint32_t*>(x[u]);
+        unsigned most = 0u;  // the bits of the row's largest finite element, as a bf16
+#pragma unroll
+        for (int i = 0; i < kEach / 2; ++i) {
+          const unsigned lo = bits[i] & 0x7FFFu, hi = (bits[i] >> 16) & 0x7FFFu;
+          if (lo < 0x7F80u && lo > most) most = lo;
+          if (hi < 0x7F80u && hi > most) most = hi;
         }
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-          if (r0 + 4 * u >= p.R) break;
-          const int r = r0 + 4 * u + (lane >> 3);
-          const uint32_t* bits = reinterpret_cast<const uint32_t*>(x[u]);
-          unsigned most = 0u;  // the bits of the row's largest finite element, as a bf16
+        for (int h = 4; h > 0; h >>= 1) {
+          const unsigned other = __shfl_xor_sync(0xFFFFFFFFu, most, h);
+          most = other > most ? other : most;
+        }
+        // the largest power of two that leaves it at 448 = 1.75 2^8 or less
+        int up = ((most & 0x7Fu) > 0x60u ? 7 : 8) - (static_cast<int>(most >> 7) - 127);
+        if (up > 100) up = 100;  // (nothing is lost: such a row's scores are zero whatever the keys are)
+        const float by = __uint_as_float(static_cast<unsigned>(up + 127) << 23);
+        uint32_t q1[kEach / 4], q2[kEach / 4];
 #pragma unroll
-          for (int i = 0; i < kEach / 2; ++i) {
-            const unsigned lo = bits[i] & 0x7FFFu, hi = (bits[i] >> 16) & 0x7FFFu;
-            if (lo < 0x7F80u && lo > most) most = lo;
-            if (hi < 0x7F80u && hi > most) most = hi;
-          }
+        for (int i = 0; i < kEach / 4; ++i) q1[i] = q2[i] = 0u;
 #pragma unroll
-          for (int h = 4; h > 0; h >>= 1) {
-            const unsigned other = __shfl_xor_sync(0xFFFFFFFFu, most, h);
-            most = other > most ? other : most;
+        for (int i = 0; i < kEach / 2; ++i) {
+          const float a = __uint_as_float(bits[i] << 16) * by, b = __uint_as_float(bits[i] & 0xFFFF0000u) * by;
+          const float a1 = fabsf(a) <= 448.f ? a : NAN, b1 = fabsf(b) <= 448.f ? b : NAN;
+          const uint32_t c = p8_code2(a1, b1), two = p8_two(c);
+          const float2 got = __half22float2(*reinterpret_cast<const __half2*>(&two));
+          q1[i / 2] |= c << (16 * (i & 1));
+          q2[i / 2] |= p8_code2(a1 - got.x, b1 - got.y) << (16 * (i & 1));
+        }
+        if (r < p.R) {
+          if constexpr (D == 128) {
+            unsigned char* at = qd + p8_piece<D>(r, sub);
+            *reinterpret_cast<uint4*>(at) = make_uint4(q1[0], q1[1], q1[kEach / 4 - 2], q1[kEach / 4 - 1]);
+            *reinterpret_cast<uint4*>(at + C::kTerm) = make_uint4(q2[0], q2[1], q2[kEach / 4 - 2], q2[kEach / 4 - 1]);
+          } else {
+            unsigned char* at = qd + p8_piece<D>(r, sub >> 1) + 8 * (sub & 1);
+            *reinterpret_cast<uint2*>(at) = make_uint2(q1[0], q1[1]);
+            *reinterpret_cast<uint2*>(at + C::kTerm) = make_uint2(q2[0], q2[1]);
           }
-          // the largest power of two that leaves it at 448 = 1.75 2^8 or less
-          int up = ((most & 0x7Fu) > 0x60u ? 7 : 8) - (static_cast<int>(most >> 7) - 127);
-          if (up > 100) up = 100;  // (nothing is lost: such a row's scores are zero whatever the keys are)
-          const float by = __uint_as_float(static_cast<unsigned>(up + 127) << 23);
-          uint32_t q1[kEach / 4], q2[kEach / 4];
-#pragma unroll
-          for (int i = 0; i < kEach / 4; ++i) q1[i] = q2[i] = 0u;
-#pragma unroll
-          for (int i = 0; i < kEach / 2; ++i) {
-            const float a = __uint_as_float(bits[i] << 16) * by, b = __uint_as_float(bits[i] & 0xFFFF0000u) * by;
-            const float a1 = fabsf(a) <= 448.f ? a : NAN, b1 = fabsf(b) <= 448.f ? b : NAN;
-            const uint32_t c = p8_code2(a1, b1), two = p8_two(c);
-            const float2 got = __half22float2(*reinterpret_cast<const __half2*>(&two));
-            q1[i / 2] |= c << (16 * (i & 1));
-            q2[i / 2] |= p8_code2(a1 - got.x, b1 - got.y) << (16 * (i & 1));
-          }
-          if (r < p.R) {
-            if constexpr (D == 128) {
-              unsigned char* at = qd + p8_piece<D>(r, sub);
-              *reinterpret_cast<uint4*>(at) = make_uint4(q1[0], q1[1], q1[kEach / 4 - 2], q1[kEach / 4 - 1]);
-              *reinterpret_cast<uint4*>(at + C::kTerm) = make_uint4(q2[0], q2[1], q2[kEach / 4 - 2], q2[kEach / 4 - 1]);
-            } else {
-              unsigned char* at = qd + p8_piece<D>(r, sub >> 1) + 8 * (sub & 1);
-              *reinterpret_cast<uint2*>(at) = make_uint2(q1[0], q1[1]);
-              *reinterpret_cast<uint2*>(at + C::kTerm) = make_uint2(q2[0], q2[1]);
-            }
-            if (sub == 0) s_factor[qb][r] = p.scale_log2 * __uint_as_float(static_cast<unsigned>(127 - up) << 23);
-          }
+          if (sub == 0) s_factor[qb][r] = p.scale_log2 * __uint_as_float(static_cast<unsigned>(127 - up) << 23);
         }
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads Q through the async proxy
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[qb]);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads Q through the async proxy
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&q_full[qb]);
   };
 
   if (warp == 0 || warp == 2) {  // load: the keys, the values; the whole warp, one page's box a lane
@@ -669,30 +652,18 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
     constexpr int kParts = D / 64;  // pieces of 16 columns a warp has
     const int part0 = (warp & 3) * kParts;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const unsigned set = static_cast<unsigned>(warp - 4) >> 2;
     unsigned g = 0, at = 1, par = 0;
-    auto advance = [&] {
-      at += 2;
-      if (at > stages) {
-        at = 1;
-        par ^= 1u;
-      }
-    };
     // queries, where they are these warps': a segment ahead, when the first buffers are full and nothing else is to do
     const bool ours = !C::kOwnQ || third;
     PaSeg sg = pa_next(p, cum, w), next{};
-    if (ours && sg.nblk) queries(sg, 0, warp - 4, 4 * C::kSets);
+    if (ours && sg.nblk) queries(sg, 0, warp - 4, 4);
     for (int si = 0; ok && sg.nblk; sg = next, ++si) {
       const int len = lens[sg.b], common = pa_common(p, len);
       for (int j = 0; j < sg.nblk && ok; ++j, ++g) {
         if (j == (sg.nblk > kVs ? kVs : sg.nblk - 1)) {
           next = pa_next(p, cum, w);
-          if (ours && next.nblk) queries(next, si + 1, warp - 4, 4 * C::kSets);
+          if (ours && next.nblk) queries(next, si + 1, warp - 4, 4);
           if (!ok) break;
-        }
-        if (g % C::kSets != set) {
-          advance();
-          continue;
         }
         const unsigned vb = g % kVs;
         const int kbase = (sg.j0 + j) * kPaKeys;
@@ -742,8 +713,7 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
               const uint32_t y = __byte_perm(x[m], 0u, 0x3120);  // two keys of a column, then of the next
-              r[2 * (4 * kk + m)] = p8_two(y);
-              r[2 * (4 * kk + m) + 1] = p8_two(y >> 16);
+              p8_four(y, r[2 * (4 * kk + m)], r[2 * (4 * kk + m) + 1]);
             }
           }
           p8_st_v(tmem + lanes + (static_cast<uint32_t>(16 * h) << 16) + C::kV + vb * 64u, r);
@@ -754,7 +724,11 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&v_full[vb]);
-        advance();
+        at += 2;
+        if (at > stages) {
+          at = 1;
+          par ^= 1u;
+        }
       }
     }
   } else {  // softmax
@@ -881,20 +855,18 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
             s_nref[r] = now;
           }
           p8_meet<kMeet>(bar);
-          if constexpr (C::kSteps == 1) {
-            if (!fresh) {
-#pragma unroll
-              for (int i = 0; i < M; i += 4) {
-                const float4 a = *reinterpret_cast<const float4*>(&s_alpha[first + i]);
-                l[i] *= a.x;
-                l[i + 1] *= a.y;
-                l[i + 2] *= a.z;
-                l[i + 3] *= a.w;
-              }
-            }
-          } else {
+          if constexpr (C::kWarpSums) {
 #pragma unroll
             for (int i = 0; i < C::kSums; ++i) l[i] *= s_alpha[first + kStep * i + lane / (32 / kStep)];
+          } else if (!fresh) {
+#pragma unroll
+            for (int i = 0; i < M; i += 4) {
+              const float4 a = *reinterpret_cast<const float4*>(&s_alpha[first + i]);
+              l[i] *= a.x;
+              l[i + 1] *= a.y;
+              l[i + 2] *= a.z;
+              l[i + 3] *= a.w;
+            }
           }
           if constexpr (C::kKeep) {
 #pragma unroll
@@ -950,16 +922,16 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
 #pragma unroll
             for (int i = 0; i < kStep; i += 2) {
               float a = at_exp2(x[i]), b = at_exp2(x[i + 1]);
-              if constexpr (C::kSteps == 1) {
-                at_unpair(at_add2(at_pair(l[i], l[i + 1]), at_pair(a, b)), l[i], l[i + 1]);
-              } else {
+              if constexpr (C::kWarpSums) {
                 sums[i] = a;
                 sums[i + 1] = b;
+              } else {
+                at_unpair(at_add2(at_pair(l[r + i], l[r + i + 1]), at_pair(a, b)), l[r + i], l[r + i + 1]);
               }
               at_unpair(p8_mul2(at_pair(a, b), vs), a, b);
               h[i / 2] = p8_pack(a, b);
             }
-            if constexpr (C::kSteps > 1) l[r / kStep] += p8_warp_sums(sums, lane);
+            if constexpr (C::kWarpSums) l[r / kStep] += p8_warp_sums(sums, lane);
 #pragma unroll
             for (int c = 0; c < kStep / 8; ++c) {
               const int at = first + r + 8 * c, atom = at / C::kAtom, piece = at % C::kAtom / 8;
@@ -976,13 +948,13 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
       if (!ok) break;
       g -= kPar * ((sg.nblk + kPar - 1) / kPar) - sg.nblk;  // the blocks of the last step that were not there
       // the sums over the keys, while the last product runs: by warps, then over the warps
-      if constexpr (C::kSteps == 1) {
-        const float sum = p8_warp_sums(l, lane);
-        if (lane % (32 / M) == 0) s_red[four][first + lane / (32 / M)] = sum;
-      } else {
+      if constexpr (C::kWarpSums) {
 #pragma unroll
         for (int i = 0; i < C::kSums; ++i)
           if (lane % (32 / kStep) == 0) s_red[four][first + kStep * i + lane / (32 / kStep)] = l[i];
+      } else {
+        const float sum = p8_warp_sums(l, lane);
+        if (lane % (32 / M) == 0) s_red[four][first + lane / (32 / M)] = sum;
       }
       ok = !p8_any<kMeet>(bar, failed);
       if (!ok) break;
@@ -1089,40 +1061,37 @@ __global__ void __launch_bounds__(P8<D, N, M, kPar_, kSets_, kStep_>::kThreads, 
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
-template <int D, int N, int M, int kPar_, int kSets_, int kStep_>
+template <int D, int N, int M, int kPar_, int kStep_>
 dt_status pa8_launch(Pa8Params& p, const Pa8Maps& maps, WsHeader* hdr, cudaStream_t stream) {
-  using C = P8<D, N, M, kPar_, kSets_, kStep_>;
+  using C = P8<D, N, M, kPar_, kStep_>;
   const size_t fixed = C::kFixed + align_up(sizeof(int) * (2 * p.B + 1), 16);
   const int fit = static_cast<int>((kPa8SmemCap - fixed) / C::kEntry);
   // an even number: a slot then always holds keys or always values
   p.stages = (fit > kP8MaxStages ? kP8MaxStages : fit) & ~1;
   const size_t smem = fixed + static_cast<size_t>(p.stages) * C::kEntry;
-  if (ensure_dynamic_smem(reinterpret_cast<const void*>(paged_attn8_kernel<D, N, M, kPar_, kSets_, kStep_>), kPa8SmemCap) != cudaSuccess)
+  if (ensure_dynamic_smem(reinterpret_cast<const void*>(paged_attn8_kernel<D, N, M, kPar_, kStep_>), kPa8SmemCap) != cudaSuccess)
     return DT_ERR_CUDA;
-  return at_launch(paged_attn8_kernel<D, N, M, kPar_, kSets_, kStep_>, p.grid, C::kThreads, smem, stream, p, maps, hdr);
+  return at_launch(paged_attn8_kernel<D, N, M, kPar_, kStep_>, p.grid, C::kThreads, smem, stream, p, maps, hdr);
 }
+// By the rows R = G n that share a head. Columns of the products: the next of 16, 32, 64 and 128 (16 is what the weights'
+// layout allows). Softmax: two blocks a step wherever tensor memory holds two steps of their scores (not beside 128 rows),
+// because a step waits more than it computes; and so many rows a thread that its warps find their registers. Measured in
+// us, 32 query and 8 key/value heads, pages of 64, lengths from a 32nd of the largest up, D = 128 and D = 64:
+//   R <= 8 (64 requests of up to 8191 keys): two blocks a step 92.9 and 74; one 94.1 and 82.8
+//   R <= 16 (3 nodes each, up to 4099): two blocks, eight rows at once 64.4 and 57.1; sixteen 66.8 and 67.7; four blocks
+//     69.3 and 63.8
+//   R <= 32 (8 nodes): two blocks, 16 rows a thread 80.9 and 74.5; one block 95.8 and 86.5; 32 rows a thread 82.8 and 83.8
+//   R <= 64 (16 nodes): two blocks, 32 rows a thread, sixteen at once 113.5 and 101.5; eight at once 115.1 and 107.3; one
+//     block 120.0 and 116.1; 16 rows a thread 139.8 and 131.4
+//   R <= 128 (32 requests of 32 nodes, D = 128): 32 rows a thread, sixteen at once 104; in an earlier form 134, with 64 rows
+//     a thread 148
 template <int D>
 dt_status pa8_pick(Pa8Params& p, const Pa8Maps& maps, WsHeader* hdr, cudaStream_t stream) {
-#ifndef V8
-#define V8 8, 2, 1, 8
-#endif
-#ifndef V16
-#define V16 16, 2, 1, 16
-#endif
-#ifndef V32
-#define V32 16, 2, 1, 8
-#endif
-#ifndef V64
-#define V64 32, 2, 1, 16
-#endif
-#ifndef V128
-#define V128 32, 1, 1, 16
-#endif
-  if (p.R <= 8) return pa8_launch<D, 16, V8>(p, maps, hdr, stream);
-  if (p.R <= 16) return pa8_launch<D, 16, V16>(p, maps, hdr, stream);
-  if (p.R <= 32) return pa8_launch<D, 32, V32>(p, maps, hdr, stream);
-  if (p.R <= 64) return pa8_launch<D, 64, V64>(p, maps, hdr, stream);
-  return pa8_launch<D, 128, V128>(p, maps, hdr, stream);
+  if (p.R <= 8) return pa8_launch<D, 16, 8, 2, 8>(p, maps, hdr, stream);
+  if (p.R <= 16) return pa8_launch<D, 16, 16, 2, 8>(p, maps, hdr, stream);
+  if (p.R <= 32) return pa8_launch<D, 32, 16, 2, 8>(p, maps, hdr, stream);
+  if (p.R <= 64) return pa8_launch<D, 64, 32, 2, 16>(p, maps, hdr, stream);
+  return pa8_launch<D, 128, 32, 1, 16>(p, maps, hdr, stream);
 }
 
 }  // namespace
