@@ -305,7 +305,8 @@ dt_status dt_tree_attention(int B, int n, int L, int Hq, int Hkv, int d, const v
  * max_pages pages hold, fewer pages held than lens[b] needs, or rows behind N; and a row whose page lies outside the
  * pool. A pool that contradicts itself (free_count out of range, more pages given back than there is room for) sets
  * DT_ERR_INVALID_ARG and no page moves.
- * No array may overlap another. B <= DT_PAGED_MAX_BATCH; page sizes, pool and max_pages as dt_paged_attention.
+ * No array may overlap another, but out_lens may be lens or grow. B <= DT_PAGED_MAX_BATCH; page sizes, pool and max_pages
+ * as dt_paged_attention.
  * ------------------------------------------------------------------------------------------------------------- */
 size_t dt_page_plan_workspace_bytes(int B);
 dt_status dt_page_plan(int B, int n, int N, int page_size, int num_pages, int max_pages, const int32_t* lens,

@@ -12,7 +12,7 @@
 //
 // Bound by latency: a few hundred bytes to a few hundred kilobytes. Every CTA scans all requests (two a thread, all in
 // shared memory) and does its part of the moves and of the rows; nothing that it reads is written by another, but for the
-// state's counts, which the last CTA to finish writes.
+// lengths and the state's counts, which the last CTA to finish writes.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -206,7 +206,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(PlanParams p
     s.held[b] = held[k];
     s.base[b] = served ? len[k] : -1;
     s.tokens[b] = tokens[k];
-    if (first_cta && p.out_lens) p.out_lens[b] = served ? len[k] + tokens[k] : 0;
     if (first_cta && p.cu) p.cu[b] = s.rows[b];
   }
   if (t == 0) {
@@ -224,8 +223,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(PlanParams p
       p.free_pages[s.count + m] = plan_given(p, s, s.given - 1 - static_cast<int>(m));
   }
   for (long long row = own; row < p.N; row += step) plan_row(p, s, static_cast<int>(row), hdr);
-  if (!pool || !sound) return;
-  // the state's counts, when every CTA has read them
+  // the lengths, which may take the old ones' place, and the state's counts, when every CTA has read them
   if (gridDim.x > 1) {
     __syncthreads();
     if (t == 0) s_last = atom_add_acq_rel_gpu(&hdr->deal_done, 1u) + 1u == gridDim.x;
@@ -236,9 +234,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(PlanParams p
     __syncthreads();
   }
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-    if (2 * t + k < p.B && s.base[2 * t + k] >= 0) p.held[2 * t + k] = want[k];
-  if (t == 0) p.free_count[0] = s.count + s.given - taken;
+  for (int k = 0; k < 2; ++k) {
+    const int b = 2 * t + k;
+    if (b >= p.B) continue;
+    const bool served = s.base[b] >= 0;
+    if (p.out_lens) p.out_lens[b] = served ? len[k] + tokens[k] : 0;
+    if (pool && sound && served) p.held[b] = want[k];
+  }
+  if (t == 0 && pool && sound) p.free_count[0] = s.count + s.given - taken;
 }
 
 }  // namespace

@@ -374,14 +374,20 @@ def dt_page_plan(lens: torch.Tensor, grow: torch.Tensor, page_table: torch.Tenso
     else:
         rows = 0
 
-    def opt(t, name, shape):
-        return None if t is None else _on(t, name, dev, i32, shape)
+    out_lens, cu, positions = out.get("lens"), out.get("cu_seqlens"), out.get("positions")
+    many, nodes = (B,), (B, n)
     status = lib().dt_page_plan(
-        B, n, rows, page_size, num_pages, max_pages, _on(lens, "lens", dev, i32, (B,)), _on(grow, "grow", dev, i32, (B,)),
-        opt(depth, "depth", (B, n)), opt(path, "path", (B, n)), _on(page_table, "page_table", dev, i32, (B, max_pages)),
-        opt(held, "held", (B,)), opt(free_pages, "free_pages", (num_pages,)), opt(free_count, "free_count", (1,)),
-        opt(out.get("lens"), "out lens", (B,)), opt(out.get("cu_seqlens"), "cu_seqlens", (B + 1,)),
-        opt(slots, "slots", (rows,)), opt(out.get("positions"), "positions", (rows,)), *_room(workspace, dev),
+        B, n, rows, page_size, num_pages, max_pages, _on(lens, "lens", dev, i32, many), _on(grow, "grow", dev, i32, many),
+        None if depth is None else _on(depth, "depth", dev, i32, nodes),
+        None if path is None else _on(path, "path", dev, i32, nodes),
+        _on(page_table, "page_table", dev, i32, (B, max_pages)),
+        None if held is None else _on(held, "held", dev, i32, many),
+        None if free_pages is None else _on(free_pages, "free_pages", dev, i32, (num_pages,)),
+        None if free_count is None else _on(free_count, "free_count", dev, i32, (1,)),
+        None if out_lens is None else _on(out_lens, "out lens", dev, i32, many),
+        None if cu is None else _on(cu, "cu_seqlens", dev, i32, (B + 1,)),
+        None if slots is None else _on(slots, "slots", dev, i32, (rows,)),
+        None if positions is None else _on(positions, "positions", dev, i32, (rows,)), *_room(workspace, dev),
         _raw(stream, dev))
     if status:
         raise DTError(status, "dt_page_plan")

@@ -159,7 +159,8 @@ SHAPES = [
     (65, 3, 3, 128, 128, 32, 48, False, True, False),
     (2500, 40, 8, 128, 64, 16, 128, False, True, False),   # tokens found through the index
     (2500, 12, 2, 64, 256, 128, 64, False, True, True),
-    (2048, 4, 1, 64, 16, 16, 64, False, True, False), (2049, 4, 1, 64, 16, 16, 64, False, True, False),  # the border
+    (2048, 4, 1, 64, 16, 16, 64, False, True, False), (2049, 4, 1, 64, 16, 16, 64, False, True, False),
+    (512, 4, 1, 64, 16, 16, 64, False, True, False), (513, 4, 1, 64, 16, 16, 64, False, True, False),  # the border
 ]
 
 
@@ -349,6 +350,26 @@ def test_far_into_a_large_pool(dtlib):
             scale = s[at, :, row // 16].double()[..., None]
             got = c.view(torch.uint8)[at, :, row].view(F8).double()
             assert torch.equal(got, to_f8(x.double() / scale).double())
+
+
+def test_two_calls_at_once(dtlib):
+    """Two streams, two caches, a workspace each: tokens found by a look at all of them, and through the index."""
+    calls = []
+    for N, seed in ((200, 3), (5000, 4)):
+        _, k, v, kc, _, slots, _ = make(N, 4, 2, 64, 16, 0, seed=seed)
+        (kc, ks), (vc, vs) = (pool(kc.shape[0], 2, 16, 64, 16, seed + i) for i in (1, 2))
+        ws = dtlib.new_workspace(dtlib.dt_kv_append8_workspace_bytes(N, kc.shape[0], 16))
+        want = [x.clone() for x in (kc, vc, ks, vs)]
+        for _ in range(5):
+            dtlib.dt_kv_append8(k, v, *want, slots)
+        calls.append((k, v, (kc, vc, ks, vs), slots, ws, want, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for k, v, cache, slots, ws, _, stream in calls:
+            dtlib.dt_kv_append8(k, v, *cache, slots, workspace=ws, stream=stream)
+    torch.cuda.synchronize()
+    for _, _, cache, _, ws, want, _ in calls:
+        assert all(same(a, b) for a, b in zip(cache, want)) and dtlib.dt_get_error(ws) == dtlib.Status.OK
 
 
 def test_nothing_to_append(dtlib):

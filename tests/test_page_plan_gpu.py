@@ -264,6 +264,30 @@ def test_captured_and_replayed(dtlib):
     assert state["page_table"].tolist() == ref.table and state["free_count"].tolist() == [ref.count]
 
 
+@pytest.mark.parametrize("pool", [True, False])
+@pytest.mark.parametrize("over", ["lens", "grow"])
+def test_lengths_in_the_place_of_the_old_ones(dtlib, over, pool):
+    """out lens is lens, or grow, themselves: of a plan by one block and by many."""
+    for B, most in ((3, 20), (300, 900)):
+        r = random.Random(B)
+        lens, grow = [r.randint(0, 40) for _ in range(B)], [r.randint(0, most) for _ in range(B)]
+        ref = Pool(B, B * 60, 60, 16)
+        state = ref.tensors()
+        check(dtlib, ref, state, [0] * B, lens, rows=sum(lens))
+        if pool:
+            want, _ = ref.step(lens, grow, rows=sum(grow) + 5)
+        else:
+            check(dtlib, ref, state, lens, grow, rows=sum(grow) + 5)
+            want, _ = ref.step(lens, grow, rows=sum(grow) + 5)
+        old = dict(lens=ints(lens), grow=ints(grow))
+        out = dict(lens=old[over], cu_seqlens=ints([0] * (B + 1)), slots=ints([0] * (sum(grow) + 5)),
+                   positions=ints([0] * (sum(grow) + 5)))
+        given = state if pool else dict(page_table=state["page_table"])
+        dtlib.dt_page_plan(old["lens"], old["grow"], page_size=16, num_pages=ref.pages, out=out, **given)
+        got = [out[k].tolist() for k in ("lens", "cu_seqlens", "slots", "positions")]
+        assert got == list(want)
+
+
 def test_refuses(dtlib):
     table, lens = ints([[7, 3, -1], [9, 1, 2]]), ints([1, 2])
     held, free, count = ints([1, 1]), ints([0] * 10), ints([0])

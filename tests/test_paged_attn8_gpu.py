@@ -227,6 +227,52 @@ def test_late_keys_above_all_before_them(dtlib):
     parity(dtlib, s)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [2, 3, 4, 8, 16, 32])
+def test_late_keys_above_all_before_them_for_any_rows(dtlib, n, d):
+    """The same under trees of 8 to 128 rows a head, and in some heads' rows alone."""
+    s = make8([1500, 700], n, 8, 2, d, 16, 16)
+    at = s["table"][0, :94].long()
+    s["ks"][at] = s["ks"][at] * torch.linspace(0.02, 3, 94, device="cuda")[:, None, None]
+    q = s["q"].float()
+    q[:, :, ::3] *= 4
+    s["q"] = q.to(BF)
+    parity(dtlib, s, requests=[0, 1], heads=[0, 1, 3, 6])
+
+
+@pytest.mark.parametrize("lens,n,Hq,Hkv,d,page", [
+    ([20011, 70, 9000], 64, 4, 2, 128, 16),        # 128 rows, one pair over many CTAs
+    ([20011, 16, 9000, 400], 16, 32, 8, 128, 64),  # 64 rows, several segments a CTA
+    ([6001, 8, 250], 8, 8, 2, 64, 8),              # 32 rows, the smallest pages
+    ([9001, 4, 129], 4, 16, 4, 64, 8),             # 16 rows
+])
+def test_long_contexts_under_trees(dtlib, lens, n, Hq, Hkv, d, page):
+    parity(dtlib, make8(lens, n, Hq, Hkv, d, page, 8), heads=[0, Hq - 1])
+
+
+def test_the_largest_batch(dtlib):
+    """As many requests as there may be, most of them short, some unused: segments that are parts of a block's worth."""
+    lens = [(i * 53) % 190 + 1 if i % 7 else 0 for i in range(2048)]
+    lens[1000] = 4000
+    parity(dtlib, make8(lens, 1, 8, 4, 64, 16, 16, mask=None), requests=[0, 1, 6, 999, 1000, 1001, 2046, 2047])
+
+
+def test_two_calls_at_once(dtlib):
+    """Two streams, a workspace each: a long call and many short ones beside it."""
+    a, b = make8([60000, 31000], 3, 16, 2, 128, 64, 16), make8([700] * 9, 16, 8, 2, 64, 16, 16)
+    rooms = [room(dtlib, s) for s in (a, b)]
+    want = run(dtlib, a).clone(), run(dtlib, b).clone()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for i, s in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(run(dtlib, s, workspace=rooms[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i]) and dtlib.dt_get_error(rooms[i]) == dtlib.Status.OK
+
+
 def nan_code(s, name, b, token, head, column):
     page = int(s["table"][b, token // s["kc"].shape[2]])
     s[name].view(torch.uint8)[page, head, token % s["kc"].shape[2], column] = 0x7F
