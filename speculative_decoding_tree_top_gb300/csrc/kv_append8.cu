@@ -10,6 +10,12 @@
 // call when those are few. Otherwise a launch before fills an index from slots to tokens, and a row's token is looked for
 // first where it is when tokens are in order, then in the index. An entry of the index counts if the token that it names
 // has that slot, so the index needs no clearing, and what an earlier call left there does no harm.
+//
+// Bound by memory when it is large: rows are read once, codes, scales and rotated queries written once. Measured (16384
+// tokens, 32/8 heads, d = 128, 411 MB): 84 us, 4.9 TB/s, 72% of the copy rate; the queries' part alone 43, that of keys and
+// values 48, whose CTAs are chains of loads (slots, index, rows) and hold the rest up: the two share the SMs, but not
+// wholly. One kind of CTA for all took 90, rows kept in registers over both passes 189 (100 registers). 64 trees of 16
+// nodes: 14 us, of which the index's launch is 3; one token: the launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -25,7 +31,8 @@ constexpr int kA8Threads = 256;
 constexpr int kA8Warps = kA8Threads / 32;
 constexpr int kA8PerSm = 5;      // CTAs: 48 registers a thread
 // Up to so many tokens every CTA looks at all slots, past it a launch before makes an index. Measured (32/8 heads, d = 128,
-// pages of 16), looks and index: 256 tokens 8.8 and 10.3 us, 512 11.3 and 12.3, 1024 15.5 and 14.5, 2048 21.1 and 18.0.
+// pages of 16), looks and index: 256 tokens 8.8 and 10.3 us, 512 11.3 and 12.3, 1024 15.5 and 14.5, 2048 21.1 and 18.0
+// (since then 11.1 and, with the index, 11.8 at 513, 14.0, 17.6).
 constexpr int kA8Scan = 512;
 constexpr int kA8Chunk = 16;     // tokens that a CTA looks after, at most
 constexpr int kA8TileBytes = 4096;  // of rows as they come, for each warp
@@ -48,23 +55,33 @@ struct Append8Params {
   int32_t* index;            // [slots_end], or null: look at all slots
 };
 
-// A token's slot, -1 for one that is left out.
-__device__ __forceinline__ int a8_slot(const Append8Params& p, int t, bool* bad) {
-  const int slot = p.slots[t];
-  if (slot < 0) return -1;
-  const int pos = p.half ? p.positions[t] : 0;
-  if (slot >= p.slots_end || (p.half && (pos < 0 || pos >= p.max_pos))) {
+// A token as the arrays have it: its slot, -1 for one that is left out, and its position. Both are loaded at once, and
+// several tokens' before any is looked at: a CTA's first microseconds are a chain of such loads.
+struct A8Token {
+  int slot, pos;
+};
+__device__ __forceinline__ A8Token a8_fetch(const Append8Params& p, int t, bool there) {
+  A8Token x{-1, 0};
+  if (there) {
+    x.slot = p.slots[t];
+    if (p.half) x.pos = p.positions[t];
+  }
+  return x;
+}
+__device__ __forceinline__ int a8_slot(const Append8Params& p, const A8Token& x, bool* bad) {
+  if (x.slot < 0) return -1;
+  if (x.slot >= p.slots_end || x.pos < 0 || (p.half && x.pos >= p.max_pos)) {
     *bad = true;
     return -1;
   }
-  return slot;
+  return x.slot;
 }
 
 __global__ void __launch_bounds__(kA8Threads) append8_index_kernel(Append8Params p) {
   at_launch_order();
   const int t = blockIdx.x * kA8Threads + threadIdx.x;
   bool bad = false;
-  const int slot = t < p.N ? a8_slot(p, t, &bad) : -1;
+  const int slot = a8_slot(p, a8_fetch(p, t, t < p.N), &bad);
   if (slot >= 0) p.index[slot] = t;
 }
 
@@ -362,11 +379,14 @@ __global__ void __launch_bounds__(kA8Threads, kA8PerSm) kv_append8_kernel(Append
   for (int i = t; i < p.chunk << p.block_shift; i += kA8Threads) s_who[i] = make_int2(INT_MAX, 0);
   if (t < p.chunk) {
     bool bad = false;
-    const int token = token0 + t, slot = token < p.N ? a8_slot(p, token, &bad) : -1;
+    const int token = token0 + t;
+    const A8Token own = a8_fetch(p, token, token < p.N);
+    const A8Token last = a8_fetch(p, token - 1, token > 0 && token <= p.N);
+    const int slot = a8_slot(p, own, &bad);
     if (bad) record_error(hdr, DT_ERR_INVALID_ARG);
     // the token before it in the row before it: it does not lead, as most do not
     bool other = false;
-    const bool follows = token > 0 && token < p.N && (slot & (block - 1)) > 0 && a8_slot(p, token - 1, &other) == slot - 1;
+    const bool follows = slot > 0 && (slot & (block - 1)) > 0 && a8_slot(p, last, &other) == slot - 1;
     s_low[t] = block;
     s_lead[t] = -1;
     s_first[t] = slot < 0 || follows ? -1 : slot;
@@ -381,14 +401,16 @@ __global__ void __launch_bounds__(kA8Threads, kA8PerSm) kv_append8_kernel(Append
       for (int r = lane; r < block; r += 32) {
         // the row's token where tokens are in order, else by the index
         const int named = p.index[first + r], near = token + first + r - slot;
+        A8Token x = a8_fetch(p, near, near >= 0 && near < p.N);
         int u = near;
-        bool bad = false, there = near >= 0 && near < p.N && a8_slot(p, near, &bad) == first + r;
+        bool bad = false, there = a8_slot(p, x, &bad) == first + r;
         if (!there) {
           u = named;
-          there = u >= 0 && u < p.N && a8_slot(p, u, &bad) == first + r;
+          x = a8_fetch(p, u, u >= 0 && u < p.N);
+          there = a8_slot(p, x, &bad) == first + r;
         }
         if (there) {
-          s_who[(c << p.block_shift) + r] = make_int2(u, p.half ? p.positions[u] : 0);
+          s_who[(c << p.block_shift) + r] = make_int2(u, x.pos);
           if (r < low) {
             low = r;
             lead = named;  // of two tokens with one slot the index names one

@@ -12,7 +12,8 @@
 //
 // Bound by latency: a few hundred bytes to a few hundred kilobytes. Every CTA scans all requests (two a thread, all in
 // shared memory) and does its part of the moves and of the rows; nothing that it reads is written by another, but for the
-// lengths and the state's counts, which the last CTA to finish writes.
+// lengths and the state's counts, which the last CTA to finish writes. Measured: one tree of 8 nodes 6.0 us, 64 trees of 16
+// 8.8, 256 prompts of up to 2500 tokens 12 (two launches, one for the rows, took 32); a call costs the host 10.
 #include <cuda_runtime.h>
 
 #include <climits>
