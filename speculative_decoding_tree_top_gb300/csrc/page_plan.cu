@@ -110,7 +110,7 @@ __device__ __forceinline__ void plan_row(const PlanParams& p, const PlanSums& s,
   if (live) {
     const int from = s.base[b], count = s.tokens[b];
     int j = i;
-    if (p.path) {
+    if (p.path && from >= 0) {  // (a served request has n tokens at most: the search ends within its path)
       const int32_t* path = p.path + static_cast<size_t>(b) * p.n;
       j = 0;
       while (j < count && path[j] != i) ++j;

@@ -235,6 +235,30 @@ def test_paths_of_any_content_stay_in_bounds(dtlib):
         assert out["slots"].tolist() == want
 
 
+@pytest.mark.parametrize("n,grow", [(4, 5), (4, 1000), (4, 2 ** 31 - 1), (1, 2), (64, 65)])
+def test_a_path_of_a_request_that_grows_by_too_much_is_not_read(dtlib, n, grow):
+    """More accepted nodes than the tree has: reported, no tokens, the neighbours as they are. The path's rows lie inside a
+    larger array, whose other entries would name every node; the last request's row is the array's last."""
+    B, page = 3, 16
+    around = torch.arange(5000 + B * n, dtype=I32, device="cuda") % n
+    path = around[-B * n:].view(B, n)
+    for which in range(B):
+        ref = Pool(B, 40, 20, page)
+        state = ref.tensors()
+        check(dtlib, ref, state, [0] * B, [40] * B, rows=40 * B)
+        kept = [min(2, n)] * B
+        kept[which] = grow
+        ws = dtlib.new_workspace(dtlib.dt_page_plan_workspace_bytes(B))
+        want, bad = ref.step([30] * B, kept, n, n * B, path=path.tolist())
+        out = dtlib.dt_page_plan(ints([30] * B), ints(kept), page_size=page, num_pages=40, n=n, path=path, workspace=ws,
+                                 **state)
+        assert bad == [b == which for b in range(B)]
+        assert dtlib.dt_get_error(ws) == dtlib.Status.INVALID_ARG
+        assert [out[k].tolist() for k in ("lens", "cu_seqlens", "slots", "positions")] == list(want)
+        assert (out["slots"].view(B, n)[which] == -1).all() and (out["positions"].view(B, n)[which] == 0).all()
+        assert state["page_table"].tolist() == ref.table and state["held"].tolist() == ref.held
+
+
 def test_some_outputs_alone(dtlib):
     table, ws = ints([[7, 3, -1], [9, 1, 2]]), dtlib.new_workspace(dtlib.dt_page_plan_workspace_bytes(2))
     for out in (dict(lens=ints([0, 0])), dict(cu_seqlens=ints([0, 0, 0])), {}, dict(slots=ints([0] * 5), positions=ints([0] * 5))):
