@@ -305,7 +305,8 @@ dt_status dt_tree_attention(int B, int n, int L, int Hq, int Hkv, int d, const v
  * requests that need pages get none either). DT_ERR_INVALID_ARG: grow[b] negative (or above n > 0), more tokens than
  * max_pages pages hold, fewer pages held than lens[b] needs, or rows behind N; and a row whose page lies outside the
  * pool. A pool that contradicts itself (free_count out of range, more pages given back than there is room for) sets
- * DT_ERR_INVALID_ARG and no page moves.
+ * DT_ERR_INVALID_ARG and no page moves. An entry outside 0 .. num_pages - 1 that moves, given back or taken, moves as it
+ * is and sets DT_ERR_INVALID_ARG.
  * No array may overlap another, but out_lens may be lens or grow. B <= DT_PAGED_MAX_BATCH; page sizes, pool and max_pages
  * as dt_paged_attention.
  * ------------------------------------------------------------------------------------------------------------- */

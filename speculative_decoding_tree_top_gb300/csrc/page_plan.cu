@@ -217,11 +217,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(PlanParams p
   const int taken = s_taken, step = gridDim.x * blockDim.x, own = blockIdx.x * blockDim.x + t;
   if (pool && sound) {
     for (long long k = own; k < taken; k += step) {
-      const int at = static_cast<int>(k), b = plan_find(s.take, p.B, at);
-      p.table[static_cast<size_t>(b) * p.max_pages + s.held[b] + at - s.take[b]] = plan_taken(p, s, at);
+      const int at = static_cast<int>(k), b = plan_find(s.take, p.B, at), page = plan_taken(p, s, at);
+      if (page < 0 || page >= p.num_pages) record_error(hdr, DT_ERR_INVALID_ARG);
+      p.table[static_cast<size_t>(b) * p.max_pages + s.held[b] + at - s.take[b]] = page;
     }
-    for (long long m = own; m < s.given - taken; m += step)
-      p.free_pages[s.count + m] = plan_given(p, s, s.given - 1 - static_cast<int>(m));
+    for (long long m = own; m < s.given - taken; m += step) {
+      const int page = plan_given(p, s, s.given - 1 - static_cast<int>(m));
+      if (page < 0 || page >= p.num_pages) record_error(hdr, DT_ERR_INVALID_ARG);
+      p.free_pages[s.count + m] = page;
+    }
   }
   for (long long row = own; row < p.N; row += step) plan_row(p, s, static_cast<int>(row), hdr);
   // the lengths, which may take the old ones' place, and the state's counts, when every CTA has read them

@@ -212,6 +212,35 @@ def test_a_pool_that_contradicts_itself_moves_nothing(dtlib, count):
     assert (out["slots"][:2] >= 0).all() and (out["slots"][2:] == -1).all()
 
 
+def test_pages_outside_the_pool_that_move_are_reported(dtlib):
+    """An entry that is no page, given back by a request or taken from the stack: it moves as it is, and the status says so,
+    with rows and without, of one block and of many."""
+    for B, rows in ((3, 0), (3, 90), (300, 0), (300, 9000)):
+        for page in (-1, 40 * B, 2 ** 31 - 1, -2 ** 31):
+            ref = Pool(B, 40 * B, 500, 16)
+            state = ref.tensors()
+            check(dtlib, ref, state, [0] * B, [30] * B, rows=30 * B)
+            # given back
+            state["page_table"][1, 1] = ref.table[1][1] = page
+            lens = [30, -1] + [30] * (B - 2)
+            check(dtlib, ref, state, lens, [0] * B, status=dtlib.Status.INVALID_ARG)
+            # taken: it lies on top of the stack, under the first page of request 1
+            grow = [0, 30] + [0] * (B - 2)
+            lens[1] = 0
+            assert ref.free[ref.count - 2] == page
+            ws = dtlib.new_workspace(dtlib.dt_page_plan_workspace_bytes(B))
+            want, bad = ref.step(lens, grow, rows=rows)
+            out = dtlib.dt_page_plan(ints(lens), ints(grow), page_size=16, num_pages=40 * B, rows=rows, workspace=ws, **state)
+            assert dtlib.dt_get_error(ws) == dtlib.Status.INVALID_ARG and not any(bad)
+            assert out["lens"].tolist() == want[0] and state["held"].tolist() == ref.held
+            assert state["page_table"].tolist() == ref.table and state["free_count"].tolist() == [ref.count]
+            if rows:  # the page's rows are no tokens, the others' are
+                assert out["slots"].tolist() == [-1 if i >= 16 and i < 30 else x for i, x in enumerate(want[2])]
+            # nothing that moves is outside: nothing is reported
+            lens[1] = 30
+            check(dtlib, ref, state, [-1 if b == 0 else x for b, x in enumerate(lens)], [0] * B)
+
+
 def test_without_a_pool_the_table_is_read(dtlib):
     table = ints([[7, 3, -1], [9, 1, 2]])
     ws = dtlib.new_workspace(dtlib.dt_page_plan_workspace_bytes(2))
