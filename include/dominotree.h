@@ -263,8 +263,8 @@ dt_status dt_tree_attention(int B, int n, int L, int Hq, int Hkv, int d, const v
  *
  * The cache is two pools of pages, k_cache and v_cache [num_pages,Hkv,page_size,d] bf16: a page holds page_size tokens,
  * head by head. Token i of request b sits in page page_table[b][i / page_size] at row i % page_size; its slot is
- * page * page_size + row. Pages may be shared by requests and lie in any order; what unused rows hold is never looked
- * at (it may be NaN). Common limits (DT_ERR_UNSUPPORTED beyond): dtype DT_BF16, d = 64 or 128, page_size a power of two
+ * page * page_size + row. Pages may be shared by requests (not those of dt_page_plan's pool) and lie in any order; what
+ * unused rows hold is never looked at (it may be NaN). Common limits (DT_ERR_UNSUPPORTED beyond): dtype DT_BF16, d = 64 or 128, page_size a power of two
  * in DT_MIN_PAGE .. DT_MAX_PAGE, num_pages * page_size and num_pages * Hkv below 2^31, Hq, Hkv up to DT_MAX_HEADS. */
 #define DT_MIN_PAGE 8
 #define DT_MAX_PAGE 256
@@ -283,6 +283,9 @@ dt_status dt_tree_attention(int B, int n, int L, int Hq, int Hkv, int d, const v
  * The free pages are a stack, free_pages[0 .. free_count[0] - 1]. First those given back are pushed, the last request's
  * first and each request's from its last page; then the requests take theirs from the top in their order, each from its
  * first missing page: what one step took and the next gives back leaves the stack as it was.
+ * A page of the pool has one holder: it is named once, by one request's row within its held pages or by the stack. The plan
+ * keeps no count of holders and does not look for a second one: a page that two requests hold would be given back, and
+ * handed out, twice. Requests that share pages are planned without a pool.
  * The rows of the slot map, as dt_kv_append and dt_paged_attention take them:
  *   n = 0     the requests' grow[b] new tokens, packed one request after the other (prompts);
  *   n > 0     n rows per request, N = B n. Row i is the request's i-th new token while i < grow[b] (one token each: n = 1;
