@@ -269,7 +269,7 @@ extern "C" dt_status dt_page_plan(int B, int n, int N, int page_size, int num_pa
   if ((slots != nullptr) != (positions != nullptr)) return DT_ERR_INVALID_ARG;
   if (slots ? (n > 0 && N != static_cast<long long>(B) * n) : N != 0) return DT_ERR_INVALID_ARG;
   const bool pool = held || free_pages || free_count;
-  if (pool && !(held && free_pages && free_count)) return DT_ERR_INVALID_ARG;
+  if (pool && !((held || B == 0) && free_pages && free_count)) return DT_ERR_INVALID_ARG;
   if (B == 0 && N == 0) return DT_OK;
   const void* need[] = {lens, grow, page_table};
   for (const void* x : need)

@@ -107,3 +107,15 @@ def test_new_cache(dtlib):
     kc, vc, ks, vs = dtlib.new_paged_cache8(5, 2, 64, 128, scale_block=32, device="cpu")
     assert kc.shape == vc.shape == (5, 2, 64, 128) and kc.dtype == vc.dtype == torch.float8_e4m3fn
     assert ks.shape == vs.shape == (5, 2, 2) and ks.dtype == torch.float32 and not ks.any() and not vs.any()
+
+
+def test_a_plan_without_requests_holds_nothing(dtlib):
+    """No requests: an array of what each holds may have no address, with a pool as without one."""
+    f = dtlib.lib().dt_page_plan
+
+    def call(free=A, count=A):
+        return f(0, 0, 0, 16, 40, 10, None, None, None, None, None, None, free, count, None, None, None, None, A, 1 << 20,
+                 None)
+    assert call() == OK
+    assert call(free=None, count=None) == OK
+    assert call(free=None) == INVALID and call(count=None) == INVALID
