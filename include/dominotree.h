@@ -264,8 +264,9 @@ dt_status dt_tree_attention(int B, int n, int L, int Hq, int Hkv, int d, const v
  * The cache is two pools of pages, k_cache and v_cache [num_pages,Hkv,page_size,d] bf16: a page holds page_size tokens,
  * head by head. Token i of request b sits in page page_table[b][i / page_size] at row i % page_size; its slot is
  * page * page_size + row. Pages may be shared by requests (not those of dt_page_plan's pool) and lie in any order; what
- * unused rows hold is never looked at (it may be NaN). Common limits (DT_ERR_UNSUPPORTED beyond): dtype DT_BF16, d = 64 or 128, page_size a power of two
- * in DT_MIN_PAGE .. DT_MAX_PAGE, num_pages * page_size and num_pages * Hkv below 2^31, Hq, Hkv up to DT_MAX_HEADS. */
+ * unused rows hold is never looked at (it may be NaN). Common limits (DT_ERR_UNSUPPORTED beyond): dtype DT_BF16, d = 64 or
+ * 128, page_size a power of two in DT_MIN_PAGE .. DT_MAX_PAGE, num_pages * page_size and num_pages * Hkv below 2^31, Hq,
+ * Hkv up to DT_MAX_HEADS. */
 #define DT_MIN_PAGE 8
 #define DT_MAX_PAGE 256
 #define DT_MAX_HEADS 256
@@ -310,6 +311,7 @@ dt_status dt_tree_attention(int B, int n, int L, int Hq, int Hkv, int d, const v
  * pool. A pool that contradicts itself (free_count out of range, more pages given back than there is room for) sets
  * DT_ERR_INVALID_ARG and no page moves. An entry outside 0 .. num_pages - 1 that moves, given back or taken, moves as it
  * is and sets DT_ERR_INVALID_ARG.
+ * Without requests and rows (B = 0, N = 0) nothing is launched and nothing written, cu_seqlens[0] neither.
  * No array may overlap another, but out_lens may be lens or grow. B <= DT_PAGED_MAX_BATCH; page sizes, pool and max_pages
  * as dt_paged_attention.
  * ------------------------------------------------------------------------------------------------------------- */

@@ -391,6 +391,9 @@ def dt_page_plan(lens: torch.Tensor, grow: torch.Tensor, page_table: torch.Tenso
         _raw(stream, dev))
     if status:
         raise DTError(status, "dt_page_plan")
+    if B == 0 and rows == 0 and cu is not None:  # the library writes nothing then
+        with _side(stream, dev):
+            cu.zero_()
     return out
 
 

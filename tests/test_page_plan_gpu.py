@@ -297,6 +297,34 @@ def test_some_outputs_alone(dtlib):
         assert all(out[k].tolist() == want[k] for k in out)
 
 
+@pytest.mark.parametrize("pool", [True, False])
+def test_an_empty_batch_has_a_first_row(dtlib, pool):
+    """cu_seqlens has one entry, 0, also without requests and rows, as a call or in a graph; the pool stays as it is."""
+    state = dict(page_table=ints([[]] * 0).view(0, 4))
+    if pool:
+        state.update(held=ints([]), free_pages=ints([3, 1, 2, 0, -9]), free_count=ints([4]))
+    before = {k: v.clone() for k, v in state.items()}
+    none = ints([])
+    call = lambda **kw: dtlib.dt_page_plan(none, none, page_size=16, num_pages=5, **state, **kw)
+    for n in (0, 3):
+        out = dict(lens=ints([]), cu_seqlens=ints([77, 78])[:1])
+        call(n=n, out=out)
+        assert out["cu_seqlens"].tolist() == [0]
+        assert call(n=n)["cu_seqlens"].tolist() == [0]
+        g, out = torch.cuda.CUDAGraph(), dict(cu_seqlens=ints([77]))
+        ws = dtlib.new_workspace(256)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            call(n=n, out=out, workspace=ws)
+        out["cu_seqlens"].fill_(5)
+        g.replay()
+        assert out["cu_seqlens"].tolist() == [0]
+    rows = dict(cu_seqlens=ints([77]), slots=ints([5] * 9), positions=ints([5] * 9))
+    call(out=rows)
+    assert rows["cu_seqlens"].tolist() == [0] and rows["slots"].tolist() == [-1] * 9
+    assert all(torch.equal(before[k], state[k]) for k in state)
+
+
 def test_captured_and_replayed(dtlib):
     """A step of a loop as a graph: each replay takes the pages of one more token per request."""
     ref = Pool(3, 40, 10, 8)
