@@ -370,7 +370,7 @@ dt_status dt_kv_append(int N, int Hq, int Hkv, int d, const void* q, int64_t q_s
  *   Two calls that write to one block are ordered by the caller, as any two calls that write to one place.
  *   workspace   dt_kv_append8_workspace_bytes(N,num_pages,page_size) bytes, initialised by dt_workspace_init.
  * Supported beyond dt_kv_append: scale_block a power of two in DT_MIN_PAGE .. page_size. If two tokens of a call name one
- * slot, one of them is stored.
+ * slot, one of them is stored, its key and its value; out_q and out_k have both.
  * ------------------------------------------------------------------------------------------------------------- */
 #define DT_SCALE_LOW (-48)
 #define DT_SCALE_HIGH 48

@@ -209,7 +209,7 @@ __device__ __forceinline__ void a8_load(const Append8Params& p, const int2* who,
 }
 // kKind: values (or keys that are not rotated) 0; keys whose rows' parts of the rotation's table are in shared memory at
 // `turns`, row by row, and whose first tile is there if `loaded`: 1; keys that read the table: 2.
-template <int D, int kKind>
+template <int D, int kKind, bool kDense>
 __device__ __forceinline__ void a8_block(const Append8Params& p, const int2* who, int low, int first_slot, int head,
                                          bool is_k, unsigned char* tile, uint32_t turns, bool loaded) {
   constexpr int kItems = A8<D>::kItems, kRows = A8<D>::kRows, kTile = A8<D>::kTile;
@@ -287,7 +287,6 @@ __device__ __forceinline__ void a8_block(const Append8Params& p, const int2* who
     }
   }
   const float inv = a8_pow2(-e);
-  unsigned short* dense = is_k && p.out_k ? p.out_k + head * D : nullptr;
 #pragma unroll 1
   for (int r0 = from; r0 < block; r0 += kTile) {
     if (block > kTile) load(r0);
@@ -298,8 +297,8 @@ __device__ __forceinline__ void a8_block(const Append8Params& p, const int2* who
       const int2 token = w[u];
       if (token.x == INT_MAX) continue;
       Eight x = item_of(u, token.y);
-      if (dense) {
-        unsigned short* o = dense + static_cast<size_t>(token.x) * (p.Hkv * D);
+      if (kDense && is_k) {
+        unsigned short* o = p.out_k + (static_cast<size_t>(token.x) * p.Hkv + head) * D;
         const uint4 y = pack8(x);
         *reinterpret_cast<uint2*>(o + cols.a) = make_uint2(y.x, y.y);
         *reinterpret_cast<uint2*>(o + cols.b) = make_uint2(y.z, y.w);
@@ -316,15 +315,37 @@ __device__ __forceinline__ void a8_block(const Append8Params& p, const int2* who
   }
 }
 
+// The dense row of a head's key whose token another one of the same slot keeps out of the cache: as a8_block writes the
+// others'. Rare. A lane reads and writes the same columns: the row may be the key's own.
+template <int D>
+__device__ __noinline__ void a8_dense(const Append8Params& p, int token, int head) {
+  const int item = threadIdx.x & 31;
+  if (item >= A8<D>::kItems) return;
+  const Cols cols = p.half ? a8_cols(item, p.half, p.interleaved) : Cols{8 * item, 8 * item + 4, -1};
+  const unsigned short* src = p.k + token * p.k_stride + head * D;
+  const uint2 a = *reinterpret_cast<const uint2*>(src + cols.a), b = *reinterpret_cast<const uint2*>(src + cols.b);
+  Eight x = unpack8(make_uint4(a.x, a.y, b.x, b.y));
+  if (cols.pair >= 0) {
+    const float* at = p.rope + static_cast<size_t>(p.positions[token]) * (2 * p.half) + cols.pair;
+    a8_rotate(x, *reinterpret_cast<const float4*>(at), *reinterpret_cast<const float4*>(at + p.half), p.interleaved);
+  }
+  unsigned short* o = p.out_k + (static_cast<size_t>(token) * p.Hkv + head) * D;
+  const uint4 y = pack8(x);
+  *reinterpret_cast<uint2*>(o + cols.a) = make_uint2(y.x, y.y);
+  *reinterpret_cast<uint2*>(o + cols.b) = make_uint2(y.z, y.w);
+}
+
 // Two kinds of CTAs, in turn, so that they share the SMs: those of keys and values compute while those of queries wait for
 // memory. Keys (the even ones of their kind) or values: of the blocks whose leaders are among the CTA's tokens. Queries: a
-// token or several at a time, each thread in the same columns of its heads (as dt_kv_append).
-template <int D>
+// token or several at a time, each thread in the same columns of its heads (as dt_kv_append). kDense: keys go to out_k as
+// well (an instance for both spills more: trees without out_k 15.5 us where theirs takes 15.0; prompts with it 83.3, 83.4).
+template <int D, bool kDense>
 __global__ void __launch_bounds__(kA8Threads, kA8PerSm) kv_append8_kernel(Append8Params p, WsHeader* hdr) {
   extern __shared__ __align__(16) unsigned char s_tiles[];  // a tile a warp
   // [chunk][block]: the token of each row, INT_MAX for none, and its position
   int2* s_who = reinterpret_cast<int2*>(s_tiles + kA8Warps * kA8TileBytes);
   __shared__ int s_low[kA8Chunk], s_first[kA8Chunk], s_lead[kA8Chunk];
+  __shared__ int s_slot[kA8Chunk], s_lost[kA8Chunk];  // kDense: the tokens' slots, and whether another of a slot is kept
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, block = 1 << p.block_shift;
   at_launch_order();
   const int both = 2 * (p.kv_ctas < p.q_ctas ? p.kv_ctas : p.q_ctas), b = blockIdx.x;
@@ -389,10 +410,16 @@ __global__ void __launch_bounds__(kA8Threads, kA8PerSm) kv_append8_kernel(Append
     const bool follows = slot > 0 && (slot & (block - 1)) > 0 && a8_slot(p, last, &other) == slot - 1;
     s_low[t] = block;
     s_lead[t] = -1;
+    s_slot[t] = slot;
+    s_lost[t] = 0;
     s_first[t] = slot < 0 || follows ? -1 : slot;
   }
   __syncthreads();
   if (p.index) {
+    // of tokens with one slot the index names the one that is kept: looked up by the last warp, used below
+    const int own = t - (kA8Threads - 32);
+    const bool looks = kDense && is_k && own >= 0 && own < p.chunk && s_slot[own] >= 0;
+    const int kept = looks ? p.index[s_slot[own]] : -1;
     for (int c = warp; c < p.chunk; c += kA8Warps) {
       const int slot = s_first[c];
       if (slot < 0) continue;
@@ -403,7 +430,7 @@ __global__ void __launch_bounds__(kA8Threads, kA8PerSm) kv_append8_kernel(Append
         const int named = p.index[first + r], near = token + first + r - slot;
         A8Token x = a8_fetch(p, near, near >= 0 && near < p.N);
         int u = near;
-        bool bad = false, there = a8_slot(p, x, &bad) == first + r;
+        bool bad = false, there = named == near && a8_slot(p, x, &bad) == first + r;
         if (!there) {
           u = named;
           x = a8_fetch(p, u, u >= 0 && u < p.N);
@@ -413,7 +440,7 @@ __global__ void __launch_bounds__(kA8Threads, kA8PerSm) kv_append8_kernel(Append
           s_who[(c << p.block_shift) + r] = make_int2(u, x.pos);
           if (r < low) {
             low = r;
-            lead = named;  // of two tokens with one slot the index names one
+            lead = u;
           }
         }
       }
@@ -423,6 +450,7 @@ __global__ void __launch_bounds__(kA8Threads, kA8PerSm) kv_append8_kernel(Append
         s_lead[c] = lead;
       }
     }
+    if (looks && kept != token0 + own) s_lost[own] = 1;
   } else {
 #pragma unroll
     for (int i = 0; i < kLooks; ++i) {
@@ -434,6 +462,17 @@ __global__ void __launch_bounds__(kA8Threads, kA8PerSm) kv_append8_kernel(Append
           if (p.half && (pos < 0 || pos >= p.max_pos)) continue;
           atomicMin(&s_who[(c << p.block_shift) + r].x, u);
           atomicMin(&s_low[c], r);
+        }
+    }
+    if (kDense && is_k) {
+#pragma unroll 1
+      for (int c = 0; c < p.chunk; ++c)
+#pragma unroll
+        for (int i = 0; i < kLooks; ++i) {
+          const int u = t + i * kA8Threads;
+          if (look[i] == s_slot[c] && u < token0 + c && look[i] >= 0 &&  // the first token of a slot is kept
+              (!p.half || static_cast<unsigned>(p.positions[u]) < static_cast<unsigned>(p.max_pos)))
+            s_lost[c] = 1;
         }
     }
     __syncthreads();
@@ -466,10 +505,15 @@ __global__ void __launch_bounds__(kA8Threads, kA8PerSm) kv_append8_kernel(Append
     }
     const uint32_t turns = smem_u32(s_turns);
     for (int head = warp; head < p.Hkv; head += kA8Warps) {
-      if (staged) a8_block<D, 1>(p, who, low, first, head, true, tile, turns, head == warp);
-      else if (is_k && p.half > 0) a8_block<D, 2>(p, who, low, first, head, true, tile, 0u, false);
-      else a8_block<D, 0>(p, who, low, first, head, is_k, tile, 0u, false);
+      if (staged) a8_block<D, 1, kDense>(p, who, low, first, head, true, tile, turns, head == warp);
+      else if (is_k && p.half > 0) a8_block<D, 2, kDense>(p, who, low, first, head, true, tile, 0u, false);
+      else a8_block<D, 0, kDense>(p, who, low, first, head, is_k, tile, 0u, false);
     }
+  }
+  if (kDense && is_k) {  // the tokens that the cache does not keep
+    unsigned lost = __ballot_sync(0xFFFFFFFFu, lane < p.chunk && s_lost[lane] != 0);
+    for (; __builtin_expect(lost != 0u, 0); lost &= lost - 1u)
+      for (int head = warp; head < p.Hkv; head += kA8Warps) a8_dense<D>(p, token0 + __ffs(lost) - 1, head);
   }
 }
 
@@ -557,9 +601,8 @@ extern "C" dt_status dt_kv_append8(int N, int Hq, int Hkv, int d, const void* q,
   }
   const int grid = p.kv_ctas + p.q_ctas;
   const size_t smem = sizeof(int2) * static_cast<size_t>(p.chunk) * scale_block + kA8Warps * kA8TileBytes + 2 * kA8TileBytes;
-  const void* fn = d == 64 ? reinterpret_cast<const void*>(kv_append8_kernel<64>)
-                           : reinterpret_cast<const void*>(kv_append8_kernel<128>);
-  if (ensure_dynamic_smem(fn, kA8Smem) != cudaSuccess) return DT_ERR_CUDA;
-  return d == 64 ? at_launch(kv_append8_kernel<64>, grid, kA8Threads, smem, stream, p, hdr)
-                 : at_launch(kv_append8_kernel<128>, grid, kA8Threads, smem, stream, p, hdr);
+  auto* kernel = d == 64 ? (out_k ? kv_append8_kernel<64, true> : kv_append8_kernel<64, false>)
+                         : (out_k ? kv_append8_kernel<128, true> : kv_append8_kernel<128, false>);
+  if (ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), kA8Smem) != cudaSuccess) return DT_ERR_CUDA;
+  return at_launch(kernel, grid, kA8Threads, smem, stream, p, hdr);
 }

@@ -281,6 +281,49 @@ def test_a_slot_named_twice_holds_one_of_the_two(dtlib):
             assert torch.equal(got, both[0]) or torch.equal(got, both[1])
 
 
+@pytest.mark.parametrize("N", [64, 512, 513, 2600])
+@pytest.mark.parametrize("d,block,rot,interleaved", [(64, 16, 64, False), (128, 64, 64, True), (128, 16, 0, False)])
+def test_out_k_of_a_slot_named_twice_is_written_for_both(dtlib, N, d, block, rot, interleaved):
+    """The cache keeps one of the tokens, the dense keys and queries hold each: far apart, side by side, three of a slot, the
+    first and the last token; into arrays of their own and in place."""
+    page, max_pos = 64, 5000
+    q, k, v, kc, _, slots, positions = make(N, 4, 2, d, page, rot, fused=False)
+    for seed in (0, 1):
+        if seed:  # tokens in order, as a prompt's
+            slots = torch.arange(7, N + 7, dtype=torch.int32, device="cuda")
+        slots[N - 5] = slots[9]
+        slots[21] = slots[20]
+        slots[40], slots[N // 2] = slots[33], slots[33]
+        slots[0] = slots[N - 1]
+        table = dtlib.rope_table(max_pos, rot) if rot else None
+        kw = dict(positions=positions, rope=table) if rot else {}
+        want_k, want_q = ((turned(x, table, positions, rot, interleaved) if rot else
+                           (x.double(), torch.zeros_like(x.double()))) for x in (k, q))
+        caches = []
+        for place in (False, True):
+            (c, ks), (vc, vs) = (pool(kc.shape[0] + 2, 2, page, d, block, s) for s in (1, 2))
+            kk, qq = k.clone(), q.clone()
+            out_k, out_q = (kk, qq) if place else (torch.full_like(k, 7.0), torch.full_like(q, 7.0))
+            ws = dtlib.new_workspace(dtlib.dt_kv_append8_workspace_bytes(N, c.shape[0], page))
+            dtlib.dt_kv_append8(kk, v, c, vc, ks, vs, slots, interleaved=interleaved, q=qq, out_q=out_q, out_k=out_k,
+                                workspace=ws, **kw)
+            assert dtlib.dt_get_error(ws) == dtlib.Status.OK
+            close(out_q, want_q)
+            close(out_k, want_k)
+            caches.append((c, vc, ks, vs))
+        turn = 2.0 ** -21 * k.abs().max().double()  # the rotation's error, at most
+        bound = lambda x, s: torch.maximum(2.0 ** -4 * (x.abs() + turn), 2.0 ** -10 * s) + turn
+        for c, vc, ks, vs in caches:
+            for named in ((9, N - 5), (20, 21), (33, 40, N // 2), (0, N - 1)):  # the key and the value are one token's
+                at, row = int(slots[named[0]]) // page, int(slots[named[0]]) % page
+                near = []
+                for x, cache, scale in ((want_k[0], c, ks), (v.double(), vc, vs)):
+                    s = scale[at, :, row // block, None].double()
+                    got = cache.view(torch.uint8)[at, :, row].view(F8).double() * s
+                    near.append([bool(((got - x[t]).abs() <= bound(x[t], s)).all()) for t in named])
+                assert any(a and b for a, b in zip(*near)), (named, near)
+
+
 def test_in_place_on_dense_queries_and_keys(dtlib):
     for N in (50, 2100):
         q, k, v, kc, _, slots, positions = make(N, 8, 2, 128, 16, 128, fused=False)
