@@ -273,6 +273,8 @@ def new_paged_cache(num_pages: int, Hkv: int, page_size: int, d: int, device="cu
 def new_paged_cache8(num_pages: int, Hkv: int, page_size: int, d: int, scale_block: int = 16, device="cuda"):
     """A paged cache in 8 bits -> (k_cache, v_cache) [num_pages,Hkv,page_size,d] float8_e4m3fn, not initialised, and
     (k_scale, v_scale) [num_pages,Hkv,page_size/scale_block] fp32, zero (no rows yet): four tensors in that order."""
+    if scale_block < 1 or page_size % scale_block:
+        raise ValueError(f"scale_block must divide page_size {page_size}, not be {scale_block}")
     caches = (torch.empty((num_pages, Hkv, page_size, d), dtype=torch.float8_e4m3fn, device=device) for _ in range(2))
     scales = (torch.zeros((num_pages, Hkv, page_size // scale_block), dtype=torch.float32, device=device)
               for _ in range(2))

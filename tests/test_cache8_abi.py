@@ -119,3 +119,9 @@ def test_a_plan_without_requests_holds_nothing(dtlib):
     assert call() == OK
     assert call(free=None, count=None) == OK
     assert call(free=None) == INVALID and call(count=None) == INVALID
+
+
+def test_new_cache_refuses_blocks_that_do_not_fill_a_page(dtlib):
+    for page, block in ((64, 48), (16, 12), (16, 32), (16, 0), (16, -4)):
+        with pytest.raises(ValueError):
+            dtlib.new_paged_cache8(5, 2, page, 128, scale_block=block, device="cpu")
