@@ -299,8 +299,9 @@ extern "C" dt_status dt_page_plan(int B, int n, int N, int page_size, int num_pa
   if (ensure_dynamic_smem(reinterpret_cast<const void*>(page_plan_kernel), 6 * sizeof(int) * (DT_PAGED_MAX_BATCH + 1)) !=
       cudaSuccess)
     return DT_ERR_CUDA;
-  // few requests and rows: fewer threads start, and meet, sooner (one tree: 6.0 us, with 1024 threads 7.0; 64 trees: 11.2,
-  // with 1024 threads 8.8)
-  const int threads = N <= 256 && B <= 512 && grid == 1 ? 256 : kPlanThreads;
+  // few rows: fewer threads start, and meet, sooner. Measured in us (device, other kernels before and behind it), 256 and
+  // 1024 threads: one tree of 8 nodes 2.7 and 4.0, 256 tokens 3.1 and 4.4, 512 3.8 and 4.6, 48 trees of 16 nodes 4.1 and 4.4,
+  // 62 4.7 and 4.5, one prompt of 1000 tokens 3.9 and 4.1, of 2000 5.5 and 4.6. A thread has two requests.
+  const int threads = N <= 768 && B <= 512 && grid == 1 ? 256 : kPlanThreads;
   return at_launch(page_plan_kernel, grid, threads, smem, stream, p, static_cast<WsHeader*>(workspace));
 }

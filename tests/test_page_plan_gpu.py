@@ -151,6 +151,23 @@ def test_many_rows_take_a_second_launch(dtlib):
             check(dtlib, ref, state, grow, [1] * B, n=1)
 
 
+@pytest.mark.parametrize("B,n", [(256, 1), (257, 1), (48, 16), (769, 1), (511, 1), (512, 1), (513, 1), (12, 64), (13, 64)])
+def test_around_the_sizes_of_a_block(dtlib, B, n):
+    """Requests and rows about what 256 threads take, of trees, of their accepted paths and of prompts with as many rows."""
+    r = random.Random(B)
+    ref = Pool(B, B * 12, 12, 16)
+    state = ref.tensors()
+    lens = [r.randint(0, 90) for _ in range(B)]
+    check(dtlib, ref, state, [0] * B, lens, rows=sum(lens))
+    check(dtlib, ref, state, lens, [n] * B, n=n, depth=[[r.randint(1, n) for _ in range(n)] for _ in range(B)])
+    kept = [r.randint(0, n) for _ in range(B)]
+    check(dtlib, ref, state, lens, kept, n=n, path=[sorted(r.sample(range(n), a)) + [-1] * (n - a) for a in kept])
+    lens = [x + a for x, a in zip(lens, kept)]
+    grow = [B * n // B if b else B * n - (B - 1) * (B * n // B) for b in range(B)]
+    check(dtlib, ref, state, lens, [min(g, 30) for g in grow], rows=B * n)
+    check(dtlib, ref, state, [-1 if b % 2 else x + min(g, 30) for b, (x, g) in enumerate(zip(lens, grow))], [0] * B)
+
+
 def test_a_pool_that_runs_out(dtlib):
     ref = Pool(5, 10, 20, 16)
     state = ref.tensors()
