@@ -12,8 +12,9 @@
 //
 // Bound by latency: a few hundred bytes to a few hundred kilobytes. Every CTA scans all requests (two a thread, all in
 // shared memory) and does its part of the moves and of the rows; nothing that it reads is written by another, but for the
-// lengths and the state's counts, which the last CTA to finish writes. Measured: one tree of 8 nodes 6.0 us, 64 trees of 16
-// 8.8, 256 prompts of up to 2500 tokens 12 (two launches, one for the rows, took 32); a call costs the host 10.
+// lengths and the state's counts, which the last CTA to finish writes. Measured on the device, call behind call in a graph:
+// a plan for one tree of 8 nodes 3.2 us, for 64 trees of 16 5.8; 256 prompts of up to 2500 tokens, in and out again, 19 for the
+// two (in two launches each, one for the rows, the prompts alone took 32). A call costs the host 10.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -291,8 +292,8 @@ extern "C" dt_status dt_page_plan(int B, int n, int N, int page_size, int num_pa
   p.held = held; p.free_pages = free_pages; p.free_count = free_count;
   p.out_lens = out_lens; p.cu = cu_seqlens; p.slots = slots; p.positions = positions;
   // CTAs for the rows, and for the pages that may move: many when prompts come or requests end, few around a tree or a token
-  // (64 trees of 16 nodes: 8.8 us with one CTA, 9.4 with five; 256 prompts: 12 us, with one CTA and a second launch for the
-  // rows 32)
+  // (call by call from the host, 64 trees of 16 nodes: 8.8 us with one CTA, 9.4 with five; 256 prompts: 12 us, with one CTA
+  // and a second launch for the rows 32)
   const long long work = N / 2048 + (pool && n == 0 ? static_cast<long long>(B) * max_pages / 8192 : 0);
   const int grid = work < kPlanMostCtas ? 1 + static_cast<int>(work) : kPlanMostCtas;
   const size_t smem = 6 * sizeof(int) * (static_cast<size_t>(B) + 1);

@@ -23,8 +23,9 @@
 // element in all, and the chain of waits that a step is. d = 64, a token each 73 (floor 40): that chain. Keys brought to
 // fp16 like the values instead of two products: 119 where this took 97. The maximum looked for after the weights, which
 // are made again if one left the headroom: trees 118, of 8 nodes 88. A segment's outputs by the warps of the values: trees
-// the same, pages of 16 112 for 100. The bf16 cache takes 164.8, 101.4 (of 8 96.3, of 3 91.8) and 91.4 for the first, the
-// trees and the last: past 32 rows this one saves memory alone.
+// the same, pages of 16 112 for 100. The bf16 cache takes 167.6, 101.8 (of 8 97.1, of 3 92.3) and 92.6 for the first, the
+// trees and the last: this one is the faster up to 32 rows at d = 128; at d = 64, where trees of 2, 3, 4 and 8 nodes take 49.4,
+// 56.3, 58.1 and 74.3 here and 57.7, 57.4, 57.2 and 64.3 there, up to 8 rows. Past that it saves memory alone.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -1093,8 +1094,8 @@ dt_status pa8_launch(Pa8Params& p, const Pa8Maps& maps, WsHeader* hdr, cudaStrea
 //   R <= 32 (8 nodes): two blocks, 16 rows a thread 80.9 and 74.5; one block 95.8 and 86.5; 32 rows a thread 82.8 and 83.8
 //   R <= 64 (16 nodes): two blocks, 32 rows a thread, sixteen at once 113.5 and 101.5; eight at once 115.1 and 107.3; one
 //     block 120.0 and 116.1; 16 rows a thread 139.8 and 131.4
-//   R <= 128 (32 requests of 32 nodes, D = 128): 32 rows a thread, sixteen at once 104; in an earlier form 134, with 64 rows
-//     a thread 148
+//   R <= 128 (32 requests of 32 nodes): 32 rows a thread, sixteen at once 102.8 and 95.0; eight at once 106.4 and 99.2 (in an
+//     earlier form at D = 128, 64 rows a thread 148 where 32 took 134; 16 rows are more warps than a CTA has)
 template <int D>
 dt_status pa8_pick(Pa8Params& p, const Pa8Maps& maps, WsHeader* hdr, cudaStream_t stream) {
   if (p.R <= 8) return pa8_launch<D, 16, 8, 2, 8>(p, maps, hdr, stream);
